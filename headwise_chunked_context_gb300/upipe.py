@@ -46,6 +46,12 @@ EXPORTS = (
     "upipe_ce_fwd_bwd",
     "upipe_mlp_choose_t",
     "upipe_ce_choose_t",
+    "upipe_rope_freqs",
+    "upipe_rope_init",
+    "upipe_rope_apply",
+    "upipe_qk_norm_rope_fwd",
+    "upipe_qk_norm_rope_workspace_bytes",
+    "upipe_qk_norm_rope_bwd",
     "upipe_offload_async",
     "upipe_prefetch_async",
     "upipe_copies_join",
@@ -59,7 +65,7 @@ EXPORTS = (
 
 KINDS = ("rope_table", "qkv_gemm", "attn_fwd", "oproj_gemm", "do_gemm", "dwo_gemm", "attn_bwd_dq",
          "attn_bwd_dkdv", "dwqkv_gemm", "dx_gemm", "delta", "zero_rows", "alst_gu", "alst_gemm", "alst_wgrad",
-         "ce_rows")
+         "ce_rows", "qk_rope", "norm_sum")
 
 
 class UpipeError(RuntimeError):
@@ -93,6 +99,26 @@ class CeCfg(ctypes.Structure):
     """Mirror of ``upipe_ce_cfg``."""
 
     _fields_ = [("L", ctypes.c_int64), ("D", ctypes.c_int32), ("V", ctypes.c_int32), ("T", ctypes.c_int32)]
+
+
+class RopeTable(ctypes.Structure):
+    """Mirror of ``upipe_rope``."""
+
+    _fields_ = [("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("magnitude", ctypes.c_double), ("step", ctypes.c_uint64 * 128)]
+
+
+class Rows(ctypes.Structure):
+    """Mirror of ``upipe_rows``."""
+
+    _fields_ = [("p", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class QkCfg(ctypes.Structure):
+    """Mirror of ``upipe_qk_cfg``."""
+
+    _fields_ = [("L", ctypes.c_int64), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("pos0", ctypes.c_int64),
+                ("eps", ctypes.c_float)]
 
 
 @dataclass(frozen=True)
@@ -159,6 +185,22 @@ def lib() -> ctypes.CDLL:
         L.upipe_ce_choose_t.argtypes = [ccfg, ctypes.c_size_t]
         L.upipe_ce_fwd_bwd.restype = ctypes.c_int
         L.upipe_ce_fwd_bwd.argtypes = [ccfg, P, P, P, ctypes.c_float, P, P, P, P, ctypes.c_size_t, P]
+        rope, rows, qk = ctypes.POINTER(RopeTable), ctypes.POINTER(Rows), ctypes.POINTER(QkCfg)
+        f64p = ctypes.POINTER(ctypes.c_double)
+        L.upipe_rope_freqs.restype = ctypes.c_int
+        L.upipe_rope_freqs.argtypes = [ctypes.c_int, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
+                                       ctypes.c_double, ctypes.c_int64, f64p]
+        L.upipe_rope_init.restype = ctypes.c_int
+        L.upipe_rope_init.argtypes = [rope, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_double, f64p]
+        L.upipe_rope_apply.restype = ctypes.c_int
+        L.upipe_rope_apply.argtypes = [rope, qk, rows, rows, P, rows, rows, ctypes.c_int, P]
+        L.upipe_qk_norm_rope_fwd.restype = ctypes.c_int
+        L.upipe_qk_norm_rope_fwd.argtypes = [rope, qk, rows, rows, P, P, P, rows, rows, P]
+        L.upipe_qk_norm_rope_workspace_bytes.restype = ctypes.c_size_t
+        L.upipe_qk_norm_rope_workspace_bytes.argtypes = [rope, qk]
+        L.upipe_qk_norm_rope_bwd.restype = ctypes.c_int
+        L.upipe_qk_norm_rope_bwd.argtypes = [rope, qk, rows, rows, P, P, P, rows, rows, rows, rows, P, P, P,
+                                             ctypes.c_size_t, P]
         L.upipe_offload_async.restype = ctypes.c_int
         L.upipe_offload_async.argtypes = [P, P, ctypes.c_size_t, P]
         L.upipe_prefetch_async.restype = ctypes.c_int
@@ -630,3 +672,179 @@ def ce_loss(h, W, labels, scale, T):
     dW = torch.empty(W.shape, dtype=torch.float32, device=h.device)
     ce_fwd_bwd(h, W, labels, scale, loss, dh, dW, T)
     return loss, dh, dW
+
+
+# --------------------------- rotary positions, norms of queries and keys
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+class Rope:
+    """Rotary positions of heads of `d` elements: made once (host arithmetic,
+    upipe_rope_freqs and upipe_rope_init) and handed to the calls below.
+
+    rot: rotated leading elements of each head (None: all of them).
+    layout: "half" pairs (i, i + rot/2), "interleaved" (2i, 2i + 1).
+    scaling: None, ("linear", factor) or ("bands", factor, low, high, orig_len).
+    magnitude: factor of the rotated elements.
+    freqs: radians per position of each pair, in place of theta and scaling."""
+
+    def __init__(self, d: int = 128, rot=None, layout: str = "half", theta: float = 500000.0, scaling=None,
+                 magnitude: float = 1.0, freqs=None):
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout: expected 'half' or 'interleaved', got {layout!r}")
+        self.d, self.rot, self.layout, self.magnitude = d, d if rot is None else rot, layout, float(magnitude)
+        if not 0 <= self.rot <= 256 or self.rot % 2:
+            raise ValueError(f"rot: expected an even number of 0 .. {min(d, 256)}, got {self.rot}")
+        n = self.rot // 2
+        f = (ctypes.c_double * max(n, 1))()
+        if freqs is None:
+            kind, *args = scaling or (None,)
+            if (kind, len(args)) not in ((None, 0), ("linear", 1), ("bands", 4)):
+                raise ValueError("scaling: expected None, ('linear', factor) or ('bands', factor, low, high, "
+                                 f"orig_len), got {scaling!r}")
+            factor, low, high, orig = (*args, 0.0, 0.0, 0)[:4] if args else (1.0, 0.0, 0.0, 0)
+            _check(lib().upipe_rope_freqs(self.rot, theta, {None: 0, "linear": 1, "bands": 2}[kind], factor, low, high,
+                                          int(orig), f), "upipe_rope_freqs")
+        else:
+            if scaling is not None:
+                raise ValueError("freqs and scaling: give one of them")
+            freqs = [float(x) for x in freqs]
+            if len(freqs) != n:
+                raise ValueError(f"freqs: expected {n}, got {len(freqs)}")
+            f[:n] = freqs
+        self.freqs = tuple(f[:n])
+        self.table = RopeTable()
+        _check(lib().upipe_rope_init(ctypes.byref(self.table), d, self.rot, ROPE_LAYOUTS[layout], self.magnitude, f),
+               "upipe_rope_init")
+        self._ref = ctypes.byref(self.table)
+
+
+def _rows(t, L, d, heads, name):
+    """A bf16 [L, heads, d] tensor, its rows and heads at any stride that
+    keeps every head 16-byte aligned, as the library's description of it."""
+    if t is None:
+        raise ValueError(f"{name}: missing")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != L or shape[2] != d or shape[1] != heads or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: expected {(L, heads, d)} {torch.bfloat16}, got {tuple(shape)} {t.dtype}")
+    row, head, one = t.stride()
+    p = t.data_ptr()
+    if one != 1 or row % 8 or head % 8 or p % 16:
+        raise ValueError(f"{name}: expected heads of contiguous elements on 16-byte boundaries, got strides "
+                         f"{(row, head, one)} at {p:#x}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return ctypes.byref(Rows(p, row, head))
+
+
+def _qk_call(rope, q, k, pos0, positions, eps=0.0):
+    """(L, H, Hkv, upipe_qk_cfg, positions' pointer) of one call."""
+    if q is None or q.dim() != 3:
+        raise ValueError("q: expected a [L, heads, d] tensor")
+    L, H = q.shape[0], q.shape[1]
+    Hkv = 0 if k is None else k.shape[1] if k.dim() == 3 else -1
+    if positions is not None:
+        if pos0:
+            raise ValueError("pos0 and positions: give one of them")
+        _expect(positions, (L,), torch.int32, "positions")
+        _on_device(positions=positions)
+    return L, H, Hkv, ctypes.byref(QkCfg(L, H, Hkv, pos0, eps)), _ptr(positions)
+
+
+def rope_apply(rope: Rope, q, k, qo, ko, pos0: int = 0, positions=None, transpose: bool = False, stream=None):
+    """upipe_rope_apply: q [L, H, d] into qo and k [L, Hkv, d] (or None) into
+    ko, bf16, rotated to positions pos0, pos0 + 1, ... or `positions` [L]
+    int32; `transpose` rotates gradients back.  qo may be q, and ko k."""
+    L, H, Hkv, c, pos = _qk_call(rope, q, k, pos0, positions)
+    d = rope.d
+    rq, ro = _rows(q, L, d, H, "q"), _rows(qo, L, d, H, "qo")
+    rk, rko = (_rows(k, L, d, Hkv, "k"), _rows(ko, L, d, Hkv, "ko")) if k is not None else (None, None)
+    _check(lib().upipe_rope_apply(rope._ref, c, rq, rk, pos, ro, rko, int(transpose), _stream(stream)),
+           "upipe_rope_apply")
+
+
+def qk_norm_rope_fwd(rope: Rope, q, k, wq, wk, qo, ko, eps: float = 1e-6, pos0: int = 0, positions=None, stream=None):
+    """upipe_qk_norm_rope_fwd: RMS norm of each head with weights wq, wk [d]
+    fp32, then the rotation, q into qo and k (or None, with wk None) into ko."""
+    L, H, Hkv, c, pos = _qk_call(rope, q, k, pos0, positions, eps)
+    d = rope.d
+    rq, ro = _rows(q, L, d, H, "q"), _rows(qo, L, d, H, "qo")
+    rk, rko = (_rows(k, L, d, Hkv, "k"), _rows(ko, L, d, Hkv, "ko")) if k is not None else (None, None)
+    _norm_weights(d, wq=wq, wk=wk if k is not None else wq)
+    _check(lib().upipe_qk_norm_rope_fwd(rope._ref, c, rq, rk, _ptr(wq), _ptr(wk) if k is not None else None, pos, ro,
+                                        rko, _stream(stream)), "upipe_qk_norm_rope_fwd")
+
+
+def _norm_weights(d, **ws):
+    for name, w in ws.items():
+        _expect(w, (d,), torch.float32, name)
+    _on_device(**ws)
+
+
+def qk_norm_rope_workspace_bytes(rope: Rope, L: int, H: int, Hkv: int = 0) -> int:
+    return int(lib().upipe_qk_norm_rope_workspace_bytes(rope._ref, ctypes.byref(QkCfg(L, H, Hkv, 0, 0.0))))
+
+
+def qk_norm_rope_bwd(rope: Rope, q, k, wq, wk, dqo, dko, dq, dk, dwq, dwk, eps: float = 1e-6, pos0: int = 0,
+                     positions=None, ws=None, stream=None):
+    """upipe_qk_norm_rope_bwd: from q, k and the gradients dqo, dko of the
+    outputs to dq, dk (bf16) and dwq, dwk [d] fp32 (all written)."""
+    L, H, Hkv, c, pos = _qk_call(rope, q, k, pos0, positions, eps)
+    d, keys = rope.d, k is not None
+    tq = [_rows(t, L, d, H, n) for t, n in ((q, "q"), (dqo, "dqo"), (dq, "dq"))]
+    tk = [_rows(t, L, d, Hkv, n) for t, n in ((k, "k"), (dko, "dko"), (dk, "dk"))] if keys else [None] * 3
+    _norm_weights(d, wq=wq, dwq=dwq)
+    if keys:
+        _norm_weights(d, wk=wk, dwk=dwk)
+    need = int(lib().upipe_qk_norm_rope_workspace_bytes(rope._ref, c))
+    ws, nbytes = _call_ws(need, ws, q.device, stream)
+    _check(lib().upipe_qk_norm_rope_bwd(rope._ref, c, tq[0], tk[0], _ptr(wq), _ptr(wk) if keys else None, pos, tq[1],
+                                        tk[1], tq[2], tk[2], _ptr(dwq), _ptr(dwk) if keys else None, _ptr(ws), nbytes,
+                                        _stream(stream)), "upipe_qk_norm_rope_bwd")
+
+
+def _call_ws(need, ws, device, stream):
+    """The caller's workspace, checked, or one made for this call: it belongs
+    to the current stream's memory, so it is told of the stream it is used on."""
+    if ws is None:
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if stream is not None:
+            ws.record_stream(stream)
+    _expect_ws(ws, need)
+    return ws, ws.numel() * ws.element_size()
+
+
+def _dense(t):
+    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def rope_forward(rope: Rope, q, k=None, pos0: int = 0, positions=None):
+    """Allocates and returns (q, k) rotated to their positions (k None: None)."""
+    qo, ko = _dense(q), _dense(k)
+    rope_apply(rope, q, k, qo, ko, pos0, positions)
+    return qo, ko
+
+
+def rope_backward(rope: Rope, dqo, dko=None, pos0: int = 0, positions=None):
+    """Gradients (dq, dk) of rope_forward's inputs from those of its outputs."""
+    dq, dk = _dense(dqo), _dense(dko)
+    rope_apply(rope, dqo, dko, dq, dk, pos0, positions, transpose=True)
+    return dq, dk
+
+
+def qk_norm_rope_forward(rope: Rope, q, k, wq, wk, eps: float = 1e-6, pos0: int = 0, positions=None):
+    """Allocates and returns (q, k) normalised and rotated."""
+    qo, ko = _dense(q), _dense(k)
+    qk_norm_rope_fwd(rope, q, k, wq, wk, qo, ko, eps, pos0, positions)
+    return qo, ko
+
+
+def qk_norm_rope_backward(rope: Rope, q, k, wq, wk, dqo, dko, eps: float = 1e-6, pos0: int = 0, positions=None):
+    """Allocates and returns (dq, dk, dwq, dwk) of qk_norm_rope_forward."""
+    dq, dk = _dense(q), _dense(k)
+    dwq, dwk = _dense(wq), _dense(wk) if k is not None else None
+    qk_norm_rope_bwd(rope, q, k, wq, wk, dqo, dko, dq, dk, dwq, dwk, eps, pos0, positions)
+    return dq, dk, dwq, dwk

@@ -28,7 +28,10 @@
  *
  * Around the layer the library also computes, tiled along the sequence, the
  * block's SwiGLU MLP and the LM-head cross-entropy loss (upipe_mlp_*,
- * upipe_ce_*, below).
+ * upipe_ce_*, below).  For callers of the attention core it computes what
+ * stands before it, rotary positions and the norms of queries and keys
+ * (upipe_rope_*, upipe_qk_norm_rope_*), and the core with a sliding window
+ * and sink tokens in place of the full causal mask (upipe_window_*).
  *
  * Conventions (readings of points the pages leave open)
  * -----------------------------------------------------
@@ -369,6 +372,100 @@ int upipe_ce_choose_t(const upipe_ce_cfg* cfg, size_t budget_bytes);
 int upipe_ce_fwd_bwd(const upipe_ce_cfg* cfg, const uint16_t* h, const uint16_t* W, const int32_t* labels,
                      float scale, float* loss, uint16_t* dh, float* dW, void* ws, size_t ws_bytes, void* stream);
 
+/* Rotary positions of queries and keys, for callers of the attention core
+ * (the layer entries above rotate inside their projection).  RoFormer, listed
+ * under "Builds on" on the "Untied Ulysses" index page, with the forms that
+ * long contexts use.  For a head x of d elements at position p, frequencies
+ * f_i (radians per position, i < rot/2) and a magnitude c:
+ *   y_a = c (x_a cos(p f_i) - x_b sin(p f_i)),
+ *   y_b = c (x_a sin(p f_i) + x_b cos(p f_i)),
+ * (a, b) = (i, i + rot/2) in the half layout, (2i, 2i + 1) in the
+ * interleaved one; elements from rot on are copied.
+ *
+ * upipe_rope_freqs writes f_0 .. f_{rot/2-1} = theta^(-2i/rot) to `freqs`:
+ *   UPIPE_ROPE_UNSCALED  as they are
+ *   UPIPE_ROPE_LINEAR    divided by factor (positions interpolated)
+ *   UPIPE_ROPE_BANDS     f_i (k_i + (1 - k_i) / factor), k_i = the turns that
+ *                        f_i makes in orig_len positions, taken from [low,
+ *                        high] to [0, 1] and clamped: fast pairs are kept,
+ *                        slow ones divided, those between blended
+ * (factor is ignored when unscaled; low, high and orig_len unless BANDS.)
+ * upipe_rope_init fills a upipe_rope from given frequencies (any finite
+ * values); the caller keeps it and may copy it.  Both are host arithmetic.
+ *   d          head size, a multiple of 8, 8 .. UPIPE_ROPE_MAX_D
+ *   rot        rotated leading elements, even, 0 .. d (0: none)
+ *   magnitude  finite, at most 1e30 in size; 1 leaves lengths as they are   */
+#define UPIPE_ROPE_MAX_D 256
+#define UPIPE_ROPE_HALF 0
+#define UPIPE_ROPE_INTERLEAVED 1
+#define UPIPE_ROPE_UNSCALED 0
+#define UPIPE_ROPE_LINEAR 1
+#define UPIPE_ROPE_BANDS 2
+typedef struct upipe_rope {
+  int32_t d;
+  int32_t rot;
+  int32_t layout;
+  int32_t reserved;
+  double magnitude;
+  uint64_t step[UPIPE_ROPE_MAX_D / 2]; /* f_i / 2 pi modulo 1, in units of 2^-64 turns */
+} upipe_rope;
+int upipe_rope_freqs(int rot, double theta, int scaling, double factor, double low, double high, int64_t orig_len,
+                     double* freqs);
+int upipe_rope_init(upipe_rope* r, int d, int rot, int layout, double magnitude, const double* freqs);
+
+/* A bf16 tensor [L, heads, d]: element (t, h, i) at p[t*row + h*head + i].
+ * p 16-byte aligned, row and head multiples of 8 and not negative.  A
+ * written tensor has no element at two places: either head >= d and
+ * row >= (heads-1)*head + d (token-major, a slice of a fused projection's
+ * output included), or row >= d and head >= (L-1)*row + d (head-major).    */
+typedef struct upipe_rows {
+  uint16_t* p;
+  int64_t row;
+  int64_t head;
+} upipe_rows;
+
+/* L tokens (1 .. 2^31-1); H query heads (1 .. 65536) and Hkv key heads (0:
+ * no keys, the key arguments are then ignored); pos0: the position of row 0
+ * when `positions` is NULL (a rank's first row of a sequence-sharded input,
+ * a new token's index), below 2^62 in size; eps: of the norm, >= 0 (ignored
+ * by upipe_rope_apply; with eps = 0 a head of zeros gives NaN).            */
+typedef struct upipe_qk_cfg {
+  int64_t L;
+  int32_t H;
+  int32_t Hkv;
+  int64_t pos0;
+  float eps;
+} upipe_qk_cfg;
+
+/* Rotates q into qo and k into ko.  transpose = 1 applies the transposed
+ * rotation (by -p f_i, with the same magnitude): the gradients of q and k
+ * from those of qo and ko.
+ *   positions  [L] int32 (any values) or NULL: pos0, pos0 + 1, ...
+ * An output may be its own input (same p, row and head), and must not
+ * overlap an input in any other way.                                       */
+int upipe_rope_apply(const upipe_rope* r, const upipe_qk_cfg* c, const upipe_rows* q, const upipe_rows* k,
+                     const int32_t* positions, const upipe_rows* qo, const upipe_rows* ko, int transpose,
+                     void* stream);
+
+/* RMS norm of each query and key head and the rotation in one pass:
+ * z = w x / sqrt(mean(x^2) + eps), then as above.  wq, wk [d] fp32.
+ * In-place and overlap rules as upipe_rope_apply.                          */
+int upipe_qk_norm_rope_fwd(const upipe_rope* r, const upipe_qk_cfg* c, const upipe_rows* q, const upipe_rows* k,
+                           const float* wq, const float* wk, const int32_t* positions, const upipe_rows* qo,
+                           const upipe_rows* ko, void* stream);
+
+/* Its gradients, from the same q, k (the norm is recomputed) and the
+ * gradients dqo, dko of qo, ko.
+ *   dq, dk    written; dq may be dqo (or q) and dk dko (or k) with equal strides
+ *   dwq, dwk  [d] fp32 (written, not accumulated), sums over all tokens and
+ *             heads in an order fixed by the sizes
+ *   ws        at least upipe_qk_norm_rope_workspace_bytes (0: invalid)     */
+size_t upipe_qk_norm_rope_workspace_bytes(const upipe_rope* r, const upipe_qk_cfg* c);
+int upipe_qk_norm_rope_bwd(const upipe_rope* r, const upipe_qk_cfg* c, const upipe_rows* q, const upipe_rows* k,
+                           const float* wq, const float* wk, const int32_t* positions, const upipe_rows* dqo,
+                           const upipe_rows* dko, const upipe_rows* dq, const upipe_rows* dk, float* dwq, float* dwk,
+                           void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads and clears the device status word of
  * the current device.  Returns UPIPE_OK, UPIPE_ERR_DEVICE_TIMEOUT if a
  * bounded wait of any earlier call ran out, or UPIPE_ERR_CUDA.              */
@@ -403,7 +500,9 @@ int upipe_debug_wait_timeout(uint64_t limit_ns, void* stream);
 #define UPIPE_KIND_ALST_GEMM 13   /* MLP and loss GEMMs with one output per row: y, dH, dx, logits, dh */
 #define UPIPE_KIND_ALST_WGRAD 14  /* MLP and loss weight gradients, carried across sequence tiles */
 #define UPIPE_KIND_CE_ROWS 15     /* softmax rows of the loss */
-#define UPIPE_KIND_COUNT 16
+#define UPIPE_KIND_QK_ROPE 16     /* rotation of queries and keys, with or without their norm */
+#define UPIPE_KIND_NORM_SUM 17    /* sums of the norm weights' gradients */
+#define UPIPE_KIND_COUNT 18
 int64_t upipe_launch_count(void);
 void upipe_profile_enable(int on);
 int upipe_profile_read(double* ms, int64_t* launches, int n);

@@ -1,0 +1,220 @@
+"""Pins of the oracle of rotary positions, query/key norms and windowed
+attention (oracle/local_oracle.py) against things other than itself: complex
+multiplication, torch float64 autograd, finite differences, closed forms and
+the full causal oracle; and the host side of the library's rotary tables."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from headwise_chunked_context_gb300 import upipe
+from oracle import local_oracle as loc
+from oracle import upipe_oracle as orc
+
+R = np.random.default_rng
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot", [(8, 8), (16, 6), (12, 0), (16, 2)])
+def test_rope_is_complex_multiplication_and_its_transpose_undoes_it(layout, d, rot):
+    x = R(0).standard_normal((5, 3, d))
+    pos = np.array([0, 1, 7, -4, 1 << 20])
+    f = loc.frequencies(rot) if rot else np.zeros(0)
+    y = loc.rope(x, pos, f, rot, layout, magnitude=1.5)
+    a, b = loc.pairs(rot, layout)
+    z = (x[..., a] + 1j * x[..., b]) * np.exp(1j * pos[:, None, None] * f) * 1.5
+    np.testing.assert_allclose(y[..., a], z.real, atol=1e-12)
+    np.testing.assert_allclose(y[..., b], z.imag, atol=1e-12)
+    assert np.array_equal(y[..., rot:], x[..., rot:])
+    back = loc.rope(y, pos, f, rot, layout, magnitude=1.5, transpose=True)
+    np.testing.assert_allclose(back[..., :rot], 2.25 * x[..., :rot], atol=1e-12)
+
+
+def test_frequencies_of_the_scalings():
+    f = loc.frequencies(8, theta=16.0)
+    np.testing.assert_allclose(f, [1.0, 0.5, 0.25, 0.125])
+    np.testing.assert_allclose(loc.frequencies(8, 16.0, ("linear", 4.0)), f / 4)
+    # turns in 16 pi positions: 8, 4, 2, 1: above 4 kept, at 1 divided, 2 blended by 1/3
+    got = loc.frequencies(8, 16.0, ("bands", 4.0, 1.0, 4.0, 16 * math.pi))
+    np.testing.assert_allclose(got, [1.0, 0.5, 0.25 * (1 / 3 + 2 / 3 / 4), 0.125 / 4])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_norm_rope_gradients_match_torch_autograd_and_differences(layout):
+    r = R(1)
+    L, n, d, rot = 6, 2, 12, 8
+    x, w, dy = r.standard_normal((L, n, d)), 1 + 0.1 * r.standard_normal(d), r.standard_normal((L, n, d))
+    pos, f = np.arange(L) + 3, loc.frequencies(rot, 100.0)
+    dx, dw, mag = loc.norm_rope_bwd(x, w, 1e-3, dy, pos, f, rot, layout, 0.7)
+    tx, tw = torch.tensor(x, requires_grad=True), torch.tensor(w, requires_grad=True)
+    z = tx * torch.rsqrt(tx.square().mean(-1, keepdim=True) + 1e-3) * tw
+    a, b = loc.pairs(rot, layout)
+    ang = torch.tensor(pos[:, None] * f)[:, None]
+    u = torch.complex(z[..., a], z[..., b]) * torch.polar(torch.full_like(ang, 0.7), ang)
+    loss = (u.real * torch.tensor(dy[..., a])).sum() + (u.imag * torch.tensor(dy[..., b])).sum() + \
+        (z[..., rot:] * torch.tensor(dy[..., rot:])).sum()
+    loss.backward()
+    np.testing.assert_allclose(dx, tx.grad.numpy(), atol=1e-12)
+    np.testing.assert_allclose(dw, tw.grad.numpy(), atol=1e-12)
+    assert np.all(mag >= np.abs(dw) - 1e-12)
+    fn = lambda x_, w_: float(np.sum(loc.norm_rope(x_, w_, 1e-3, pos, f, rot, layout, 0.7) * dy))  # noqa: E731
+    v, u = r.standard_normal(x.shape), r.standard_normal(d)
+    e = 1e-6
+    np.testing.assert_allclose((fn(x + e * v, w) - fn(x - e * v, w)) / (2 * e), np.sum(dx * v), rtol=1e-6)
+    np.testing.assert_allclose((fn(x, w + e * u) - fn(x, w - e * u)) / (2 * e), np.sum(dw * u), rtol=1e-6)
+
+
+def test_window_mask_by_hand():
+    got = loc.visible(np.arange(5), np.arange(5), window=2, sinks=1).astype(int)
+    assert got.tolist() == [[1, 0, 0, 0, 0], [1, 1, 0, 0, 0], [1, 1, 1, 0, 0], [1, 0, 1, 1, 0], [1, 0, 0, 1, 1]]
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 2), (3, 0), (4, 2), (9, 1), (100, 0), (2, 50)])
+def test_window_matches_torch_autograd(window, sinks):
+    r = R(2)
+    L, H, Hkv, d = 17, 4, 2, 8
+    q, k, v, do = (r.standard_normal((L, h, d)) for h in (H, Hkv, Hkv, H))
+    o, lse = loc.window_fwd(q, k, v, window, sinks)
+    dq, dk, dv = loc.window_bwd(q, k, v, o, do, window, sinks)
+    t = [torch.tensor(x, requires_grad=True) for x in (q, k, v)]
+    i, j = torch.arange(L)[:, None], torch.arange(L)[None]
+    keep = (j <= i) & ((j > i - window) | (j < sinks))
+    kk, vv = (x.repeat_interleave(H // Hkv, 1).transpose(0, 1) for x in t[1:])
+    y = torch.nn.functional.scaled_dot_product_attention(t[0].transpose(0, 1), kk, vv, attn_mask=keep).transpose(0, 1)
+    y.backward(torch.tensor(do))
+    np.testing.assert_allclose(o, y.detach().numpy(), atol=1e-12)
+    for got, x in zip((dq, dk, dv), t):
+        np.testing.assert_allclose(got, x.grad.numpy(), atol=1e-12)
+    if window >= L or sinks >= L:  # the full causal attention
+        fo, fl = orc.attention_core_fwd(q, k, v)
+        np.testing.assert_allclose(o, fo, atol=1e-12)
+        np.testing.assert_allclose(lse, fl, atol=1e-12)
+    if window == 1 and not sinks:  # each query sees itself alone
+        np.testing.assert_allclose(o, np.repeat(v, 2, 1), atol=1e-12)
+
+
+# ------------------------------------------------ the library's host side
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+    if not os.path.exists(upipe.LIB_PATH):
+        from headwise_chunked_context_gb300 import build
+        build.build()
+    return upipe.lib()
+
+
+@pytest.mark.parametrize("scaling", [None, ("linear", 4.0), ("bands", 8.0, 1.0, 4.0, 8192)])
+@pytest.mark.parametrize("rot", [2, 10, 128, 256])
+def test_rope_table_holds_the_frequencies(lib, rot, scaling):
+    r = upipe.Rope(256, rot=rot, theta=500000.0, scaling=scaling)
+    f = loc.frequencies(rot, 500000.0, scaling)
+    np.testing.assert_allclose(r.freqs, f, rtol=1e-14)
+    # step / 2^64 turns per position, modulo one turn, cut off at 2^-64
+    steps = np.array([int(r.table.step[i]) for i in range(rot // 2)], dtype=np.float64) / 2.0 ** 64
+    np.testing.assert_allclose(steps, (f / (2 * np.pi)) % 1.0, rtol=1e-14, atol=2.0 ** -64)
+
+
+def test_rope_table_turns_are_exact_at_far_positions(lib):
+    """The wrapping 64-bit product of the table's step and a position is the
+    angle: against 80-digit arithmetic, off by no more than the position
+    times half a step of the frequency's fp64 value (and of pi's)."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 80
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281257241799725606965068")
+    r = upipe.Rope(128)
+    for p in (1, 12345, (1 << 21) + 7, (1 << 31) - 1, -5, -(1 << 31)):
+        for i in (0, 1, 17, 63):
+            turn = (int(r.table.step[i]) * p) % (1 << 64) / 2.0 ** 64
+            want = float((Decimal(r.freqs[i]) * p / two_pi) % 1) % 1.0
+            off = abs(turn - want)
+            off = min(off, 1 - off)
+            assert off <= abs(p) * (r.freqs[i] / (2 * math.pi) * 2.0 ** -52 + 2.0 ** -64) + 2.0 ** -52
+
+
+def test_rope_given_frequencies_negative_and_large(lib):
+    r = upipe.Rope(16, rot=6, freqs=[-0.25, 1e-300, 1000.0])
+    got = [int(r.table.step[i]) / 2.0 ** 64 for i in range(3)]
+    np.testing.assert_allclose(got, [1 - 0.25 / (2 * math.pi), 0.0, (1000.0 / (2 * math.pi)) % 1.0], rtol=1e-13)
+    assert int(upipe.Rope(8, rot=2, freqs=[-1e-300]).table.step[0]) == 0  # 1 - 1e-300 turns is one turn
+
+
+@pytest.mark.parametrize("kw", [
+    dict(d=12), dict(d=0), dict(d=264), dict(d=64, rot=66), dict(d=64, freqs=[math.inf] * 32),
+    dict(d=64, magnitude=math.nan), dict(d=64, magnitude=1e31), dict(d=64, theta=0.0), dict(d=64, theta=math.inf),
+    dict(d=64, scaling=("linear", 0.0)), dict(d=64, scaling=("bands", 8.0, 4.0, 1.0, 8192)),
+    dict(d=64, scaling=("bands", 8.0, 1.0, 4.0, 0)),
+])
+def test_rope_refuses_what_it_cannot_hold(lib, kw):
+    with pytest.raises((upipe.UpipeError, ValueError)):
+        upipe.Rope(**kw)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rot=5), dict(rot=-2), dict(layout="pairs"), dict(scaling=("cubic", 2.0)), dict(scaling=("linear",)),
+    dict(freqs=[1.0]), dict(freqs=[1.0] * 64, scaling=("linear", 2.0)),
+])
+def test_rope_binding_refuses(lib, kw):
+    with pytest.raises(ValueError):
+        upipe.Rope(128, **kw)
+
+
+def test_qk_binding_refuses_before_any_launch(lib):
+    """CPU tensors: nothing can launch."""
+    n0 = upipe.launch_count()
+    r = upipe.Rope(128)
+    q, k = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    w = torch.ones(128)
+    for bad in (q.float(), q[:, :, :64], q[0], q.transpose(0, 2), q[:3]):
+        with pytest.raises(ValueError):
+            upipe.rope_apply(r, q, k, bad, k)
+    with pytest.raises(ValueError, match="16-byte"):
+        upipe.rope_apply(r, torch.zeros(4, 8, 129, dtype=torch.bfloat16)[:, :, 1:], None, q, None)
+    with pytest.raises(ValueError, match="16-byte"):
+        upipe.rope_apply(r, torch.zeros(4, 8, 132, dtype=torch.bfloat16)[:, :, :128], None, q, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        upipe.rope_apply(r, q, k, q, k)
+    with pytest.raises(ValueError, match="pos0"):
+        upipe.rope_apply(r, q, k, q, k, pos0=3, positions=torch.zeros(4, dtype=torch.int32))
+    for bad in (torch.zeros(4, dtype=torch.int64), torch.zeros(3, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="positions"):
+            upipe.rope_apply(r, q, k, q, k, positions=bad)
+    with pytest.raises(ValueError):
+        upipe.qk_norm_rope_fwd(r, q, k, w.double(), w, q, k)
+    with pytest.raises(ValueError):
+        upipe.qk_norm_rope_bwd(r, q, k, w, w, q, k, q, k, w[:64], w)
+    assert upipe.launch_count() == n0
+
+
+def _entry(lib, r, **kw):
+    """upipe_rope_apply on made-up aligned addresses; what is wrong is
+    refused before the device is asked for."""
+    import ctypes
+    a = dict(L=4, H=2, Hkv=1, pos0=0, q=(1 << 20, 256, 128), k=(1 << 21, 128, 128), qo=(1 << 22, 256, 128),
+             ko=(1 << 23, 128, 128), transpose=0)
+    a.update(kw)
+    ref = lambda t: ctypes.byref(upipe.Rows(*t)) if t else None  # noqa: E731
+    c = upipe.QkCfg(a["L"], a["H"], a["Hkv"], a["pos0"], 0.0)
+    return lib.upipe_rope_apply(r._ref, ctypes.byref(c), ref(a["q"]), ref(a["k"]), None, ref(a["qo"]), ref(a["ko"]),
+                                a["transpose"], None)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would launch on made-up addresses")
+def test_rope_entry_refuses_bad_shapes_pointers_and_strides(lib):
+    r = upipe.Rope(128)
+    bad = [dict(L=0), dict(L=1 << 31), dict(H=0), dict(H=65537), dict(Hkv=-1), dict(pos0=1 << 62),
+           dict(q=None), dict(qo=None), dict(k=None), dict(ko=None), dict(q=(0, 256, 128)), dict(q=((1 << 20) + 8, 256, 128)),
+           dict(q=(1 << 20, 260, 128)), dict(q=(1 << 20, -256, 128)), dict(q=(1 << 20, 1 << 62, 128)),
+           dict(qo=(1 << 22, 128, 128)), dict(qo=(1 << 22, 256, 64)), dict(qo=(1 << 22, 0, 128)),
+           dict(qo=(1 << 22, 128, 256)), dict(transpose=2)]
+    for kw in bad:
+        assert _entry(lib, r, **kw) == upipe.UPIPE_ERR_INVALID_ARG, kw
+    # without a GPU an accepted call ends at the device check
+    for kw in (dict(), dict(k=None, ko=None, Hkv=0), dict(qo=(1 << 22, 128, 512)), dict(q=(1 << 20, 0, 0)),
+               dict(qo=(1 << 22, 4096, 136))):
+        assert _entry(lib, r, **kw) in (upipe.UPIPE_ERR_CUDA, upipe.UPIPE_ERR_UNSUPPORTED_DEVICE), kw
+    assert lib.upipe_qk_norm_rope_workspace_bytes(r._ref, None) == 0
+    assert upipe.qk_norm_rope_workspace_bytes(r, 1 << 20, 32, 8) == 456 * 2 * 128 * 4
+    assert upipe.qk_norm_rope_workspace_bytes(r, 0, 32, 8) == 0
