@@ -1,0 +1,1259 @@
+// Causal attention with a sliding window and sink tokens, forward and
+// backward, tcgen05 + TMEM, and its C entry points.
+//
+// Query i sees key j iff j <= i and (i - j < W or j < S): the last W keys and
+// the first S.  With these keys, per query head h and KV head h / g:
+//   s_ij = q_i k_j / sqrt(d),  LSE_i = ln sum_j exp(s_ij),  P = exp(s - LSE),
+//   O = P V;  dP = dO V^T,  Delta_i = sum_c dO_ic O_ic,  dS = P (dP - Delta),
+//   dQ = dS K / sqrt(d),  dK = dS^T Q / sqrt(d),  dV = P^T dO.
+// Every query sees itself, so no row is empty and the running maximum is
+// finite from a tile's first block (the diagonal one) on.
+//
+// Tiles are 128 queries by 128 keys.  A query tile walks the blocks that hold
+// the windows of its queries, the diagonal one first, then the sink blocks
+// before them; a key tile walks the query tiles up to the last one whose
+// window reaches it, all later ones if it holds a sink.  Blocks that every
+// query of a tile sees whole take no mask.
+//
+// Scores, statistics and every sum are fp32.  P and dS are rounded to bf16
+// where they enter a product (the tensor core's operand type); O, dQ, dK and
+// dV are rounded to bf16 once, from TMEM.
+#include <cmath>
+#include <cstring>
+
+#include "host.h"
+#include "sm103_ptx.cuh"
+
+namespace upipe {
+namespace {
+
+constexpr uint32_t kTmemCols = 512;
+
+struct WinParams {
+  int L, H, Hkv, g;   // q [L, H, 128], k and v [L, Hkv, 128]; g = H / Hkv
+  int window, sinks;  // at most L each
+  __nv_bfloat16* o;   // [L, H, 128]
+  float* lse;         // [H, L]
+  // Per head and 64-query tile a 128-float record: -LSE * log2(e) of the 64
+  // queries (-inf past L), then their Delta (0 past L).
+  const float* ld;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  float scale;       // 1/sqrt(d)
+  float scale_log2;  // log2(e)/sqrt(d)
+  int* status;
+  uint64_t limit_ns;
+};
+
+__device__ __forceinline__ bool sees(int i, int j, const WinParams& p) {
+  return j <= i && (j > i - p.window || j < p.sinks);
+}
+
+// Whether some query of tile qb does not see some key of block kb (of a pair
+// that is walked at all).
+__device__ __forceinline__ bool hides(int qb, int kb, const WinParams& p) {
+  return qb == kb || (kb * 128 <= qb * 128 + 127 - p.window && kb * 128 + 127 >= p.sinks);
+}
+
+// The 128-key blocks that query tile qb walks.
+struct QuerySpan {
+  int qb, n_win, n_sink;
+  __device__ __forceinline__ QuerySpan(int qb_, const WinParams& p) : qb(qb_) {
+    const int lowest = qb * 128 - p.window + 1;  // first key in the first query's window
+    const int first = lowest > 0 ? lowest >> 7 : 0;
+    n_win = qb - first + 1;
+    const int sink_blocks = (p.sinks >> 7) + ((p.sinks & 127) != 0);
+    n_sink = sink_blocks < first ? sink_blocks : first;
+  }
+  __device__ __forceinline__ int count() const { return n_win + n_sink; }
+  __device__ __forceinline__ int block(int j) const { return j < n_win ? qb - j : j - n_win; }
+  __device__ __forceinline__ bool masked(int kb, const WinParams& p) const { return hides(qb, kb, p); }
+};
+
+// Number of 128-query tiles, from kb on, that see key tile kb.
+__device__ __forceinline__ int key_tile_queries(int kb, const WinParams& p) {
+  const int last = (p.L - 1) >> 7;
+  if (kb * 128 < p.sinks) return last - kb + 1;
+  const int64_t reach = (static_cast<int64_t>(kb) * 128 + 126 + p.window) >> 7;  // tile of the last key's last query
+  return (reach < last ? static_cast<int>(reach) : last) - kb + 1;
+}
+
+// Last query that sees key j.
+__device__ __forceinline__ int last_query(int j, const WinParams& p) {
+  const int64_t q = static_cast<int64_t>(j) + p.window - 1;
+  return j < p.sinks || q > 0x7fffffff ? 0x7fffffff : static_cast<int>(q);
+}
+
+// Scores of one query row against keys k0 .. k0 + 127: -inf where hidden.
+__device__ __forceinline__ void hide_row(float (&x)[128], int qpos, int k0, const WinParams& p) {
+  const int after = qpos - k0;              // columns past it are later keys
+  const int before = qpos - p.window - k0;  // columns up to it have left the window
+  const int sink = p.sinks - k0;            // columns before it are sinks
+#pragma unroll
+  for (int c = 0; c < 128; ++c)
+    if (c > after || (c <= before && c >= sink)) x[c] = -INFINITY;
+}
+
+// 32 fp32 accumulators of one row, scaled and rounded to bf16.
+__device__ __forceinline__ void store32_bf16(__nv_bfloat16* out, const uint32_t (&a)[32], float scale) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      h[e] = pack_bf16x2(__uint_as_float(a[8 * q + 2 * e]) * scale, __uint_as_float(a[8 * q + 2 * e + 1]) * scale);
+    st_global_v4(out + q * 8, h[0], h[1], h[2], h[3]);
+  }
+}
+
+// ================================================================= forward
+//
+// One CTA per (head, query tile).  Warp 4 streams Q once and K/V blocks of
+// 128 keys through 3-stage TMA rings; the softmax warps copy Q into TMEM
+// once.  Warp 5 issues S(j) = Q K^T (Q from TMEM) into the TMEM score buffer,
+// warp 6 O += P V (P from TMEM); one thread issues a tcgen05.mma only about
+// every 100 cycles, hence two.  Warps 0-3 own one query row per thread: row
+// maximum and sum are thread-local, P goes to one of two TMEM buffers as
+// packed bf16, and O is rescaled in TMEM only when a row's maximum grows by
+// more than 2^8, which bounds every exponent.
+
+namespace wf {
+constexpr int kTile = 128 * 128 * 2;  // [128][128] bf16, stored as two 64-column halves
+constexpr int kHalf = kTile / 2;
+constexpr int kStages = 3;            // K and V ring depth
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + kTile;
+constexpr int OFF_V = OFF_K + kStages * kTile;
+constexpr int OFF_BAR = OFF_V + kStages * kTile;
+
+enum {
+  B_Q_FULL,
+  B_Q_TMEM,  // Q copied into TMEM by the softmax warps
+  B_K_FULL,
+  B_K_EMPTY = B_K_FULL + kStages,
+  B_V_FULL = B_K_EMPTY + kStages,
+  B_V_EMPTY = B_V_FULL + kStages,
+  B_S_FULL = B_V_EMPTY + kStages,
+  B_S_READ,                  // the softmax warps have read the score buffer
+  B_P_FULL,                  // P written, per P buffer
+  B_P_EMPTY = B_P_FULL + 2,  // P V done: that P buffer free, O up to date
+  B_DRAIN = B_P_EMPTY + 2,
+  B_DRAIN_PV,
+  B_COUNT
+};
+constexpr int OFF_TMEM_SLOT = OFF_BAR + B_COUNT * 8;
+constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+constexpr int kSmemBytes = OFF_ABORT + 8 + 1024;  // + alignment slack
+
+constexpr int kThreads = 224;  // softmax warps 0-3, producer 4, S issuer 5, PV issuer 6
+constexpr int TM_Q = 0;    // Q, packed bf16: columns [0, 64)
+constexpr int TM_S = 64;   // scores: [64, 192)
+constexpr int TM_O = 192;  // O accumulator: [192, 320)
+constexpr int TM_P = 320;  // two P buffers, packed bf16: [320, 384), [384, 448)
+
+}  // namespace wf
+
+__global__ void __launch_bounds__(wf::kThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ WinParams p) {
+  using namespace wf;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // Heads vary fastest: the CTAs in flight hold the same query blocks of
+  // every head, whose K/V blocks (shared within a GQA group) stay in L2, and
+  // the query blocks with the most KV blocks launch first.
+  const int h = static_cast<int>(blockIdx.x) % p.H;
+  const int qb = static_cast<int>(gridDim.x) / p.H - 1 - static_cast<int>(blockIdx.x) / p.H;
+  const int kz = h / p.g;
+  const QuerySpan sp(qb, p);
+  const int n_kv = sp.count();
+  auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+  const WaitCtl w{abort_flag, p.status, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_Q_FULL), 1);
+    mbar_init(bar(B_Q_TMEM), 4);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(B_K_FULL + s), 1);
+      mbar_init(bar(B_K_EMPTY + s), 1);
+      mbar_init(bar(B_V_FULL + s), 1);
+      mbar_init(bar(B_V_EMPTY + s), 1);
+    }
+    mbar_init(bar(B_S_FULL), 1);
+    mbar_init(bar(B_S_READ), 4);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(B_P_FULL + b), 4);
+      mbar_init(bar(B_P_EMPTY + b), 1);
+    }
+    mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN_PV), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(sb + OFF_TMEM_SLOT, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_map(&mq);
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+      mbar_expect_tx(bar(B_Q_FULL), kTile);
+      tma_load_3d(sb + OFF_Q, &mq, bar(B_Q_FULL), 0, qb * 128, h);
+      tma_load_3d(sb + OFF_Q + kHalf, &mq, bar(B_Q_FULL), 64, qb * 128, h);
+      int last_k[kStages], last_v[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) last_k[s] = last_v[s] = -1;
+      for (int j = 0; j < n_kv; ++j) {
+        const int s = j % kStages;
+        const uint32_t ph = (j / kStages) & 1;
+        if (!mbar_wait(bar(B_K_EMPTY + s), ph ^ 1, w)) break;
+        mbar_expect_tx(bar(B_K_FULL + s), kTile);
+        tma_load_3d(sb + OFF_K + s * kTile, &mk, bar(B_K_FULL + s), 0, sp.block(j) * 128, kz);
+        tma_load_3d(sb + OFF_K + s * kTile + kHalf, &mk, bar(B_K_FULL + s), 64, sp.block(j) * 128, kz);
+        last_k[s] = j;
+        if (!mbar_wait(bar(B_V_EMPTY + s), ph ^ 1, w)) break;
+        mbar_expect_tx(bar(B_V_FULL + s), kTile);
+        tma_load_3d(sb + OFF_V + s * kTile, &mv, bar(B_V_FULL + s), 0, sp.block(j) * 128, kz);
+        tma_load_3d(sb + OFF_V + s * kTile + kHalf, &mv, bar(B_V_FULL + s), 64, sp.block(j) * 128, kz);
+        last_v[s] = j;
+      }
+      if (*abort_flag) {  // let every issued copy land before the CTA exits
+        mbar_wait_drain(bar(B_Q_FULL), 0, p.status);
+        for (int s = 0; s < kStages; ++s) {
+          if (last_k[s] >= 0) mbar_wait_drain(bar(B_K_FULL + s), (last_k[s] / kStages) & 1, p.status);
+          if (last_v[s] >= 0) mbar_wait_drain(bar(B_V_FULL + s), (last_v[s] / kStages) & 1, p.status);
+        }
+      }
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ S issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);  // Q (TMEM) x K (smem, K-major)
+      // S(j) once K(j) has landed and the softmax warps have read S(j - 1).
+      bool ok = mbar_spin(bar(B_Q_TMEM), 0, w);
+      for (int j = 0; ok && j < n_kv; ++j) {
+        const int s = j % kStages;
+        if (!(ok = mbar_spin(bar(B_K_FULL + s), (j / kStages) & 1, w))) break;
+        if (!(ok = mbar_spin(bar(B_S_READ), (j & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t ka = sb + OFF_K + s * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          umma_bf16_ts(tmem + TM_S, tmem + TM_Q + kk * 8,
+                       sdesc_sw128(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(bar(B_S_FULL));
+        umma_commit(bar(B_K_EMPTY + s));
+      }
+      umma_commit(bar(B_DRAIN));
+      mbar_wait_drain(bar(B_DRAIN), 0, p.status);
+    }
+  } else if (warp == 6) {
+    // ----------------------------------------------------------- PV issuer
+    if (lane == 0) {
+      constexpr uint32_t id_o = idesc_bf16(128, 128, 0, 1);  // P (TMEM) x V (smem, MN-major)
+      bool ok = true;
+      for (int j = 0; ok && j < n_kv; ++j) {
+        const int b = j & 1;
+        const int s = j % kStages;
+        if (!(ok = mbar_spin(bar(B_P_FULL + b), (j >> 1) & 1, w))) break;
+        if (!(ok = mbar_spin(bar(B_V_FULL + s), (j / kStages) & 1, w))) break;
+        tc_fence_after();
+        const uint32_t va = sb + OFF_V + s * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          umma_bf16_ts(tmem + TM_O, tmem + TM_P + b * 64 + kk * 8, sdesc_sw128(va + kk * 2048, kHalf, 1024), id_o,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        umma_commit(bar(B_P_EMPTY + b));
+        umma_commit(bar(B_V_EMPTY + s));
+      }
+      umma_commit(bar(B_DRAIN_PV));
+      mbar_wait_drain(bar(B_DRAIN_PV), 0, p.status);
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int r = warp * 32 + lane;  // query row in the tile = TMEM lane
+    const int qpos = qb * 128 + r;
+    const uint32_t trow = tmem_lane_addr(tmem, warp, 0);
+    const float sl2 = p.scale_log2;
+    float m_use = -INFINITY;  // running max used as the exponent offset (log2 domain)
+    float l = 0.f;
+    // Q row r -> TMEM (packed bf16, element pairs per column).
+    bool ok = warp_wait(bar(B_Q_FULL), 0, w);
+    if (ok) {
+#pragma unroll
+      for (int hq = 0; hq < 2; ++hq) {
+        uint32_t q[32];
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint4 v = ld_shared_v4(sb + OFF_Q + hq * kHalf + sw128_offset(r, ch));
+          q[4 * ch] = v.x;
+          q[4 * ch + 1] = v.y;
+          q[4 * ch + 2] = v.z;
+          q[4 * ch + 3] = v.w;
+        }
+        tmem_st32(trow + TM_Q + hq * 32, q);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_Q_TMEM));
+    }
+    for (int j = 0; ok && j < n_kv; ++j) {
+      const int b = j & 1;  // P buffer
+      if (!(ok = warp_wait(bar(B_S_FULL), j & 1, w))) break;
+      tc_fence_after();
+      const uint32_t tsb = trow + TM_S;
+      uint32_t v0[32], v1[32], v2[32], v3[32];
+      tmem_ld32(tsb + 0, v0);
+      tmem_ld32(tsb + 32, v1);
+      tmem_ld32(tsb + 64, v2);
+      tmem_ld32(tsb + 96, v3);
+      tmem_ld_wait(v0);
+      tmem_ld_wait(v1);
+      tmem_ld_wait(v2);
+      tmem_ld_wait(v3);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_S_READ));  // S(j + 1) may overwrite the scores
+
+      float x[128];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        x[c] = __uint_as_float(v0[c]);
+        x[32 + c] = __uint_as_float(v1[c]);
+        x[64 + c] = __uint_as_float(v2[c]);
+        x[96 + c] = __uint_as_float(v3[c]);
+      }
+      const int kb = sp.block(j);
+      if (sp.masked(kb, p)) hide_row(x, qpos, kb * 128, p);
+      // Row max: four independent chains of 3-input max.
+      float mc[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int c = 4; c < 124; c += 8) {
+        mc[0] = fmax3(mc[0], x[c], x[c + 1]);
+        mc[1] = fmax3(mc[1], x[c + 2], x[c + 3]);
+        mc[2] = fmax3(mc[2], x[c + 4], x[c + 5]);
+        mc[3] = fmax3(mc[3], x[c + 6], x[c + 7]);
+      }
+      mc[0] = fmax3(mc[0], x[124], x[125]);
+      mc[1] = fmax3(mc[1], x[126], x[127]);
+      const float mx = fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]);
+      const float m_new = fmaxf(m_use, mx * sl2);
+      const bool need = m_new > m_use + 8.0f;
+      if (j > 0 && __any_sync(0xffffffffu, need)) {
+        // O holds PV(0..j-1) once PV(j - 1) completes: rescale the rows
+        // that moved.
+        if (!(ok = warp_wait(bar(B_P_EMPTY + ((j - 1) & 1)), ((j - 1) >> 1) & 1, w))) break;
+        tc_fence_after();
+        const float f = need ? ex2_approx(m_use - m_new) : 1.f;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          uint32_t o[32];
+          tmem_ld32(trow + TM_O + c4 * 32, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+          tmem_st32(trow + TM_O + c4 * 32, o);
+        }
+        l *= f;
+      }
+      if (need) m_use = m_new;
+
+      uint32_t pk0[32], pk1[32];
+      const uint64_t sl2x2 = f2_pack(sl2, sl2);
+      const uint64_t nmx2 = f2_pack(-m_use, -m_use);
+      uint64_t acc[4] = {0, 0, 0, 0};  // (+0, +0) pairs
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float t0, t1, t2, t3;
+        f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sl2x2, nmx2), t0, t1);
+        f2_unpack(f2_fma(f2_pack(x[64 + c], x[64 + c + 1]), sl2x2, nmx2), t2, t3);
+        const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+        const float p2 = ex2_approx(t2), p3 = ex2_approx(t3);
+        acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2_pack(p0, p1));
+        acc[2 + ((c >> 1) & 1)] = f2_add(acc[2 + ((c >> 1) & 1)], f2_pack(p2, p3));
+        pk0[c >> 1] = pack_bf16x2(p0, p1);
+        pk1[c >> 1] = pack_bf16x2(p2, p3);
+      }
+      float rs = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2_unpack(acc[i], a, b);
+        rs += a + b;
+      }
+      l += rs;
+      // P buffer b held P(j - 2) until PV(j - 2) completed.
+      if (j >= 2) {
+        if (!(ok = warp_wait(bar(B_P_EMPTY + b), ((j >> 1) & 1) ^ 1, w))) break;
+        tc_fence_after();
+      }
+      tmem_st32(trow + TM_P + b * 64 + 0, pk0);
+      tmem_st32(trow + TM_P + b * 64 + 32, pk1);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_P_FULL + b));
+    }
+    // PV products complete in issue order: the last one completing means O is final.
+    if (ok) ok = warp_wait(bar(B_P_EMPTY + ((n_kv - 1) & 1)), ((n_kv - 1) >> 1) & 1, w);
+    if (ok) {
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const bool valid = qpos < p.L;
+      __nv_bfloat16* orow = p.o + (static_cast<int64_t>(qpos) * p.H + h) * kHeadDim;
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) {
+        uint32_t o[32];
+        tmem_ld32(trow + TM_O + c4 * 32, o);
+        tmem_ld_wait(o);
+        if (valid) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            st_global_v4(orow + c4 * 32 + q * 8,
+                         pack_bf16x2(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv),
+                         pack_bf16x2(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv),
+                         pack_bf16x2(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv),
+                         pack_bf16x2(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv));
+          }
+        }
+      }
+      if (valid) p.lse[static_cast<int64_t>(h) * p.L + qpos] = (m_use + log2f(l)) * 0.69314718055994530942f;
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+
+// dS row slice of the dq kernel: 32 keys of one query row, paired fp32
+// math.  kMask applies the causal mask (only the diagonal tile needs it).
+template <bool kMask>
+__device__ __forceinline__ void ds_slice(const uint32_t (&sv)[32], const uint32_t (&dv)[32], float sl2, float nlse2,
+                                         float dlt, int k0, int qpos, const WinParams& p,
+                                         uint32_t (&pk)[16]) {
+  const uint64_t sl2x2 = f2_pack(sl2, sl2);
+  const uint64_t nlx2 = f2_pack(nlse2, nlse2);
+  const uint64_t dlx2 = f2_pack(dlt, dlt);
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    float t0, t1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl2x2, nlx2), t0, t1);
+    float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+    if (kMask) {
+      if (!sees(qpos, k0 + c, p)) p0 = 0.f;
+      if (!sees(qpos, k0 + c + 1, p)) p1 = 0.f;
+    }
+    const uint64_t d = f2_sub(f2_pack(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])), dlx2);
+    float d0, d1;
+    f2_unpack(f2_mul(f2_pack(p0, p1), d), d0, d1);
+    pk[c >> 1] = pack_bf16x2(d0, d1);
+  }
+}
+
+// P^T row slice of the dkdv kernel: 16 queries (columns c0 .. c0 + 15 of
+// this warp's 32) of one key row, kept in fp32 for the dS^T phase.  Lane c of
+// the warp holds -LSE * log2(e) of the warp's query c in `nl`; kMask zeroes
+// queries before the key (the diagonal tile only).
+template <bool kMask>
+__device__ __forceinline__ void p_slice(const uint32_t (&sv)[16], float nl, int c0, float sl2, int q0, int kpos,
+                                        int last_q, float* pf) {
+  const uint64_t sl2x2 = f2_pack(sl2, sl2);
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    const float l0 = __shfl_sync(0xffffffffu, nl, c0 + c);
+    const float l1 = __shfl_sync(0xffffffffu, nl, c0 + c + 1);
+    float t0, t1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl2x2, f2_pack(l0, l1)), t0, t1);
+    float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+    if (kMask) {
+      const int q = q0 + c0 + c;
+      if (q < kpos || q > last_q) p0 = 0.f;
+      if (q + 1 < kpos || q + 1 > last_q) p1 = 0.f;
+    }
+    pf[c] = p0;
+    pf[c + 1] = p1;
+  }
+}
+
+// dS^T row slice of the dkdv kernel: dS = P * (dP - Delta) for 16 queries
+// (columns c0 .. c0 + 15), packed bf16.  Lane c holds Delta of query c in `dl`.
+__device__ __forceinline__ void dst_slice(const uint32_t (&dv)[16], const float* pf, float dl, int c0,
+                                          uint32_t (&dd)[8]) {
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    const float d0 = __shfl_sync(0xffffffffu, dl, c0 + c);
+    const float d1 = __shfl_sync(0xffffffffu, dl, c0 + c + 1);
+    float s0, s1;
+    f2_unpack(f2_mul(f2_pack(pf[c], pf[c + 1]),
+                     f2_sub(f2_pack(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])), f2_pack(d0, d1))),
+              s0, s1);
+    dd[c >> 1] = pack_bf16x2(s0, s1);
+  }
+}
+
+// ================================================================ backward
+//
+// Two kernels without atomics, so every sum has one order: dQ by query tiles
+// and dK/dV by key tiles, each recomputing S and dP.
+
+namespace wq {
+constexpr int kComputeWarps = 8;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;    // issues S; allocates TMEM
+constexpr int kGradWarp = 10;  // issues dQ, which consumes dS from TMEM
+constexpr int kTile = 128 * 128 * 2;   // [128][128] bf16 as two 64-column halves
+constexpr int kHalf = kTile / 2;
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr int OFF_Q = 0;
+constexpr int OFF_DO = OFF_Q + kTile;
+constexpr int OFF_K = OFF_DO + kTile;              // kKStages
+constexpr int OFF_V = OFF_K + kKStages * kTile;    // kVStages
+constexpr int OFF_BAR = OFF_V + kVStages * kTile;
+enum {
+  B_QDO_FULL,
+  B_K_FULL,
+  B_K_EMPTY = B_K_FULL + kKStages,
+  B_V_FULL = B_K_EMPTY + kKStages,
+  B_V_EMPTY = B_V_FULL + kVStages,
+  B_S_FULL = B_V_EMPTY + kVStages,
+  B_S_FREE = B_S_FULL + 2,   // dQ of that buffer done: its S/dS columns free
+  B_DS_FULL = B_S_FREE + 2,
+  B_DP_FULL = B_DS_FULL + 2,
+  B_DP_EMPTY,                // the compute warps have read dP
+  B_DQ_DONE,
+  B_DRAIN,
+  B_DRAIN_G,
+  B_DRAIN_P,
+  B_COUNT
+};
+constexpr int OFF_TMEM_SLOT = OFF_BAR + B_COUNT * 8;
+constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+constexpr int kSmemBytes = OFF_ABORT + 8 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "dq kernel shared memory");
+constexpr int TM_S = 0, TM_DP = 256, TM_DQ = 384;  // S: two 128-column buffers
+// Warps 0-7 compute, 8 producer, 9 issues S, 10 issues dQ, 11 issues dP.
+constexpr int kDpWarp = 11;
+constexpr int kThreadsDq = 384;
+}  // namespace wq
+
+__global__ void __launch_bounds__(wq::kThreadsDq, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                       const __grid_constant__ WinParams p) {
+  using namespace wq;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // Heads vary fastest (GQA siblings share K/V blocks in L2); the query
+  // blocks with the most KV blocks launch first.
+  const int h = static_cast<int>(blockIdx.x) % p.H;
+  const int qb = static_cast<int>(gridDim.x) / p.H - 1 - static_cast<int>(blockIdx.x) / p.H;
+  const int kz = h / p.g;
+  const QuerySpan sp(qb, p);
+  const int n_kv = sp.count();
+  auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+  const WaitCtl w{abort_flag, p.status, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_QDO_FULL), 1);
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(bar(B_K_FULL + s), 1);
+      mbar_init(bar(B_K_EMPTY + s), 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(bar(B_V_FULL + s), 1);
+      mbar_init(bar(B_V_EMPTY + s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(B_S_FULL + b), 1);
+      mbar_init(bar(B_S_FREE + b), 1);
+      mbar_init(bar(B_DS_FULL + b), kComputeWarps);
+    }
+    mbar_init(bar(B_DP_FULL), 1);
+    mbar_init(bar(B_DP_EMPTY), kComputeWarps);
+    mbar_init(bar(B_DQ_DONE), 1);
+    mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN_G), 1);
+    mbar_init(bar(B_DRAIN_P), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(sb + OFF_TMEM_SLOT, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      tma_prefetch_map(&mq);
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+      tma_prefetch_map(&mdo);
+      mbar_expect_tx(bar(B_QDO_FULL), 2 * kTile);
+      tma_load_3d(sb + OFF_Q, &mq, bar(B_QDO_FULL), 0, qb * 128, h);
+      tma_load_3d(sb + OFF_Q + kHalf, &mq, bar(B_QDO_FULL), 64, qb * 128, h);
+      tma_load_3d(sb + OFF_DO, &mdo, bar(B_QDO_FULL), 0, qb * 128, h);
+      tma_load_3d(sb + OFF_DO + kHalf, &mdo, bar(B_QDO_FULL), 64, qb * 128, h);
+      int last_k[kKStages], last_v[kVStages];
+#pragma unroll
+      for (int s = 0; s < kKStages; ++s) last_k[s] = -1;
+#pragma unroll
+      for (int s = 0; s < kVStages; ++s) last_v[s] = -1;
+      // Whichever ring has a free stage gets its next block, K first (S(j)
+      // needs K(j) before dP(j) needs V(j)).
+      int nk = 0, nv = 0;
+      Watchdog wd;
+      wd.reset();
+      bool ok = true;
+      while (ok && (nk < n_kv || nv < n_kv)) {
+        bool did = false;
+        if (nk < n_kv && mbar_test(bar(B_K_EMPTY + nk % kKStages), ((nk / kKStages) & 1) ^ 1)) {
+          const int s = nk % kKStages;
+          mbar_expect_tx(bar(B_K_FULL + s), kTile);
+          tma_load_3d(sb + OFF_K + s * kTile, &mk, bar(B_K_FULL + s), 0, sp.block(nk) * 128, kz);
+          tma_load_3d(sb + OFF_K + s * kTile + kHalf, &mk, bar(B_K_FULL + s), 64, sp.block(nk) * 128, kz);
+          last_k[s] = nk++;
+          did = true;
+        }
+        if (nv < n_kv && mbar_test(bar(B_V_EMPTY + nv % kVStages), ((nv / kVStages) & 1) ^ 1)) {
+          const int s = nv % kVStages;
+          mbar_expect_tx(bar(B_V_FULL + s), kTile);
+          tma_load_3d(sb + OFF_V + s * kTile, &mv, bar(B_V_FULL + s), 0, sp.block(nv) * 128, kz);
+          tma_load_3d(sb + OFF_V + s * kTile + kHalf, &mv, bar(B_V_FULL + s), 64, sp.block(nv) * 128, kz);
+          last_v[s] = nv++;
+          did = true;
+        }
+        if (did) wd.reset();
+        else ok = wd.alive(w);
+      }
+      if (*abort_flag) {
+        mbar_wait_drain(bar(B_QDO_FULL), 0, p.status);
+        for (int s = 0; s < kKStages; ++s)
+          if (last_k[s] >= 0) mbar_wait_drain(bar(B_K_FULL + s), (last_k[s] / kKStages) & 1, p.status);
+        for (int s = 0; s < kVStages; ++s)
+          if (last_v[s] >= 0) mbar_wait_drain(bar(B_V_FULL + s), (last_v[s] / kVStages) & 1, p.status);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      // S(j) = Q K(j)^T into buffer j & 1 once K(j) has landed and dQ(j - 2)
+      // has released the buffer.
+      constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
+      bool ok = mbar_spin(bar(B_QDO_FULL), 0, w);
+      for (int j = 0; ok && j < n_kv; ++j) {
+        const int s = j % kKStages;
+        if (!(ok = mbar_spin(bar(B_K_FULL + s), (j / kKStages) & 1, w))) break;
+        if (!(ok = mbar_spin(bar(B_S_FREE + (j & 1)), ((j >> 1) & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t ka = sb + OFF_K + s * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_bf16(tmem + TM_S + (j & 1) * 128, sdesc_sw128(sb + OFF_Q + off, 16, 1024),
+                    sdesc_sw128(ka + off, 16, 1024), id_kk, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(bar(B_S_FULL + (j & 1)));
+      }
+      umma_commit(bar(B_DRAIN));
+      mbar_wait_drain(bar(B_DRAIN), 0, p.status);
+    }
+  } else if (warp == kDpWarp) {
+    if (lane == 0) {
+      // dP(j) = dO V(j)^T once V(j) has landed and dP(j - 1) has been read.
+      constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
+      bool ok = mbar_spin(bar(B_QDO_FULL), 0, w);
+      for (int j = 0; ok && j < n_kv; ++j) {
+        const int s = j % kVStages;
+        if (!(ok = mbar_spin(bar(B_V_FULL + s), (j / kVStages) & 1, w))) break;
+        if (!(ok = mbar_spin(bar(B_DP_EMPTY), (j & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t va = sb + OFF_V + s * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_bf16(tmem + TM_DP, sdesc_sw128(sb + OFF_DO + off, 16, 1024), sdesc_sw128(va + off, 16, 1024), id_kk,
+                    kk > 0 ? 1u : 0u);
+        }
+        umma_commit(bar(B_DP_FULL));
+        umma_commit(bar(B_V_EMPTY + s));
+      }
+      umma_commit(bar(B_DRAIN_P));
+      mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
+    }
+  } else if (warp == kGradWarp) {
+    if (lane == 0) {
+      // dQ(j) += dS(j) K(j) once dS(j) is written; then S buffer j & 1 and
+      // K stage j % kKStages are free (S(j) had completed before dS(j) existed).
+      constexpr uint32_t id_q = idesc_bf16(128, 128, 0, 1);  // dS from TMEM, K MN-major
+      bool ok = true;
+      for (int j = 0; ok && j < n_kv; ++j) {
+        const int b = j & 1;
+        const int s = j % kKStages;
+        if (!(ok = mbar_spin(bar(B_DS_FULL + b), (j >> 1) & 1, w))) break;
+        tc_fence_after();
+        const uint32_t ka = sb + OFF_K + s * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          // keys 16 kk .. 16 kk + 15: compute half kk / 4 wrote them at its own
+          // 64-column slice of the S buffer
+          const uint32_t a = tmem + TM_S + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8;
+          umma_bf16_ts(tmem + TM_DQ, a, sdesc_sw128(ka + kk * 2048, kHalf, 1024), id_q, (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        umma_commit(bar(B_S_FREE + b));
+        umma_commit(bar(B_K_EMPTY + s));
+      }
+      if (ok) umma_commit(bar(B_DQ_DONE));
+      umma_commit(bar(B_DRAIN_G));
+      mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
+    }
+  } else {
+    // Compute warps: quadrant (warp & 3) of the TMEM lanes = query rows,
+    // half (warp >> 2) of the 128 key columns of each block.
+    const int quad = warp & 3;
+    const int half = warp >> 2;
+    const int r = quad * 32 + lane;
+    const int qpos = qb * 128 + r;
+    const bool valid = qpos < p.L;
+    const uint32_t trow = tmem_lane_addr(tmem, quad, 0);
+    const float sl2 = p.scale_log2;
+    const int n_q64 = (p.L + 63) / 64;
+    const float* rec = p.ld + (static_cast<int64_t>(h) * n_q64 + (qpos >> 6)) * 128;
+    const float nlse2 = valid ? rec[qpos & 63] : 0.f;  // -LSE * log2(e)
+    const float dlt = valid ? rec[64 + (qpos & 63)] : 0.f;
+    bool ok = true;
+    for (int j = 0; j < n_kv; ++j) {
+      const int b = j & 1;
+      if (!(ok = warp_wait<false, true>(bar(B_S_FULL + b), (j >> 1) & 1, w))) break;
+      if (!(ok = warp_wait<false, true>(bar(B_DP_FULL), j & 1, w))) break;
+      tc_fence_after();
+      const uint32_t ts = trow + TM_S + b * 128 + half * 64;
+      uint32_t s0[32], s1[32], d0[32], d1[32];
+      tmem_ld32(ts, s0);
+      tmem_ld32(ts + 32, s1);
+      tmem_ld32(trow + TM_DP + half * 64, d0);
+      tmem_ld32(trow + TM_DP + half * 64 + 32, d1);
+      tmem_ld_wait(s0);
+      tmem_ld_wait(s1);
+      tmem_ld_wait(d0);
+      tmem_ld_wait(d1);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_DP_EMPTY));
+      const int kb = sp.block(j);
+      const int k0 = kb * 128 + half * 64;  // key of this warp's first column
+      uint32_t pk0[16], pk1[16];
+      if (sp.masked(kb, p)) {  // warp-uniform
+        ds_slice<true>(s0, d0, sl2, nlse2, dlt, k0, qpos, p, pk0);
+        ds_slice<true>(s1, d1, sl2, nlse2, dlt, k0 + 32, qpos, p, pk1);
+      } else {
+        ds_slice<false>(s0, d0, sl2, nlse2, dlt, k0, qpos, p, pk0);
+        ds_slice<false>(s1, d1, sl2, nlse2, dlt, k0 + 32, qpos, p, pk1);
+      }
+      // dS over the first 32 of the 64 S columns this warp just read.
+      tmem_st16(ts, pk0);
+      tmem_st16(ts + 16, pk1);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_DS_FULL + b));
+    }
+    if (ok) ok = warp_wait<false, true>(bar(B_DQ_DONE), 0, w);
+    if (ok) {
+      // Epilogue: this warp writes 64 columns of its rows.
+      tc_fence_after();
+      __nv_bfloat16* out = p.dq + (static_cast<int64_t>(qpos) * p.H + h) * kHeadDim + half * 64;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t a[32];
+        tmem_ld32(trow + TM_DQ + half * 64 + c * 32, a);
+        tmem_ld_wait(a);
+        if (valid) store32_bf16(out + c * 32, a, p.scale);
+      }
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+
+namespace wkv {
+constexpr int kTile = 128 * 128 * 2;  // K, V, Q or dO tile: [128 rows][128 d]
+constexpr int kHalf = kTile / 2;
+constexpr int kStages = 2;            // Q/dO ring depth
+constexpr int OFF_K = 0;
+constexpr int OFF_V = OFF_K + kTile;
+constexpr int OFF_Q = OFF_V + kTile;             // kStages stages
+constexpr int OFF_DO = OFF_Q + kStages * kTile;
+constexpr int OFF_BAR = OFF_DO + kStages * kTile;
+enum {
+  B_KV_FULL,
+  B_QDO_FULL,
+  B_QDO_EMPTY = B_QDO_FULL + kStages,
+  B_S_FULL = B_QDO_EMPTY + kStages,  // per 64-query half of S^T
+  B_P_FULL = B_S_FULL + 2,           // P^T of that half written (its 8 compute warps)
+  B_S_FREE = B_P_FULL + 2,           // dV of that half done: its S^T / P^T columns free
+  B_DP_FULL = B_S_FREE + 2,
+  B_DS_FULL,   // dS^T written (compute warps)
+  B_DP_FREE,   // dK done: dP^T / dS^T columns free
+  B_DKV_DONE,
+  B_DRAIN,
+  B_DRAIN_G,
+  B_DRAIN_P,
+  B_COUNT
+};
+constexpr int OFF_TMEM_SLOT = OFF_BAR + B_COUNT * 8;
+constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+constexpr int kSmemBytes = OFF_ABORT + 8 + 1024;
+constexpr int TM_ST = 0, TM_DPT = 128, TM_DV = 256, TM_DK = 384;
+// 16 compute warps: four per TMEM lane quadrant, each owning 32 of the 128
+// query columns, so each SM sub-partition has four to hide TMEM and exp2
+// latency; then the producer and three MMA-issuing warps (S^T; dV and dK;
+// dP^T).
+constexpr int kCompute = 16;
+constexpr int kProducer = 16;
+constexpr int kMma = 17;
+constexpr int kGrad = 18;
+constexpr int kDpMma = 19;
+constexpr int kThreadsKv = 640;
+}  // namespace wkv
+
+__global__ void __launch_bounds__(wkv::kThreadsKv, 1)
+    window_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                         const __grid_constant__ WinParams p) {
+  using namespace wkv;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int kb = static_cast<int>(blockIdx.x) / p.Hkv;
+  const int kv = static_cast<int>(blockIdx.x) % p.Hkv;
+  const int n_q64 = (p.L + 63) / 64;
+  const int nqt = key_tile_queries(kb, p);  // query tiles from the key tile's own on
+  const int n_it = p.g * nqt;
+  auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+  const WaitCtl w{abort_flag, p.status, p.limit_ns};
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_KV_FULL), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(B_QDO_FULL + s), 1);
+      mbar_init(bar(B_QDO_EMPTY + s), 1);
+    }
+    for (int hf = 0; hf < 2; ++hf) {
+      mbar_init(bar(B_S_FULL + hf), 1);
+      mbar_init(bar(B_P_FULL + hf), kCompute / 2);
+      mbar_init(bar(B_S_FREE + hf), 1);
+    }
+    mbar_init(bar(B_DP_FULL), 1);
+    mbar_init(bar(B_DS_FULL), kCompute);
+    mbar_init(bar(B_DP_FREE), 1);
+    mbar_init(bar(B_DKV_DONE), 1);
+    mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN_G), 1);
+    mbar_init(bar(B_DRAIN_P), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(sb + OFF_TMEM_SLOT, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
+
+  if (warp == kProducer) {
+    // Q and dO tiles (TMA), both on one barrier per stage.
+    if (lane == 0) {
+      int last[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) last[s] = -1;
+      tma_prefetch_map(&mq);
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+      tma_prefetch_map(&mdo);
+      mbar_expect_tx(bar(B_KV_FULL), 2 * kTile);
+      tma_load_3d(sb + OFF_K, &mk, bar(B_KV_FULL), 0, kb * 128, kv);
+      tma_load_3d(sb + OFF_K + kHalf, &mk, bar(B_KV_FULL), 64, kb * 128, kv);
+      tma_load_3d(sb + OFF_V, &mv, bar(B_KV_FULL), 0, kb * 128, kv);
+      tma_load_3d(sb + OFF_V + kHalf, &mv, bar(B_KV_FULL), 64, kb * 128, kv);
+      for (int it = 0; it < n_it; ++it) {
+        const int s = it % kStages;
+        const uint32_t ph = (it / kStages) & 1;
+        const int hl = kv * p.g + it / nqt;
+        const int qt = kb + it % nqt;
+        if (!mbar_wait(bar(B_QDO_EMPTY + s), ph ^ 1, w)) break;
+        mbar_expect_tx(bar(B_QDO_FULL + s), 2 * kTile);
+        tma_load_3d(sb + OFF_Q + s * kTile, &mq, bar(B_QDO_FULL + s), 0, qt * 128, hl);
+        tma_load_3d(sb + OFF_Q + s * kTile + kHalf, &mq, bar(B_QDO_FULL + s), 64, qt * 128, hl);
+        tma_load_3d(sb + OFF_DO + s * kTile, &mdo, bar(B_QDO_FULL + s), 0, qt * 128, hl);
+        tma_load_3d(sb + OFF_DO + s * kTile + kHalf, &mdo, bar(B_QDO_FULL + s), 64, qt * 128, hl);
+        last[s] = it;
+      }
+      if (*abort_flag) {
+        mbar_wait_drain(bar(B_KV_FULL), 0, p.status);
+        for (int s = 0; s < kStages; ++s)
+          if (last[s] >= 0) mbar_wait_drain(bar(B_QDO_FULL + s), (last[s] / kStages) & 1, p.status);
+      }
+    }
+  } else if (warp == kMma) {
+    if (lane == 0) {
+      // S^T(i) in two 64-query halves (N=64): half h once the Q/dO stage has
+      // landed and dV of half h of tile i - 1 has consumed the P^T there.
+      // The halves pipeline independently, which shortens the chain
+      // S^T -> P^T -> dV -> next S^T that a single buffer imposes.
+      constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);
+      bool ok = mbar_spin(bar(B_KV_FULL), 0, w);
+      for (int it = 0; ok && it < n_it; ++it) {
+        const int qs = it % kStages;
+        if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!(ok = mbar_spin(bar(B_S_FREE + hf), (it & 1) ^ 1, w))) break;
+          tc_fence_after();
+          const uint32_t bq = sb + OFF_Q + qs * kTile + hf * 64 * 128;  // query rows 64 hf ..
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            umma_bf16(tmem + TM_ST + hf * 64, sdesc_sw128(sb + OFF_K + off, 16, 1024), sdesc_sw128(bq + off, 16, 1024),
+                      id_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar(B_S_FULL + hf));
+        }
+      }
+      umma_commit(bar(B_DRAIN));
+      mbar_wait_drain(bar(B_DRAIN), 0, p.status);
+    }
+  } else if (warp == kDpMma) {
+    if (lane == 0) {
+      // dP^T(i) = V dO(i)^T once the stage has landed and dK(i - 1) is done.
+      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
+      bool ok = mbar_spin(bar(B_KV_FULL), 0, w);
+      for (int it = 0; ok && it < n_it; ++it) {
+        const int qs = it % kStages;
+        if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
+        if (!(ok = mbar_spin(bar(B_DP_FREE), (it & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t bq = sb + OFF_DO + qs * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_bf16(tmem + TM_DPT, sdesc_sw128(sb + OFF_V + off, 16, 1024), sdesc_sw128(bq + off, 16, 1024), id_s,
+                    kk > 0 ? 1u : 0u);
+        }
+        umma_commit(bar(B_DP_FULL));
+      }
+      umma_commit(bar(B_DRAIN_P));
+      mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
+    }
+  } else if (warp == kGrad) {
+    if (lane == 0) {
+      // dV(i) += P^T(i) dO(i) half by half as each half's P^T is written
+      // (then that half's S^T columns are free); dK(i) += dS^T(i) Q(i) once
+      // dS^T is written (then the dP^T columns and the Q/dO stage are free:
+      // S^T(i) and dP^T(i) had completed before the compute warps could write
+      // P^T and dS^T).
+      constexpr uint32_t id_g = idesc_bf16(128, 128, 0, 1);  // A from TMEM, B MN-major
+      auto issue_grad = [&](int it, int tm_a, uint32_t b_base, int tm_d, int kk0, int kk1) {
+        const uint32_t bq = b_base + (it % kStages) * kTile;
+        for (int kk = kk0; kk < kk1; ++kk) {
+          // queries 16 kk .. 16 kk + 15: compute group kk / 2 wrote them at
+          // its own 32-column slice
+          const uint32_t a = tmem + tm_a + (kk >> 1) * 32 + (kk & 1) * 8;
+          umma_bf16_ts(tmem + tm_d, a, sdesc_sw128(bq + kk * 2048, kHalf, 1024), id_g,
+                       (it > 0 || kk > 0) ? 1u : 0u);
+        }
+      };
+      bool ok = true;
+      for (int it = 0; ok && it < n_it; ++it) {
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!(ok = mbar_spin(bar(B_P_FULL + hf), it & 1, w))) break;
+          tc_fence_after();
+          issue_grad(it, TM_ST, sb + OFF_DO, TM_DV, 4 * hf, 4 * hf + 4);
+          umma_commit(bar(B_S_FREE + hf));
+        }
+        if (!ok) break;
+        if (!(ok = mbar_spin(bar(B_DS_FULL), it & 1, w))) break;
+        tc_fence_after();
+        issue_grad(it, TM_DPT, sb + OFF_Q, TM_DK, 0, 8);
+        umma_commit(bar(B_DP_FREE));
+        umma_commit(bar(B_QDO_EMPTY + it % kStages));
+      }
+      if (ok) umma_commit(bar(B_DKV_DONE));
+      umma_commit(bar(B_DRAIN_G));
+      mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
+    }
+  } else {
+    // Compute warps: quadrant (warp & 3) of the key rows, group (warp >> 2)
+    // of 32 query columns of each tile.
+    const int quad = warp & 3;
+    const int grp = warp >> 2;
+    const int r = quad * 32 + lane;  // key row = TMEM lane
+    const int kpos = kb * 128 + r;
+    const bool valid = kpos < p.L;
+    const int last_q = last_query(kpos, p);
+    const uint32_t trow = tmem_lane_addr(tmem, quad, 0);
+    const float sl2 = p.scale_log2;
+    // Epilogue: groups 0-1 own dK, 2-3 own dV, 64 columns each.
+    const int which = grp >> 1;
+    const int col0 = (grp & 1) * 64;
+    const uint32_t my_tm = trow + (which == 0 ? TM_DK : TM_DV) + col0;
+    bool ok = true;
+    const uint32_t ts = trow + TM_ST + grp * 32;
+    const uint32_t td = trow + TM_DPT + grp * 32;
+    for (int it = 0; it < n_it; ++it) {
+      const int hl = kv * p.g + it / nqt;
+      const int qt = kb + it % nqt;
+      const int q0 = qt * 128 + grp * 32;  // query of this warp's first column
+      // Without its record (all 64 queries past L) the slice is all zero.
+      const bool masked = hides(qt, kb, p);  // warp-uniform
+      const bool live = 2 * qt + (grp >> 1) < n_q64;
+      // This warp's 32 queries in their record: -LSE*log2(e) at +0, Delta at
+      // +64.  Lane c loads query c's pair now, ahead of the waits, and the
+      // values reach the other lanes by shuffle.
+      const float* rec = p.ld + (static_cast<int64_t>(hl) * n_q64 + 2 * qt + (grp >> 1)) * 128 + (grp & 1) * 32;
+      const float nl = live ? __ldg(rec + lane) : 0.f;
+      const float dl = live ? __ldg(rec + 64 + lane) : 0.f;
+      // ---- phase 1: P^T over the S^T columns, 16 at a time; the packed
+      // P^T of columns 16 h .. 16 h + 15 goes to columns 8 h .. 8 h + 7, which
+      // this warp has already read.
+      if (!(ok = warp_wait<false, true>(bar(B_S_FULL + (grp >> 1)), it & 1, w))) break;
+      tc_fence_after();
+      float pf[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t sv[16];
+        tmem_ld16(ts + 16 * h, sv);
+        tmem_ld_wait(sv);
+        if (!live) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pf[16 * h + c] = 0.f;
+        } else if (masked) {
+          p_slice<true>(sv, nl, 16 * h, sl2, q0, kpos, last_q, pf + 16 * h);
+        } else {
+          p_slice<false>(sv, nl, 16 * h, sl2, q0, kpos, last_q, pf + 16 * h);
+        }
+        uint32_t pk[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(pf[16 * h + 2 * c], pf[16 * h + 2 * c + 1]);
+        tmem_st8(ts + 8 * h, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_P_FULL + (grp >> 1)));
+      // ---- phase 2: dS^T = P^T * (dP^T - Delta) over the dP^T columns
+      if (!(ok = warp_wait<false, true>(bar(B_DP_FULL), it & 1, w))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t dv[16];
+        tmem_ld16(td + 16 * h, dv);
+        tmem_ld_wait(dv);
+        uint32_t dd[8];
+        if (!live) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dd[c] = 0u;
+        } else {
+          dst_slice(dv, pf + 16 * h, dl, 16 * h, dd);
+        }
+        tmem_st8(td + 8 * h, dd);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_DS_FULL));
+    }
+    if (ok) ok = warp_wait<false, true>(bar(B_DKV_DONE), 0, w);
+    if (ok) {
+      tc_fence_after();
+      __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<int64_t>(kpos) * p.Hkv + kv) * kHeadDim + col0;
+      const float scale = which == 0 ? p.scale : 1.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tmem_ld32(my_tm + c * 32, v);
+        tmem_ld_wait(v);
+        if (valid) store32_bf16(out + c * 32, v, scale);
+      }
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+struct WinShape {
+  int64_t L;
+  int H, Hkv, m_tiles;
+  int window, sinks;
+};
+
+bool check_window(const upipe_window_cfg* c, WinShape* s) {
+  if (!c || c->L < 1 || c->L > 0x7fffffffLL || c->d != kHeadDim) return false;
+  if (c->H < 1 || c->Hkv < 1 || c->H % c->Hkv != 0 || c->H + 2 * static_cast<int64_t>(c->Hkv) > kMaxSlots) return false;
+  if (c->window < 1 || c->sinks < 0) return false;
+  s->L = c->L;
+  s->H = c->H;
+  s->Hkv = c->Hkv;
+  s->m_tiles = static_cast<int>((c->L + 127) / 128);
+  s->window = static_cast<int>(c->window < c->L ? c->window : c->L);
+  s->sinks = static_cast<int>(c->sinks < c->L ? c->sinks : c->L);
+  return true;
+}
+
+size_t records_bytes(const WinShape& s) {
+  return static_cast<size_t>(s.H) * static_cast<size_t>((s.L + 63) / 64) * 128 * sizeof(float);
+}
+
+WinParams base_params(const WinShape& s, int* status) {
+  WinParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.L = static_cast<int>(s.L);
+  p.H = s.H;
+  p.Hkv = s.Hkv;
+  p.g = s.H / s.Hkv;
+  p.window = s.window;
+  p.sinks = s.sinks;
+  p.scale = static_cast<float>(1.0 / std::sqrt(128.0));
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(128.0));
+  p.status = status;
+  p.limit_ns = spin_limit_ns();
+  return p;
+}
+
+cudaError_t launch_window_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const WinParams& p,
+                              int m_tiles, cudaStream_t st) {
+  cudaError_t e =
+      cudaFuncSetAttribute(window_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wf::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  window_fwd_kernel<<<m_tiles * p.H, wf::kThreads, wf::kSmemBytes, st>>>(q, k, v, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_window_dq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO,
+                             const WinParams& p, int m_tiles, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wq::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  window_dq_kernel<<<m_tiles * p.H, wq::kThreadsDq, wq::kSmemBytes, st>>>(q, k, v, dO, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_window_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                               const CUtensorMap& dO, const WinParams& p, int m_tiles, cudaStream_t st) {
+  cudaError_t e =
+      cudaFuncSetAttribute(window_dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wkv::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  window_dkdv_kernel<<<m_tiles * p.Hkv, wkv::kThreadsKv, wkv::kSmemBytes, st>>>(q, k, v, dO, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace upipe
+
+using namespace upipe;
+
+extern "C" {
+
+size_t upipe_window_workspace_bytes(const upipe_window_cfg* cfg) {
+  WinShape s;
+  return check_window(cfg, &s) ? records_bytes(s) : 0;
+}
+
+int upipe_window_fwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* o,
+                     float* lse, void* stream) {
+  WinShape s;
+  if (!check_window(cfg, &s)) return UPIPE_ERR_INVALID_ARG;
+  if (!q || !k || !v || !o || !lse) return UPIPE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
+    return UPIPE_ERR_INVALID_ARG;
+  int* status = nullptr;
+  if (int e = device_ready(&status)) return e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CUtensorMap mq, mk, mv;
+  UPIPE_MAP(map3d(&mq, q, s.L, s.H, s.H * 128, 128, 128));
+  UPIPE_MAP(map3d(&mk, k, s.L, s.Hkv, s.Hkv * 128, 128, 128));
+  UPIPE_MAP(map3d(&mv, v, s.L, s.Hkv, s.Hkv * 128, 128, 128));
+  WinParams p = base_params(s, status);
+  p.o = reinterpret_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  UPIPE_LAUNCH(UPIPE_KIND_WINDOW_FWD, launch_window_fwd(mq, mk, mv, p, s.m_tiles, st));
+  return UPIPE_OK;
+}
+
+int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                     const uint16_t* o, const float* lse, const uint16_t* dout_o, uint16_t* dq, uint16_t* dk,
+                     uint16_t* dv, void* ws, size_t ws_bytes, void* stream) {
+  WinShape s;
+  if (!check_window(cfg, &s)) return UPIPE_ERR_INVALID_ARG;
+  if (!q || !k || !v || !o || !lse || !dout_o || !dq || !dk || !dv || !ws) return UPIPE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dout_o) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(ws))
+    return UPIPE_ERR_INVALID_ARG;
+  if (ws_bytes < records_bytes(s)) return UPIPE_ERR_WS_TOO_SMALL;
+  int* status = nullptr;
+  if (int e = device_ready(&status)) return e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CUtensorMap mq, mk, mv, mdo;
+  UPIPE_MAP(map3d(&mq, q, s.L, s.H, s.H * 128, 128, 128));
+  UPIPE_MAP(map3d(&mk, k, s.L, s.Hkv, s.Hkv * 128, 128, 128));
+  UPIPE_MAP(map3d(&mv, v, s.L, s.Hkv, s.Hkv * 128, 128, 128));
+  UPIPE_MAP(map3d(&mdo, dout_o, s.L, s.H, s.H * 128, 128, 128));
+  WinParams p = base_params(s, status);
+  float* ld = static_cast<float*>(ws);
+  p.ld = ld;
+  p.dq = reinterpret_cast<__nv_bfloat16*>(dq);
+  p.dk = reinterpret_cast<__nv_bfloat16*>(dk);
+  p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
+  UPIPE_LAUNCH(UPIPE_KIND_DELTA,
+               launch_delta(reinterpret_cast<const __nv_bfloat16*>(o), s.H * 128, 128,
+                            reinterpret_cast<const __nv_bfloat16*>(dout_o), s.H * 128, 128, lse, ld, s.L, s.H, st));
+  UPIPE_LAUNCH(UPIPE_KIND_WINDOW_DKDV, launch_window_dkdv(mq, mk, mv, mdo, p, s.m_tiles, st));
+  UPIPE_LAUNCH(UPIPE_KIND_WINDOW_DQ, launch_window_dq(mq, mk, mv, mdo, p, s.m_tiles, st));
+  return UPIPE_OK;
+}
+
+}  // extern "C"

@@ -52,6 +52,9 @@ EXPORTS = (
     "upipe_qk_norm_rope_fwd",
     "upipe_qk_norm_rope_workspace_bytes",
     "upipe_qk_norm_rope_bwd",
+    "upipe_window_workspace_bytes",
+    "upipe_window_fwd",
+    "upipe_window_bwd",
     "upipe_offload_async",
     "upipe_prefetch_async",
     "upipe_copies_join",
@@ -65,7 +68,7 @@ EXPORTS = (
 
 KINDS = ("rope_table", "qkv_gemm", "attn_fwd", "oproj_gemm", "do_gemm", "dwo_gemm", "attn_bwd_dq",
          "attn_bwd_dkdv", "dwqkv_gemm", "dx_gemm", "delta", "zero_rows", "alst_gu", "alst_gemm", "alst_wgrad",
-         "ce_rows", "qk_rope", "norm_sum")
+         "ce_rows", "qk_rope", "norm_sum", "window_fwd", "window_dq", "window_dkdv")
 
 
 class UpipeError(RuntimeError):
@@ -101,6 +104,13 @@ class CeCfg(ctypes.Structure):
     _fields_ = [("L", ctypes.c_int64), ("D", ctypes.c_int32), ("V", ctypes.c_int32), ("T", ctypes.c_int32)]
 
 
+class WinCfg(ctypes.Structure):
+    """Mirror of ``upipe_window_cfg``."""
+
+    _fields_ = [("L", ctypes.c_int64), ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("H", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
 class RopeTable(ctypes.Structure):
     """Mirror of ``upipe_rope``."""
 
@@ -134,6 +144,22 @@ class Config:
 
     def c(self) -> Cfg:
         return Cfg(self.L, self.D, self.H, self.Hkv, self.d, self.U, self.causal, self.rope_theta)
+
+
+@dataclass(frozen=True)
+class WindowConfig:
+    """Windowed attention: query i sees key j iff j <= i and (i - j < window
+    or j < sinks)."""
+
+    L: int
+    H: int
+    Hkv: int
+    window: int
+    sinks: int = 0
+    d: int = 128
+
+    def c(self) -> WinCfg:
+        return WinCfg(self.L, self.window, self.sinks, self.H, self.Hkv, self.d)
 
 
 _lib = None
@@ -201,6 +227,13 @@ def lib() -> ctypes.CDLL:
         L.upipe_qk_norm_rope_bwd.restype = ctypes.c_int
         L.upipe_qk_norm_rope_bwd.argtypes = [rope, qk, rows, rows, P, P, P, rows, rows, rows, rows, P, P, P,
                                              ctypes.c_size_t, P]
+        win = ctypes.POINTER(WinCfg)
+        L.upipe_window_workspace_bytes.restype = ctypes.c_size_t
+        L.upipe_window_workspace_bytes.argtypes = [win]
+        L.upipe_window_fwd.restype = ctypes.c_int
+        L.upipe_window_fwd.argtypes = [win, P, P, P, P, P, P]
+        L.upipe_window_bwd.restype = ctypes.c_int
+        L.upipe_window_bwd.argtypes = [win, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         L.upipe_offload_async.restype = ctypes.c_int
         L.upipe_offload_async.argtypes = [P, P, ctypes.c_size_t, P]
         L.upipe_prefetch_async.restype = ctypes.c_int
@@ -848,3 +881,43 @@ def qk_norm_rope_backward(rope: Rope, q, k, wq, wk, dqo, dko, eps: float = 1e-6,
     dwq, dwk = _dense(wq), _dense(wk) if k is not None else None
     qk_norm_rope_bwd(rope, q, k, wq, wk, dqo, dko, dq, dk, dwq, dwk, eps, pos0, positions)
     return dq, dk, dwq, dwk
+
+
+# ---------------------------------- attention with a window and sink tokens
+
+def window_workspace_bytes(cfg: WindowConfig) -> int:
+    return int(lib().upipe_window_workspace_bytes(ctypes.byref(cfg.c())))
+
+
+def window_fwd(cfg: WindowConfig, q, k, v, o, lse, stream=None):
+    """upipe_window_fwd: tensors as attn_core_fwd."""
+    _core_tensors(cfg, q, k, v, lse, o)
+    _on_device(q=q, k=k, v=v, o=o, lse=lse)
+    _check(lib().upipe_window_fwd(ctypes.byref(cfg.c()), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                  _stream(stream)), "upipe_window_fwd")
+
+
+def window_bwd(cfg: WindowConfig, q, k, v, o, lse, do, dq, dk, dv, ws=None, stream=None):
+    """upipe_window_bwd: tensors as attn_core_bwd."""
+    _core_tensors(cfg, q, k, v, lse, o)
+    _core_grads(cfg, do, dq, dk, dv)
+    _on_device(q=q, k=k, v=v, o=o, lse=lse, dout_o=do, dq=dq, dk=dk, dv=dv)
+    c = cfg.c()
+    ws, nbytes = _call_ws(int(lib().upipe_window_workspace_bytes(ctypes.byref(c))), ws, q.device, stream)
+    _check(lib().upipe_window_bwd(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
+                                  _ptr(dk), _ptr(dv), _ptr(ws), nbytes, _stream(stream)), "upipe_window_bwd")
+
+
+def window_forward(cfg: WindowConfig, q, k, v):
+    """Allocates and returns (o, lse)."""
+    o = torch.empty_like(q)
+    lse = torch.empty((cfg.H, cfg.L), dtype=torch.float32, device=q.device)
+    window_fwd(cfg, q, k, v, o, lse)
+    return o, lse
+
+
+def window_backward(cfg: WindowConfig, q, k, v, o, lse, do):
+    """Allocates and returns (dq, dk, dv)."""
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    window_bwd(cfg, q, k, v, o, lse, do, dq, dk, dv)
+    return dq, dk, dv

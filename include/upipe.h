@@ -466,6 +466,39 @@ int upipe_qk_norm_rope_bwd(const upipe_rope* r, const upipe_qk_cfg* c, const upi
                            const upipe_rows* dko, const upipe_rows* dq, const upipe_rows* dk, float* dwq, float* dwk,
                            void* ws, size_t ws_bytes, void* stream);
 
+/* Attention core with a sliding window and sink tokens: query i sees key j
+ * iff j <= i and (i - j < window or j < sinks), the last `window` keys (its
+ * own among them) and the first `sinks`.  Tensors, scale and LSE as
+ * upipe_attn_core_fwd / _bwd; all heads in one call.
+ *   L, H, Hkv, d   as upipe_cfg          window >= 1 (>= L: the full causal
+ *   mask)                                sinks  >= 0
+ * Work and time grow with L (window + sinks), not with L^2.  q, k, v and
+ * dout_o have to be finite: a tile multiplies hidden keys by zero.         */
+typedef struct upipe_window_cfg {
+  int64_t L;
+  int64_t window;
+  int64_t sinks;
+  int32_t H;
+  int32_t Hkv;
+  int32_t d;
+} upipe_window_cfg;
+
+/* Workspace bytes of upipe_window_bwd (the forward needs none); 0 for an
+ * invalid configuration.                                                   */
+size_t upipe_window_workspace_bytes(const upipe_window_cfg* cfg);
+
+/*   q, o [L, H, 128] bf16   k, v [L, Hkv, 128] bf16   lse [H, L] fp32 (o and
+ *   lse written)                                                           */
+int upipe_window_fwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* o,
+                     float* lse, void* stream);
+
+/* Gradients of sum(o * dout_o): dq [L, H, 128], dk, dv [L, Hkv, 128] bf16
+ * (written), from o and lse of the forward.  Sums have one order: the same
+ * inputs give the same bits.                                               */
+int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                     const uint16_t* o, const float* lse, const uint16_t* dout_o, uint16_t* dq, uint16_t* dk,
+                     uint16_t* dv, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads and clears the device status word of
  * the current device.  Returns UPIPE_OK, UPIPE_ERR_DEVICE_TIMEOUT if a
  * bounded wait of any earlier call ran out, or UPIPE_ERR_CUDA.              */
@@ -502,7 +535,10 @@ int upipe_debug_wait_timeout(uint64_t limit_ns, void* stream);
 #define UPIPE_KIND_CE_ROWS 15     /* softmax rows of the loss */
 #define UPIPE_KIND_QK_ROPE 16     /* rotation of queries and keys, with or without their norm */
 #define UPIPE_KIND_NORM_SUM 17    /* sums of the norm weights' gradients */
-#define UPIPE_KIND_COUNT 18
+#define UPIPE_KIND_WINDOW_FWD 18  /* windowed attention: forward, dQ, dK and dV */
+#define UPIPE_KIND_WINDOW_DQ 19
+#define UPIPE_KIND_WINDOW_DKDV 20
+#define UPIPE_KIND_COUNT 21
 int64_t upipe_launch_count(void);
 void upipe_profile_enable(int on);
 int upipe_profile_read(double* ms, int64_t* launches, int n);

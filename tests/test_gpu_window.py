@@ -1,0 +1,177 @@
+"""GPU parity of windowed attention with sinks against the fp64 oracle: the
+tolerances of the attention core (tests/tolerance.py), against the precision
+model (P and dS enter their products as bf16) and the plain definition; and
+masks read back exactly from uniform scores."""
+
+import numpy as np
+import pytest
+import torch
+
+from headwise_chunked_context_gb300 import synth, upipe
+from oracle import local_oracle as loc
+from tests.gpu_common import dev, ensure_lib, f64, status_ok
+from tests.tolerance import assert_close, assert_close_plain
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_lib()
+
+
+# L, H, Hkv, window, sinks: one token, windows of one key, inside a tile, of whole tiles, one more or
+# less, past the sequence; sinks of none, one, part of a tile, whole tiles, more than the sequence
+CASES = [
+    (1, 1, 1, 1, 0), (1, 2, 1, 5, 3), (2, 1, 1, 1, 1), (127, 2, 1, 1, 0), (128, 4, 2, 128, 0), (129, 4, 1, 64, 4),
+    (300, 4, 1, 100, 4), (300, 2, 2, 300, 0), (257, 2, 1, 2, 1), (385, 4, 2, 129, 1), (640, 2, 1, 127, 130),
+    (640, 2, 1, 128, 128), (641, 2, 1, 1, 640), (1000, 4, 1, 257, 5), (1000, 2, 1, 1, 1), (700, 2, 1, 2000, 3),
+    (500, 2, 1, 40, 9000), (1100, 8, 2, 200, 300), (1500, 4, 4, 513, 16), (2049, 2, 1, 129, 1),
+]
+
+
+def _run(L, H, Hkv, W, S, seed_shift=0):
+    q, k, v, do = synth.core_inputs(L, H, Hkv)
+    cfg = upipe.WindowConfig(L=L, H=H, Hkv=Hkv, window=W, sinks=S)
+    qd, kd, vd, dod = dev(q, k, v, do)
+    o, lse = upipe.window_forward(cfg, qd, kd, vd)
+    grads = upipe.window_backward(cfg, qd, kd, vd, o, lse, dod)
+    torch.cuda.synchronize()
+    status_ok()
+    return (q, k, v, do), (o, lse, *grads)
+
+
+@pytest.mark.parametrize("L,H,Hkv,W,S", CASES)
+def test_window_matches_oracle(L, H, Hkv, W, S):
+    (q, k, v, do), got = _run(L, H, Hkv, W, S)
+    q, k, v, do = (f64(t) for t in (q, k, v, do))
+    o, lse = loc.window_fwd(q, k, v, W, S)
+    # The backward is a function of the o it is given, so the model gets the same one.  With the exact o
+    # instead, Delta = sum_c dO_c o_c would be off by the given o's own error, 128^.5 * 2^-8 |o| (P and o are
+    # rounded to bf16), 0.03 for o of 0.7; a sink's dK adds that up over every query: P 0.03 |q| / 128^.5 n^.5,
+    # 0.02 for n = 514 queries with P = 1/3, 0.06 at the largest of 128 columns (3 sigma), past the 0.02.
+    model = (o, lse, *loc.window_bwd(q, k, v, f64(got[0]), do, W, S, bf16_operands=True))
+    plain = (o, lse, *loc.window_bwd(q, k, v, o, do, W, S))
+    for a, m, p, n in zip(got, model, plain, ("o", "lse", "dq", "dk", "dv")):
+        assert_close(f64(a), m, n)
+        assert_close_plain(f64(a), p, m, n)
+
+
+@pytest.mark.parametrize("L,W,S", [(1, 1, 0), (300, 1, 0), (300, 100, 4), (640, 128, 0), (640, 129, 128),
+                                   (641, 127, 129), (900, 256, 300), (2500, 700, 200), (2500, 5000, 0)])
+def test_window_visits_exactly_the_visible_keys(L, W, S):
+    """Scores are all zero and key j's value is 1 in column j % 128: row i of O
+    is the count of visible keys per column over their number n.  P is 2^0
+    and the count is exact; O is rounded to bf16 (2^-8 of it) after one fp32
+    division (1e-6).  LSE is ln n.  One key too many or too few changes a
+    column by at least 1 / 20 of it here."""
+    q = torch.zeros(L, 2, 128, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(L, 1, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros(L, 1, 128, dtype=torch.bfloat16, device="cuda")
+    v[torch.arange(L), 0, torch.arange(L) % 128] = 1.0
+    cfg = upipe.WindowConfig(L=L, H=2, Hkv=1, window=W, sinks=S)
+    o, lse = upipe.window_forward(cfg, q, k, v)
+    seen = loc.visible(np.arange(L), np.arange(L), W, S)
+    n = seen.sum(1)
+    want = (seen @ f64(v)[:, 0]) / n[:, None]
+    for h in range(2):
+        assert np.all(np.abs(f64(o)[:, h] - want) <= (2.0 ** -8 + 1e-6) * want)
+        np.testing.assert_allclose(f64(lse)[h], np.log(n), rtol=0, atol=2e-6)
+    # dV of a dO of ones in one column: sum over the queries that see key j of 1/n_i.  P is rounded to
+    # bf16 (2^-8), the sum over at most 2500 queries in fp32, dV to bf16 (2^-8).
+    do = torch.zeros_like(q)
+    do[:, :, 5] = 1.0
+    dq, dk, dv = upipe.window_backward(cfg, q, k, v, o, lse, do)
+    want = 2 * (seen / n[:, None]).sum(0)
+    assert np.all(np.abs(f64(dv)[:, 0, 5] - want) <= (2 * 2.0 ** -8 + 1e-4) * want)
+    assert not dq.any() and not dk.any()  # k and q are zero
+    status_ok()
+
+
+def test_window_past_the_sequence_is_the_causal_core():
+    q, k, v, do = dev(*synth.core_inputs(777, 4, 2))
+    cfg = upipe.Config(L=777, H=4, Hkv=2, U=4)
+    o, lse = upipe.core_forward(cfg, q, k, v)
+    want = (o, lse, *upipe.core_backward(cfg, q, k, v, o, lse, do))
+    for W, S in ((777, 0), (10 ** 12, 0), (5, 10 ** 12)):
+        wc = upipe.WindowConfig(L=777, H=4, Hkv=2, window=W, sinks=S)
+        o, lse = upipe.window_forward(wc, q, k, v)
+        for a, b, n in zip((o, lse, *upipe.window_backward(wc, q, k, v, o, lse, do)), want,
+                           ("o", "lse", "dq", "dk", "dv")):
+            assert_close(f64(a), f64(b), n)
+
+
+def test_window_large_scores_and_the_same_bits_again():
+    """Scores of some hundreds: the running maximum moves, rows keep one key."""
+    L, H, Hkv, W, S = 520, 2, 1, 150, 2
+    q, k, v, do = synth.core_inputs(L, H, Hkv)
+    q = (q.float() * 16).bfloat16()
+    cfg = upipe.WindowConfig(L=L, H=H, Hkv=Hkv, window=W, sinks=S)
+    qd, kd, vd, dod = dev(q, k, v, do)
+    runs = []
+    for _ in range(2):
+        o, lse = upipe.window_forward(cfg, qd, kd, vd)
+        runs.append((o, lse, *upipe.window_backward(cfg, qd, kd, vd, o, lse, dod)))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    ro, rl = loc.window_fwd(f64(q), f64(k), f64(v), W, S)
+    assert_close(f64(runs[0][0]), ro, "o")
+    np.testing.assert_allclose(f64(runs[0][1]), rl, rtol=1e-5, atol=1e-4)
+    status_ok()
+
+
+def test_window_on_another_stream_and_captured():
+    L, H, Hkv = 400, 4, 2
+    q, k, v, do = dev(*synth.core_inputs(L, H, Hkv))
+    cfg = upipe.WindowConfig(L=L, H=H, Hkv=Hkv, window=90, sinks=3)
+    o, lse = upipe.window_forward(cfg, q, k, v)
+    want = (o, lse, *upipe.window_backward(cfg, q, k, v, o, lse, do))
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    out = [torch.empty_like(t) for t in want]
+    upipe.window_fwd(cfg, q, k, v, out[0], out[1], stream=st)
+    upipe.window_bwd(cfg, q, k, v, out[0], out[1], do, *out[2:], stream=st)
+    st.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, lse2 = upipe.window_forward(cfg, q, k, v)
+        got = (o2, lse2, *upipe.window_backward(cfg, q, k, v, o2, lse2, do))
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    status_ok()
+
+
+def test_window_writes_nothing_past_its_rows():
+    """Rows behind the last token, in the same allocation, stay as they were."""
+    L, H, Hkv = 130, 2, 1
+    q, k, v, do = dev(*synth.core_inputs(L, H, Hkv))
+    cfg = upipe.WindowConfig(L=L, H=H, Hkv=Hkv, window=50, sinks=2)
+    big = {n: torch.full((L + 200, h, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+           for n, h in (("o", H), ("dq", H), ("dk", Hkv), ("dv", Hkv))}
+    lse = torch.full((H * L + 500,), 7.0, device="cuda")
+    upipe.window_fwd(cfg, q, k, v, big["o"][:L], lse[:H * L].view(H, L))
+    upipe.window_bwd(cfg, q, k, v, big["o"][:L], lse[:H * L].view(H, L), do, big["dq"][:L], big["dk"][:L],
+                     big["dv"][:L])
+    torch.cuda.synchronize()
+    for t in big.values():
+        assert bool((t[L:] == 7.0).all())
+    assert bool((lse[H * L:] == 7.0).all())
+    status_ok()
+
+
+def test_window_workspace_refusal():
+    L, H, Hkv = 64, 2, 1
+    q, k, v, do = dev(*synth.core_inputs(L, H, Hkv))
+    cfg = upipe.WindowConfig(L=L, H=H, Hkv=Hkv, window=5)
+    o, lse = upipe.window_forward(cfg, q, k, v)
+    need = upipe.window_workspace_bytes(cfg)
+    with pytest.raises(ValueError, match="ws"):
+        upipe.window_bwd(cfg, q, k, v, o, lse, do, q.clone(), k.clone(), v.clone(),
+                         ws=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))

@@ -218,3 +218,51 @@ def test_rope_entry_refuses_bad_shapes_pointers_and_strides(lib):
     assert lib.upipe_qk_norm_rope_workspace_bytes(r._ref, None) == 0
     assert upipe.qk_norm_rope_workspace_bytes(r, 1 << 20, 32, 8) == 456 * 2 * 128 * 4
     assert upipe.qk_norm_rope_workspace_bytes(r, 0, 32, 8) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(window=0), dict(window=-3), dict(sinks=-1), dict(L=0), dict(L=1 << 31), dict(d=64),
+                                dict(H=6, Hkv=4), dict(H=96, Hkv=8), dict(Hkv=0)])
+def test_window_refuses_bad_configurations(lib, kw):
+    import ctypes
+    base = dict(L=64, H=4, Hkv=2, window=9, sinks=1)
+    cfg = upipe.WindowConfig(**{**base, **kw})
+    assert upipe.window_workspace_bytes(cfg) == 0
+    a = [ctypes.c_void_p(1 << (20 + i)) for i in range(9)]
+    assert lib.upipe_window_fwd(ctypes.byref(cfg.c()), *a[:5], None) == upipe.UPIPE_ERR_INVALID_ARG
+    assert lib.upipe_window_bwd(ctypes.byref(cfg.c()), *a, a[0], 1 << 30, None) == upipe.UPIPE_ERR_INVALID_ARG
+
+
+def test_window_refuses_bad_pointers_and_workspaces(lib):
+    import ctypes
+    cfg = upipe.WindowConfig(L=200, H=4, Hkv=2, window=9, sinks=1)
+    c = ctypes.byref(cfg.c())
+    a = [ctypes.c_void_p(1 << (20 + i)) for i in range(9)]
+    for i in range(5):
+        for bad in (None, ctypes.c_void_p((1 << 20) + 8)):
+            b = list(a[:5])
+            b[i] = bad
+            assert lib.upipe_window_fwd(c, *b, None) == upipe.UPIPE_ERR_INVALID_ARG
+    need = upipe.window_workspace_bytes(cfg)
+    assert need > 0
+    for i in range(9):
+        b = list(a)
+        b[i] = ctypes.c_void_p((1 << 20) + 4)
+        assert lib.upipe_window_bwd(c, *b, a[0], need, None) == upipe.UPIPE_ERR_INVALID_ARG
+    assert lib.upipe_window_bwd(c, *a, None, need, None) == upipe.UPIPE_ERR_INVALID_ARG
+    assert lib.upipe_window_bwd(c, *a, a[0], need - 1, None) == upipe.UPIPE_ERR_WS_TOO_SMALL
+
+
+def test_window_binding_refuses_before_any_launch(lib):
+    n0 = upipe.launch_count()
+    cfg = upipe.WindowConfig(L=64, H=4, Hkv=2, window=9, sinks=1)
+    q, k = torch.zeros(64, 4, 128, dtype=torch.bfloat16), torch.zeros(64, 2, 128, dtype=torch.bfloat16)
+    lse = torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="q"):
+        upipe.window_fwd(cfg, q[:63], k, k, q, lse)
+    with pytest.raises(ValueError, match="lse"):
+        upipe.window_fwd(cfg, q, k, k, q, lse.double())
+    with pytest.raises(ValueError, match="dk"):
+        upipe.window_bwd(cfg, q, k, k, q, lse, q, q, q, k)
+    with pytest.raises(ValueError, match="CUDA"):
+        upipe.window_fwd(cfg, q, k, k, q, lse)
+    assert upipe.launch_count() == n0
