@@ -40,6 +40,9 @@ struct WinParams {
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
+  // Sink key tiles and the query tiles past their windows (see SinkPlan).
+  int sink_tiles, near_tiles, far_chunk, far_slots, sink_rows, shared_keys;
+  float* sink_part;
   float scale;       // 1/sqrt(d)
   float scale_log2;  // log2(e)/sqrt(d)
   int* status;
@@ -71,13 +74,35 @@ struct QuerySpan {
   __device__ __forceinline__ bool masked(int kb, const WinParams& p) const { return hides(qb, kb, p); }
 };
 
-// Number of 128-query tiles, from kb on, that see key tile kb.
-__device__ __forceinline__ int key_tile_queries(int kb, const WinParams& p) {
-  const int last = (p.L - 1) >> 7;
-  if (kb * 128 < p.sinks) return last - kb + 1;
-  const int64_t reach = (static_cast<int64_t>(kb) * 128 + 126 + p.window) >> 7;  // tile of the last key's last query
-  return (reach < last ? static_cast<int>(reach) : last) - kb + 1;
-}
+// One CTA's share of dK and dV: key tile kb of a KV head and the query tiles
+// [q0, q1) of the heads that read it.
+struct KeyItem {
+  int kv, kb, q0, q1;
+  int slot;  // of sink_part; -1: the CTA alone sums its keys
+  __device__ __forceinline__ KeyItem(int item, const WinParams& p) {
+    const int tiles = ((p.L - 1) >> 7) + 1;
+    kv = item % p.Hkv;
+    item /= p.Hkv;
+    const int far_items = p.sink_tiles * p.far_slots;
+    if (item < far_items) {  // the longest first
+      kb = item % p.sink_tiles;
+      slot = 1 + item / p.sink_tiles;
+      q0 = kb + p.near_tiles + (slot - 1) * p.far_chunk;
+      q1 = q0 + p.far_chunk;
+    } else {
+      kb = item - far_items;
+      slot = kb < p.sink_tiles && p.far_slots ? 0 : -1;
+      q0 = kb;
+      q1 = kb + p.near_tiles;
+    }
+    q1 = q1 < tiles ? q1 : tiles;
+  }
+  // fp32 share [2][sink_rows][128] of dK and dV
+  __device__ __forceinline__ float* part(const WinParams& p) const {
+    const int64_t at = (static_cast<int64_t>(kv) * p.sink_tiles + kb) * (p.far_slots + 1) + slot;
+    return p.sink_part + at * 2 * p.sink_rows * kHeadDim;
+  }
+};
 
 // Last query that sees key j.
 __device__ __forceinline__ int last_query(int j, const WinParams& p) {
@@ -861,11 +886,12 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int kb = static_cast<int>(blockIdx.x) / p.Hkv;
-  const int kv = static_cast<int>(blockIdx.x) % p.Hkv;
+  const KeyItem item(static_cast<int>(blockIdx.x), p);
+  const int kb = item.kb, kv = item.kv;
   const int n_q64 = (p.L + 63) / 64;
-  const int nqt = key_tile_queries(kb, p);  // query tiles from the key tile's own on
+  const int nqt = item.q1 - item.q0;
   const int n_it = p.g * nqt;
+  if (n_it <= 0) return;  // a later sink tile's last share
   auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
   const WaitCtl w{abort_flag, p.status, p.limit_ns};
@@ -919,7 +945,7 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
         const int s = it % kStages;
         const uint32_t ph = (it / kStages) & 1;
         const int hl = kv * p.g + it / nqt;
-        const int qt = kb + it % nqt;
+        const int qt = item.q0 + it % nqt;
         if (!mbar_wait(bar(B_QDO_EMPTY + s), ph ^ 1, w)) break;
         mbar_expect_tx(bar(B_QDO_FULL + s), 2 * kTile);
         tma_load_3d(sb + OFF_Q + s * kTile, &mq, bar(B_QDO_FULL + s), 0, qt * 128, hl);
@@ -1040,7 +1066,7 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     const uint32_t td = trow + TM_DPT + grp * 32;
     for (int it = 0; it < n_it; ++it) {
       const int hl = kv * p.g + it / nqt;
-      const int qt = kb + it % nqt;
+      const int qt = item.q0 + it % nqt;
       const int q0 = qt * 128 + grp * 32;  // query of this warp's first column
       // Without its record (all 64 queries past L) the slice is all zero.
       const bool masked = hides(qt, kb, p);  // warp-uniform
@@ -1106,12 +1132,20 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
       tc_fence_after();
       __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<int64_t>(kpos) * p.Hkv + kv) * kHeadDim + col0;
       const float scale = which == 0 ? p.scale : 1.f;
+      // a sink's sum is shared by several CTAs, every other key's is complete in its tile's own
+      float* part = item.slot >= 0 && kpos < p.sinks ? item.part(p) + (which * p.sink_rows + r) * kHeadDim + col0 : nullptr;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t v[32];
         tmem_ld32(my_tm + c * 32, v);
         tmem_ld_wait(v);
-        if (valid) store32_bf16(out + c * 32, v, scale);
+        if (part) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_global_v4(part + c * 32 + q * 4, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else if (valid && item.slot <= 0) {
+          store32_bf16(out + c * 32, v, scale);
+        }
       }
     }
     tc_fence_before();
@@ -1122,6 +1156,36 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// dK and dV of the sinks: the shares of one key are added in the order of
+// their slots, the tile's own first.  One warp per (KV head, sink, dK or dV).
+__global__ void __launch_bounds__(256) window_sink_kernel(const __grid_constant__ WinParams p) {
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (row >= static_cast<int64_t>(2) * p.shared_keys * p.Hkv) return;
+  const int which = static_cast<int>(row & 1);
+  const int key = static_cast<int>((row >> 1) % p.shared_keys);
+  const int kv = static_cast<int>((row >> 1) / p.shared_keys);
+  const int kb = key >> 7;
+  const int far = ((p.L - 1) >> 7) + 1 - kb - p.near_tiles;  // query tiles past the tile's window
+  const int slots = 1 + (far + p.far_chunk - 1) / p.far_chunk;
+  const int64_t size = static_cast<int64_t>(2) * p.sink_rows * kHeadDim;
+  const float* part = p.sink_part + (static_cast<int64_t>(kv) * p.sink_tiles + kb) * (p.far_slots + 1) * size +
+                      (which * p.sink_rows + (key & 127)) * kHeadDim + lane * 4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < slots; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(part + i * size);
+    sum.x += x.x;
+    sum.y += x.y;
+    sum.z += x.z;
+    sum.w += x.w;
+  }
+  const float scale = which == 0 ? p.scale : 1.f;
+  __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<int64_t>(key) * p.Hkv + kv) * kHeadDim + lane * 4;
+  *reinterpret_cast<uint2*>(out) =
+      make_uint2(pack_bf16x2(sum.x * scale, sum.y * scale), pack_bf16x2(sum.z * scale, sum.w * scale));
 }
 
 // ------------------------------------------------------------------- host
@@ -1143,6 +1207,37 @@ bool check_window(const upipe_window_cfg* c, WinShape* s) {
   s->window = static_cast<int>(c->window < c->L ? c->window : c->L);
   s->sinks = static_cast<int>(c->sinks < c->L ? c->sinks : c->L);
   return true;
+}
+
+// Key tiles that hold sinks are seen by every later query.  Their query tiles
+// past the window are cut into chunks, one CTA each, whose fp32 sums of the
+// sink rows window_sink_kernel adds up: one CTA for all of them would run on
+// alone for most of a long sequence's backward (L = 131072, 8 heads of one KV
+// head, window 1024: 14 of 17 ms).  A chunk is half of what an SM gets on
+// average, so that the longest shares still balance.
+struct SinkPlan {
+  int tiles = 0, near = 0, chunk = 1, slots = 0, rows = 0;
+  size_t bytes = 0;
+};
+
+SinkPlan sink_plan(const WinShape& s) {
+  SinkPlan f;
+  const int64_t reach = (static_cast<int64_t>(s.window) + 126) / 128 + 1;  // query tiles that a key tile's windows reach
+  f.near = static_cast<int>(reach < s.m_tiles ? reach : s.m_tiles);
+  f.tiles = (s.sinks + 127) / 128;
+  f.rows = s.sinks < 128 ? s.sinks : 128;
+  const int64_t far = s.m_tiles - f.near;  // of the first key tile; later ones have fewer
+  if (f.tiles == 0 || far <= 0) {
+    f.tiles = 0;
+    return f;
+  }
+  if (f.tiles > far) f.tiles = static_cast<int>(far);  // key tiles that have queries past their window
+  const int64_t all = static_cast<int64_t>(s.Hkv) * (static_cast<int64_t>(s.m_tiles) * f.near + far * f.tiles);
+  const int64_t chunk = (all + 2 * 152 - 1) / (2 * 152);
+  f.chunk = static_cast<int>(chunk < far ? chunk : far);
+  f.slots = static_cast<int>((far + f.chunk - 1) / f.chunk);
+  f.bytes = static_cast<size_t>(s.Hkv) * f.tiles * (f.slots + 1) * 2 * f.rows * kHeadDim * sizeof(float);
+  return f;
 }
 
 size_t records_bytes(const WinShape& s) {
@@ -1187,7 +1282,13 @@ cudaError_t launch_window_dkdv(const CUtensorMap& q, const CUtensorMap& k, const
   cudaError_t e =
       cudaFuncSetAttribute(window_dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wkv::kSmemBytes);
   if (e != cudaSuccess) return e;
-  window_dkdv_kernel<<<m_tiles * p.Hkv, wkv::kThreadsKv, wkv::kSmemBytes, st>>>(q, k, v, dO, p);
+  window_dkdv_kernel<<<(m_tiles + p.sink_tiles * p.far_slots) * p.Hkv, wkv::kThreadsKv, wkv::kSmemBytes, st>>>(q, k, v, dO, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_window_sinks(const WinParams& p, cudaStream_t st) {
+  const int64_t warps = static_cast<int64_t>(2) * p.shared_keys * p.Hkv;
+  window_sink_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -1200,7 +1301,7 @@ extern "C" {
 
 size_t upipe_window_workspace_bytes(const upipe_window_cfg* cfg) {
   WinShape s;
-  return check_window(cfg, &s) ? records_bytes(s) : 0;
+  return check_window(cfg, &s) ? records_bytes(s) + sink_plan(s).bytes : 0;
 }
 
 int upipe_window_fwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* o,
@@ -1233,7 +1334,8 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dout_o) ||
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(ws))
     return UPIPE_ERR_INVALID_ARG;
-  if (ws_bytes < records_bytes(s)) return UPIPE_ERR_WS_TOO_SMALL;
+  const SinkPlan f = sink_plan(s);
+  if (ws_bytes < records_bytes(s) + f.bytes) return UPIPE_ERR_WS_TOO_SMALL;
   int* status = nullptr;
   if (int e = device_ready(&status)) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1245,14 +1347,40 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   WinParams p = base_params(s, status);
   float* ld = static_cast<float*>(ws);
   p.ld = ld;
+  p.sink_tiles = f.tiles;
+  p.near_tiles = f.near;
+  p.far_chunk = f.chunk;
+  p.far_slots = f.slots;
+  p.sink_rows = f.rows;
+  p.shared_keys = s.sinks < f.tiles * 128 ? s.sinks : f.tiles * 128;
+  p.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + records_bytes(s));
   p.dq = reinterpret_cast<__nv_bfloat16*>(dq);
   p.dk = reinterpret_cast<__nv_bfloat16*>(dk);
   p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
   UPIPE_LAUNCH(UPIPE_KIND_DELTA,
                launch_delta(reinterpret_cast<const __nv_bfloat16*>(o), s.H * 128, 128,
                             reinterpret_cast<const __nv_bfloat16*>(dout_o), s.H * 128, 128, lse, ld, s.L, s.H, st));
-  UPIPE_LAUNCH(UPIPE_KIND_WINDOW_DKDV, launch_window_dkdv(mq, mk, mv, mdo, p, s.m_tiles, st));
-  UPIPE_LAUNCH(UPIPE_KIND_WINDOW_DQ, launch_window_dq(mq, mk, mv, mdo, p, s.m_tiles, st));
+  // Neither reads what the other writes: dQ's many short CTAs fill the SMs
+  // that the last of dK/dV's leave idle.
+  struct Job {
+    const CUtensorMap &q, &k, &v, &dO;
+    const WinParams& p;
+    int m_tiles;
+  } job{mq, mk, mv, mdo, p, s.m_tiles};
+  if (int e = launch_beside(
+          UPIPE_KIND_WINDOW_DKDV,
+          [](void* x, cudaStream_t on) {
+            const Job& j = *static_cast<Job*>(x);
+            return launch_window_dkdv(j.q, j.k, j.v, j.dO, j.p, j.m_tiles, on);
+          },
+          UPIPE_KIND_WINDOW_DQ,
+          [](void* x, cudaStream_t on) {
+            const Job& j = *static_cast<Job*>(x);
+            return launch_window_dq(j.q, j.k, j.v, j.dO, j.p, j.m_tiles, on);
+          },
+          &job, st))
+    return e;
+  if (f.slots) UPIPE_LAUNCH(UPIPE_KIND_WINDOW_SINKS, launch_window_sinks(p, st));
   return UPIPE_OK;
 }
 

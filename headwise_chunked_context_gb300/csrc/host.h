@@ -50,6 +50,12 @@ cudaError_t counted(int kind, cudaStream_t st, F&& launch) {
   return e;
 }
 
+// Runs two launches that read nothing of each other's at once: `side` on the
+// device's second stream (greatest priority, forked from `st` and joined back
+// by events), `own` on `st`.  Both are counted.  UPIPE_OK or an error code.
+using LaunchFn = cudaError_t (*)(void* job, cudaStream_t on);
+int launch_beside(int side_kind, LaunchFn side, int own_kind, LaunchFn own, void* job, cudaStream_t st);
+
 inline GemmParams gemm_base(int* status, uint64_t limit) {
   GemmParams g;
   std::memset(&g, 0, sizeof(g));

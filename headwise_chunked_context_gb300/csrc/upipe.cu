@@ -282,18 +282,44 @@ int side_stream(Side** out) {
   return UPIPE_OK;
 }
 
-int launch_attn_bwd_pair(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                         const CUtensorMap& mdo, const AttnBwdParams& b, int m_tiles, cudaStream_t st) {
+}  // namespace
+
+int launch_beside(int side_kind, LaunchFn side, int own_kind, LaunchFn own, void* job, cudaStream_t st) {
   std::lock_guard<std::mutex> lock(g_side_mu);
   Side* sd = nullptr;
   if (int e = side_stream(&sd)) return e;
   UPIPE_CU(cudaEventRecord(sd->fork, st));
   UPIPE_CU(cudaStreamWaitEvent(sd->s, sd->fork, 0));
-  UPIPE_CU(counted(UPIPE_KIND_ATTN_BWD_DKDV, sd->s, [&] { return launch_attn_bwd_dkdv(mq, mk, mv, mdo, b, m_tiles, sd->s); }));
-  UPIPE_CU(counted(UPIPE_KIND_ATTN_BWD_DQ, st, [&] { return launch_attn_bwd_dq(mq, mk, mv, mdo, b, m_tiles, st); }));
+  UPIPE_CU(counted(side_kind, sd->s, [&] { return side(job, sd->s); }));
+  UPIPE_CU(counted(own_kind, st, [&] { return own(job, st); }));
   UPIPE_CU(cudaEventRecord(sd->join, sd->s));
   UPIPE_CU(cudaStreamWaitEvent(st, sd->join, 0));
   return UPIPE_OK;
+}
+
+namespace {
+
+struct BwdPairJob {
+  const CUtensorMap &mq, &mk, &mv, &mdo;
+  const AttnBwdParams& b;
+  int m_tiles;
+};
+
+int launch_attn_bwd_pair(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                         const CUtensorMap& mdo, const AttnBwdParams& b, int m_tiles, cudaStream_t st) {
+  BwdPairJob job{mq, mk, mv, mdo, b, m_tiles};
+  return launch_beside(
+      UPIPE_KIND_ATTN_BWD_DKDV,
+      [](void* x, cudaStream_t on) {
+        const BwdPairJob& j = *static_cast<BwdPairJob*>(x);
+        return launch_attn_bwd_dkdv(j.mq, j.mk, j.mv, j.mdo, j.b, j.m_tiles, on);
+      },
+      UPIPE_KIND_ATTN_BWD_DQ,
+      [](void* x, cudaStream_t on) {
+        const BwdPairJob& j = *static_cast<BwdPairJob*>(x);
+        return launch_attn_bwd_dq(j.mq, j.mk, j.mv, j.mdo, j.b, j.m_tiles, on);
+      },
+      &job, st);
 }
 
 // Copy streams of the activation offload: one per direction and device,

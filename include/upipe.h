@@ -494,7 +494,8 @@ int upipe_window_fwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
 
 /* Gradients of sum(o * dout_o): dq [L, H, 128], dk, dv [L, Hkv, 128] bf16
  * (written), from o and lse of the forward.  Sums have one order: the same
- * inputs give the same bits.                                               */
+ * inputs give the same bits.  Uses the library's second stream as the other
+ * backward entries do (first backward call on a device outside capture).    */
 int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                      const uint16_t* o, const float* lse, const uint16_t* dout_o, uint16_t* dq, uint16_t* dk,
                      uint16_t* dv, void* ws, size_t ws_bytes, void* stream);
@@ -535,10 +536,11 @@ int upipe_debug_wait_timeout(uint64_t limit_ns, void* stream);
 #define UPIPE_KIND_CE_ROWS 15     /* softmax rows of the loss */
 #define UPIPE_KIND_QK_ROPE 16     /* rotation of queries and keys, with or without their norm */
 #define UPIPE_KIND_NORM_SUM 17    /* sums of the norm weights' gradients */
-#define UPIPE_KIND_WINDOW_FWD 18  /* windowed attention: forward, dQ, dK and dV */
+#define UPIPE_KIND_WINDOW_FWD 18  /* windowed attention: forward, dQ, dK and dV, sums of the sinks' */
 #define UPIPE_KIND_WINDOW_DQ 19
 #define UPIPE_KIND_WINDOW_DKDV 20
-#define UPIPE_KIND_COUNT 21
+#define UPIPE_KIND_WINDOW_SINKS 21
+#define UPIPE_KIND_COUNT 22
 int64_t upipe_launch_count(void);
 void upipe_profile_enable(int on);
 int upipe_profile_read(double* ms, int64_t* launches, int n);

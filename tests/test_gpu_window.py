@@ -27,6 +27,7 @@ CASES = [
     (300, 4, 1, 100, 4), (300, 2, 2, 300, 0), (257, 2, 1, 2, 1), (385, 4, 2, 129, 1), (640, 2, 1, 127, 130),
     (640, 2, 1, 128, 128), (641, 2, 1, 1, 640), (1000, 4, 1, 257, 5), (1000, 2, 1, 1, 1), (700, 2, 1, 2000, 3),
     (500, 2, 1, 40, 9000), (1100, 8, 2, 200, 300), (1500, 4, 4, 513, 16), (2049, 2, 1, 129, 1),
+    (1300, 2, 1, 900, 700), (1300, 4, 2, 640, 1000), (3000, 2, 1, 1, 130), (2200, 1, 1, 300, 2100),
 ]
 
 
