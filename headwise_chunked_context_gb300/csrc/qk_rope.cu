@@ -24,9 +24,8 @@
 // its heads when there are few tokens), a lane 16 elements of a head as two
 // 16-byte vectors that hold both members of its 8 pairs, so the rotation
 // stays in the lane and the norm is a reduction over d / 16 lanes.  Heads
-// whose pairs do not fall on 16-byte vectors (d not a multiple of 16, or
-// rot / 2 not a multiple of 8 in the half layout) take the same kernel with
-// two-byte accesses, up to four pairs per lane and one head per warp.
+// whose pairs do not fall on such vectors take the same kernel with 8-byte
+// ones, or with single elements (path_of).
 #include <cmath>
 #include <cstring>
 
@@ -42,7 +41,11 @@ constexpr int kMaxPairs = UPIPE_ROPE_MAX_D / 2;
 constexpr int kWarps = 8;  // per CTA
 
 enum Mode { kTurn = 0, kNormTurn = 1, kNormTurnBwd = 2 };
-enum Path { kHalfVec = 0, kInterVec = 1, kScalar = 2 };
+// How a lane holds its pairs: vectors of 8 or 4 elements in either layout, or
+// single elements.
+enum Path { kHalf8 = 0, kInter8 = 1, kHalf4 = 2, kInter4 = 3, kScalar = 4 };
+__host__ __device__ constexpr bool is_half(int path) { return path == kHalf8 || path == kHalf4; }
+__host__ __device__ constexpr int vec_of(int path) { return path == kHalf8 || path == kInter8 ? 8 : 4; }
 
 // A [L, heads, d] tensor of bf16 with its strides in elements.
 struct Rows {
@@ -67,23 +70,15 @@ struct QkParams {
   uint64_t step[kMaxPairs];
 };
 
-// Global reads that may alias this kernel's own later writes (in-place
-// calls): plain loads, not the read-only path; every element is read and
-// then written by one lane.
-__device__ __forceinline__ uint4 ld_stream(const bf16* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// Which elements of a head a lane holds: N pairs (a[e], b[e]).
+// Which elements of a head a lane holds: N pairs (a[e], b[e]), kept as N/2
+// packed fp32 pairs of the first members and N/2 of the second (u[i] = (a[2i],
+// a[2i+1]), v likewise), which halves the arithmetic's issue slots.
 template <int PATH>
 struct Lane {
-  static constexpr int N = PATH == kScalar ? 4 : 8;
+  static constexpr int N = vec_of(PATH);  // elements per vector, pairs per lane
+  static constexpr int M = N / 2;
   int sub;    // lane within its head
-  int off_a;  // vector paths: first element of the two 8-element vectors
+  int off_a;  // vector paths: first elements of the lane's two vectors
   int off_b;
   bool live;
   int d, rot, interleaved;
@@ -93,75 +88,131 @@ struct Lane {
     rot = p.rot;
     interleaved = p.interleaved;
     sub = lane % p.lanes;
-    live = PATH == kScalar || sub * 16 < d;
-    off_a = 16 * sub;
-    off_b = off_a + 8;
-    if (PATH == kHalfVec && sub * 16 < rot) {
-      off_a = 8 * sub;
-      off_b = rot / 2 + 8 * sub;
+    live = PATH == kScalar || sub * 2 * N < d;
+    // Neighbouring lanes hold neighbouring vectors, so that each access of a
+    // warp covers whole sectors: of the rotated half the first vectors and,
+    // rot/2 further, their partners; of what passes (and in the interleaved
+    // layout, whose pairs lie inside a vector) the two halves likewise.
+    const int turned = is_half(PATH) ? rot / (2 * N) : 0;  // lanes of the rotated part
+    if (sub < turned) {
+      off_a = N * sub;
+      off_b = rot / 2 + N * sub;
+    } else {
+      const int from = 2 * N * turned;
+      off_a = from + N * (sub - turned);
+      off_b = off_a + (d - from) / 2;
     }
   }
-  __device__ __forceinline__ int pair(int e) const { return PATH == kScalar ? sub + 32 * e : 8 * sub + e; }
+  __device__ __forceinline__ int pair(int e) const {
+    if (PATH == kScalar) return sub + 32 * e;
+    if (is_half(PATH)) return N * sub + e;
+    return e < M ? off_a / 2 + e : off_b / 2 + e - M;
+  }
   __device__ __forceinline__ bool holds(int e) const { return PATH == kScalar ? 2 * pair(e) < d : live; }
   __device__ __forceinline__ bool turns(int e) const { return 2 * pair(e) < rot; }
   __device__ __forceinline__ int first(int e) const {
-    if (PATH == kHalfVec) return off_a + e;
-    if (PATH == kInterVec) return 2 * pair(e);
-    return turns(e) && !interleaved ? pair(e) : 2 * pair(e);
+    if (is_half(PATH)) return off_a + e;
+    return PATH == kScalar && turns(e) && !interleaved ? pair(e) : 2 * pair(e);
   }
   __device__ __forceinline__ int second(int e) const {
-    if (PATH == kHalfVec) return off_b + e;
-    if (PATH == kInterVec) return 2 * pair(e) + 1;
-    return turns(e) && !interleaved ? pair(e) + rot / 2 : 2 * pair(e) + 1;
+    if (is_half(PATH)) return off_b + e;
+    return PATH == kScalar && turns(e) && !interleaved ? pair(e) + rot / 2 : 2 * pair(e) + 1;
   }
 };
 
-// What a lane has in flight of one head: its raw bits.
+// What a lane has in flight of one head: the words of its two vectors (the
+// scalar path: one word per pair).
 template <int PATH>
 struct Raw {
-  uint4 a, b;  // scalar path: the pairs' halves in the words of a
-  __device__ __forceinline__ void load(const bf16* head, const Lane<PATH>& ln) {
-    if constexpr (PATH == kScalar) {
-      uint32_t w[4];
+  uint32_t w[Lane<PATH>::N];
+  // Two-byte reads, volatile: an in-place call's own writes follow them.
+  __device__ __forceinline__ void load(const bf16* head, bool on, const Lane<PATH>& ln) {
+    const volatile uint16_t* h = reinterpret_cast<const volatile uint16_t*>(head);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e] = 0u;
-        if (ln.holds(e)) {
-          const uint16_t* h = reinterpret_cast<const uint16_t*>(head);
-          const uint32_t lo = *reinterpret_cast<const volatile uint16_t*>(h + ln.first(e));
-          const uint32_t hi = *reinterpret_cast<const volatile uint16_t*>(h + ln.second(e));
-          w[e] = lo | (hi << 16);
-        }
+    for (int e = 0; e < 4; ++e) {
+      w[e] = 0u;
+      if (on && ln.holds(e)) {
+        const uint32_t lo = h[ln.first(e)], hi = h[ln.second(e)];
+        w[e] = lo | (hi << 16);
       }
-      a = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      a = ld_stream(head + ln.off_a);
-      b = ld_stream(head + ln.off_b);
     }
   }
-  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void unpack(float (&u)[Lane<PATH>::N], float (&v)[Lane<PATH>::N]) const {
-    const uint32_t wa[4] = {a.x, a.y, a.z, a.w};
+  __device__ __forceinline__ void unpack(uint64_t (&u)[Lane<PATH>::M], uint64_t (&v)[Lane<PATH>::M]) const {
+    constexpr int M = Lane<PATH>::M;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      if (is_half(PATH)) {
+        u[i] = f2_pack(bf16_lo(w[i]), bf16_hi(w[i]));
+        v[i] = f2_pack(bf16_lo(w[M + i]), bf16_hi(w[M + i]));
+      } else {
+        u[i] = f2_pack(bf16_lo(w[2 * i]), bf16_lo(w[2 * i + 1]));
+        v[i] = f2_pack(bf16_hi(w[2 * i]), bf16_hi(w[2 * i + 1]));
+      }
+    }
+  }
+};
+
+// T tensors' heads in flight ahead of the arithmetic.  The vector paths copy
+// them asynchronously into the lane's own slots of a ring of S steps in
+// shared memory: what is in flight then costs no registers, and one warp
+// keeps S steps of loads open (in registers there was room for one, and a
+// backward of 16 warps per SM ran at 4.4 TB/s).  A lane reads back only what
+// it copied itself, so there is nothing to synchronise.  The scalar path
+// holds one step in registers (a copy is four bytes at least).
+template <int PATH, int T, int S>
+struct Pipe {
+  static constexpr int kBytes = PATH == kScalar ? 0 : S * T * 2 * 32 * 16;  // per warp
+  uint32_t slot;
+  int at;
+  Raw<PATH> held[PATH == kScalar ? T : 1];
+
+  __device__ __forceinline__ Pipe(uint32_t ring, int warp, int lane)
+      : slot(ring + warp * kBytes + lane * 16), at(0) {}
+  // One vector; off: zeros, and nothing is read.
+  static __device__ __forceinline__ void copy(uint32_t to, const bf16* from, bool on) {
+    if constexpr (vec_of(PATH) == 8)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(on ? 8 : 0) : "memory");
+  }
+  // Starts the copies of one step.
+  __device__ __forceinline__ void start(const bf16* const (&head)[T], bool on, const Lane<PATH>& ln) {
     if constexpr (PATH == kScalar) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        u[e] = bf16_lo(wa[e]);
-        v[e] = bf16_hi(wa[e]);
-      }
+      for (int t = 0; t < T; ++t) held[t].load(head[t], on, ln);
     } else {
-      const uint32_t wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (PATH == kHalfVec) {
-          u[2 * e] = bf16_lo(wa[e]);
-          u[2 * e + 1] = bf16_hi(wa[e]);
-          v[2 * e] = bf16_lo(wb[e]);
-          v[2 * e + 1] = bf16_hi(wb[e]);
+      for (int t = 0; t < T; ++t) {
+        const uint32_t to = slot + (at * T + t) * 1024;
+        copy(to, on ? head[t] + ln.off_a : head[t], on);
+        copy(to + 512, on ? head[t] + ln.off_b : head[t], on);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      at = at + 1 == S ? 0 : at + 1;
+    }
+  }
+  static constexpr int kAhead = PATH == kScalar ? 1 : S - 1;  // steps to start before the first turn
+  // Starts one more step and takes the oldest.
+  __device__ __forceinline__ void turn(const bf16* const (&head)[T], bool on, const Lane<PATH>& ln,
+                                       Raw<PATH> (&out)[T]) {
+    if constexpr (PATH == kScalar) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) out[t] = held[t];
+      start(head, on, ln);
+    } else {
+      start(head, on, ln);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+#pragma unroll
+      for (int t = 0; t < T; ++t) {  // the slot after the newest one's
+        const uint32_t from = slot + (at * T + t) * 1024;
+        if constexpr (vec_of(PATH) == 8) {
+          const uint4 a = ld_shared_v4(from), b = ld_shared_v4(from + 512);
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[t].w[i] = w[i];
         } else {
-          u[e] = bf16_lo(wa[e]);
-          v[e] = bf16_hi(wa[e]);
-          u[4 + e] = bf16_lo(wb[e]);
-          v[4 + e] = bf16_hi(wb[e]);
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(out[t].w[0]), "=r"(out[t].w[1]) : "r"(from));
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(out[t].w[2]), "=r"(out[t].w[3]) : "r"(from + 512));
         }
       }
     }
@@ -170,26 +221,39 @@ struct Raw {
 
 // Rounds the lane's pairs to bf16, the only rounding of the pass, and stores them.
 template <int PATH>
-__device__ __forceinline__ void store(bf16* head, const Lane<PATH>& ln, const float (&u)[Lane<PATH>::N],
-                                      const float (&v)[Lane<PATH>::N]) {
+__device__ __forceinline__ void store(bf16* head, const Lane<PATH>& ln, const uint64_t (&u)[Lane<PATH>::M],
+                                      const uint64_t (&v)[Lane<PATH>::M]) {
+  constexpr int M = Lane<PATH>::M;
+  uint32_t w[2 * M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    float a0, a1, b0, b1;
+    f2_unpack(u[i], a0, a1);
+    f2_unpack(v[i], b0, b1);
+    w[is_half(PATH) ? i : 2 * i] = is_half(PATH) ? pack_bf16x2(a0, a1) : pack_bf16x2(a0, b0);
+    w[is_half(PATH) ? M + i : 2 * i + 1] = is_half(PATH) ? pack_bf16x2(b0, b1) : pack_bf16x2(a1, b1);
+  }
   if constexpr (PATH == kScalar) {
+    uint16_t* h = reinterpret_cast<uint16_t*>(head);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (ln.holds(e)) {
-        head[ln.first(e)] = __float2bfloat16_rn(u[e]);
-        head[ln.second(e)] = __float2bfloat16_rn(v[e]);
+        h[ln.first(e)] = static_cast<uint16_t>(w[e]);
+        h[ln.second(e)] = static_cast<uint16_t>(w[e] >> 16);
       }
-  } else if constexpr (PATH == kHalfVec) {
-    st_global_v4(head + ln.off_a, pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]),
-                 pack_bf16x2(u[6], u[7]));
-    st_global_v4(head + ln.off_b, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                 pack_bf16x2(v[6], v[7]));
+  } else if constexpr (M == 4) {
+    st_global_v4(head + ln.off_a, w[0], w[1], w[2], w[3]);
+    st_global_v4(head + ln.off_b, w[4], w[5], w[6], w[7]);
   } else {
-    st_global_v4(head + ln.off_a, pack_bf16x2(u[0], v[0]), pack_bf16x2(u[1], v[1]), pack_bf16x2(u[2], v[2]),
-                 pack_bf16x2(u[3], v[3]));
-    st_global_v4(head + ln.off_b, pack_bf16x2(u[4], v[4]), pack_bf16x2(u[5], v[5]), pack_bf16x2(u[6], v[6]),
-                 pack_bf16x2(u[7], v[7]));
+    *reinterpret_cast<uint2*>(head + ln.off_a) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(head + ln.off_b) = make_uint2(w[2], w[3]);
   }
+}
+
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
 }
 
 // Sum over the lanes that share a head.
@@ -204,8 +268,8 @@ __device__ __forceinline__ float head_sum(float x, int lanes) {
 // shared-memory table, then every lane takes its pairs' values.
 template <int PATH>
 __device__ __forceinline__ void token_turns(const QkParams& p, int64_t token, int lane, float2* tab,
-                                            const Lane<PATH>& ln, float (&c)[Lane<PATH>::N],
-                                            float (&s)[Lane<PATH>::N]) {
+                                            const Lane<PATH>& ln, uint64_t (&c)[Lane<PATH>::M],
+                                            uint64_t (&s)[Lane<PATH>::M]) {
   const int64_t pos = p.positions ? static_cast<int64_t>(p.positions[token]) : p.pos0 + token;
   __syncwarp();
   for (int i = lane; i < p.rot / 2; i += 32) {
@@ -217,91 +281,142 @@ __device__ __forceinline__ void token_turns(const QkParams& p, int64_t token, in
   }
   __syncwarp();
 #pragma unroll
-  for (int e = 0; e < Lane<PATH>::N; ++e) {
-    const float2 t = ln.holds(e) && ln.turns(e) ? tab[ln.pair(e)] : make_float2(1.f, 0.f);
-    c[e] = t.x;
-    s[e] = t.y;
+  for (int i = 0; i < Lane<PATH>::M; ++i) {
+    const float2 t0 = ln.holds(2 * i) && ln.turns(2 * i) ? tab[ln.pair(2 * i)] : make_float2(1.f, 0.f);
+    const float2 t1 = ln.holds(2 * i + 1) && ln.turns(2 * i + 1) ? tab[ln.pair(2 * i + 1)] : make_float2(1.f, 0.f);
+    c[i] = f2_pack(t0.x, t1.x);
+    s[i] = f2_pack(t0.y, t1.y);
   }
 }
 
+// A lane's pairs of a weight held in shared memory.
 template <int PATH>
-__device__ __forceinline__ void load_weight(const float* w, const Lane<PATH>& ln, float (&wu)[Lane<PATH>::N],
-                                            float (&wv)[Lane<PATH>::N]) {
+__device__ __forceinline__ void lane_weight(const float* w, const Lane<PATH>& ln, uint64_t (&wu)[Lane<PATH>::M],
+                                            uint64_t (&wv)[Lane<PATH>::M]) {
+  if constexpr (PATH == kScalar) {
+    float f[8];
 #pragma unroll
-  for (int e = 0; e < Lane<PATH>::N; ++e) {
-    wu[e] = ln.holds(e) ? __ldg(w + ln.first(e)) : 0.f;
-    wv[e] = ln.holds(e) ? __ldg(w + ln.second(e)) : 0.f;
-  }
-}
-
-template <int MODE, int PATH>
-__global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const __grid_constant__ QkParams p) {
-  constexpr int N = Lane<PATH>::N;
-  constexpr int U = 4;  // heads in flight per lane
-  __shared__ float2 tables[kWarps][kMaxPairs];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int64_t token = unit / p.parts;
-  if (token >= p.L) return;
-  const int part = static_cast<int>(unit % p.parts);
-  const Lane<PATH> ln(p, lane);
-  const int per = 32 / p.lanes;  // heads per step of the warp
-  const int mine = lane / p.lanes;
-  const float inv_d = 1.f / p.d;
-  float c[N], s[N];
-  token_turns<PATH>(p, token, lane, tables[warp], ln, c, s);
-  for (int t = 0; t < 2; ++t) {
-    const int nh = p.nheads[t];
-    const bf16* x = p.x[t].p + token * p.x[t].row;
-    bf16* y = p.y[t].p + token * p.y[t].row;
-    float wu[N], wv[N];
-    if (MODE == kNormTurn && nh) load_weight<PATH>(p.w[t], ln, wu, wv);
-    for (int h0 = part * per; h0 < nh; h0 += p.parts * per * U) {
-      Raw<PATH> raw[U];
+    for (int e = 0; e < 4; ++e) {
+      f[e] = ln.holds(e) ? w[ln.first(e)] : 0.f;
+      f[4 + e] = ln.holds(e) ? w[ln.second(e)] : 0.f;
+    }
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int h = h0 + i * p.parts * per + mine;
-        raw[i].zero();
-        if (h < nh && ln.live) raw[i].load(x + h * p.x[t].head, ln);
-      }
+    for (int i = 0; i < 2; ++i) {
+      wu[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+      wv[i] = f2_pack(f[4 + 2 * i], f[4 + 2 * i + 1]);
+    }
+  } else {
+    constexpr int N = Lane<PATH>::N, M = Lane<PATH>::M;
+    float f[2 * N];  // the lane's two vectors
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int h = h0 + i * p.parts * per + mine;
-        float u[N], v[N];
-        raw[i].unpack(u, v);
-        if constexpr (MODE == kNormTurn) {
-          float q = 0.f;
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 a = reinterpret_cast<const float4*>(w + (ln.live ? ln.off_a : 0))[i];
+      const float4 b = reinterpret_cast<const float4*>(w + (ln.live ? ln.off_b : 0))[i];
+      f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = a.z, f[4 * i + 3] = a.w;
+      f[N + 4 * i] = b.x, f[N + 4 * i + 1] = b.y, f[N + 4 * i + 2] = b.z, f[N + 4 * i + 3] = b.w;
+    }
 #pragma unroll
-          for (int e = 0; e < N; ++e) q = fmaf(u[e], u[e], fmaf(v[e], v[e], q));
-          const float r = rsqrtf(head_sum(q, p.lanes) * inv_d + p.eps);
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            u[e] *= r * wu[e];
-            v[e] *= r * wv[e];
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float a = u[e] * c[e] - v[e] * s[e];
-          v[e] = u[e] * s[e] + v[e] * c[e];
-          u[e] = a;
-        }
-        if (h < nh && ln.live) store<PATH>(y + h * p.y[t].head, ln, u, v);
-      }
+    for (int i = 0; i < M; ++i) {
+      wu[i] = is_half(PATH) ? f2_pack(f[2 * i], f[2 * i + 1]) : f2_pack(f[4 * i], f[4 * i + 2]);
+      wv[i] = is_half(PATH) ? f2_pack(f[N + 2 * i], f[N + 2 * i + 1]) : f2_pack(f[4 * i + 1], f[4 * i + 3]);
     }
   }
 }
 
+// One step of a warp: `per` heads of one token, the queries' steps first,
+// then the keys'.
+struct Steps {
+  int per, q_steps, all;
+  __device__ __forceinline__ explicit Steps(const QkParams& p)
+      : per(32 / p.lanes), q_steps((p.nheads[0] + per - 1) / per), all(q_steps + (p.nheads[1] + per - 1) / per) {}
+};
+
+constexpr int kFwdSteps = 4, kBwdSteps = 4;  // steps in flight per warp
+
+template <int MODE, int PATH>
+__global__ void __launch_bounds__(kWarps * 32, 3) qk_rope_kernel(const __grid_constant__ QkParams p) {
+  constexpr int M = Lane<PATH>::M;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 tables[kWarps][kMaxPairs];
+  __shared__ __align__(16) float weights[2][MODE == kNormTurn ? UPIPE_ROPE_MAX_D : 4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if constexpr (MODE == kNormTurn) {
+    for (int i = threadIdx.x; i < 2 * p.d; i += kWarps * 32) {
+      const int t = i >= p.d;
+      if (p.nheads[t]) weights[t][i - t * p.d] = __ldg(p.w[t] + i - t * p.d);
+    }
+    __syncthreads();
+  }
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t token = p.parts == 1 ? unit : unit / p.parts;
+  if (token >= p.L) return;
+  const int part = static_cast<int>(unit - token * p.parts);
+  const Lane<PATH> ln(p, lane);
+  const Steps st(p);
+  const int mine = lane / p.lanes;
+  const float inv_d = 1.f / p.d;
+  const bf16 *const xq = p.x[0].p + token * p.x[0].row, *const xk = p.x[1].p + token * p.x[1].row;
+  bf16 *const yq = p.y[0].p + token * p.y[0].row, *const yk = p.y[1].p + token * p.y[1].row;
+
+  Pipe<PATH, 1, kFwdSteps> pipe(smem_u32(ring), warp, lane);
+  auto head_at = [&](int step, bool& on) -> const bf16* {
+    const int t = step >= st.q_steps;
+    const int h = (step - (t ? st.q_steps : 0)) * st.per + mine;
+    on = step < st.all && h < p.nheads[t] && ln.live;
+    return on ? (t ? xk + h * p.x[1].head : xq + h * p.x[0].head) : p.x[0].p;
+  };
+  int ahead = part;
+  bool on;
+#pragma unroll
+  for (int i = 0; i < Pipe<PATH, 1, kFwdSteps>::kAhead; ++i, ahead += p.parts) {
+    const bf16* src[1] = {head_at(ahead, on)};
+    pipe.start(src, on, ln);
+  }
+  uint64_t c[M], s[M];
+  token_turns<PATH>(p, token, lane, tables[warp], ln, c, s);
+  for (int step = part; step < st.all; step += p.parts, ahead += p.parts) {
+    Raw<PATH> raw[1];
+    const bf16* src[1] = {head_at(ahead, on)};
+    pipe.turn(src, on, ln, raw);
+    const int t = step >= st.q_steps;
+    const int h = (step - (t ? st.q_steps : 0)) * st.per + mine;
+    uint64_t u[M], v[M];
+    raw[0].unpack(u, v);
+    if constexpr (MODE == kNormTurn) {
+      uint64_t q = 0;
+#pragma unroll
+      for (int e = 0; e < M; ++e) q = f2_fma(u[e], u[e], f2_fma(v[e], v[e], q));
+      const float r = rsqrtf(head_sum(f2_sum(q), p.lanes) * inv_d + p.eps);
+      const uint64_t rr = f2_pack(r, r);
+      uint64_t wu[M], wv[M];
+      lane_weight<PATH>(weights[t], ln, wu, wv);
+#pragma unroll
+      for (int e = 0; e < M; ++e) {
+        u[e] = f2_mul(u[e], f2_mul(rr, wu[e]));
+        v[e] = f2_mul(v[e], f2_mul(rr, wv[e]));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < M; ++e) {
+      const uint64_t a = f2_sub(f2_mul(u[e], c[e]), f2_mul(v[e], s[e]));
+      v[e] = f2_fma(u[e], s[e], f2_mul(v[e], c[e]));
+      u[e] = a;
+    }
+    if (h < p.nheads[t] && ln.live) store<PATH>(t ? yk + h * p.y[1].head : yq + h * p.y[0].head, ln, u, v);
+  }
+}
+
 // Backward of the norm and rotation.  Each warp walks tokens (or shares of
-// tokens) a grid apart, the queries first, then the keys, and keeps its
-// lanes' shares of dw in registers; a CTA adds its warps' shares in a fixed
-// order and writes one row per weight, which norm_sum_kernel adds up.
+// tokens) a grid apart, the queries of all of them first, then the keys, and
+// keeps its lanes' shares of dw in registers; a CTA adds its warps' shares in
+// a fixed order and writes one row per weight, which norm_sum_kernel adds up.
 template <int PATH>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_bwd_kernel(const __grid_constant__ QkParams p) {
-  constexpr int N = Lane<PATH>::N;
-  constexpr int U = 2;  // heads in flight per lane
+__global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const __grid_constant__ QkParams p) {
+  constexpr int M = Lane<PATH>::M;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 tables[kWarps][kMaxPairs];
   __shared__ float shares[kWarps][UPIPE_ROPE_MAX_D];
+  __shared__ __align__(16) float weights[UPIPE_ROPE_MAX_D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t units = p.L * p.parts;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -311,73 +426,120 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_bwd_kernel(const __g
   const float inv_d = 1.f / p.d;
   for (int t = 0; t < 2; ++t) {
     const int nh = p.nheads[t];
-    float wu[N], wv[N], gu[N], gv[N];
-    if (nh) load_weight<PATH>(p.w[t], ln, wu, wv);
+    const int steps = (nh + per - 1) / per;
+    __syncthreads();  // the last weight's shares have been added up
+    for (int i = threadIdx.x; i < p.d && nh; i += kWarps * 32) weights[i] = __ldg(p.w[t] + i);
+    __syncthreads();
+    uint64_t wu[M], wv[M], gu[M], gv[M];
+    lane_weight<PATH>(weights, ln, wu, wv);
 #pragma unroll
-    for (int e = 0; e < N; ++e) gu[e] = gv[e] = 0.f;
-    for (int64_t unit = nh ? static_cast<int64_t>(blockIdx.x) * kWarps + warp : units; unit < units; unit += stride) {
-      const int64_t token = unit / p.parts;
-      const int part = static_cast<int>(unit % p.parts);
-      float c[N], s[N];
-      token_turns<PATH>(p, token, lane, tables[warp], ln, c, s);
-      const bf16* x = p.x[t].p + token * p.x[t].row;
-      const bf16* dy = p.dy[t].p + token * p.dy[t].row;
-      bf16* dx = p.y[t].p + token * p.y[t].row;
-      for (int h0 = part * per; h0 < nh; h0 += p.parts * per * U) {
-        Raw<PATH> rx[U], ry[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int h = h0 + i * p.parts * per + mine;
-          rx[i].zero();
-          ry[i].zero();
-          if (h < nh && ln.live) {
-            rx[i].load(x + h * p.x[t].head, ln);
-            ry[i].load(dy + h * p.dy[t].head, ln);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int h = h0 + i * p.parts * per + mine;
-          float u[N], v[N], a[N], b[N];
-          rx[i].unpack(u, v);
-          ry[i].unpack(a, b);
-          float q = 0.f;
-#pragma unroll
-          for (int e = 0; e < N; ++e) q = fmaf(u[e], u[e], fmaf(v[e], v[e], q));
-          const float r = rsqrtf(head_sum(q, p.lanes) * inv_d + p.eps);
-          float m = 0.f;
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            u[e] *= r;  // n
-            v[e] *= r;
-            const float za = a[e] * c[e] - b[e] * s[e];  // dz: s holds -sin here
-            const float zb = a[e] * s[e] + b[e] * c[e];
-            gu[e] = fmaf(za, u[e], gu[e]);
-            gv[e] = fmaf(zb, v[e], gv[e]);
-            a[e] = za * wu[e];  // dn
-            b[e] = zb * wv[e];
-            m = fmaf(a[e], u[e], fmaf(b[e], v[e], m));
-          }
-          m = head_sum(m, p.lanes) * inv_d;
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            a[e] = r * (a[e] - u[e] * m);
-            b[e] = r * (b[e] - v[e] * m);
-          }
-          if (h < nh && ln.live) store<PATH>(dx + h * p.y[t].head, ln, a, b);
-        }
+    for (int e = 0; e < M; ++e) gu[e] = gv[e] = 0;
+
+    struct At {
+      int64_t unit, token;
+      int step;
+    };
+    // the unit's first step, or the next unit that has one
+    auto begin = [&](int64_t unit) {
+      At a{unit, 0, 0};
+      for (; a.unit < units; a.unit += stride) {
+        a.token = p.parts == 1 ? a.unit : a.unit / p.parts;
+        a.step = static_cast<int>(a.unit - a.token * p.parts);
+        if (a.step < steps) break;
       }
+      return a;
+    };
+    auto after = [&](At a) {
+      a.step += p.parts;
+      return a.step < steps ? a : begin(a.unit + stride);
+    };
+    using Loads = Pipe<PATH, 2, kBwdSteps>;
+    Loads pipe(smem_u32(ring), warp, lane);
+    auto heads_at = [&](const At& a, const bf16* (&src)[2]) {
+      const int h = a.step * per + mine;
+      const bool on = a.unit < units && h < nh && ln.live;
+      src[0] = on ? p.x[t].p + a.token * p.x[t].row + h * p.x[t].head : p.x[t].p;
+      src[1] = on ? p.dy[t].p + a.token * p.dy[t].row + h * p.dy[t].head : p.dy[t].p;
+      return on;
+    };
+    At at = begin(nh ? static_cast<int64_t>(blockIdx.x) * kWarps + warp : units), ahead = at;
+    if (at.unit < units) {
+#pragma unroll
+      for (int i = 0; i < Loads::kAhead; ++i) {
+        const bf16* src[2];
+        const bool on = heads_at(ahead, src);
+        pipe.start(src, on, ln);
+        if (ahead.unit < units) ahead = after(ahead);
+      }
+    }
+    int64_t turned = -1;  // the token that c and s belong to
+    uint64_t c[M], s[M];
+    while (at.unit < units) {
+      if (turned != at.token) {
+        token_turns<PATH>(p, at.token, lane, tables[warp], ln, c, s);
+        turned = at.token;
+      }
+      Raw<PATH> raw[2];
+      const bf16* src[2];
+      const bool on = heads_at(ahead, src);
+      pipe.turn(src, on, ln, raw);
+      if (ahead.unit < units) ahead = after(ahead);
+      const int h = at.step * per + mine;
+      uint64_t u[M], v[M], a[M], b[M];
+      raw[0].unpack(u, v);
+      raw[1].unpack(a, b);
+      // sum x^2 and sum dn x in one reduction: neither needs the other
+      uint64_t q = 0, dot = 0;
+      uint64_t gx[M], gy[M];  // dz x, the terms of dw before the norm's factor
+#pragma unroll
+      for (int e = 0; e < M; ++e) {
+        const uint64_t za = f2_sub(f2_mul(a[e], c[e]), f2_mul(b[e], s[e]));  // dz: s holds -sin here
+        const uint64_t zb = f2_fma(a[e], s[e], f2_mul(b[e], c[e]));
+        q = f2_fma(u[e], u[e], f2_fma(v[e], v[e], q));
+        gx[e] = f2_mul(za, u[e]);
+        gy[e] = f2_mul(zb, v[e]);
+        dot = f2_fma(gx[e], wu[e], f2_fma(gy[e], wv[e], dot));
+        a[e] = f2_mul(za, wu[e]);  // dn
+        b[e] = f2_mul(zb, wv[e]);
+      }
+      float qs = f2_sum(q), ds = f2_sum(dot);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < p.lanes) {
+          const float q2 = __shfl_xor_sync(0xffffffffu, qs, o), d2 = __shfl_xor_sync(0xffffffffu, ds, o);
+          qs += q2;
+          ds += d2;
+        }
+      const float r = rsqrtf(qs * inv_d + p.eps);
+      const float k = -(r * r) * (r * ds) * inv_d;  // dx = r dn - x r^3 mean(dn x)
+      const uint64_t rr = f2_pack(r, r), kk = f2_pack(k, k);
+#pragma unroll
+      for (int e = 0; e < M; ++e) {
+        gu[e] = f2_fma(gx[e], rr, gu[e]);
+        gv[e] = f2_fma(gy[e], rr, gv[e]);
+        a[e] = f2_fma(u[e], kk, f2_mul(a[e], rr));
+        b[e] = f2_fma(v[e], kk, f2_mul(b[e], rr));
+      }
+      if (h < nh && ln.live) store<PATH>(p.y[t].p + at.token * p.y[t].row + h * p.y[t].head, ln, a, b);
+      at = after(at);
     }
     // The lanes that hold the same elements of different heads, then the warps.
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int i = 0; i < M; ++i) {
       for (int o = p.lanes; o < 32; o <<= 1) {
-        gu[e] += __shfl_xor_sync(0xffffffffu, gu[e], o);
-        gv[e] += __shfl_xor_sync(0xffffffffu, gv[e], o);
+        gu[i] = f2_add(gu[i], __shfl_xor_sync(0xffffffffu, gu[i], o));
+        gv[i] = f2_add(gv[i], __shfl_xor_sync(0xffffffffu, gv[i], o));
       }
-      if (mine == 0 && ln.holds(e)) {
-        shares[warp][ln.first(e)] = gu[e];
-        shares[warp][ln.second(e)] = gv[e];
+      float a0, a1, b0, b1;
+      f2_unpack(gu[i], a0, a1);
+      f2_unpack(gv[i], b0, b1);
+      if (mine == 0 && ln.holds(2 * i)) {
+        shares[warp][ln.first(2 * i)] = a0;
+        shares[warp][ln.second(2 * i)] = b0;
+      }
+      if (mine == 0 && ln.holds(2 * i + 1)) {
+        shares[warp][ln.first(2 * i + 1)] = a1;
+        shares[warp][ln.second(2 * i + 1)] = b1;
       }
     }
     __syncthreads();
@@ -387,7 +549,6 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_bwd_kernel(const __g
       for (int k = 0; k < kWarps; ++k) g += shares[k][i];
       p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + t) * p.d + i] = g;
     }
-    __syncthreads();
   }
 }
 
@@ -399,6 +560,7 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const float* __restrict_
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 d
   float g = 0.f;
   if (col < 2 * d)
+#pragma unroll 4
     for (int r = threadIdx.y; r < n; r += 32) g += partial[static_cast<int64_t>(r) * 2 * d + col];
   share[threadIdx.y][threadIdx.x] = g;
   __syncthreads();
@@ -414,11 +576,12 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const float* __restrict_
 
 // ------------------------------------------------------------------- host
 
-constexpr int kBwdCtas = 152 * 3;  // three resident per SM; the shares of dw are one row each
+constexpr int kBwdCtas = 152 * 2;  // two resident per SM; the shares of dw are one row each
 
-int lanes_of(int d) {
+int lanes_of(int d, int path) {
+  if (path == kScalar) return 32;
   int g = 1;
-  while (g * 16 < d) g *= 2;
+  while (g * 2 * vec_of(path) < d) g *= 2;
   return g;
 }
 
@@ -459,7 +622,7 @@ QkParams base_params(const upipe_rope* r, const upipe_qk_cfg* c, const int32_t* 
   p.nheads[1] = c->Hkv;
   p.d = r->d;
   p.rot = r->rot;
-  p.lanes = path == kScalar ? 32 : lanes_of(r->d);
+  p.lanes = lanes_of(r->d, path);
   p.interleaved = r->layout == UPIPE_ROPE_INTERLEAVED;
   p.magnitude = static_cast<float>(r->magnitude);
   p.sign = 1.f;
@@ -469,30 +632,41 @@ QkParams base_params(const upipe_rope* r, const upipe_qk_cfg* c, const int32_t* 
   // tokens than 16 warps on each of the 152 SMs, what hides the latency of
   // the loads; beyond, a share would only repeat the token's sines.
   const int per = 32 / p.lanes;
-  const int steps = (c->H + per - 1) / per;
+  const int steps = (c->H + per - 1) / per + (c->Hkv + per - 1) / per;
   const int64_t want = (152 * 16 + c->L - 1) / c->L;
   p.parts = static_cast<int>(want < steps ? want : steps);
   return p;
 }
 
-// The vector paths need 16-byte vectors that hold both members of each pair.
+// The widest vectors that hold whole pairs (interleaved) or whose partners are
+// vectors too (half), rotated and passing part alike.  32768 tokens of 40
+// heads of 128: 102 us with 8 elements; heads of 72, 4 elements, 154 us; 34 of
+// 128 rotated in halves, whose partners sit at odd elements, 256 us.
 int path_of(const upipe_rope* r) {
-  if (r->d % 16 != 0) return kScalar;
-  if (r->layout == UPIPE_ROPE_INTERLEAVED) return kInterVec;
-  return r->rot % 16 == 0 ? kHalfVec : kScalar;
+  const bool half = r->layout == UPIPE_ROPE_HALF;
+  const int whole = half ? r->rot | r->d : r->d;
+  if (whole % 16 == 0) return half ? kHalf8 : kInter8;
+  if (whole % 8 == 0) return half ? kHalf4 : kInter4;
+  return kScalar;
+}
+
+template <int MODE, int PATH>
+cudaError_t launch_fwd_path(const QkParams& p, cudaStream_t st) {
+  const int64_t units = p.L * p.parts;
+  const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
+  qk_rope_kernel<MODE, PATH><<<grid, kWarps * 32, kWarps * Pipe<PATH, 1, kFwdSteps>::kBytes, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <int MODE>
 cudaError_t launch_fwd(const QkParams& p, int path, cudaStream_t st) {
-  const int64_t units = p.L * p.parts;
-  const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
-  if (path == kHalfVec)
-    qk_rope_kernel<MODE, kHalfVec><<<grid, kWarps * 32, 0, st>>>(p);
-  else if (path == kInterVec)
-    qk_rope_kernel<MODE, kInterVec><<<grid, kWarps * 32, 0, st>>>(p);
-  else
-    qk_rope_kernel<MODE, kScalar><<<grid, kWarps * 32, 0, st>>>(p);
-  return cudaGetLastError();
+  switch (path) {
+    case kHalf8: return launch_fwd_path<MODE, kHalf8>(p, st);
+    case kInter8: return launch_fwd_path<MODE, kInter8>(p, st);
+    case kHalf4: return launch_fwd_path<MODE, kHalf4>(p, st);
+    case kInter4: return launch_fwd_path<MODE, kInter4>(p, st);
+  }
+  return launch_fwd_path<MODE, kScalar>(p, st);
 }
 
 int bwd_ctas(const QkParams& p) {
@@ -500,15 +674,24 @@ int bwd_ctas(const QkParams& p) {
   return static_cast<int>(need < kBwdCtas ? need : kBwdCtas);
 }
 
-cudaError_t launch_bwd(const QkParams& p, int path, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(bwd_ctas(p));
-  if (path == kHalfVec)
-    qk_norm_rope_bwd_kernel<kHalfVec><<<grid, kWarps * 32, 0, st>>>(p);
-  else if (path == kInterVec)
-    qk_norm_rope_bwd_kernel<kInterVec><<<grid, kWarps * 32, 0, st>>>(p);
-  else
-    qk_norm_rope_bwd_kernel<kScalar><<<grid, kWarps * 32, 0, st>>>(p);
+template <int PATH>
+cudaError_t launch_bwd_path(const QkParams& p, cudaStream_t st) {
+  constexpr int kRing = kWarps * Pipe<PATH, 2, kBwdSteps>::kBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(qk_norm_rope_bwd_kernel<PATH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+  if (e != cudaSuccess) return e;
+  qk_norm_rope_bwd_kernel<PATH><<<bwd_ctas(p), kWarps * 32, kRing, st>>>(p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_bwd(const QkParams& p, int path, cudaStream_t st) {
+  switch (path) {
+    case kHalf8: return launch_bwd_path<kHalf8>(p, st);
+    case kInter8: return launch_bwd_path<kInter8>(p, st);
+    case kHalf4: return launch_bwd_path<kHalf4>(p, st);
+    case kInter4: return launch_bwd_path<kInter4>(p, st);
+  }
+  return launch_bwd_path<kScalar>(p, st);
 }
 
 cudaError_t launch_norm_sum(const QkParams& p, float* dwq, float* dwk, cudaStream_t st) {

@@ -159,6 +159,9 @@ class WindowConfig:
     sinks: int = 0
     d: int = 128
 
+    def __post_init__(self):
+        object.__setattr__(self, "ref", ctypes.byref(self.c()))
+
     def c(self) -> WinCfg:
         return WinCfg(self.L, self.window, self.sinks, self.H, self.Hkv, self.d)
 
@@ -754,68 +757,89 @@ class Rope:
         self._ref = ctypes.byref(self.table)
 
 
-def _rows(t, L, d, heads, name):
+def _rows(t, L, heads, d, name, device):
     """A bf16 [L, heads, d] tensor, its rows and heads at any stride that
     keeps every head 16-byte aligned, as the library's description of it."""
-    if t is None:
-        raise ValueError(f"{name}: missing")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != L or shape[2] != d or shape[1] != heads or t.dtype != torch.bfloat16:
-        raise ValueError(f"{name}: expected {(L, heads, d)} {torch.bfloat16}, got {tuple(shape)} {t.dtype}")
+    if t is None or t.dtype != torch.bfloat16 or t.shape != (L, heads, d):
+        _expect(t, (L, heads, d), torch.bfloat16, name)
     row, head, one = t.stride()
     p = t.data_ptr()
-    if one != 1 or row % 8 or head % 8 or p % 16:
+    if one != 1 or (row | head) & 7 or p & 15:
         raise ValueError(f"{name}: expected heads of contiguous elements on 16-byte boundaries, got strides "
                          f"{(row, head, one)} at {p:#x}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != device:
+        _here(t, name)
     return ctypes.byref(Rows(p, row, head))
 
 
-def _qk_call(rope, q, k, pos0, positions, eps=0.0):
-    """(L, H, Hkv, upipe_qk_cfg, positions' pointer) of one call."""
+def _here(t, name):
+    """Index of the current device, where t has to be."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    device = torch.cuda.current_device()
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{device}")
+    return device
+
+
+def _raw(stream, device):
+    """Raw handle of `stream`, or of the device's current stream."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+
+
+def _qk_call(q, k, pos0, positions, eps):
+    """(L, H, Hkv, upipe_qk_cfg, positions' address) of one call."""
     if q is None or q.dim() != 3:
         raise ValueError("q: expected a [L, heads, d] tensor")
-    L, H = q.shape[0], q.shape[1]
-    Hkv = 0 if k is None else k.shape[1] if k.dim() == 3 else -1
+    L, H, _ = q.shape
+    Hkv = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k: expected a [L, heads, d] tensor")
+        Hkv = k.shape[1]
+    at = None
     if positions is not None:
         if pos0:
             raise ValueError("pos0 and positions: give one of them")
         _expect(positions, (L,), torch.int32, "positions")
         _on_device(positions=positions)
-    return L, H, Hkv, ctypes.byref(QkCfg(L, H, Hkv, pos0, eps)), _ptr(positions)
+        at = positions.data_ptr()
+    return L, H, Hkv, ctypes.byref(QkCfg(L, H, Hkv, pos0, eps)), at
 
 
 def rope_apply(rope: Rope, q, k, qo, ko, pos0: int = 0, positions=None, transpose: bool = False, stream=None):
     """upipe_rope_apply: q [L, H, d] into qo and k [L, Hkv, d] (or None) into
     ko, bf16, rotated to positions pos0, pos0 + 1, ... or `positions` [L]
     int32; `transpose` rotates gradients back.  qo may be q, and ko k."""
-    L, H, Hkv, c, pos = _qk_call(rope, q, k, pos0, positions)
     d = rope.d
-    rq, ro = _rows(q, L, d, H, "q"), _rows(qo, L, d, H, "qo")
-    rk, rko = (_rows(k, L, d, Hkv, "k"), _rows(ko, L, d, Hkv, "ko")) if k is not None else (None, None)
-    _check(lib().upipe_rope_apply(rope._ref, c, rq, rk, pos, ro, rko, int(transpose), _stream(stream)),
+    L, H, Hkv, c, at = _qk_call(q, k, pos0, positions, 0.0)
+    dev = q.get_device()
+    rq, rqo = _rows(q, L, H, d, "q", dev), _rows(qo, L, H, d, "qo", dev)
+    rk, rko = (_rows(k, L, Hkv, d, "k", dev), _rows(ko, L, Hkv, d, "ko", dev)) if k is not None else (None, None)
+    _check(lib().upipe_rope_apply(rope._ref, c, rq, rk, at, rqo, rko, transpose, _raw(stream, _here(q, "q"))),
            "upipe_rope_apply")
 
 
 def qk_norm_rope_fwd(rope: Rope, q, k, wq, wk, qo, ko, eps: float = 1e-6, pos0: int = 0, positions=None, stream=None):
     """upipe_qk_norm_rope_fwd: RMS norm of each head with weights wq, wk [d]
     fp32, then the rotation, q into qo and k (or None, with wk None) into ko."""
-    L, H, Hkv, c, pos = _qk_call(rope, q, k, pos0, positions, eps)
-    d = rope.d
-    rq, ro = _rows(q, L, d, H, "q"), _rows(qo, L, d, H, "qo")
-    rk, rko = (_rows(k, L, d, Hkv, "k"), _rows(ko, L, d, Hkv, "ko")) if k is not None else (None, None)
-    _norm_weights(d, wq=wq, wk=wk if k is not None else wq)
-    _check(lib().upipe_qk_norm_rope_fwd(rope._ref, c, rq, rk, _ptr(wq), _ptr(wk) if k is not None else None, pos, ro,
-                                        rko, _stream(stream)), "upipe_qk_norm_rope_fwd")
+    d, keys = rope.d, k is not None
+    L, H, Hkv, c, at = _qk_call(q, k, pos0, positions, eps)
+    dev = q.get_device()
+    rq, rqo = _rows(q, L, H, d, "q", dev), _rows(qo, L, H, d, "qo", dev)
+    rk, rko = (_rows(k, L, Hkv, d, "k", dev), _rows(ko, L, Hkv, d, "ko", dev)) if keys else (None, None)
+    pq, pk = _weight(wq, d, "wq", dev), _weight(wk, d, "wk", dev) if keys else None
+    _check(lib().upipe_qk_norm_rope_fwd(rope._ref, c, rq, rk, pq, pk, at, rqo, rko, _raw(stream, _here(q, "q"))),
+           "upipe_qk_norm_rope_fwd")
 
 
-def _norm_weights(d, **ws):
-    for name, w in ws.items():
+def _weight(w, d, name, device):
+    """Address of a norm's weight or its gradient, [d] fp32."""
+    if w is None or w.dtype != torch.float32 or w.shape != (d,):
         _expect(w, (d,), torch.float32, name)
-    _on_device(**ws)
+    if w.get_device() != device or not w.is_contiguous():
+        _on_device(**{name: w})
+    return w.data_ptr()
 
 
 def qk_norm_rope_workspace_bytes(rope: Rope, L: int, H: int, Hkv: int = 0) -> int:
@@ -826,18 +850,17 @@ def qk_norm_rope_bwd(rope: Rope, q, k, wq, wk, dqo, dko, dq, dk, dwq, dwk, eps: 
                      positions=None, ws=None, stream=None):
     """upipe_qk_norm_rope_bwd: from q, k and the gradients dqo, dko of the
     outputs to dq, dk (bf16) and dwq, dwk [d] fp32 (all written)."""
-    L, H, Hkv, c, pos = _qk_call(rope, q, k, pos0, positions, eps)
     d, keys = rope.d, k is not None
-    tq = [_rows(t, L, d, H, n) for t, n in ((q, "q"), (dqo, "dqo"), (dq, "dq"))]
-    tk = [_rows(t, L, d, Hkv, n) for t, n in ((k, "k"), (dko, "dko"), (dk, "dk"))] if keys else [None] * 3
-    _norm_weights(d, wq=wq, dwq=dwq)
-    if keys:
-        _norm_weights(d, wk=wk, dwk=dwk)
-    need = int(lib().upipe_qk_norm_rope_workspace_bytes(rope._ref, c))
-    ws, nbytes = _call_ws(need, ws, q.device, stream)
-    _check(lib().upipe_qk_norm_rope_bwd(rope._ref, c, tq[0], tk[0], _ptr(wq), _ptr(wk) if keys else None, pos, tq[1],
-                                        tk[1], tq[2], tk[2], _ptr(dwq), _ptr(dwk) if keys else None, _ptr(ws), nbytes,
-                                        _stream(stream)), "upipe_qk_norm_rope_bwd")
+    L, H, Hkv, c, at = _qk_call(q, k, pos0, positions, eps)
+    dev = q.get_device()
+    tq = [_rows(t, L, H, d, n, dev) for t, n in ((q, "q"), (dqo, "dqo"), (dq, "dq"))]
+    tk = [_rows(t, L, Hkv, d, n, dev) for t, n in ((k, "k"), (dko, "dko"), (dk, "dk"))] if keys else [None] * 3
+    pq, gq = _weight(wq, d, "wq", dev), _weight(dwq, d, "dwq", dev)
+    pk, gk = (_weight(wk, d, "wk", dev), _weight(dwk, d, "dwk", dev)) if keys else (None, None)
+    f, here = lib(), _here(q, "q")
+    ws, nbytes = _call_ws(f.upipe_qk_norm_rope_workspace_bytes(rope._ref, c), ws, q.device, stream)
+    _check(f.upipe_qk_norm_rope_bwd(rope._ref, c, tq[0], tk[0], pq, pk, at, tq[1], tk[1], tq[2], tk[2], gq, gk,
+                                    ws.data_ptr(), nbytes, _raw(stream, here)), "upipe_qk_norm_rope_bwd")
 
 
 def _call_ws(need, ws, device, stream):
@@ -847,39 +870,40 @@ def _call_ws(need, ws, device, stream):
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
         if stream is not None:
             ws.record_stream(stream)
+        return ws, ws.numel()
     _expect_ws(ws, need)
     return ws, ws.numel() * ws.element_size()
 
 
-def _dense(t):
-    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _like(t):
+    return None if t is None else torch.empty_like(t)
 
 
 def rope_forward(rope: Rope, q, k=None, pos0: int = 0, positions=None):
     """Allocates and returns (q, k) rotated to their positions (k None: None)."""
-    qo, ko = _dense(q), _dense(k)
+    qo, ko = _like(q), _like(k)
     rope_apply(rope, q, k, qo, ko, pos0, positions)
     return qo, ko
 
 
 def rope_backward(rope: Rope, dqo, dko=None, pos0: int = 0, positions=None):
     """Gradients (dq, dk) of rope_forward's inputs from those of its outputs."""
-    dq, dk = _dense(dqo), _dense(dko)
+    dq, dk = _like(dqo), _like(dko)
     rope_apply(rope, dqo, dko, dq, dk, pos0, positions, transpose=True)
     return dq, dk
 
 
 def qk_norm_rope_forward(rope: Rope, q, k, wq, wk, eps: float = 1e-6, pos0: int = 0, positions=None):
     """Allocates and returns (q, k) normalised and rotated."""
-    qo, ko = _dense(q), _dense(k)
+    qo, ko = _like(q), _like(k)
     qk_norm_rope_fwd(rope, q, k, wq, wk, qo, ko, eps, pos0, positions)
     return qo, ko
 
 
 def qk_norm_rope_backward(rope: Rope, q, k, wq, wk, dqo, dko, eps: float = 1e-6, pos0: int = 0, positions=None):
     """Allocates and returns (dq, dk, dwq, dwk) of qk_norm_rope_forward."""
-    dq, dk = _dense(q), _dense(k)
-    dwq, dwk = _dense(wq), _dense(wk) if k is not None else None
+    dq, dk = _like(q), _like(k)
+    dwq, dwk = _like(wq), _like(wk) if k is not None else None
     qk_norm_rope_bwd(rope, q, k, wq, wk, dqo, dko, dq, dk, dwq, dwk, eps, pos0, positions)
     return dq, dk, dwq, dwk
 
@@ -887,32 +911,45 @@ def qk_norm_rope_backward(rope: Rope, q, k, wq, wk, dqo, dko, eps: float = 1e-6,
 # ---------------------------------- attention with a window and sink tokens
 
 def window_workspace_bytes(cfg: WindowConfig) -> int:
-    return int(lib().upipe_window_workspace_bytes(ctypes.byref(cfg.c())))
+    return int(lib().upipe_window_workspace_bytes(cfg.ref))
 
 
 def window_fwd(cfg: WindowConfig, q, k, v, o, lse, stream=None):
     """upipe_window_fwd: tensors as attn_core_fwd."""
-    _core_tensors(cfg, q, k, v, lse, o)
-    _on_device(q=q, k=k, v=v, o=o, lse=lse)
-    _check(lib().upipe_window_fwd(ctypes.byref(cfg.c()), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
-                                  _stream(stream)), "upipe_window_fwd")
+    p = _window_tensors(cfg, (("q", q, cfg.H), ("k", k, cfg.Hkv), ("v", v, cfg.Hkv), ("o", o, cfg.H)), lse)
+    _check(lib().upipe_window_fwd(cfg.ref, *p, _raw(stream, q.get_device())), "upipe_window_fwd")
 
 
 def window_bwd(cfg: WindowConfig, q, k, v, o, lse, do, dq, dk, dv, ws=None, stream=None):
     """upipe_window_bwd: tensors as attn_core_bwd."""
-    _core_tensors(cfg, q, k, v, lse, o)
-    _core_grads(cfg, do, dq, dk, dv)
-    _on_device(q=q, k=k, v=v, o=o, lse=lse, dout_o=do, dq=dq, dk=dk, dv=dv)
-    c = cfg.c()
-    ws, nbytes = _call_ws(int(lib().upipe_window_workspace_bytes(ctypes.byref(c))), ws, q.device, stream)
-    _check(lib().upipe_window_bwd(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
-                                  _ptr(dk), _ptr(dv), _ptr(ws), nbytes, _stream(stream)), "upipe_window_bwd")
+    H, Hkv = cfg.H, cfg.Hkv
+    *p, l = _window_tensors(cfg, (("q", q, H), ("k", k, Hkv), ("v", v, Hkv), ("o", o, H), ("dout_o", do, H),
+                                  ("dq", dq, H), ("dk", dk, Hkv), ("dv", dv, Hkv)), lse)
+    f = lib()
+    ws, nbytes = _call_ws(f.upipe_window_workspace_bytes(cfg.ref), ws, q.device, stream)
+    _check(f.upipe_window_bwd(cfg.ref, *p[:4], l, *p[4:], ws.data_ptr(), nbytes, _raw(stream, q.get_device())),
+           "upipe_window_bwd")
+
+
+def _window_tensors(cfg, heads, lse):
+    """Addresses of the [L, n, 128] bf16 tensors of one call, then of lse,
+    checked as _core_tensors and _on_device do."""
+    L, got = cfg.L, []
+    for name, t, n in heads:
+        if t is None or t.dtype != torch.bfloat16 or t.shape != (L, n, 128):
+            _expect(t, (L, n, 128), torch.bfloat16, name)
+        got.append(t.data_ptr())
+    _expect(lse, (cfg.H, L), torch.float32, "lse")
+    dev = _here(heads[0][1], heads[0][0])
+    for name, t, _ in (*heads, ("lse", lse, 0)):
+        if t.get_device() != dev or not t.is_contiguous():
+            _on_device(**{name: t})
+    return *got, lse.data_ptr()
 
 
 def window_forward(cfg: WindowConfig, q, k, v):
     """Allocates and returns (o, lse)."""
-    o = torch.empty_like(q)
-    lse = torch.empty((cfg.H, cfg.L), dtype=torch.float32, device=q.device)
+    o, lse = torch.empty_like(q), torch.empty((cfg.H, cfg.L), dtype=torch.float32, device=q.device)
     window_fwd(cfg, q, k, v, o, lse)
     return o, lse
 

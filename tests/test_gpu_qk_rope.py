@@ -61,7 +61,9 @@ CASES = [
     (40, 40, 8, 16, 2, "interleaved"), (21, 7, 1, 8, 8, "half"), (21, 7, 1, 8, 4, "interleaved"),
     (50, 3, 2, 72, 72, "half"), (50, 3, 2, 96, 48, "half"), (50, 3, 2, 80, 80, "interleaved"),
     (19, 5, 1, 192, 96, "half"), (19, 5, 1, 256, 256, "half"), (19, 5, 1, 256, 254, "half"),
-    (19, 5, 1, 256, 250, "interleaved"), (2600, 3, 1, 64, 64, "half"),
+    (19, 5, 1, 256, 250, "interleaved"), (2600, 3, 1, 64, 64, "half"), (31, 3, 2, 72, 40, "interleaved"),
+    (31, 3, 2, 72, 8, "half"), (31, 3, 2, 128, 8, "half"), (23, 5, 2, 248, 248, "half"), (23, 5, 2, 256, 24, "half"),
+    (23, 5, 2, 248, 246, "interleaved"), (23, 3, 1, 248, 244, "half"),
 ]
 
 

@@ -216,7 +216,7 @@ def test_rope_entry_refuses_bad_shapes_pointers_and_strides(lib):
                dict(qo=(1 << 22, 4096, 136))):
         assert _entry(lib, r, **kw) in (upipe.UPIPE_ERR_CUDA, upipe.UPIPE_ERR_UNSUPPORTED_DEVICE), kw
     assert lib.upipe_qk_norm_rope_workspace_bytes(r._ref, None) == 0
-    assert upipe.qk_norm_rope_workspace_bytes(r, 1 << 20, 32, 8) == 456 * 2 * 128 * 4
+    assert upipe.qk_norm_rope_workspace_bytes(r, 1 << 20, 32, 8) == 304 * 2 * 128 * 4
     assert upipe.qk_norm_rope_workspace_bytes(r, 0, 32, 8) == 0
 
 
