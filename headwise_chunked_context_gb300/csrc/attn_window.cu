@@ -49,8 +49,16 @@ struct WinParams {
   uint64_t limit_ns;
 };
 
-__device__ __forceinline__ bool sees(int i, int j, const WinParams& p) {
-  return j <= i && (j > i - p.window || j < p.sinks);
+// Bits 0 .. n - 1 of a word (none below 1, all from 32 on).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
+// Which of the 32 keys from k0 on query i sees, bit c for key k0 + c.  A bit
+// test per score costs the masked blocks half of what comparisons of each
+// key's position would (0.55 us of a 1.4 us block).
+__device__ __forceinline__ uint32_t seen_keys(int i, int k0, const WinParams& p) {
+  return bits_below(i - k0 + 1) & ~(bits_below(i - p.window - k0 + 1) & ~bits_below(p.sinks - k0));
 }
 
 // Whether some query of tile qb does not see some key of block kb (of a pair
@@ -107,17 +115,18 @@ struct KeyItem {
 // Last query that sees key j.
 __device__ __forceinline__ int last_query(int j, const WinParams& p) {
   const int64_t q = static_cast<int64_t>(j) + p.window - 1;
-  return j < p.sinks || q > 0x7fffffff ? 0x7fffffff : static_cast<int>(q);
+  return j < p.sinks || q > 0x7ffffffe ? 0x7ffffffe : static_cast<int>(q);
 }
 
 // Scores of one query row against keys k0 .. k0 + 127: -inf where hidden.
 __device__ __forceinline__ void hide_row(float (&x)[128], int qpos, int k0, const WinParams& p) {
-  const int after = qpos - k0;              // columns past it are later keys
-  const int before = qpos - p.window - k0;  // columns up to it have left the window
-  const int sink = p.sinks - k0;            // columns before it are sinks
 #pragma unroll
-  for (int c = 0; c < 128; ++c)
-    if (c > after || (c <= before && c >= sink)) x[c] = -INFINITY;
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t seen = seen_keys(qpos, k0 + 32 * w, p);
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!(seen >> c & 1u)) x[32 * w + c] = -INFINITY;
+  }
 }
 
 // 32 fp32 accumulators of one row, scaled and rounded to bf16.
@@ -188,14 +197,19 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // Heads vary fastest: the CTAs in flight hold the same query blocks of
-  // every head, whose K/V blocks (shared within a GQA group) stay in L2, and
-  // the query blocks with the most KV blocks launch first.
-  const int h = static_cast<int>(blockIdx.x) % p.H;
-  const int qb = static_cast<int>(gridDim.x) / p.H - 1 - static_cast<int>(blockIdx.x) / p.H;
-  const int kz = h / p.g;
-  const QuerySpan sp(qb, p);
-  const int n_kv = sp.count();
+  // A CTA walks query tiles gridDim.x apart.  Heads vary fastest: the CTAs in
+  // flight hold the same query blocks of every head, whose K/V blocks (shared
+  // within a GQA group) stay in L2; the query blocks with the most KV blocks
+  // come first.
+  const int m_tiles = ((p.L - 1) >> 7) + 1;
+  const int n_tiles = m_tiles * p.H;
+  const int stride = static_cast<int>(gridDim.x);
+  const int first = static_cast<int>(blockIdx.x);
+  // Every second round runs the other way, so that a sequence's first tiles,
+  // which have fewer blocks, spread over all CTAs.
+  auto tile_of = [&](int n) { return n * stride + (n & 1 ? stride - 1 - first : first); };
+  auto head_of = [&](int t) { return t % p.H; };
+  auto block_of = [&](int t) { return m_tiles - 1 - t / p.H; };
   auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
   const WaitCtl w{abort_flag, p.status, p.limit_ns};
@@ -235,28 +249,47 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
       tma_prefetch_map(&mq);
       tma_prefetch_map(&mk);
       tma_prefetch_map(&mv);
-      mbar_expect_tx(bar(B_Q_FULL), kTile);
-      tma_load_3d(sb + OFF_Q, &mq, bar(B_Q_FULL), 0, qb * 128, h);
-      tma_load_3d(sb + OFF_Q + kHalf, &mq, bar(B_Q_FULL), 64, qb * 128, h);
+      auto load_q = [&](int t) {
+        mbar_expect_tx(bar(B_Q_FULL), kTile);
+        tma_load_3d(sb + OFF_Q, &mq, bar(B_Q_FULL), 0, block_of(t) * 128, head_of(t));
+        tma_load_3d(sb + OFF_Q + kHalf, &mq, bar(B_Q_FULL), 64, block_of(t) * 128, head_of(t));
+      };
       int last_k[kStages], last_v[kStages];
 #pragma unroll
       for (int s = 0; s < kStages; ++s) last_k[s] = last_v[s] = -1;
-      for (int j = 0; j < n_kv; ++j) {
-        const int s = j % kStages;
-        const uint32_t ph = (j / kStages) & 1;
-        if (!mbar_wait(bar(B_K_EMPTY + s), ph ^ 1, w)) break;
-        mbar_expect_tx(bar(B_K_FULL + s), kTile);
-        tma_load_3d(sb + OFF_K + s * kTile, &mk, bar(B_K_FULL + s), 0, sp.block(j) * 128, kz);
-        tma_load_3d(sb + OFF_K + s * kTile + kHalf, &mk, bar(B_K_FULL + s), 64, sp.block(j) * 128, kz);
-        last_k[s] = j;
-        if (!mbar_wait(bar(B_V_EMPTY + s), ph ^ 1, w)) break;
-        mbar_expect_tx(bar(B_V_FULL + s), kTile);
-        tma_load_3d(sb + OFF_V + s * kTile, &mv, bar(B_V_FULL + s), 0, sp.block(j) * 128, kz);
-        tma_load_3d(sb + OFF_V + s * kTile + kHalf, &mv, bar(B_V_FULL + s), 64, sp.block(j) * 128, kz);
-        last_v[s] = j;
+      load_q(first);
+      int last_q = 0;  // the Q load issued last
+      int it = 0;      // KV blocks of all tiles so far
+      bool ok = true;
+      for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
+        const QuerySpan sp(block_of(t), p);
+        const int kz = head_of(t) / p.g;
+        const int n_kv = sp.count();
+        for (int j = 0; j < n_kv; ++j, ++it) {
+          const int s = it % kStages;
+          const uint32_t ph = (it / kStages) & 1;
+          const int row = sp.block(j) * 128;
+          if (!(ok = mbar_wait(bar(B_K_EMPTY + s), ph ^ 1, w))) break;
+          mbar_expect_tx(bar(B_K_FULL + s), kTile);
+          tma_load_3d(sb + OFF_K + s * kTile, &mk, bar(B_K_FULL + s), 0, row, kz);
+          tma_load_3d(sb + OFF_K + s * kTile + kHalf, &mk, bar(B_K_FULL + s), 64, row, kz);
+          last_k[s] = it;
+          if (!(ok = mbar_wait(bar(B_V_EMPTY + s), ph ^ 1, w))) break;
+          mbar_expect_tx(bar(B_V_FULL + s), kTile);
+          tma_load_3d(sb + OFF_V + s * kTile, &mv, bar(B_V_FULL + s), 0, row, kz);
+          tma_load_3d(sb + OFF_V + s * kTile + kHalf, &mv, bar(B_V_FULL + s), 64, row, kz);
+          last_v[s] = it;
+          // The next tile's Q as soon as this one's is in TMEM, a block or
+          // more before it is wanted.
+          if (j == (n_kv > 1 ? 1 : 0) && tile_of(n + 1) < n_tiles) {
+            if (!(ok = mbar_wait(bar(B_Q_TMEM), n & 1, w))) break;
+            load_q(tile_of(n + 1));
+            last_q = n + 1;
+          }
+        }
       }
       if (*abort_flag) {  // let every issued copy land before the CTA exits
-        mbar_wait_drain(bar(B_Q_FULL), 0, p.status);
+        mbar_wait_drain(bar(B_Q_FULL), last_q & 1, p.status);
         for (int s = 0; s < kStages; ++s) {
           if (last_k[s] >= 0) mbar_wait_drain(bar(B_K_FULL + s), (last_k[s] / kStages) & 1, p.status);
           if (last_v[s] >= 0) mbar_wait_drain(bar(B_V_FULL + s), (last_v[s] / kStages) & 1, p.status);
@@ -267,21 +300,27 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
     // ------------------------------------------------------------ S issuer
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);  // Q (TMEM) x K (smem, K-major)
-      // S(j) once K(j) has landed and the softmax warps have read S(j - 1).
-      bool ok = mbar_spin(bar(B_Q_TMEM), 0, w);
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int s = j % kStages;
-        if (!(ok = mbar_spin(bar(B_K_FULL + s), (j / kStages) & 1, w))) break;
-        if (!(ok = mbar_spin(bar(B_S_READ), (j & 1) ^ 1, w))) break;
-        tc_fence_after();
-        const uint32_t ka = sb + OFF_K + s * kTile;
+      // S(j) once K(j) has landed and the softmax warps have read S(j - 1);
+      // a tile's first one also wants its Q in TMEM.
+      bool ok = true;
+      int it = 0;
+      for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
+        const int n_kv = QuerySpan(block_of(t), p).count();
+        if (!(ok = mbar_spin(bar(B_Q_TMEM), n & 1, w))) break;
+        for (int j = 0; j < n_kv; ++j, ++it) {
+          const int s = it % kStages;
+          if (!(ok = mbar_spin(bar(B_K_FULL + s), (it / kStages) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_S_READ), (it & 1) ^ 1, w))) break;
+          tc_fence_after();
+          const uint32_t ka = sb + OFF_K + s * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          umma_bf16_ts(tmem + TM_S, tmem + TM_Q + kk * 8,
-                       sdesc_sw128(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            umma_bf16_ts(tmem + TM_S, tmem + TM_Q + kk * 8,
+                         sdesc_sw128(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar(B_S_FULL));
+          umma_commit(bar(B_K_EMPTY + s));
         }
-        umma_commit(bar(B_S_FULL));
-        umma_commit(bar(B_K_EMPTY + s));
       }
       umma_commit(bar(B_DRAIN));
       mbar_wait_drain(bar(B_DRAIN), 0, p.status);
@@ -291,20 +330,25 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t id_o = idesc_bf16(128, 128, 0, 1);  // P (TMEM) x V (smem, MN-major)
       bool ok = true;
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int b = j & 1;
-        const int s = j % kStages;
-        if (!(ok = mbar_spin(bar(B_P_FULL + b), (j >> 1) & 1, w))) break;
-        if (!(ok = mbar_spin(bar(B_V_FULL + s), (j / kStages) & 1, w))) break;
-        tc_fence_after();
-        const uint32_t va = sb + OFF_V + s * kTile;
+      int it = 0;
+      for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
+        const int n_kv = QuerySpan(block_of(t), p).count();
+        for (int j = 0; j < n_kv; ++j, ++it) {
+          const int b = it & 1;
+          const int s = it % kStages;
+          // a tile's first P is written after the last tile's O has been read
+          if (!(ok = mbar_spin(bar(B_P_FULL + b), (it >> 1) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_V_FULL + s), (it / kStages) & 1, w))) break;
+          tc_fence_after();
+          const uint32_t va = sb + OFF_V + s * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          umma_bf16_ts(tmem + TM_O, tmem + TM_P + b * 64 + kk * 8, sdesc_sw128(va + kk * 2048, kHalf, 1024), id_o,
-                       (j > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            umma_bf16_ts(tmem + TM_O, tmem + TM_P + b * 64 + kk * 8, sdesc_sw128(va + kk * 2048, kHalf, 1024), id_o,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(bar(B_P_EMPTY + b));
+          umma_commit(bar(B_V_EMPTY + s));
         }
-        umma_commit(bar(B_P_EMPTY + b));
-        umma_commit(bar(B_V_EMPTY + s));
       }
       umma_commit(bar(B_DRAIN_PV));
       mbar_wait_drain(bar(B_DRAIN_PV), 0, p.status);
@@ -312,14 +356,11 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
   } else {
     // ------------------------------------------------------------- softmax
     const int r = warp * 32 + lane;  // query row in the tile = TMEM lane
-    const int qpos = qb * 128 + r;
     const uint32_t trow = tmem_lane_addr(tmem, warp, 0);
     const float sl2 = p.scale_log2;
-    float m_use = -INFINITY;  // running max used as the exponent offset (log2 domain)
-    float l = 0.f;
-    // Q row r -> TMEM (packed bf16, element pairs per column).
-    bool ok = warp_wait(bar(B_Q_FULL), 0, w);
-    if (ok) {
+    // Row r of the n-th tile's Q -> TMEM (packed bf16, element pairs per column).
+    auto take_q = [&](int n) -> bool {
+      if (!warp_wait(bar(B_Q_FULL), n & 1, w)) return false;
 #pragma unroll
       for (int hq = 0; hq < 2; ++hq) {
         uint32_t q[32];
@@ -337,107 +378,120 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_Q_TMEM));
-    }
-    for (int j = 0; ok && j < n_kv; ++j) {
-      const int b = j & 1;  // P buffer
-      if (!(ok = warp_wait(bar(B_S_FULL), j & 1, w))) break;
-      tc_fence_after();
-      const uint32_t tsb = trow + TM_S;
-      uint32_t v0[32], v1[32], v2[32], v3[32];
-      tmem_ld32(tsb + 0, v0);
-      tmem_ld32(tsb + 32, v1);
-      tmem_ld32(tsb + 64, v2);
-      tmem_ld32(tsb + 96, v3);
-      tmem_ld_wait(v0);
-      tmem_ld_wait(v1);
-      tmem_ld_wait(v2);
-      tmem_ld_wait(v3);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_S_READ));  // S(j + 1) may overwrite the scores
-
-      float x[128];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        x[c] = __uint_as_float(v0[c]);
-        x[32 + c] = __uint_as_float(v1[c]);
-        x[64 + c] = __uint_as_float(v2[c]);
-        x[96 + c] = __uint_as_float(v3[c]);
-      }
-      const int kb = sp.block(j);
-      if (sp.masked(kb, p)) hide_row(x, qpos, kb * 128, p);
-      // Row max: four independent chains of 3-input max.
-      float mc[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int c = 4; c < 124; c += 8) {
-        mc[0] = fmax3(mc[0], x[c], x[c + 1]);
-        mc[1] = fmax3(mc[1], x[c + 2], x[c + 3]);
-        mc[2] = fmax3(mc[2], x[c + 4], x[c + 5]);
-        mc[3] = fmax3(mc[3], x[c + 6], x[c + 7]);
-      }
-      mc[0] = fmax3(mc[0], x[124], x[125]);
-      mc[1] = fmax3(mc[1], x[126], x[127]);
-      const float mx = fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]);
-      const float m_new = fmaxf(m_use, mx * sl2);
-      const bool need = m_new > m_use + 8.0f;
-      if (j > 0 && __any_sync(0xffffffffu, need)) {
-        // O holds PV(0..j-1) once PV(j - 1) completes: rescale the rows
-        // that moved.
-        if (!(ok = warp_wait(bar(B_P_EMPTY + ((j - 1) & 1)), ((j - 1) >> 1) & 1, w))) break;
+      return true;
+    };
+    bool ok = take_q(0);
+    int it = 0;
+    for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
+      const int h = head_of(t), qb = block_of(t);
+      const QuerySpan sp(qb, p);
+      const int n_kv = sp.count();
+      const int qpos = qb * 128 + r;
+      float m_use = -INFINITY;  // running max used as the exponent offset (log2 domain)
+      float l = 0.f;
+      for (int j = 0; j < n_kv; ++j, ++it) {
+        const int b = it & 1;  // P buffer
+        if (!(ok = warp_wait(bar(B_S_FULL), it & 1, w))) break;
         tc_fence_after();
-        const float f = need ? ex2_approx(m_use - m_new) : 1.f;
+        const uint32_t tsb = trow + TM_S;
+        uint32_t v0[32], v1[32], v2[32], v3[32];
+        tmem_ld32(tsb + 0, v0);
+        tmem_ld32(tsb + 32, v1);
+        tmem_ld32(tsb + 64, v2);
+        tmem_ld32(tsb + 96, v3);
+        tmem_ld_wait(v0);
+        tmem_ld_wait(v1);
+        tmem_ld_wait(v2);
+        tmem_ld_wait(v3);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_S_READ));  // S(j + 1) may overwrite the scores
+
+        float x[128];
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t o[32];
-          tmem_ld32(trow + TM_O + c4 * 32, o);
-          tmem_ld_wait(o);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-          tmem_st32(trow + TM_O + c4 * 32, o);
+        for (int c = 0; c < 32; ++c) {
+          x[c] = __uint_as_float(v0[c]);
+          x[32 + c] = __uint_as_float(v1[c]);
+          x[64 + c] = __uint_as_float(v2[c]);
+          x[96 + c] = __uint_as_float(v3[c]);
         }
-        l *= f;
-      }
-      if (need) m_use = m_new;
+        const int kb = sp.block(j);
+        if (sp.masked(kb, p)) hide_row(x, qpos, kb * 128, p);
+        // Row max: four independent chains of 3-input max.
+        float mc[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < 124; c += 8) {
+          mc[0] = fmax3(mc[0], x[c], x[c + 1]);
+          mc[1] = fmax3(mc[1], x[c + 2], x[c + 3]);
+          mc[2] = fmax3(mc[2], x[c + 4], x[c + 5]);
+          mc[3] = fmax3(mc[3], x[c + 6], x[c + 7]);
+        }
+        mc[0] = fmax3(mc[0], x[124], x[125]);
+        mc[1] = fmax3(mc[1], x[126], x[127]);
+        const float mx = fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]);
+        const float m_new = fmaxf(m_use, mx * sl2);
+        const bool need = m_new > m_use + 8.0f;
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+          // O holds PV(0..j-1) once PV(j - 1) completes: rescale the rows
+          // that moved.
+          if (!(ok = warp_wait(bar(B_P_EMPTY + ((it - 1) & 1)), ((it - 1) >> 1) & 1, w))) break;
+          tc_fence_after();
+          const float f = need ? ex2_approx(m_use - m_new) : 1.f;
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {
+            uint32_t o[32];
+            tmem_ld32(trow + TM_O + c4 * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_st32(trow + TM_O + c4 * 32, o);
+          }
+          l *= f;
+        }
+        if (need) m_use = m_new;
 
-      uint32_t pk0[32], pk1[32];
-      const uint64_t sl2x2 = f2_pack(sl2, sl2);
-      const uint64_t nmx2 = f2_pack(-m_use, -m_use);
-      uint64_t acc[4] = {0, 0, 0, 0};  // (+0, +0) pairs
+        uint32_t pk0[32], pk1[32];
+        const uint64_t sl2x2 = f2_pack(sl2, sl2);
+        const uint64_t nmx2 = f2_pack(-m_use, -m_use);
+        uint64_t acc[4] = {0, 0, 0, 0};  // (+0, +0) pairs
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        float t0, t1, t2, t3;
-        f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sl2x2, nmx2), t0, t1);
-        f2_unpack(f2_fma(f2_pack(x[64 + c], x[64 + c + 1]), sl2x2, nmx2), t2, t3);
-        const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-        const float p2 = ex2_approx(t2), p3 = ex2_approx(t3);
-        acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2_pack(p0, p1));
-        acc[2 + ((c >> 1) & 1)] = f2_add(acc[2 + ((c >> 1) & 1)], f2_pack(p2, p3));
-        pk0[c >> 1] = pack_bf16x2(p0, p1);
-        pk1[c >> 1] = pack_bf16x2(p2, p3);
-      }
-      float rs = 0.f;
+        for (int c = 0; c < 64; c += 2) {
+          float t0, t1, t2, t3;
+          f2_unpack(f2_fma(f2_pack(x[c], x[c + 1]), sl2x2, nmx2), t0, t1);
+          f2_unpack(f2_fma(f2_pack(x[64 + c], x[64 + c + 1]), sl2x2, nmx2), t2, t3);
+          const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+          const float p2 = ex2_approx(t2), p3 = ex2_approx(t3);
+          acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2_pack(p0, p1));
+          acc[2 + ((c >> 1) & 1)] = f2_add(acc[2 + ((c >> 1) & 1)], f2_pack(p2, p3));
+          pk0[c >> 1] = pack_bf16x2(p0, p1);
+          pk1[c >> 1] = pack_bf16x2(p2, p3);
+        }
+        float rs = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float a, b;
-        f2_unpack(acc[i], a, b);
-        rs += a + b;
+        for (int i = 0; i < 4; ++i) {
+          float a, b;
+          f2_unpack(acc[i], a, b);
+          rs += a + b;
+        }
+        l += rs;
+        // P buffer b held P(it - 2) until PV(it - 2) completed.
+        if (it >= 2) {
+          if (!(ok = warp_wait(bar(B_P_EMPTY + b), ((it >> 1) & 1) ^ 1, w))) break;
+          tc_fence_after();
+        }
+        tmem_st32(trow + TM_P + b * 64 + 0, pk0);
+        tmem_st32(trow + TM_P + b * 64 + 32, pk1);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P_FULL + b));
       }
-      l += rs;
-      // P buffer b held P(j - 2) until PV(j - 2) completed.
-      if (j >= 2) {
-        if (!(ok = warp_wait(bar(B_P_EMPTY + b), ((j >> 1) & 1) ^ 1, w))) break;
-        tc_fence_after();
-      }
-      tmem_st32(trow + TM_P + b * 64 + 0, pk0);
-      tmem_st32(trow + TM_P + b * 64 + 32, pk1);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_P_FULL + b));
-    }
-    // PV products complete in issue order: the last one completing means O is final.
-    if (ok) ok = warp_wait(bar(B_P_EMPTY + ((n_kv - 1) & 1)), ((n_kv - 1) >> 1) & 1, w);
-    if (ok) {
+      if (!ok) break;
+      // All S of this tile are done: the next tile's Q goes over this one's, so
+      // that its first S is formed under this tile's last PV and epilogue.
+      if (tile_of(n + 1) < n_tiles && !(ok = take_q(n + 1))) break;
+      // PV products complete in issue order: the last one completing means O is final.
+      if (!(ok = warp_wait(bar(B_P_EMPTY + ((it - 1) & 1)), ((it - 1) >> 1) & 1, w))) break;
       tc_fence_after();
       const float inv = 1.f / l;
       const bool valid = qpos < p.L;
@@ -472,11 +526,10 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
 
 
 // dS row slice of the dq kernel: 32 keys of one query row, paired fp32
-// math.  kMask applies the causal mask (only the diagonal tile needs it).
+// math.  kMask: bit c of `seen` tells whether the query sees key c.
 template <bool kMask>
 __device__ __forceinline__ void ds_slice(const uint32_t (&sv)[32], const uint32_t (&dv)[32], float sl2, float nlse2,
-                                         float dlt, int k0, int qpos, const WinParams& p,
-                                         uint32_t (&pk)[16]) {
+                                         float dlt, uint32_t seen, uint32_t (&pk)[16]) {
   const uint64_t sl2x2 = f2_pack(sl2, sl2);
   const uint64_t nlx2 = f2_pack(nlse2, nlse2);
   const uint64_t dlx2 = f2_pack(dlt, dlt);
@@ -486,8 +539,8 @@ __device__ __forceinline__ void ds_slice(const uint32_t (&sv)[32], const uint32_
     f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl2x2, nlx2), t0, t1);
     float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
     if (kMask) {
-      if (!sees(qpos, k0 + c, p)) p0 = 0.f;
-      if (!sees(qpos, k0 + c + 1, p)) p1 = 0.f;
+      if (!(seen >> c & 1u)) p0 = 0.f;
+      if (!(seen >> (c + 1) & 1u)) p1 = 0.f;
     }
     const uint64_t d = f2_sub(f2_pack(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])), dlx2);
     float d0, d1;
@@ -498,11 +551,11 @@ __device__ __forceinline__ void ds_slice(const uint32_t (&sv)[32], const uint32_
 
 // P^T row slice of the dkdv kernel: 16 queries (columns c0 .. c0 + 15 of
 // this warp's 32) of one key row, kept in fp32 for the dS^T phase.  Lane c of
-// the warp holds -LSE * log2(e) of the warp's query c in `nl`; kMask zeroes
-// queries before the key (the diagonal tile only).
+// the warp holds -LSE * log2(e) of the warp's query c in `nl`; kMask: bit c
+// of `seen` tells whether query c sees the key.
 template <bool kMask>
-__device__ __forceinline__ void p_slice(const uint32_t (&sv)[16], float nl, int c0, float sl2, int q0, int kpos,
-                                        int last_q, float* pf) {
+__device__ __forceinline__ void p_slice(const uint32_t (&sv)[16], float nl, int c0, float sl2, uint32_t seen,
+                                        float* pf) {
   const uint64_t sl2x2 = f2_pack(sl2, sl2);
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
@@ -512,9 +565,8 @@ __device__ __forceinline__ void p_slice(const uint32_t (&sv)[16], float nl, int 
     f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl2x2, f2_pack(l0, l1)), t0, t1);
     float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
     if (kMask) {
-      const int q = q0 + c0 + c;
-      if (q < kpos || q > last_q) p0 = 0.f;
-      if (q + 1 < kpos || q + 1 > last_q) p1 = 0.f;
+      if (!(seen >> (c0 + c) & 1u)) p0 = 0.f;
+      if (!(seen >> (c0 + c + 1) & 1u)) p1 = 0.f;
     }
     pf[c] = p0;
     pf[c + 1] = p1;
@@ -797,11 +849,11 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
       const int k0 = kb * 128 + half * 64;  // key of this warp's first column
       uint32_t pk0[16], pk1[16];
       if (sp.masked(kb, p)) {  // warp-uniform
-        ds_slice<true>(s0, d0, sl2, nlse2, dlt, k0, qpos, p, pk0);
-        ds_slice<true>(s1, d1, sl2, nlse2, dlt, k0 + 32, qpos, p, pk1);
+        ds_slice<true>(s0, d0, sl2, nlse2, dlt, seen_keys(qpos, k0, p), pk0);
+        ds_slice<true>(s1, d1, sl2, nlse2, dlt, seen_keys(qpos, k0 + 32, p), pk1);
       } else {
-        ds_slice<false>(s0, d0, sl2, nlse2, dlt, k0, qpos, p, pk0);
-        ds_slice<false>(s1, d1, sl2, nlse2, dlt, k0 + 32, qpos, p, pk1);
+        ds_slice<false>(s0, d0, sl2, nlse2, dlt, 0u, pk0);
+        ds_slice<false>(s1, d1, sl2, nlse2, dlt, 0u, pk1);
       }
       // dS over the first 32 of the 64 S columns this warp just read.
       tmem_st16(ts, pk0);
@@ -1070,6 +1122,8 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
       const int q0 = qt * 128 + grp * 32;  // query of this warp's first column
       // Without its record (all 64 queries past L) the slice is all zero.
       const bool masked = hides(qt, kb, p);  // warp-uniform
+      // queries from the key's own to the last one whose window reaches it
+      const uint32_t seen = masked ? bits_below(last_q - q0 + 1) & ~bits_below(kpos - q0) : ~0u;
       const bool live = 2 * qt + (grp >> 1) < n_q64;
       // This warp's 32 queries in their record: -LSE*log2(e) at +0, Delta at
       // +64.  Lane c loads query c's pair now, ahead of the waits, and the
@@ -1092,9 +1146,9 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
 #pragma unroll
           for (int c = 0; c < 16; ++c) pf[16 * h + c] = 0.f;
         } else if (masked) {
-          p_slice<true>(sv, nl, 16 * h, sl2, q0, kpos, last_q, pf + 16 * h);
+          p_slice<true>(sv, nl, 16 * h, sl2, seen, pf + 16 * h);
         } else {
-          p_slice<false>(sv, nl, 16 * h, sl2, q0, kpos, last_q, pf + 16 * h);
+          p_slice<false>(sv, nl, 16 * h, sl2, 0u, pf + 16 * h);
         }
         uint32_t pk[8];
 #pragma unroll
@@ -1190,6 +1244,8 @@ __global__ void __launch_bounds__(256) window_sink_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------- host
 
+constexpr int kSms = 152;  // persistent kernels: one CTA per SM
+
 struct WinShape {
   int64_t L;
   int H, Hkv, m_tiles;
@@ -1265,7 +1321,8 @@ cudaError_t launch_window_fwd(const CUtensorMap& q, const CUtensorMap& k, const 
   cudaError_t e =
       cudaFuncSetAttribute(window_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wf::kSmemBytes);
   if (e != cudaSuccess) return e;
-  window_fwd_kernel<<<m_tiles * p.H, wf::kThreads, wf::kSmemBytes, st>>>(q, k, v, p);
+  const int grid = m_tiles * p.H < kSms ? m_tiles * p.H : kSms;
+  window_fwd_kernel<<<grid, wf::kThreads, wf::kSmemBytes, st>>>(q, k, v, p);
   return cudaGetLastError();
 }
 
