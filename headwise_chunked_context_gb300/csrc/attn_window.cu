@@ -43,6 +43,7 @@ struct WinParams {
   // Sink key tiles and the query tiles past their windows (see SinkPlan).
   int sink_tiles, near_tiles, far_chunk, far_slots, sink_rows, shared_keys;
   float* sink_part;
+  int* next_tile;    // dQ: tiles given out beyond each CTA's first
   float scale;       // 1/sqrt(d)
   float scale_log2;  // log2(e)/sqrt(d)
   int* status;
@@ -603,14 +604,19 @@ constexpr int kTile = 128 * 128 * 2;   // [128][128] bf16 as two 64-column halve
 constexpr int kHalf = kTile / 2;
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
+constexpr int kTileSlots = 8;
 constexpr int OFF_Q = 0;
 constexpr int OFF_DO = OFF_Q + kTile;
 constexpr int OFF_K = OFF_DO + kTile;              // kKStages
 constexpr int OFF_V = OFF_K + kKStages * kTile;    // kVStages
 constexpr int OFF_BAR = OFF_V + kVStages * kTile;
 enum {
-  B_QDO_FULL,
-  B_K_FULL,
+  B_Q_FULL,
+  B_Q_EMPTY,   // the tile's last S done
+  B_DO_FULL,
+  B_DO_EMPTY,  // the tile's last dP done
+  B_TILE,      // a tile's number published, per slot
+  B_K_FULL = B_TILE + kTileSlots,
   B_K_EMPTY = B_K_FULL + kKStages,
   B_V_FULL = B_K_EMPTY + kKStages,
   B_V_EMPTY = B_V_FULL + kVStages,
@@ -627,7 +633,8 @@ enum {
 };
 constexpr int OFF_TMEM_SLOT = OFF_BAR + B_COUNT * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
-constexpr int kSmemBytes = OFF_ABORT + 8 + 1024;
+constexpr int OFF_TILE = OFF_ABORT + 8;
+constexpr int kSmemBytes = OFF_TILE + kTileSlots * 4 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "dq kernel shared memory");
 constexpr int TM_S = 0, TM_DP = 256, TM_DQ = 384;  // S: two 128-column buffers
 // Warps 0-7 compute, 8 producer, 9 issues S, 10 issues dQ, 11 issues dP.
@@ -645,19 +652,20 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // Heads vary fastest (GQA siblings share K/V blocks in L2); the query
-  // blocks with the most KV blocks launch first.
-  const int h = static_cast<int>(blockIdx.x) % p.H;
-  const int qb = static_cast<int>(gridDim.x) / p.H - 1 - static_cast<int>(blockIdx.x) / p.H;
-  const int kz = h / p.g;
-  const QuerySpan sp(qb, p);
-  const int n_kv = sp.count();
+  // Tile t: heads vary fastest (GQA siblings share K/V blocks in L2), the query
+  // blocks with the most KV blocks come first.
+  const int m_tiles = ((p.L - 1) >> 7) + 1;
+  const int n_tiles = m_tiles * p.H;
+  auto head_of = [&](int t) { return t % p.H; };
+  auto block_of = [&](int t) { return m_tiles - 1 - t / p.H; };
+  volatile int* tiles = reinterpret_cast<volatile int*>(smem + OFF_TILE);
   auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
   const WaitCtl w{abort_flag, p.status, p.limit_ns};
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(B_QDO_FULL), 1);
+    for (int i : {B_Q_FULL, B_Q_EMPTY, B_DO_FULL, B_DO_EMPTY}) mbar_init(bar(i), 1);
+    for (int i = 0; i < kTileSlots; ++i) mbar_init(bar(B_TILE + i), 1);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(bar(B_K_FULL + s), 1);
       mbar_init(bar(B_K_EMPTY + s), 1);
@@ -695,120 +703,196 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
       tma_prefetch_map(&mk);
       tma_prefetch_map(&mv);
       tma_prefetch_map(&mdo);
-      mbar_expect_tx(bar(B_QDO_FULL), 2 * kTile);
-      tma_load_3d(sb + OFF_Q, &mq, bar(B_QDO_FULL), 0, qb * 128, h);
-      tma_load_3d(sb + OFF_Q + kHalf, &mq, bar(B_QDO_FULL), 64, qb * 128, h);
-      tma_load_3d(sb + OFF_DO, &mdo, bar(B_QDO_FULL), 0, qb * 128, h);
-      tma_load_3d(sb + OFF_DO + kHalf, &mdo, bar(B_QDO_FULL), 64, qb * 128, h);
-      int last_k[kKStages], last_v[kVStages];
-#pragma unroll
-      for (int s = 0; s < kKStages; ++s) last_k[s] = -1;
-#pragma unroll
-      for (int s = 0; s < kVStages; ++s) last_v[s] = -1;
-      // Whichever ring has a free stage gets its next block, K first (S(j)
-      // needs K(j) before dP(j) needs V(j)).
-      int nk = 0, nv = 0;
+      // Four streams, each of which moves on as soon as it can: the tiles' Q
+      // and dO, and the K and V blocks of all tiles behind one another.
+      struct Walk {  // a stream's place among the blocks of all tiles
+        int n, j, count, kz;
+      };
+      int published = 0;  // tiles given out so far
+      int coming = 0;     // the next one's number, asked for a tile ahead
+      auto publish = [&](int t) {
+        tiles[published % kTileSlots] = t;
+        mbar_arrive(bar(B_TILE + published % kTileSlots));
+        ++published;
+        if (t < n_tiles) coming = static_cast<int>(gridDim.x) + atomicAdd(p.next_tile, 1);
+      };
+      auto enter = [&](Walk& x) {  // the stream's next tile; false: no more
+        const int t = tiles[x.n % kTileSlots];
+        if (t >= n_tiles) return false;
+        x.j = 0;
+        x.count = QuerySpan(block_of(t), p).count();
+        x.kz = head_of(t) / p.g;
+        return true;
+      };
+      auto row_of = [&](const Walk& x) { return QuerySpan(block_of(tiles[x.n % kTileSlots]), p).block(x.j) * 128; };
+      publish(static_cast<int>(blockIdx.x));
+      Walk k{0, 0, 0, 0}, v{0, 0, 0, 0};
+      enter(k);
+      enter(v);
+      int nq = 0, ndo = 0, nk = 0, nv = 0;  // loads issued
+      bool k_on = true, v_on = true, q_on = true, do_on = true;
       Watchdog wd;
       wd.reset();
       bool ok = true;
-      while (ok && (nk < n_kv || nv < n_kv)) {
+      while (ok && (q_on || do_on || k_on || v_on)) {
         bool did = false;
-        if (nk < n_kv && mbar_test(bar(B_K_EMPTY + nk % kKStages), ((nk / kKStages) & 1) ^ 1)) {
-          const int s = nk % kKStages;
-          mbar_expect_tx(bar(B_K_FULL + s), kTile);
-          tma_load_3d(sb + OFF_K + s * kTile, &mk, bar(B_K_FULL + s), 0, sp.block(nk) * 128, kz);
-          tma_load_3d(sb + OFF_K + s * kTile + kHalf, &mk, bar(B_K_FULL + s), 64, sp.block(nk) * 128, kz);
-          last_k[s] = nk++;
+        if (q_on && nq < published && mbar_test(bar(B_Q_EMPTY), (nq & 1) ^ 1)) {
+          const int t = tiles[nq % kTileSlots];
+          if ((q_on = t < n_tiles)) {
+            mbar_expect_tx(bar(B_Q_FULL), kTile);
+            tma_load_3d(sb + OFF_Q, &mq, bar(B_Q_FULL), 0, block_of(t) * 128, head_of(t));
+            tma_load_3d(sb + OFF_Q + kHalf, &mq, bar(B_Q_FULL), 64, block_of(t) * 128, head_of(t));
+            ++nq;
+          }
           did = true;
         }
-        if (nv < n_kv && mbar_test(bar(B_V_EMPTY + nv % kVStages), ((nv / kVStages) & 1) ^ 1)) {
+        if (k_on && mbar_test(bar(B_K_EMPTY + nk % kKStages), ((nk / kKStages) & 1) ^ 1)) {
+          const int s = nk % kKStages;
+          const int row = row_of(k);
+          mbar_expect_tx(bar(B_K_FULL + s), kTile);
+          tma_load_3d(sb + OFF_K + s * kTile, &mk, bar(B_K_FULL + s), 0, row, k.kz);
+          tma_load_3d(sb + OFF_K + s * kTile + kHalf, &mk, bar(B_K_FULL + s), 64, row, k.kz);
+          ++nk;
+          if (++k.j == k.count) {  // the K stream is the one that asks for tiles
+            publish(coming);
+            ++k.n;
+            k_on = enter(k);
+          }
+          did = true;
+        }
+        if (do_on && ndo < published && mbar_test(bar(B_DO_EMPTY), (ndo & 1) ^ 1)) {
+          const int t = tiles[ndo % kTileSlots];
+          if ((do_on = t < n_tiles)) {
+            mbar_expect_tx(bar(B_DO_FULL), kTile);
+            tma_load_3d(sb + OFF_DO, &mdo, bar(B_DO_FULL), 0, block_of(t) * 128, head_of(t));
+            tma_load_3d(sb + OFF_DO + kHalf, &mdo, bar(B_DO_FULL), 64, block_of(t) * 128, head_of(t));
+            ++ndo;
+          }
+          did = true;
+        }
+        if (v_on && v.j == v.count && v.n + 1 < published) {
+          ++v.n;
+          v_on = enter(v);
+          did = true;
+        }
+        if (v_on && v.j < v.count && mbar_test(bar(B_V_EMPTY + nv % kVStages), ((nv / kVStages) & 1) ^ 1)) {
           const int s = nv % kVStages;
+          const int row = row_of(v);
           mbar_expect_tx(bar(B_V_FULL + s), kTile);
-          tma_load_3d(sb + OFF_V + s * kTile, &mv, bar(B_V_FULL + s), 0, sp.block(nv) * 128, kz);
-          tma_load_3d(sb + OFF_V + s * kTile + kHalf, &mv, bar(B_V_FULL + s), 64, sp.block(nv) * 128, kz);
-          last_v[s] = nv++;
+          tma_load_3d(sb + OFF_V + s * kTile, &mv, bar(B_V_FULL + s), 0, row, v.kz);
+          tma_load_3d(sb + OFF_V + s * kTile + kHalf, &mv, bar(B_V_FULL + s), 64, row, v.kz);
+          ++nv;
+          ++v.j;
           did = true;
         }
         if (did) wd.reset();
         else ok = wd.alive(w);
       }
-      if (*abort_flag) {
-        mbar_wait_drain(bar(B_QDO_FULL), 0, p.status);
-        for (int s = 0; s < kKStages; ++s)
-          if (last_k[s] >= 0) mbar_wait_drain(bar(B_K_FULL + s), (last_k[s] / kKStages) & 1, p.status);
-        for (int s = 0; s < kVStages; ++s)
-          if (last_v[s] >= 0) mbar_wait_drain(bar(B_V_FULL + s), (last_v[s] / kVStages) & 1, p.status);
+      if (*abort_flag) {  // let every issued copy land before the CTA exits
+        if (nq) mbar_wait_drain(bar(B_Q_FULL), (nq - 1) & 1, p.status);
+        if (ndo) mbar_wait_drain(bar(B_DO_FULL), (ndo - 1) & 1, p.status);
+        for (int i = nk > kKStages ? nk - kKStages : 0; i < nk; ++i)
+          mbar_wait_drain(bar(B_K_FULL + i % kKStages), (i / kKStages) & 1, p.status);
+        for (int i = nv > kVStages ? nv - kVStages : 0; i < nv; ++i)
+          mbar_wait_drain(bar(B_V_FULL + i % kVStages), (i / kVStages) & 1, p.status);
       }
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
-      // S(j) = Q K(j)^T into buffer j & 1 once K(j) has landed and dQ(j - 2)
-      // has released the buffer.
+      // S = Q K^T into buffer it & 1 once K has landed and the dQ product
+      // two blocks ago has released the buffer.
       constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
-      bool ok = mbar_spin(bar(B_QDO_FULL), 0, w);
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int s = j % kKStages;
-        if (!(ok = mbar_spin(bar(B_K_FULL + s), (j / kKStages) & 1, w))) break;
-        if (!(ok = mbar_spin(bar(B_S_FREE + (j & 1)), ((j >> 1) & 1) ^ 1, w))) break;
-        tc_fence_after();
-        const uint32_t ka = sb + OFF_K + s * kTile;
+      bool ok = true;
+      int it = 0;
+      for (int n = 0; ok; ++n) {
+        if (!(ok = mbar_wait(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
+        const int t = tiles[n % kTileSlots];
+        if (t >= n_tiles) break;
+        const int n_kv = QuerySpan(block_of(t), p).count();
+        if (!(ok = mbar_spin(bar(B_Q_FULL), n & 1, w))) break;
+        for (int j = 0; j < n_kv; ++j, ++it) {
+          const int s = it % kKStages;
+          if (!(ok = mbar_spin(bar(B_K_FULL + s), (it / kKStages) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_S_FREE + (it & 1)), ((it >> 1) & 1) ^ 1, w))) break;
+          tc_fence_after();
+          const uint32_t ka = sb + OFF_K + s * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_bf16(tmem + TM_S + (j & 1) * 128, sdesc_sw128(sb + OFF_Q + off, 16, 1024),
-                    sdesc_sw128(ka + off, 16, 1024), id_kk, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            umma_bf16(tmem + TM_S + (it & 1) * 128, sdesc_sw128(sb + OFF_Q + off, 16, 1024),
+                      sdesc_sw128(ka + off, 16, 1024), id_kk, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar(B_S_FULL + (it & 1)));
         }
-        umma_commit(bar(B_S_FULL + (j & 1)));
+        if (ok) umma_commit(bar(B_Q_EMPTY));
       }
       umma_commit(bar(B_DRAIN));
       mbar_wait_drain(bar(B_DRAIN), 0, p.status);
     }
   } else if (warp == kDpWarp) {
     if (lane == 0) {
-      // dP(j) = dO V(j)^T once V(j) has landed and dP(j - 1) has been read.
+      // dP = dO V^T once V has landed and the last block's dP has been read.
       constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
-      bool ok = mbar_spin(bar(B_QDO_FULL), 0, w);
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int s = j % kVStages;
-        if (!(ok = mbar_spin(bar(B_V_FULL + s), (j / kVStages) & 1, w))) break;
-        if (!(ok = mbar_spin(bar(B_DP_EMPTY), (j & 1) ^ 1, w))) break;
-        tc_fence_after();
-        const uint32_t va = sb + OFF_V + s * kTile;
+      bool ok = true;
+      int it = 0;
+      for (int n = 0; ok; ++n) {
+        if (!(ok = mbar_wait(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
+        const int t = tiles[n % kTileSlots];
+        if (t >= n_tiles) break;
+        const int n_kv = QuerySpan(block_of(t), p).count();
+        if (!(ok = mbar_spin(bar(B_DO_FULL), n & 1, w))) break;
+        for (int j = 0; j < n_kv; ++j, ++it) {
+          const int s = it % kVStages;
+          if (!(ok = mbar_spin(bar(B_V_FULL + s), (it / kVStages) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_DP_EMPTY), (it & 1) ^ 1, w))) break;
+          tc_fence_after();
+          const uint32_t va = sb + OFF_V + s * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_bf16(tmem + TM_DP, sdesc_sw128(sb + OFF_DO + off, 16, 1024), sdesc_sw128(va + off, 16, 1024), id_kk,
-                    kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            umma_bf16(tmem + TM_DP, sdesc_sw128(sb + OFF_DO + off, 16, 1024), sdesc_sw128(va + off, 16, 1024), id_kk,
+                      kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar(B_DP_FULL));
+          umma_commit(bar(B_V_EMPTY + s));
         }
-        umma_commit(bar(B_DP_FULL));
-        umma_commit(bar(B_V_EMPTY + s));
+        if (ok) umma_commit(bar(B_DO_EMPTY));
       }
       umma_commit(bar(B_DRAIN_P));
       mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
     }
   } else if (warp == kGradWarp) {
     if (lane == 0) {
-      // dQ(j) += dS(j) K(j) once dS(j) is written; then S buffer j & 1 and
-      // K stage j % kKStages are free (S(j) had completed before dS(j) existed).
+      // dQ += dS K once dS is written; then its S buffer and K stage are free
+      // (S had completed before dS existed).  A tile's first dS is written
+      // after the compute warps have read the last tile's dQ.
       constexpr uint32_t id_q = idesc_bf16(128, 128, 0, 1);  // dS from TMEM, K MN-major
       bool ok = true;
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int b = j & 1;
-        const int s = j % kKStages;
-        if (!(ok = mbar_spin(bar(B_DS_FULL + b), (j >> 1) & 1, w))) break;
-        tc_fence_after();
-        const uint32_t ka = sb + OFF_K + s * kTile;
+      int it = 0;
+      for (int n = 0; ok; ++n) {
+        if (!(ok = mbar_wait(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
+        const int t = tiles[n % kTileSlots];
+        if (t >= n_tiles) break;
+        const int n_kv = QuerySpan(block_of(t), p).count();
+        for (int j = 0; j < n_kv; ++j, ++it) {
+          const int b = it & 1;
+          const int s = it % kKStages;
+          if (!(ok = mbar_spin(bar(B_DS_FULL + b), (it >> 1) & 1, w))) break;
+          tc_fence_after();
+          const uint32_t ka = sb + OFF_K + s * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          // keys 16 kk .. 16 kk + 15: compute half kk / 4 wrote them at its own
-          // 64-column slice of the S buffer
-          const uint32_t a = tmem + TM_S + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8;
-          umma_bf16_ts(tmem + TM_DQ, a, sdesc_sw128(ka + kk * 2048, kHalf, 1024), id_q, (j > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            // keys 16 kk .. 16 kk + 15: compute half kk / 4 wrote them at its own
+            // 64-column slice of the S buffer
+            const uint32_t a = tmem + TM_S + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8;
+            umma_bf16_ts(tmem + TM_DQ, a, sdesc_sw128(ka + kk * 2048, kHalf, 1024), id_q,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(bar(B_S_FREE + b));
+          umma_commit(bar(B_K_EMPTY + s));
         }
-        umma_commit(bar(B_S_FREE + b));
-        umma_commit(bar(B_K_EMPTY + s));
+        if (ok) umma_commit(bar(B_DQ_DONE));
       }
-      if (ok) umma_commit(bar(B_DQ_DONE));
       umma_commit(bar(B_DRAIN_G));
       mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
     }
@@ -818,53 +902,69 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
     const int quad = warp & 3;
     const int half = warp >> 2;
     const int r = quad * 32 + lane;
-    const int qpos = qb * 128 + r;
-    const bool valid = qpos < p.L;
     const uint32_t trow = tmem_lane_addr(tmem, quad, 0);
     const float sl2 = p.scale_log2;
     const int n_q64 = (p.L + 63) / 64;
-    const float* rec = p.ld + (static_cast<int64_t>(h) * n_q64 + (qpos >> 6)) * 128;
-    const float nlse2 = valid ? rec[qpos & 63] : 0.f;  // -LSE * log2(e)
-    const float dlt = valid ? rec[64 + (qpos & 63)] : 0.f;
-    bool ok = true;
-    for (int j = 0; j < n_kv; ++j) {
-      const int b = j & 1;
-      if (!(ok = warp_wait<false, true>(bar(B_S_FULL + b), (j >> 1) & 1, w))) break;
-      if (!(ok = warp_wait<false, true>(bar(B_DP_FULL), j & 1, w))) break;
-      tc_fence_after();
-      const uint32_t ts = trow + TM_S + b * 128 + half * 64;
-      uint32_t s0[32], s1[32], d0[32], d1[32];
-      tmem_ld32(ts, s0);
-      tmem_ld32(ts + 32, s1);
-      tmem_ld32(trow + TM_DP + half * 64, d0);
-      tmem_ld32(trow + TM_DP + half * 64 + 32, d1);
-      tmem_ld_wait(s0);
-      tmem_ld_wait(s1);
-      tmem_ld_wait(d0);
-      tmem_ld_wait(d1);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_DP_EMPTY));
-      const int kb = sp.block(j);
-      const int k0 = kb * 128 + half * 64;  // key of this warp's first column
-      uint32_t pk0[16], pk1[16];
-      if (sp.masked(kb, p)) {  // warp-uniform
-        ds_slice<true>(s0, d0, sl2, nlse2, dlt, seen_keys(qpos, k0, p), pk0);
-        ds_slice<true>(s1, d1, sl2, nlse2, dlt, seen_keys(qpos, k0 + 32, p), pk1);
-      } else {
-        ds_slice<false>(s0, d0, sl2, nlse2, dlt, 0u, pk0);
-        ds_slice<false>(s1, d1, sl2, nlse2, dlt, 0u, pk1);
+    // The n-th tile's number and this row's record of it.
+    float nlse2 = 0.f, dlt = 0.f;  // -LSE * log2(e), Delta
+    auto open = [&](int n, int& t) -> bool {
+      if (!warp_wait<false, true>(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w)) return false;
+      t = tiles[n % kTileSlots];
+      if (t < n_tiles) {
+        const int qpos = block_of(t) * 128 + r;
+        const float* rec = p.ld + (static_cast<int64_t>(head_of(t)) * n_q64 + (qpos >> 6)) * 128 + (qpos & 63);
+        nlse2 = qpos < p.L ? __ldg(rec) : 0.f;
+        dlt = qpos < p.L ? __ldg(rec + 64) : 0.f;
       }
-      // dS over the first 32 of the 64 S columns this warp just read.
-      tmem_st16(ts, pk0);
-      tmem_st16(ts + 16, pk1);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_DS_FULL + b));
-    }
-    if (ok) ok = warp_wait<false, true>(bar(B_DQ_DONE), 0, w);
-    if (ok) {
+      return true;
+    };
+    int t = 0, it = 0;
+    bool ok = open(0, t);
+    for (int n = 0; ok && t < n_tiles; ++n) {
+      const int h = head_of(t);
+      const QuerySpan sp(block_of(t), p);
+      const int n_kv = sp.count();
+      const int qpos = sp.qb * 128 + r;
+      for (int j = 0; j < n_kv; ++j, ++it) {
+        const int b = it & 1;
+        if (!(ok = warp_wait<false, true>(bar(B_S_FULL + b), (it >> 1) & 1, w))) break;
+        if (!(ok = warp_wait<false, true>(bar(B_DP_FULL), it & 1, w))) break;
+        tc_fence_after();
+        const uint32_t ts = trow + TM_S + b * 128 + half * 64;
+        uint32_t s0[32], s1[32], d0[32], d1[32];
+        tmem_ld32(ts, s0);
+        tmem_ld32(ts + 32, s1);
+        tmem_ld32(trow + TM_DP + half * 64, d0);
+        tmem_ld32(trow + TM_DP + half * 64 + 32, d1);
+        tmem_ld_wait(s0);
+        tmem_ld_wait(s1);
+        tmem_ld_wait(d0);
+        tmem_ld_wait(d1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_DP_EMPTY));
+        const int kb = sp.block(j);
+        const int k0 = kb * 128 + half * 64;  // key of this warp's first column
+        uint32_t pk0[16], pk1[16];
+        if (sp.masked(kb, p)) {  // warp-uniform
+          ds_slice<true>(s0, d0, sl2, nlse2, dlt, seen_keys(qpos, k0, p), pk0);
+          ds_slice<true>(s1, d1, sl2, nlse2, dlt, seen_keys(qpos, k0 + 32, p), pk1);
+        } else {
+          ds_slice<false>(s0, d0, sl2, nlse2, dlt, 0u, pk0);
+          ds_slice<false>(s1, d1, sl2, nlse2, dlt, 0u, pk1);
+        }
+        // dS over the first 32 of the 64 S columns this warp just read.
+        tmem_st16(ts, pk0);
+        tmem_st16(ts + 16, pk1);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_DS_FULL + b));
+      }
+      if (!ok) break;
+      // The next tile's record is on its way under the last dQ product.
+      if (!(ok = open(n + 1, t))) break;
+      if (!(ok = warp_wait<false, true>(bar(B_DQ_DONE), n & 1, w))) break;
       // Epilogue: this warp writes 64 columns of its rows.
       tc_fence_after();
       __nv_bfloat16* out = p.dq + (static_cast<int64_t>(qpos) * p.H + h) * kHeadDim + half * 64;
@@ -873,7 +973,7 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
         uint32_t a[32];
         tmem_ld32(trow + TM_DQ + half * 64 + c * 32, a);
         tmem_ld_wait(a);
-        if (valid) store32_bf16(out + c * 32, a, p.scale);
+        if (qpos < p.L) store32_bf16(out + c * 32, a, p.scale);
       }
     }
     tc_fence_before();
@@ -1296,9 +1396,14 @@ SinkPlan sink_plan(const WinShape& s) {
   return f;
 }
 
+// Workspace: counters, the records of LSE and Delta, the shares of the sinks.
+constexpr size_t kCounterBytes = 128;
+
 size_t records_bytes(const WinShape& s) {
   return static_cast<size_t>(s.H) * static_cast<size_t>((s.L + 63) / 64) * 128 * sizeof(float);
 }
+
+size_t workspace_bytes(const WinShape& s) { return kCounterBytes + records_bytes(s) + sink_plan(s).bytes; }
 
 WinParams base_params(const WinShape& s, int* status) {
   WinParams p;
@@ -1330,7 +1435,8 @@ cudaError_t launch_window_dq(const CUtensorMap& q, const CUtensorMap& k, const C
                              const WinParams& p, int m_tiles, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wq::kSmemBytes);
   if (e != cudaSuccess) return e;
-  window_dq_kernel<<<m_tiles * p.H, wq::kThreadsDq, wq::kSmemBytes, st>>>(q, k, v, dO, p);
+  const int grid = m_tiles * p.H < kSms ? m_tiles * p.H : kSms;
+  window_dq_kernel<<<grid, wq::kThreadsDq, wq::kSmemBytes, st>>>(q, k, v, dO, p);
   return cudaGetLastError();
 }
 
@@ -1358,7 +1464,7 @@ extern "C" {
 
 size_t upipe_window_workspace_bytes(const upipe_window_cfg* cfg) {
   WinShape s;
-  return check_window(cfg, &s) ? records_bytes(s) + sink_plan(s).bytes : 0;
+  return check_window(cfg, &s) ? workspace_bytes(s) : 0;
 }
 
 int upipe_window_fwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v, uint16_t* o,
@@ -1392,7 +1498,7 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(ws))
     return UPIPE_ERR_INVALID_ARG;
   const SinkPlan f = sink_plan(s);
-  if (ws_bytes < records_bytes(s) + f.bytes) return UPIPE_ERR_WS_TOO_SMALL;
+  if (ws_bytes < workspace_bytes(s)) return UPIPE_ERR_WS_TOO_SMALL;
   int* status = nullptr;
   if (int e = device_ready(&status)) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1402,7 +1508,8 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   UPIPE_MAP(map3d(&mv, v, s.L, s.Hkv, s.Hkv * 128, 128, 128));
   UPIPE_MAP(map3d(&mdo, dout_o, s.L, s.H, s.H * 128, 128, 128));
   WinParams p = base_params(s, status);
-  float* ld = static_cast<float*>(ws);
+  uint8_t* const at = static_cast<uint8_t*>(ws);
+  float* ld = reinterpret_cast<float*>(at + kCounterBytes);
   p.ld = ld;
   p.sink_tiles = f.tiles;
   p.near_tiles = f.near;
@@ -1410,10 +1517,12 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   p.far_slots = f.slots;
   p.sink_rows = f.rows;
   p.shared_keys = s.sinks < f.tiles * 128 ? s.sinks : f.tiles * 128;
-  p.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + records_bytes(s));
+  p.sink_part = reinterpret_cast<float*>(at + kCounterBytes + records_bytes(s));
+  p.next_tile = reinterpret_cast<int*>(at);
   p.dq = reinterpret_cast<__nv_bfloat16*>(dq);
   p.dk = reinterpret_cast<__nv_bfloat16*>(dk);
   p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
+  UPIPE_CU(cudaMemsetAsync(at, 0, kCounterBytes, st));
   UPIPE_LAUNCH(UPIPE_KIND_DELTA,
                launch_delta(reinterpret_cast<const __nv_bfloat16*>(o), s.H * 128, 128,
                             reinterpret_cast<const __nv_bfloat16*>(dout_o), s.H * 128, 128, lse, ld, s.L, s.H, st));
