@@ -43,7 +43,10 @@ struct WinParams {
   // Sink key tiles and the query tiles past their windows (see SinkPlan).
   int sink_tiles, near_tiles, far_chunk, far_slots, sink_rows, shared_keys;
   float* sink_part;
-  int* next_tile;    // dQ: tiles given out beyond each CTA's first
+  // Tiles (dQ) and key items (dK/dV) handed out beyond each CTA's first.
+  int* next_tile;
+  int* next_item;
+  int key_items;
   float scale;       // 1/sqrt(d)
   float scale_log2;  // log2(e)/sqrt(d)
   int* status;
@@ -106,10 +109,25 @@ struct KeyItem {
     }
     q1 = q1 < tiles ? q1 : tiles;
   }
+  __device__ __forceinline__ int tiles() const { return q1 - q0; }
+  __device__ __forceinline__ bool empty() const { return q1 <= q0; }
   // fp32 share [2][sink_rows][128] of dK and dV
   __device__ __forceinline__ float* part(const WinParams& p) const {
     const int64_t at = (static_cast<int64_t>(kv) * p.sink_tiles + kb) * (p.far_slots + 1) + slot;
     return p.sink_part + at * 2 * p.sink_rows * kHeadDim;
+  }
+};
+
+// An item's (query head, query tile) pairs in the order of its sums: the heads
+// that read the KV head ascending, each one's tiles ascending.
+struct KeyWalk {
+  int h, qt, last_h, q0, q1;
+  __device__ __forceinline__ KeyWalk(const KeyItem& item, const WinParams& p)
+      : h(item.kv * p.g), qt(item.q0), last_h(h + p.g - 1), q0(item.q0), q1(item.q1) {}
+  __device__ __forceinline__ bool next() {
+    if (++qt < q1) return true;
+    qt = q0;
+    return ++h <= last_h;
   }
 };
 
@@ -996,9 +1014,14 @@ constexpr int OFF_V = OFF_K + kTile;
 constexpr int OFF_Q = OFF_V + kTile;             // kStages stages
 constexpr int OFF_DO = OFF_Q + kStages * kTile;
 constexpr int OFF_BAR = OFF_DO + kStages * kTile;
+constexpr int kItemSlots = 8;
 enum {
-  B_KV_FULL,
-  B_QDO_FULL,
+  B_K_FULL,
+  B_K_EMPTY,  // the item's last S^T done
+  B_V_FULL,
+  B_V_EMPTY,  // the item's last dP^T done
+  B_ITEM,     // an item's number published, per slot
+  B_QDO_FULL = B_ITEM + kItemSlots,
   B_QDO_EMPTY = B_QDO_FULL + kStages,
   B_S_FULL = B_QDO_EMPTY + kStages,  // per 64-query half of S^T
   B_P_FULL = B_S_FULL + 2,           // P^T of that half written (its 8 compute warps)
@@ -1014,7 +1037,8 @@ enum {
 };
 constexpr int OFF_TMEM_SLOT = OFF_BAR + B_COUNT * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
-constexpr int kSmemBytes = OFF_ABORT + 8 + 1024;
+constexpr int OFF_ITEM = OFF_ABORT + 8;
+constexpr int kSmemBytes = OFF_ITEM + kItemSlots * 4 + 1024;
 constexpr int TM_ST = 0, TM_DPT = 128, TM_DV = 256, TM_DK = 384;
 // 16 compute warps: four per TMEM lane quadrant, each owning 32 of the 128
 // query columns, so each SM sub-partition has four to hide TMEM and exp2
@@ -1038,18 +1062,16 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const KeyItem item(static_cast<int>(blockIdx.x), p);
-  const int kb = item.kb, kv = item.kv;
   const int n_q64 = (p.L + 63) / 64;
-  const int nqt = item.q1 - item.q0;
-  const int n_it = p.g * nqt;
-  if (n_it <= 0) return;  // a later sink tile's last share
+  const int n_items = p.key_items;
+  volatile int* items = reinterpret_cast<volatile int*>(smem + OFF_ITEM);
   auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
   const WaitCtl w{abort_flag, p.status, p.limit_ns};
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(B_KV_FULL), 1);
+    for (int i : {B_K_FULL, B_K_EMPTY, B_V_FULL, B_V_EMPTY}) mbar_init(bar(i), 1);
+    for (int i = 0; i < kItemSlots; ++i) mbar_init(bar(B_ITEM + i), 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(B_QDO_FULL + s), 1);
       mbar_init(bar(B_QDO_EMPTY + s), 1);
@@ -1079,37 +1101,80 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
   if (warp == kProducer) {
-    // Q and dO tiles (TMA), both on one barrier per stage.
+    // Three streams, each of which moves on as soon as it can: the items' K
+    // and V, and the Q and dO tiles of all items behind one another (both on
+    // one barrier per stage).
     if (lane == 0) {
-      int last[kStages];
-#pragma unroll
-      for (int s = 0; s < kStages; ++s) last[s] = -1;
       tma_prefetch_map(&mq);
       tma_prefetch_map(&mk);
       tma_prefetch_map(&mv);
       tma_prefetch_map(&mdo);
-      mbar_expect_tx(bar(B_KV_FULL), 2 * kTile);
-      tma_load_3d(sb + OFF_K, &mk, bar(B_KV_FULL), 0, kb * 128, kv);
-      tma_load_3d(sb + OFF_K + kHalf, &mk, bar(B_KV_FULL), 64, kb * 128, kv);
-      tma_load_3d(sb + OFF_V, &mv, bar(B_KV_FULL), 0, kb * 128, kv);
-      tma_load_3d(sb + OFF_V + kHalf, &mv, bar(B_KV_FULL), 64, kb * 128, kv);
-      for (int it = 0; it < n_it; ++it) {
-        const int s = it % kStages;
-        const uint32_t ph = (it / kStages) & 1;
-        const int hl = kv * p.g + it / nqt;
-        const int qt = item.q0 + it % nqt;
-        if (!mbar_wait(bar(B_QDO_EMPTY + s), ph ^ 1, w)) break;
-        mbar_expect_tx(bar(B_QDO_FULL + s), 2 * kTile);
-        tma_load_3d(sb + OFF_Q + s * kTile, &mq, bar(B_QDO_FULL + s), 0, qt * 128, hl);
-        tma_load_3d(sb + OFF_Q + s * kTile + kHalf, &mq, bar(B_QDO_FULL + s), 64, qt * 128, hl);
-        tma_load_3d(sb + OFF_DO + s * kTile, &mdo, bar(B_QDO_FULL + s), 0, qt * 128, hl);
-        tma_load_3d(sb + OFF_DO + s * kTile + kHalf, &mdo, bar(B_QDO_FULL + s), 64, qt * 128, hl);
-        last[s] = it;
+      int published = 0;  // items given out so far
+      int coming = 0;     // the next one's number, asked for an item ahead
+      auto ask = [&] { return static_cast<int>(gridDim.x) + atomicAdd(p.next_item, 1); };
+      auto publish = [&](int i) {
+        // a later sink tile's last shares hold nothing: no role sees them
+        while (i < n_items && KeyItem(i, p).empty()) i = ask();
+        items[published % kItemSlots] = i;
+        mbar_arrive(bar(B_ITEM + published % kItemSlots));
+        ++published;
+        if (i < n_items) coming = ask();
+      };
+      publish(static_cast<int>(blockIdx.x));
+      int nk = 0, nv = 0, nt = 0;  // loads issued
+      int n = 0;                   // the Q/dO stream's item
+      bool t_on = items[0] < n_items, k_on = true, v_on = true;
+      KeyWalk x(KeyItem(t_on ? items[0] : 0, p), p);
+      Watchdog wd;
+      wd.reset();
+      bool ok = true;
+      while (ok && (t_on || k_on || v_on)) {
+        bool did = false;
+        if (k_on && nk < published && mbar_test(bar(B_K_EMPTY), (nk & 1) ^ 1)) {
+          const int i = items[nk % kItemSlots];
+          if ((k_on = i < n_items)) {
+            const KeyItem item(i, p);
+            mbar_expect_tx(bar(B_K_FULL), kTile);
+            tma_load_3d(sb + OFF_K, &mk, bar(B_K_FULL), 0, item.kb * 128, item.kv);
+            tma_load_3d(sb + OFF_K + kHalf, &mk, bar(B_K_FULL), 64, item.kb * 128, item.kv);
+            ++nk;
+          }
+          did = true;
+        }
+        if (t_on && mbar_test(bar(B_QDO_EMPTY + nt % kStages), ((nt / kStages) & 1) ^ 1)) {
+          const int s = nt % kStages;
+          mbar_expect_tx(bar(B_QDO_FULL + s), 2 * kTile);
+          tma_load_3d(sb + OFF_Q + s * kTile, &mq, bar(B_QDO_FULL + s), 0, x.qt * 128, x.h);
+          tma_load_3d(sb + OFF_Q + s * kTile + kHalf, &mq, bar(B_QDO_FULL + s), 64, x.qt * 128, x.h);
+          tma_load_3d(sb + OFF_DO + s * kTile, &mdo, bar(B_QDO_FULL + s), 0, x.qt * 128, x.h);
+          tma_load_3d(sb + OFF_DO + s * kTile + kHalf, &mdo, bar(B_QDO_FULL + s), 64, x.qt * 128, x.h);
+          ++nt;
+          if (!x.next()) {  // this stream is the one that asks for items
+            publish(coming);
+            const int i = items[++n % kItemSlots];
+            if ((t_on = i < n_items)) x = KeyWalk(KeyItem(i, p), p);
+          }
+          did = true;
+        }
+        if (v_on && nv < published && mbar_test(bar(B_V_EMPTY), (nv & 1) ^ 1)) {
+          const int i = items[nv % kItemSlots];
+          if ((v_on = i < n_items)) {
+            const KeyItem item(i, p);
+            mbar_expect_tx(bar(B_V_FULL), kTile);
+            tma_load_3d(sb + OFF_V, &mv, bar(B_V_FULL), 0, item.kb * 128, item.kv);
+            tma_load_3d(sb + OFF_V + kHalf, &mv, bar(B_V_FULL), 64, item.kb * 128, item.kv);
+            ++nv;
+          }
+          did = true;
+        }
+        if (did) wd.reset();
+        else ok = wd.alive(w);
       }
-      if (*abort_flag) {
-        mbar_wait_drain(bar(B_KV_FULL), 0, p.status);
-        for (int s = 0; s < kStages; ++s)
-          if (last[s] >= 0) mbar_wait_drain(bar(B_QDO_FULL + s), (last[s] / kStages) & 1, p.status);
+      if (*abort_flag) {  // let every issued copy land before the CTA exits
+        if (nk) mbar_wait_drain(bar(B_K_FULL), (nk - 1) & 1, p.status);
+        if (nv) mbar_wait_drain(bar(B_V_FULL), (nv - 1) & 1, p.status);
+        for (int i = nt > kStages ? nt - kStages : 0; i < nt; ++i)
+          mbar_wait_drain(bar(B_QDO_FULL + i % kStages), (i / kStages) & 1, p.status);
       }
     }
   } else if (warp == kMma) {
@@ -1119,22 +1184,31 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
       // The halves pipeline independently, which shortens the chain
       // S^T -> P^T -> dV -> next S^T that a single buffer imposes.
       constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);
-      bool ok = mbar_spin(bar(B_KV_FULL), 0, w);
-      for (int it = 0; ok && it < n_it; ++it) {
-        const int qs = it % kStages;
-        if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
-        for (int hf = 0; hf < 2; ++hf) {
-          if (!(ok = mbar_spin(bar(B_S_FREE + hf), (it & 1) ^ 1, w))) break;
-          tc_fence_after();
-          const uint32_t bq = sb + OFF_Q + qs * kTile + hf * 64 * 128;  // query rows 64 hf ..
+      bool ok = true;
+      int it = 0;
+      for (int n = 0; ok; ++n) {
+        if (!(ok = mbar_wait(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
+        const int i = items[n % kItemSlots];
+        if (i >= n_items) break;
+        const int n_it = KeyItem(i, p).tiles() * p.g;
+        if (!(ok = mbar_spin(bar(B_K_FULL), n & 1, w))) break;
+        for (const int end = it + n_it; ok && it < end; ++it) {
+          const int qs = it % kStages;
+          if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!(ok = mbar_spin(bar(B_S_FREE + hf), (it & 1) ^ 1, w))) break;
+            tc_fence_after();
+            const uint32_t bq = sb + OFF_Q + qs * kTile + hf * 64 * 128;  // query rows 64 hf ..
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_bf16(tmem + TM_ST + hf * 64, sdesc_sw128(sb + OFF_K + off, 16, 1024), sdesc_sw128(bq + off, 16, 1024),
-                      id_s, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+              umma_bf16(tmem + TM_ST + hf * 64, sdesc_sw128(sb + OFF_K + off, 16, 1024),
+                        sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(bar(B_S_FULL + hf));
           }
-          umma_commit(bar(B_S_FULL + hf));
         }
+        if (ok) umma_commit(bar(B_K_EMPTY));
       }
       umma_commit(bar(B_DRAIN));
       mbar_wait_drain(bar(B_DRAIN), 0, p.status);
@@ -1143,20 +1217,29 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     if (lane == 0) {
       // dP^T(i) = V dO(i)^T once the stage has landed and dK(i - 1) is done.
       constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
-      bool ok = mbar_spin(bar(B_KV_FULL), 0, w);
-      for (int it = 0; ok && it < n_it; ++it) {
-        const int qs = it % kStages;
-        if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
-        if (!(ok = mbar_spin(bar(B_DP_FREE), (it & 1) ^ 1, w))) break;
-        tc_fence_after();
-        const uint32_t bq = sb + OFF_DO + qs * kTile;
+      bool ok = true;
+      int it = 0;
+      for (int n = 0; ok; ++n) {
+        if (!(ok = mbar_wait(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
+        const int i = items[n % kItemSlots];
+        if (i >= n_items) break;
+        const int n_it = KeyItem(i, p).tiles() * p.g;
+        if (!(ok = mbar_spin(bar(B_V_FULL), n & 1, w))) break;
+        for (const int end = it + n_it; it < end; ++it) {
+          const int qs = it % kStages;
+          if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_DP_FREE), (it & 1) ^ 1, w))) break;
+          tc_fence_after();
+          const uint32_t bq = sb + OFF_DO + qs * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_bf16(tmem + TM_DPT, sdesc_sw128(sb + OFF_V + off, 16, 1024), sdesc_sw128(bq + off, 16, 1024), id_s,
-                    kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            umma_bf16(tmem + TM_DPT, sdesc_sw128(sb + OFF_V + off, 16, 1024), sdesc_sw128(bq + off, 16, 1024), id_s,
+                      kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar(B_DP_FULL));
         }
-        umma_commit(bar(B_DP_FULL));
+        if (ok) umma_commit(bar(B_V_EMPTY));
       }
       umma_commit(bar(B_DRAIN_P));
       mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
@@ -1169,32 +1252,41 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
       // S^T(i) and dP^T(i) had completed before the compute warps could write
       // P^T and dS^T).
       constexpr uint32_t id_g = idesc_bf16(128, 128, 0, 1);  // A from TMEM, B MN-major
-      auto issue_grad = [&](int it, int tm_a, uint32_t b_base, int tm_d, int kk0, int kk1) {
+      auto issue_grad = [&](int it, bool more, int tm_a, uint32_t b_base, int tm_d, int kk0, int kk1) {
         const uint32_t bq = b_base + (it % kStages) * kTile;
         for (int kk = kk0; kk < kk1; ++kk) {
           // queries 16 kk .. 16 kk + 15: compute group kk / 2 wrote them at
           // its own 32-column slice
           const uint32_t a = tmem + tm_a + (kk >> 1) * 32 + (kk & 1) * 8;
-          umma_bf16_ts(tmem + tm_d, a, sdesc_sw128(bq + kk * 2048, kHalf, 1024), id_g,
-                       (it > 0 || kk > 0) ? 1u : 0u);
+          umma_bf16_ts(tmem + tm_d, a, sdesc_sw128(bq + kk * 2048, kHalf, 1024), id_g, (more || kk > 0) ? 1u : 0u);
         }
       };
+      // An item's first P^T is written after the last item's dK and dV have
+      // been read.
       bool ok = true;
-      for (int it = 0; ok && it < n_it; ++it) {
-        for (int hf = 0; hf < 2; ++hf) {
-          if (!(ok = mbar_spin(bar(B_P_FULL + hf), it & 1, w))) break;
+      int it = 0;
+      for (int n = 0; ok; ++n) {
+        if (!(ok = mbar_wait(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
+        const int i = items[n % kItemSlots];
+        if (i >= n_items) break;
+        const int n_it = KeyItem(i, p).tiles() * p.g;
+        const int begin = it;
+        for (const int end = it + n_it; ok && it < end; ++it) {
+          for (int hf = 0; hf < 2; ++hf) {
+            if (!(ok = mbar_spin(bar(B_P_FULL + hf), it & 1, w))) break;
+            tc_fence_after();
+            issue_grad(it, it > begin, TM_ST, sb + OFF_DO, TM_DV, 4 * hf, 4 * hf + 4);
+            umma_commit(bar(B_S_FREE + hf));
+          }
+          if (!ok) break;
+          if (!(ok = mbar_spin(bar(B_DS_FULL), it & 1, w))) break;
           tc_fence_after();
-          issue_grad(it, TM_ST, sb + OFF_DO, TM_DV, 4 * hf, 4 * hf + 4);
-          umma_commit(bar(B_S_FREE + hf));
+          issue_grad(it, it > begin, TM_DPT, sb + OFF_Q, TM_DK, 0, 8);
+          umma_commit(bar(B_DP_FREE));
+          umma_commit(bar(B_QDO_EMPTY + it % kStages));
         }
-        if (!ok) break;
-        if (!(ok = mbar_spin(bar(B_DS_FULL), it & 1, w))) break;
-        tc_fence_after();
-        issue_grad(it, TM_DPT, sb + OFF_Q, TM_DK, 0, 8);
-        umma_commit(bar(B_DP_FREE));
-        umma_commit(bar(B_QDO_EMPTY + it % kStages));
+        if (ok) umma_commit(bar(B_DKV_DONE));
       }
-      if (ok) umma_commit(bar(B_DKV_DONE));
       umma_commit(bar(B_DRAIN_G));
       mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
     }
@@ -1204,87 +1296,92 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     const int quad = warp & 3;
     const int grp = warp >> 2;
     const int r = quad * 32 + lane;  // key row = TMEM lane
-    const int kpos = kb * 128 + r;
-    const bool valid = kpos < p.L;
-    const int last_q = last_query(kpos, p);
     const uint32_t trow = tmem_lane_addr(tmem, quad, 0);
     const float sl2 = p.scale_log2;
     // Epilogue: groups 0-1 own dK, 2-3 own dV, 64 columns each.
     const int which = grp >> 1;
     const int col0 = (grp & 1) * 64;
     const uint32_t my_tm = trow + (which == 0 ? TM_DK : TM_DV) + col0;
-    bool ok = true;
     const uint32_t ts = trow + TM_ST + grp * 32;
     const uint32_t td = trow + TM_DPT + grp * 32;
-    for (int it = 0; it < n_it; ++it) {
-      const int hl = kv * p.g + it / nqt;
-      const int qt = item.q0 + it % nqt;
-      const int q0 = qt * 128 + grp * 32;  // query of this warp's first column
-      // Without its record (all 64 queries past L) the slice is all zero.
-      const bool masked = hides(qt, kb, p);  // warp-uniform
-      // queries from the key's own to the last one whose window reaches it
-      const uint32_t seen = masked ? bits_below(last_q - q0 + 1) & ~bits_below(kpos - q0) : ~0u;
-      const bool live = 2 * qt + (grp >> 1) < n_q64;
-      // This warp's 32 queries in their record: -LSE*log2(e) at +0, Delta at
-      // +64.  Lane c loads query c's pair now, ahead of the waits, and the
-      // values reach the other lanes by shuffle.
-      const float* rec = p.ld + (static_cast<int64_t>(hl) * n_q64 + 2 * qt + (grp >> 1)) * 128 + (grp & 1) * 32;
-      const float nl = live ? __ldg(rec + lane) : 0.f;
-      const float dl = live ? __ldg(rec + 64 + lane) : 0.f;
-      // ---- phase 1: P^T over the S^T columns, 16 at a time; the packed
-      // P^T of columns 16 h .. 16 h + 15 goes to columns 8 h .. 8 h + 7, which
-      // this warp has already read.
-      if (!(ok = warp_wait<false, true>(bar(B_S_FULL + (grp >> 1)), it & 1, w))) break;
-      tc_fence_after();
-      float pf[32];
+    bool ok = true;
+    int it = 0;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = warp_wait<false, true>(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
+      const int i = items[n % kItemSlots];
+      if (i >= n_items) break;
+      const KeyItem item(i, p);
+      const int kpos = item.kb * 128 + r;
+      const int last_q = last_query(kpos, p);
+      KeyWalk x(item, p);
+      do {
+        const int qt = x.qt;
+        const int q0 = qt * 128 + grp * 32;  // query of this warp's first column
+        const bool masked = hides(qt, item.kb, p);  // warp-uniform
+        // queries from the key's own to the last one whose window reaches it
+        const uint32_t seen = masked ? bits_below(last_q - q0 + 1) & ~bits_below(kpos - q0) : ~0u;
+        // Without its record (all 64 queries past L) the slice is all zero.
+        const bool live = 2 * qt + (grp >> 1) < n_q64;
+        // This warp's 32 queries in their record: -LSE*log2(e) at +0, Delta at
+        // +64.  Lane c loads query c's pair now, ahead of the waits, and the
+        // values reach the other lanes by shuffle.
+        const float* rec = p.ld + (static_cast<int64_t>(x.h) * n_q64 + 2 * qt + (grp >> 1)) * 128 + (grp & 1) * 32;
+        const float nl = live ? __ldg(rec + lane) : 0.f;
+        const float dl = live ? __ldg(rec + 64 + lane) : 0.f;
+        // ---- phase 1: P^T over the S^T columns, 16 at a time; the packed
+        // P^T of columns 16 h .. 16 h + 15 goes to columns 8 h .. 8 h + 7, which
+        // this warp has already read.
+        if (!(ok = warp_wait<false, true>(bar(B_S_FULL + (grp >> 1)), it & 1, w))) break;
+        tc_fence_after();
+        float pf[32];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t sv[16];
-        tmem_ld16(ts + 16 * h, sv);
-        tmem_ld_wait(sv);
-        if (!live) {
+        for (int h = 0; h < 2; ++h) {
+          uint32_t sv[16];
+          tmem_ld16(ts + 16 * h, sv);
+          tmem_ld_wait(sv);
+          if (!live) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) pf[16 * h + c] = 0.f;
-        } else if (masked) {
-          p_slice<true>(sv, nl, 16 * h, sl2, seen, pf + 16 * h);
-        } else {
-          p_slice<false>(sv, nl, 16 * h, sl2, 0u, pf + 16 * h);
+            for (int c = 0; c < 16; ++c) pf[16 * h + c] = 0.f;
+          } else if (masked) {
+            p_slice<true>(sv, nl, 16 * h, sl2, seen, pf + 16 * h);
+          } else {
+            p_slice<false>(sv, nl, 16 * h, sl2, 0u, pf + 16 * h);
+          }
+          uint32_t pk[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(pf[16 * h + 2 * c], pf[16 * h + 2 * c + 1]);
+          tmem_st8(ts + 8 * h, pk);
         }
-        uint32_t pk[8];
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P_FULL + (grp >> 1)));
+        // ---- phase 2: dS^T = P^T * (dP^T - Delta) over the dP^T columns
+        if (!(ok = warp_wait<false, true>(bar(B_DP_FULL), it & 1, w))) break;
+        tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(pf[16 * h + 2 * c], pf[16 * h + 2 * c + 1]);
-        tmem_st8(ts + 8 * h, pk);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_P_FULL + (grp >> 1)));
-      // ---- phase 2: dS^T = P^T * (dP^T - Delta) over the dP^T columns
-      if (!(ok = warp_wait<false, true>(bar(B_DP_FULL), it & 1, w))) break;
-      tc_fence_after();
+        for (int h = 0; h < 2; ++h) {
+          uint32_t dv[16];
+          tmem_ld16(td + 16 * h, dv);
+          tmem_ld_wait(dv);
+          uint32_t dd[8];
+          if (!live) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t dv[16];
-        tmem_ld16(td + 16 * h, dv);
-        tmem_ld_wait(dv);
-        uint32_t dd[8];
-        if (!live) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) dd[c] = 0u;
-        } else {
-          dst_slice(dv, pf + 16 * h, dl, 16 * h, dd);
+            for (int c = 0; c < 8; ++c) dd[c] = 0u;
+          } else {
+            dst_slice(dv, pf + 16 * h, dl, 16 * h, dd);
+          }
+          tmem_st8(td + 8 * h, dd);
         }
-        tmem_st8(td + 8 * h, dd);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_DS_FULL));
-    }
-    if (ok) ok = warp_wait<false, true>(bar(B_DKV_DONE), 0, w);
-    if (ok) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_DS_FULL));
+        ++it;
+      } while (x.next());
+      if (!ok || !(ok = warp_wait<false, true>(bar(B_DKV_DONE), n & 1, w))) break;
       tc_fence_after();
-      __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<int64_t>(kpos) * p.Hkv + kv) * kHeadDim + col0;
+      __nv_bfloat16* out = (which == 0 ? p.dk : p.dv) + (static_cast<int64_t>(kpos) * p.Hkv + item.kv) * kHeadDim + col0;
       const float scale = which == 0 ? p.scale : 1.f;
       // a sink's sum is shared by several CTAs, every other key's is complete in its tile's own
       float* part = item.slot >= 0 && kpos < p.sinks ? item.part(p) + (which * p.sink_rows + r) * kHeadDim + col0 : nullptr;
@@ -1297,7 +1394,7 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             st_global_v4(part + c * 32 + q * 4, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        } else if (valid && item.slot <= 0) {
+        } else if (kpos < p.L && item.slot <= 0) {
           store32_bf16(out + c * 32, v, scale);
         }
       }
@@ -1441,11 +1538,12 @@ cudaError_t launch_window_dq(const CUtensorMap& q, const CUtensorMap& k, const C
 }
 
 cudaError_t launch_window_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                               const CUtensorMap& dO, const WinParams& p, int m_tiles, cudaStream_t st) {
+                               const CUtensorMap& dO, const WinParams& p, cudaStream_t st) {
   cudaError_t e =
       cudaFuncSetAttribute(window_dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wkv::kSmemBytes);
   if (e != cudaSuccess) return e;
-  window_dkdv_kernel<<<(m_tiles + p.sink_tiles * p.far_slots) * p.Hkv, wkv::kThreadsKv, wkv::kSmemBytes, st>>>(q, k, v, dO, p);
+  const int grid = p.key_items < kSms ? p.key_items : kSms;
+  window_dkdv_kernel<<<grid, wkv::kThreadsKv, wkv::kSmemBytes, st>>>(q, k, v, dO, p);
   return cudaGetLastError();
 }
 
@@ -1519,6 +1617,8 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   p.shared_keys = s.sinks < f.tiles * 128 ? s.sinks : f.tiles * 128;
   p.sink_part = reinterpret_cast<float*>(at + kCounterBytes + records_bytes(s));
   p.next_tile = reinterpret_cast<int*>(at);
+  p.next_item = reinterpret_cast<int*>(at) + 16;
+  p.key_items = (s.m_tiles + f.tiles * f.slots) * s.Hkv;
   p.dq = reinterpret_cast<__nv_bfloat16*>(dq);
   p.dk = reinterpret_cast<__nv_bfloat16*>(dk);
   p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
@@ -1526,23 +1626,23 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   UPIPE_LAUNCH(UPIPE_KIND_DELTA,
                launch_delta(reinterpret_cast<const __nv_bfloat16*>(o), s.H * 128, 128,
                             reinterpret_cast<const __nv_bfloat16*>(dout_o), s.H * 128, 128, lse, ld, s.L, s.H, st));
-  // Neither reads what the other writes: dQ's many short CTAs fill the SMs
-  // that the last of dK/dV's leave idle.
+  // Neither reads what the other writes: dQ's CTAs, with the shorter tiles,
+  // take the SMs that the last of dK/dV's items leave idle.
   struct Job {
     const CUtensorMap &q, &k, &v, &dO;
     const WinParams& p;
     int m_tiles;
   } job{mq, mk, mv, mdo, p, s.m_tiles};
   if (int e = launch_beside(
-          UPIPE_KIND_WINDOW_DKDV,
-          [](void* x, cudaStream_t on) {
-            const Job& j = *static_cast<Job*>(x);
-            return launch_window_dkdv(j.q, j.k, j.v, j.dO, j.p, j.m_tiles, on);
-          },
           UPIPE_KIND_WINDOW_DQ,
           [](void* x, cudaStream_t on) {
             const Job& j = *static_cast<Job*>(x);
             return launch_window_dq(j.q, j.k, j.v, j.dO, j.p, j.m_tiles, on);
+          },
+          UPIPE_KIND_WINDOW_DKDV,
+          [](void* x, cudaStream_t on) {
+            const Job& j = *static_cast<Job*>(x);
+            return launch_window_dkdv(j.q, j.k, j.v, j.dO, j.p, on);
           },
           &job, st))
     return e;
