@@ -34,9 +34,12 @@ struct WinParams {
   int window, sinks;  // at most L each
   __nv_bfloat16* o;   // [L, H, 128]
   float* lse;         // [H, L]
-  // Per head and 64-query tile a 128-float record: -LSE * log2(e) of the 64
-  // queries (-inf past L), then their Delta (0 past L).
-  const float* ld;
+  // Backward: what a query adds to its scores and to its dP, -LSE sqrt(d) and
+  // -Delta, each as three bf16 whose sum is the fp32 value (a0 a1 a2 b0 b1 b2
+  // and ten zeros): a K = 16 row that one more tcgen05.mma step multiplies by
+  // ones.  [H, L, 16].
+  const __nv_bfloat16* rec;
+  const __nv_bfloat16* dout;  // [L, H, 128]
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
@@ -568,50 +571,112 @@ __device__ __forceinline__ void ds_slice(const uint32_t (&sv)[32], const uint32_
   }
 }
 
-// P^T row slice of the dkdv kernel: 16 queries (columns c0 .. c0 + 15 of
-// this warp's 32) of one key row, kept in fp32 for the dS^T phase.  Lane c of
-// the warp holds -LSE * log2(e) of the warp's query c in `nl`; kMask: bit c
-// of `seen` tells whether query c sees the key.
+// P^T row slice of the dkdv kernel: 16 queries of one key row, from scores
+// that hold S - LSE sqrt(d).  kMask: bit c of `seen` tells whether query c
+// sees the key.
 template <bool kMask>
-__device__ __forceinline__ void p_slice(const uint32_t (&sv)[16], float nl, int c0, float sl2, uint32_t seen,
-                                        float* pf) {
+__device__ __forceinline__ void p_slice(const uint32_t (&sv)[16], float sl2, uint32_t seen, float* pf) {
   const uint64_t sl2x2 = f2_pack(sl2, sl2);
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
-    const float l0 = __shfl_sync(0xffffffffu, nl, c0 + c);
-    const float l1 = __shfl_sync(0xffffffffu, nl, c0 + c + 1);
     float t0, t1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl2x2, f2_pack(l0, l1)), t0, t1);
-    float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+    f2_unpack(f2_mul(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sl2x2), t0, t1);
+    pf[c] = ex2_approx(t0);
+    pf[c + 1] = ex2_approx(t1);
     if (kMask) {
-      if (!(seen >> (c0 + c) & 1u)) p0 = 0.f;
-      if (!(seen >> (c0 + c + 1) & 1u)) p1 = 0.f;
+      if (!(seen >> c & 1u)) pf[c] = 0.f;
+      if (!(seen >> (c + 1) & 1u)) pf[c + 1] = 0.f;
     }
-    pf[c] = p0;
-    pf[c + 1] = p1;
   }
 }
 
-// dS^T row slice of the dkdv kernel: dS = P * (dP - Delta) for 16 queries
-// (columns c0 .. c0 + 15), packed bf16.  Lane c holds Delta of query c in `dl`.
-__device__ __forceinline__ void dst_slice(const uint32_t (&dv)[16], const float* pf, float dl, int c0,
-                                          uint32_t (&dd)[8]) {
+// dS^T row slice of the dkdv kernel: P (dP - Delta) for 16 queries, packed
+// bf16, from sums that hold dP - Delta.
+__device__ __forceinline__ void dst_slice(const uint32_t (&dv)[16], const float* pf, uint32_t (&dd)[8]) {
 #pragma unroll
   for (int c = 0; c < 16; c += 2) {
-    const float d0 = __shfl_sync(0xffffffffu, dl, c0 + c);
-    const float d1 = __shfl_sync(0xffffffffu, dl, c0 + c + 1);
     float s0, s1;
-    f2_unpack(f2_mul(f2_pack(pf[c], pf[c + 1]),
-                     f2_sub(f2_pack(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])), f2_pack(d0, d1))),
-              s0, s1);
+    f2_unpack(f2_mul(f2_pack(pf[c], pf[c + 1]), f2_pack(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1]))), s0, s1);
     dd[c >> 1] = pack_bf16x2(s0, s1);
   }
 }
 
+// Shared-memory descriptor of a K-major operand of 16 columns (32-byte rows,
+// 32-byte swizzle, groups of 8 rows 256 bytes apart).
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(256 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;  // tcgen05 descriptor version
+  d |= static_cast<uint64_t>(6) << 61;  // 32-byte swizzle
+  return d;
+}
+
 // ================================================================ backward
 //
-// Two kernels without atomics, so every sum has one order: dQ by query tiles
-// and dK/dV by key tiles, each recomputing S and dP.
+// Two kernels, in which every sum has one order: dQ by query tiles and dK/dV
+// by key tiles, each recomputing S and dP.
+
+// The queries' records, and the counters' zeros.  16 lanes per (query, head),
+// 16 bytes of O and of dO each; four such items per group are in flight.
+__global__ void __launch_bounds__(256) window_records_kernel(const __grid_constant__ WinParams p,
+                                                             __nv_bfloat16* __restrict__ rec) {
+  constexpr int U = 4;
+  const int64_t items = static_cast<int64_t>(p.L) * p.H;
+  const int sub = threadIdx.x & 15;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * 16 * U + (threadIdx.x >> 4);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.next_tile = *p.next_item = 0;
+  uint4 o[U], g[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = base + u * 16;
+    o[u] = g[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < items) {
+      o[u] = ld_global_nc_v4(p.o + i * kHeadDim + sub * 8);
+      g[u] = ld_global_nc_v4(p.dout + i * kHeadDim + sub * 8);
+    }
+  }
+  int64_t row = base / p.H;
+  int h = static_cast<int>(base - row * p.H);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t ov[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, gv[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+    float acc = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc = fmaf(bf16_lo(ov[e]), bf16_lo(gv[e]), acc);
+      acc = fmaf(bf16_hi(ov[e]), bf16_hi(gv[e]), acc);
+    }
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
+    if (sub < 2 && row < p.L) {
+      const int64_t at = static_cast<int64_t>(h) * p.L + row;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (sub == 0) {
+        const float v[2] = {-p.lse[at] * 11.3137084989847603904f, -acc};  // sqrt(128)
+        float part[6];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float left = v[k];
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            part[3 * k + e] = __bfloat162float(__float2bfloat16_rn(left));
+            left -= part[3 * k + e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e) w[e] = pack_bf16x2(part[2 * e], part[2 * e + 1]);
+      }
+      st_global_v4(rec + at * 16 + sub * 8, w[0], w[1], w[2], w[3]);
+    }
+    h += 16;
+    while (h >= p.H) {
+      h -= p.H;
+      ++row;
+    }
+  }
+}
 
 namespace wq {
 constexpr int kComputeWarps = 8;
@@ -922,7 +987,6 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
     const int r = quad * 32 + lane;
     const uint32_t trow = tmem_lane_addr(tmem, quad, 0);
     const float sl2 = p.scale_log2;
-    const int n_q64 = (p.L + 63) / 64;
     // The n-th tile's number and this row's record of it.
     float nlse2 = 0.f, dlt = 0.f;  // -LSE * log2(e), Delta
     auto open = [&](int n, int& t) -> bool {
@@ -930,9 +994,10 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
       t = tiles[n % kTileSlots];
       if (t < n_tiles) {
         const int qpos = block_of(t) * 128 + r;
-        const float* rec = p.ld + (static_cast<int64_t>(head_of(t)) * n_q64 + (qpos >> 6)) * 128 + (qpos & 63);
-        nlse2 = qpos < p.L ? __ldg(rec) : 0.f;
-        dlt = qpos < p.L ? __ldg(rec + 64) : 0.f;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (qpos < p.L) x = ld_global_nc_v4(p.rec + (static_cast<int64_t>(head_of(t)) * p.L + qpos) * 16);
+        nlse2 = ((bf16_lo(x.x) + bf16_hi(x.x)) + bf16_lo(x.y)) * sl2;
+        dlt = -((bf16_hi(x.y) + bf16_lo(x.z)) + bf16_hi(x.z));
       }
       return true;
     };
@@ -1008,12 +1073,16 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
 namespace wkv {
 constexpr int kTile = 128 * 128 * 2;  // K, V, Q or dO tile: [128 rows][128 d]
 constexpr int kHalf = kTile / 2;
-constexpr int kStages = 2;            // Q/dO ring depth
+constexpr int kQStages = 2;           // Q and its records are held until dK, dO until dV
+constexpr int kDoStages = 2;
 constexpr int OFF_K = 0;
 constexpr int OFF_V = OFF_K + kTile;
-constexpr int OFF_Q = OFF_V + kTile;             // kStages stages
-constexpr int OFF_DO = OFF_Q + kStages * kTile;
-constexpr int OFF_BAR = OFF_DO + kStages * kTile;
+constexpr int OFF_Q = OFF_V + kTile;
+constexpr int OFF_DO = OFF_Q + kQStages * kTile;
+constexpr int kRec = 128 * 16 * 2;    // the records of a query tile
+constexpr int OFF_REC = OFF_DO + kDoStages * kTile;
+constexpr int OFF_ONES = OFF_REC + kQStages * kRec;  // ones that pick the records' LSE part, then their Delta part
+constexpr int OFF_BAR = OFF_ONES + 2 * kRec;
 constexpr int kItemSlots = 8;
 enum {
   B_K_FULL,
@@ -1021,15 +1090,18 @@ enum {
   B_V_FULL,
   B_V_EMPTY,  // the item's last dP^T done
   B_ITEM,     // an item's number published, per slot
-  B_QDO_FULL = B_ITEM + kItemSlots,
-  B_QDO_EMPTY = B_QDO_FULL + kStages,
-  B_S_FULL = B_QDO_EMPTY + kStages,  // per 64-query half of S^T
-  B_P_FULL = B_S_FULL + 2,           // P^T of that half written (its 8 compute warps)
-  B_S_FREE = B_P_FULL + 2,           // dV of that half done: its S^T / P^T columns free
-  B_DP_FULL = B_S_FREE + 2,
-  B_DS_FULL,   // dS^T written (compute warps)
-  B_DP_FREE,   // dK done: dP^T / dS^T columns free
+  B_Q_FULL = B_ITEM + kItemSlots,
+  B_Q_EMPTY = B_Q_FULL + kQStages,
+  B_DO_FULL = B_Q_EMPTY + kQStages,
+  B_DO_EMPTY = B_DO_FULL + kDoStages,
+  B_S_FULL = B_DO_EMPTY + kDoStages,
+  B_P_FULL,                 // P^T written, per region and 64-query half (its 8 compute warps)
+  B_DP_FULL = B_P_FULL + 4,
+  B_DP_READ,                // the compute warps have read dP^T: its region free
+  B_DS_FULL,                // dS^T written
+  B_R_FREE,                 // dV and dK done: the region of P^T and dS^T free
   B_DKV_DONE,
+  B_DKV_READ,               // the compute warps have read an item's dK and dV
   B_DRAIN,
   B_DRAIN_G,
   B_DRAIN_P,
@@ -1039,7 +1111,10 @@ constexpr int OFF_TMEM_SLOT = OFF_BAR + B_COUNT * 8;
 constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
 constexpr int OFF_ITEM = OFF_ABORT + 8;
 constexpr int kSmemBytes = OFF_ITEM + kItemSlots * 4 + 1024;
-constexpr int TM_ST = 0, TM_DPT = 128, TM_DV = 256, TM_DK = 384;
+static_assert(kSmemBytes <= 227 * 1024, "dK/dV kernel shared memory");
+constexpr int TM_R = 0;  // two score regions of 128 columns
+constexpr int TM_P = 0, TM_DS = 16;  // of a 32-query slice: packed P^T, packed dS^T
+constexpr int TM_DV = 256, TM_DK = 384;
 // 16 compute warps: four per TMEM lane quadrant, each owning 32 of the 128
 // query columns, so each SM sub-partition has four to hide TMEM and exp2
 // latency; then the producer and three MMA-issuing warps (S^T; dV and dK;
@@ -1055,14 +1130,13 @@ constexpr int kThreadsKv = 640;
 __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
-                         const __grid_constant__ WinParams p) {
+                         const __grid_constant__ CUtensorMap mrec, const __grid_constant__ WinParams p) {
   using namespace wkv;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n_q64 = (p.L + 63) / 64;
   const int n_items = p.key_items;
   volatile int* items = reinterpret_cast<volatile int*>(smem + OFF_ITEM);
   auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8 * i; };
@@ -1072,24 +1146,33 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
   if (threadIdx.x == 0) {
     for (int i : {B_K_FULL, B_K_EMPTY, B_V_FULL, B_V_EMPTY}) mbar_init(bar(i), 1);
     for (int i = 0; i < kItemSlots; ++i) mbar_init(bar(B_ITEM + i), 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(B_QDO_FULL + s), 1);
-      mbar_init(bar(B_QDO_EMPTY + s), 1);
+    for (int s = 0; s < kQStages; ++s) {
+      mbar_init(bar(B_Q_FULL + s), 1);
+      mbar_init(bar(B_Q_EMPTY + s), 1);
     }
-    for (int hf = 0; hf < 2; ++hf) {
-      mbar_init(bar(B_S_FULL + hf), 1);
-      mbar_init(bar(B_P_FULL + hf), kCompute / 2);
-      mbar_init(bar(B_S_FREE + hf), 1);
+    for (int s = 0; s < kDoStages; ++s) {
+      mbar_init(bar(B_DO_FULL + s), 1);
+      mbar_init(bar(B_DO_EMPTY + s), 2);  // dP^T and dV read it
     }
-    mbar_init(bar(B_DP_FULL), 1);
-    mbar_init(bar(B_DS_FULL), kCompute);
-    mbar_init(bar(B_DP_FREE), 1);
+    for (int i : {B_S_FULL, B_DP_FULL, B_R_FREE}) mbar_init(bar(i), 1);
+    for (int i : {B_DP_READ, B_DS_FULL, B_DKV_READ}) mbar_init(bar(i), kCompute);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(B_P_FULL + i), kCompute / 2);
     mbar_init(bar(B_DKV_DONE), 1);
     mbar_init(bar(B_DRAIN), 1);
     mbar_init(bar(B_DRAIN_G), 1);
     mbar_init(bar(B_DRAIN_P), 1);
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (threadIdx.x < 256) {  // row r of the two tiles of ones, swizzled as TMA does
+    const int r = threadIdx.x & 127, k = threadIdx.x >> 7;
+    const uint32_t row = sb + OFF_ONES + k * kRec + r * 32, flip = (r >> 2 & 1) << 4;
+    if (k == 0)
+      st_shared_v4(row + flip, 0x3F803F80u, 0x00003F80u, 0u, 0u);  // columns 0 1 2
+    else
+      st_shared_v4(row + flip, 0u, 0x3F800000u, 0x3F803F80u, 0u);  // columns 3 4 5
+    st_shared_v4(row + (flip ^ 16), 0u, 0u, 0u, 0u);
+    fence_async_smem();
   }
   if (warp == kMma) {
     tmem_alloc(sb + OFF_TMEM_SLOT, kTmemCols);
@@ -1101,14 +1184,14 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
 
   if (warp == kProducer) {
-    // Three streams, each of which moves on as soon as it can: the items' K
-    // and V, and the Q and dO tiles of all items behind one another (both on
-    // one barrier per stage).
+    // Four streams, each of which moves on as soon as it can: the items' K and
+    // V, and the Q and dO tiles of all items behind one another.
     if (lane == 0) {
       tma_prefetch_map(&mq);
       tma_prefetch_map(&mk);
       tma_prefetch_map(&mv);
       tma_prefetch_map(&mdo);
+      tma_prefetch_map(&mrec);
       int published = 0;  // items given out so far
       int coming = 0;     // the next one's number, asked for an item ahead
       auto ask = [&] { return static_cast<int>(gridDim.x) + atomicAdd(p.next_item, 1); };
@@ -1121,14 +1204,15 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
         if (i < n_items) coming = ask();
       };
       publish(static_cast<int>(blockIdx.x));
-      int nk = 0, nv = 0, nt = 0;  // loads issued
-      int n = 0;                   // the Q/dO stream's item
-      bool t_on = items[0] < n_items, k_on = true, v_on = true;
-      KeyWalk x(KeyItem(t_on ? items[0] : 0, p), p);
+      int nk = 0, nv = 0, nq = 0, ndo = 0;  // loads issued
+      int q_item = 0, do_item = 0;          // the items that the Q and dO streams are in
+      bool q_on = items[0] < n_items, do_on = q_on, k_on = true, v_on = true;
+      KeyWalk xq(KeyItem(q_on ? items[0] : 0, p), p), xdo = xq;
+      bool do_next = false;  // the dO stream is past its item's last tile
       Watchdog wd;
       wd.reset();
       bool ok = true;
-      while (ok && (t_on || k_on || v_on)) {
+      while (ok && (q_on || do_on || k_on || v_on)) {
         bool did = false;
         if (k_on && nk < published && mbar_test(bar(B_K_EMPTY), (nk & 1) ^ 1)) {
           const int i = items[nk % kItemSlots];
@@ -1141,19 +1225,33 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
           }
           did = true;
         }
-        if (t_on && mbar_test(bar(B_QDO_EMPTY + nt % kStages), ((nt / kStages) & 1) ^ 1)) {
-          const int s = nt % kStages;
-          mbar_expect_tx(bar(B_QDO_FULL + s), 2 * kTile);
-          tma_load_3d(sb + OFF_Q + s * kTile, &mq, bar(B_QDO_FULL + s), 0, x.qt * 128, x.h);
-          tma_load_3d(sb + OFF_Q + s * kTile + kHalf, &mq, bar(B_QDO_FULL + s), 64, x.qt * 128, x.h);
-          tma_load_3d(sb + OFF_DO + s * kTile, &mdo, bar(B_QDO_FULL + s), 0, x.qt * 128, x.h);
-          tma_load_3d(sb + OFF_DO + s * kTile + kHalf, &mdo, bar(B_QDO_FULL + s), 64, x.qt * 128, x.h);
-          ++nt;
-          if (!x.next()) {  // this stream is the one that asks for items
+        if (q_on && mbar_test(bar(B_Q_EMPTY + nq % kQStages), ((nq / kQStages) & 1) ^ 1)) {
+          const int s = nq % kQStages;
+          mbar_expect_tx(bar(B_Q_FULL + s), kTile + kRec);
+          tma_load_3d(sb + OFF_REC + s * kRec, &mrec, bar(B_Q_FULL + s), 0, xq.qt * 128, xq.h);
+          tma_load_3d(sb + OFF_Q + s * kTile, &mq, bar(B_Q_FULL + s), 0, xq.qt * 128, xq.h);
+          tma_load_3d(sb + OFF_Q + s * kTile + kHalf, &mq, bar(B_Q_FULL + s), 64, xq.qt * 128, xq.h);
+          ++nq;
+          if (!xq.next()) {  // this stream is the one that asks for items
             publish(coming);
-            const int i = items[++n % kItemSlots];
-            if ((t_on = i < n_items)) x = KeyWalk(KeyItem(i, p), p);
+            const int i = items[++q_item % kItemSlots];
+            if ((q_on = i < n_items)) xq = KeyWalk(KeyItem(i, p), p);
           }
+          did = true;
+        }
+        if (do_next && do_item + 1 < published) {
+          const int i = items[++do_item % kItemSlots];
+          do_next = false;
+          if ((do_on = i < n_items)) xdo = KeyWalk(KeyItem(i, p), p);
+          did = true;
+        }
+        if (do_on && !do_next && mbar_test(bar(B_DO_EMPTY + ndo % kDoStages), ((ndo / kDoStages) & 1) ^ 1)) {
+          const int s = ndo % kDoStages;
+          mbar_expect_tx(bar(B_DO_FULL + s), kTile);
+          tma_load_3d(sb + OFF_DO + s * kTile, &mdo, bar(B_DO_FULL + s), 0, xdo.qt * 128, xdo.h);
+          tma_load_3d(sb + OFF_DO + s * kTile + kHalf, &mdo, bar(B_DO_FULL + s), 64, xdo.qt * 128, xdo.h);
+          ++ndo;
+          do_next = !xdo.next();
           did = true;
         }
         if (v_on && nv < published && mbar_test(bar(B_V_EMPTY), (nv & 1) ^ 1)) {
@@ -1173,17 +1271,18 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
       if (*abort_flag) {  // let every issued copy land before the CTA exits
         if (nk) mbar_wait_drain(bar(B_K_FULL), (nk - 1) & 1, p.status);
         if (nv) mbar_wait_drain(bar(B_V_FULL), (nv - 1) & 1, p.status);
-        for (int i = nt > kStages ? nt - kStages : 0; i < nt; ++i)
-          mbar_wait_drain(bar(B_QDO_FULL + i % kStages), (i / kStages) & 1, p.status);
+        for (int i = nq > kQStages ? nq - kQStages : 0; i < nq; ++i)
+          mbar_wait_drain(bar(B_Q_FULL + i % kQStages), (i / kQStages) & 1, p.status);
+        for (int i = ndo > kDoStages ? ndo - kDoStages : 0; i < ndo; ++i)
+          mbar_wait_drain(bar(B_DO_FULL + i % kDoStages), (i / kDoStages) & 1, p.status);
       }
     }
   } else if (warp == kMma) {
     if (lane == 0) {
-      // S^T(i) in two 64-query halves (N=64): half h once the Q/dO stage has
-      // landed and dV of half h of tile i - 1 has consumed the P^T there.
-      // The halves pipeline independently, which shortens the chain
-      // S^T -> P^T -> dV -> next S^T that a single buffer imposes.
-      constexpr uint32_t id_s = idesc_bf16(128, 64, 0, 0);
+      // S^T = K Q^T, and -LSE sqrt(d) of each query by the records' step, into
+      // region it & 1 once Q has landed and the last tile's dP^T, which was
+      // there, has been read.
+      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
       bool ok = true;
       int it = 0;
       for (int n = 0; ok; ++n) {
@@ -1192,21 +1291,21 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
         if (i >= n_items) break;
         const int n_it = KeyItem(i, p).tiles() * p.g;
         if (!(ok = mbar_spin(bar(B_K_FULL), n & 1, w))) break;
-        for (const int end = it + n_it; ok && it < end; ++it) {
-          const int qs = it % kStages;
-          if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
-          for (int hf = 0; hf < 2; ++hf) {
-            if (!(ok = mbar_spin(bar(B_S_FREE + hf), (it & 1) ^ 1, w))) break;
-            tc_fence_after();
-            const uint32_t bq = sb + OFF_Q + qs * kTile + hf * 64 * 128;  // query rows 64 hf ..
+        for (const int end = it + n_it; it < end; ++it) {
+          const int qs = it % kQStages;
+          if (!(ok = mbar_spin(bar(B_Q_FULL + qs), (it / kQStages) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_DP_READ), (it & 1) ^ 1, w))) break;
+          tc_fence_after();
+          const uint32_t bq = sb + OFF_Q + qs * kTile;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-              umma_bf16(tmem + TM_ST + hf * 64, sdesc_sw128(sb + OFF_K + off, 16, 1024),
-                        sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(bar(B_S_FULL + hf));
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            umma_bf16(tmem + TM_R + (it & 1) * 128, sdesc_sw128(sb + OFF_K + off, 16, 1024),
+                      sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
           }
+          umma_bf16(tmem + TM_R + (it & 1) * 128, sdesc_sw32(sb + OFF_ONES), sdesc_sw32(sb + OFF_REC + qs * kRec), id_s,
+                    1u);
+          umma_commit(bar(B_S_FULL));
         }
         if (ok) umma_commit(bar(B_K_EMPTY));
       }
@@ -1215,7 +1314,9 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     }
   } else if (warp == kDpMma) {
     if (lane == 0) {
-      // dP^T(i) = V dO(i)^T once the stage has landed and dK(i - 1) is done.
+      // dP^T = V dO^T, and -Delta of each query by the records' step, into the
+      // other region once dO (and Q, with the records) has landed and the last
+      // tile's dV and dK, whose P^T and dS^T were there, are done.
       constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
       bool ok = true;
       int it = 0;
@@ -1226,18 +1327,22 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
         const int n_it = KeyItem(i, p).tiles() * p.g;
         if (!(ok = mbar_spin(bar(B_V_FULL), n & 1, w))) break;
         for (const int end = it + n_it; it < end; ++it) {
-          const int qs = it % kStages;
-          if (!(ok = mbar_spin(bar(B_QDO_FULL + qs), (it / kStages) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_DP_FREE), (it & 1) ^ 1, w))) break;
+          const int qs = it % kDoStages;
+          if (!(ok = mbar_spin(bar(B_DO_FULL + qs), (it / kDoStages) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_Q_FULL + it % kQStages), (it / kQStages) & 1, w))) break;
+          if (!(ok = mbar_spin(bar(B_R_FREE), (it & 1) ^ 1, w))) break;
           tc_fence_after();
           const uint32_t bq = sb + OFF_DO + qs * kTile;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_bf16(tmem + TM_DPT, sdesc_sw128(sb + OFF_V + off, 16, 1024), sdesc_sw128(bq + off, 16, 1024), id_s,
-                      kk > 0 ? 1u : 0u);
+            umma_bf16(tmem + TM_R + (~it & 1) * 128, sdesc_sw128(sb + OFF_V + off, 16, 1024),
+                      sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
           }
+          umma_bf16(tmem + TM_R + (~it & 1) * 128, sdesc_sw32(sb + OFF_ONES + kRec),
+                    sdesc_sw32(sb + OFF_REC + it % kQStages * kRec), id_s, 1u);
           umma_commit(bar(B_DP_FULL));
+          umma_commit(bar(B_DO_EMPTY + qs));
         }
         if (ok) umma_commit(bar(B_V_EMPTY));
       }
@@ -1246,23 +1351,21 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     }
   } else if (warp == kGrad) {
     if (lane == 0) {
-      // dV(i) += P^T(i) dO(i) half by half as each half's P^T is written
-      // (then that half's S^T columns are free); dK(i) += dS^T(i) Q(i) once
-      // dS^T is written (then the dP^T columns and the Q/dO stage are free:
-      // S^T(i) and dP^T(i) had completed before the compute warps could write
-      // P^T and dS^T).
+      // dV += P^T dO half by half as each half's P^T is written, then dK +=
+      // dS^T Q; both operands lie in region it & 1, free once both are done.
+      // (P^T of the next tile may be written before this thread has seen this
+      // one's, hence a barrier per region: the tile after next needs R_FREE.)
       constexpr uint32_t id_g = idesc_bf16(128, 128, 0, 1);  // A from TMEM, B MN-major
-      auto issue_grad = [&](int it, bool more, int tm_a, uint32_t b_base, int tm_d, int kk0, int kk1) {
-        const uint32_t bq = b_base + (it % kStages) * kTile;
+      auto issue_grad = [&](int it, bool more, int tm_a, uint32_t b, int tm_d, int kk0, int kk1) {
         for (int kk = kk0; kk < kk1; ++kk) {
           // queries 16 kk .. 16 kk + 15: compute group kk / 2 wrote them at
           // its own 32-column slice
-          const uint32_t a = tmem + tm_a + (kk >> 1) * 32 + (kk & 1) * 8;
-          umma_bf16_ts(tmem + tm_d, a, sdesc_sw128(bq + kk * 2048, kHalf, 1024), id_g, (more || kk > 0) ? 1u : 0u);
+          const uint32_t a = tmem + TM_R + (it & 1) * 128 + tm_a + (kk >> 1) * 32 + (kk & 1) * 8;
+          umma_bf16_ts(tmem + tm_d, a, sdesc_sw128(b + kk * 2048, kHalf, 1024), id_g, (more || kk > 0) ? 1u : 0u);
         }
       };
-      // An item's first P^T is written after the last item's dK and dV have
-      // been read.
+      // An item's first product waits until all compute warps have read the
+      // last item's sums (P^T of a half comes from half of them).
       bool ok = true;
       int it = 0;
       for (int n = 0; ok; ++n) {
@@ -1271,19 +1374,21 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
         if (i >= n_items) break;
         const int n_it = KeyItem(i, p).tiles() * p.g;
         const int begin = it;
+        if (!(ok = mbar_spin(bar(B_DKV_READ), (n & 1) ^ 1, w))) break;
         for (const int end = it + n_it; ok && it < end; ++it) {
+          const uint32_t bdo = sb + OFF_DO + it % kDoStages * kTile;
           for (int hf = 0; hf < 2; ++hf) {
-            if (!(ok = mbar_spin(bar(B_P_FULL + hf), it & 1, w))) break;
+            if (!(ok = mbar_spin(bar(B_P_FULL + 2 * (it & 1) + hf), (it >> 1) & 1, w))) break;
             tc_fence_after();
-            issue_grad(it, it > begin, TM_ST, sb + OFF_DO, TM_DV, 4 * hf, 4 * hf + 4);
-            umma_commit(bar(B_S_FREE + hf));
+            issue_grad(it, it > begin, TM_P, bdo, TM_DV, 4 * hf, 4 * hf + 4);
           }
           if (!ok) break;
+          umma_commit(bar(B_DO_EMPTY + it % kDoStages));
           if (!(ok = mbar_spin(bar(B_DS_FULL), it & 1, w))) break;
           tc_fence_after();
-          issue_grad(it, it > begin, TM_DPT, sb + OFF_Q, TM_DK, 0, 8);
-          umma_commit(bar(B_DP_FREE));
-          umma_commit(bar(B_QDO_EMPTY + it % kStages));
+          issue_grad(it, it > begin, TM_DS, sb + OFF_Q + it % kQStages * kTile, TM_DK, 0, 8);
+          umma_commit(bar(B_R_FREE));
+          umma_commit(bar(B_Q_EMPTY + it % kQStages));
         }
         if (ok) umma_commit(bar(B_DKV_DONE));
       }
@@ -1302,8 +1407,6 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
     const int which = grp >> 1;
     const int col0 = (grp & 1) * 64;
     const uint32_t my_tm = trow + (which == 0 ? TM_DK : TM_DV) + col0;
-    const uint32_t ts = trow + TM_ST + grp * 32;
-    const uint32_t td = trow + TM_DPT + grp * 32;
     bool ok = true;
     int it = 0;
     for (int n = 0; ok; ++n) {
@@ -1320,18 +1423,12 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
         const bool masked = hides(qt, item.kb, p);  // warp-uniform
         // queries from the key's own to the last one whose window reaches it
         const uint32_t seen = masked ? bits_below(last_q - q0 + 1) & ~bits_below(kpos - q0) : ~0u;
-        // Without its record (all 64 queries past L) the slice is all zero.
-        const bool live = 2 * qt + (grp >> 1) < n_q64;
-        // This warp's 32 queries in their record: -LSE*log2(e) at +0, Delta at
-        // +64.  Lane c loads query c's pair now, ahead of the waits, and the
-        // values reach the other lanes by shuffle.
-        const float* rec = p.ld + (static_cast<int64_t>(x.h) * n_q64 + 2 * qt + (grp >> 1)) * 128 + (grp & 1) * 32;
-        const float nl = live ? __ldg(rec + lane) : 0.f;
-        const float dl = live ? __ldg(rec + 64 + lane) : 0.f;
         // ---- phase 1: P^T over the S^T columns, 16 at a time; the packed
         // P^T of columns 16 h .. 16 h + 15 goes to columns 8 h .. 8 h + 7, which
         // this warp has already read.
-        if (!(ok = warp_wait<false, true>(bar(B_S_FULL + (grp >> 1)), it & 1, w))) break;
+        const uint32_t ts = trow + TM_R + (it & 1) * 128 + grp * 32;
+        const uint32_t td = trow + TM_R + (~it & 1) * 128 + grp * 32;
+        if (!(ok = warp_wait<false, true>(bar(B_S_FULL), it & 1, w))) break;
         tc_fence_after();
         float pf[32];
 #pragma unroll
@@ -1339,24 +1436,21 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
           uint32_t sv[16];
           tmem_ld16(ts + 16 * h, sv);
           tmem_ld_wait(sv);
-          if (!live) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) pf[16 * h + c] = 0.f;
-          } else if (masked) {
-            p_slice<true>(sv, nl, 16 * h, sl2, seen, pf + 16 * h);
-          } else {
-            p_slice<false>(sv, nl, 16 * h, sl2, 0u, pf + 16 * h);
-          }
+          if (masked)
+            p_slice<true>(sv, sl2, seen >> 16 * h, pf + 16 * h);
+          else
+            p_slice<false>(sv, sl2, 0u, pf + 16 * h);
           uint32_t pk[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) pk[c] = pack_bf16x2(pf[16 * h + 2 * c], pf[16 * h + 2 * c + 1]);
-          tmem_st8(ts + 8 * h, pk);
+          tmem_st8(ts + TM_P + 8 * h, pk);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_P_FULL + (grp >> 1)));
-        // ---- phase 2: dS^T = P^T * (dP^T - Delta) over the dP^T columns
+        if (lane == 0) mbar_arrive(bar(B_P_FULL + 2 * (it & 1) + (grp >> 1)));
+        // ---- phase 2: dS^T = P^T * (dP^T - Delta) into the other half of the
+        // S^T columns
         if (!(ok = warp_wait<false, true>(bar(B_DP_FULL), it & 1, w))) break;
         tc_fence_after();
 #pragma unroll
@@ -1364,14 +1458,14 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
           uint32_t dv[16];
           tmem_ld16(td + 16 * h, dv);
           tmem_ld_wait(dv);
-          uint32_t dd[8];
-          if (!live) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) dd[c] = 0u;
-          } else {
-            dst_slice(dv, pf + 16 * h, dl, 16 * h, dd);
+          if (h == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_DP_READ));  // the next S^T may be formed there
           }
-          tmem_st8(td + 8 * h, dd);
+          uint32_t dd[8];
+          dst_slice(dv, pf + 16 * h, dd);
+          tmem_st8(ts + TM_DS + 8 * h, dd);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -1398,6 +1492,9 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
           store32_bf16(out + c * 32, v, scale);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_DKV_READ));
     }
     tc_fence_before();
   }
@@ -1496,9 +1593,7 @@ SinkPlan sink_plan(const WinShape& s) {
 // Workspace: counters, the records of LSE and Delta, the shares of the sinks.
 constexpr size_t kCounterBytes = 128;
 
-size_t records_bytes(const WinShape& s) {
-  return static_cast<size_t>(s.H) * static_cast<size_t>((s.L + 63) / 64) * 128 * sizeof(float);
-}
+size_t records_bytes(const WinShape& s) { return static_cast<size_t>(s.H) * static_cast<size_t>(s.L) * 32; }
 
 size_t workspace_bytes(const WinShape& s) { return kCounterBytes + records_bytes(s) + sink_plan(s).bytes; }
 
@@ -1538,12 +1633,18 @@ cudaError_t launch_window_dq(const CUtensorMap& q, const CUtensorMap& k, const C
 }
 
 cudaError_t launch_window_dkdv(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                               const CUtensorMap& dO, const WinParams& p, cudaStream_t st) {
+                               const CUtensorMap& dO, const CUtensorMap& rec, const WinParams& p, cudaStream_t st) {
   cudaError_t e =
       cudaFuncSetAttribute(window_dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wkv::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = p.key_items < kSms ? p.key_items : kSms;
-  window_dkdv_kernel<<<grid, wkv::kThreadsKv, wkv::kSmemBytes, st>>>(q, k, v, dO, p);
+  window_dkdv_kernel<<<grid, wkv::kThreadsKv, wkv::kSmemBytes, st>>>(q, k, v, dO, rec, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_window_records(const WinParams& p, __nv_bfloat16* rec, cudaStream_t st) {
+  const int64_t items = static_cast<int64_t>(p.L) * p.H;
+  window_records_kernel<<<static_cast<unsigned>((items + 63) / 64), 256, 0, st>>>(p, rec);
   return cudaGetLastError();
 }
 
@@ -1607,8 +1708,13 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   UPIPE_MAP(map3d(&mdo, dout_o, s.L, s.H, s.H * 128, 128, 128));
   WinParams p = base_params(s, status);
   uint8_t* const at = static_cast<uint8_t*>(ws);
-  float* ld = reinterpret_cast<float*>(at + kCounterBytes);
-  p.ld = ld;
+  __nv_bfloat16* rec = reinterpret_cast<__nv_bfloat16*>(at + kCounterBytes);
+  CUtensorMap mrec;
+  UPIPE_MAP(map_rows16(&mrec, rec, s.L, s.H, 128));
+  p.rec = rec;
+  p.o = reinterpret_cast<__nv_bfloat16*>(const_cast<uint16_t*>(o));  // read
+  p.dout = reinterpret_cast<const __nv_bfloat16*>(dout_o);
+  p.lse = const_cast<float*>(lse);  // read
   p.sink_tiles = f.tiles;
   p.near_tiles = f.near;
   p.far_chunk = f.chunk;
@@ -1622,17 +1728,14 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   p.dq = reinterpret_cast<__nv_bfloat16*>(dq);
   p.dk = reinterpret_cast<__nv_bfloat16*>(dk);
   p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
-  UPIPE_CU(cudaMemsetAsync(at, 0, kCounterBytes, st));
-  UPIPE_LAUNCH(UPIPE_KIND_DELTA,
-               launch_delta(reinterpret_cast<const __nv_bfloat16*>(o), s.H * 128, 128,
-                            reinterpret_cast<const __nv_bfloat16*>(dout_o), s.H * 128, 128, lse, ld, s.L, s.H, st));
+  UPIPE_LAUNCH(UPIPE_KIND_WINDOW_RECORDS, launch_window_records(p, rec, st));
   // Neither reads what the other writes: dQ's CTAs, with the shorter tiles,
   // take the SMs that the last of dK/dV's items leave idle.
   struct Job {
-    const CUtensorMap &q, &k, &v, &dO;
+    const CUtensorMap &q, &k, &v, &dO, &rec;
     const WinParams& p;
     int m_tiles;
-  } job{mq, mk, mv, mdo, p, s.m_tiles};
+  } job{mq, mk, mv, mdo, mrec, p, s.m_tiles};
   if (int e = launch_beside(
           UPIPE_KIND_WINDOW_DQ,
           [](void* x, cudaStream_t on) {
@@ -1642,7 +1745,7 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
           UPIPE_KIND_WINDOW_DKDV,
           [](void* x, cudaStream_t on) {
             const Job& j = *static_cast<Job*>(x);
-            return launch_window_dkdv(j.q, j.k, j.v, j.dO, j.p, on);
+            return launch_window_dkdv(j.q, j.k, j.v, j.dO, j.rec, j.p, on);
           },
           &job, st))
     return e;

@@ -25,6 +25,9 @@ bool map2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint6
 // bf16 heads of 128: element (c, row, head) at base + row*row_stride + head*head_stride.
 bool map3d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t heads, uint64_t row_stride,
            uint64_t head_stride, uint32_t box_rows);
+// bf16 rows of 16: element (c, row, head) at base + (head*rows + row)*16 + c;
+// box 16 x box_rows, 32-byte swizzle.
+bool map_rows16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t heads, uint32_t box_rows);
 
 // Launch accounting: a counter of every kernel launch, and optional CUDA
 // event pairs recorded around each launch on the launching stream.

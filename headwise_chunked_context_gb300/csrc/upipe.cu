@@ -222,6 +222,18 @@ bool map3d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t heads, uint
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool map_rows16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t heads, uint32_t box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {16, rows, heads};
+  cuuint64_t strides[2] = {32, rows * 32};
+  cuuint32_t box[3] = {16, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Launch accounting: a counter of every kernel launch, and optional CUDA
 // event pairs recorded around each launch on the launching stream.  A host
 // thread inside the entry point that allocates nothing records no events

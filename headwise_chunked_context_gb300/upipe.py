@@ -69,7 +69,7 @@ EXPORTS = (
 KINDS = ("rope_table", "qkv_gemm", "attn_fwd", "oproj_gemm", "do_gemm", "dwo_gemm", "attn_bwd_dq",
          "attn_bwd_dkdv", "dwqkv_gemm", "dx_gemm", "delta", "zero_rows", "alst_gu", "alst_gemm", "alst_wgrad",
          "ce_rows", "qk_rope", "norm_sum", "window_fwd", "window_dq", "window_dkdv",
-         "window_sinks")
+         "window_sinks", "window_records")
 
 
 class UpipeError(RuntimeError):

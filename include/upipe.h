@@ -540,7 +540,8 @@ int upipe_debug_wait_timeout(uint64_t limit_ns, void* stream);
 #define UPIPE_KIND_WINDOW_DQ 19
 #define UPIPE_KIND_WINDOW_DKDV 20
 #define UPIPE_KIND_WINDOW_SINKS 21
-#define UPIPE_KIND_COUNT 22
+#define UPIPE_KIND_WINDOW_RECORDS 22  /* its row statistics, for the backward */
+#define UPIPE_KIND_COUNT 23
 int64_t upipe_launch_count(void);
 void upipe_profile_enable(int on);
 int upipe_profile_read(double* ms, int64_t* launches, int n);
