@@ -20,6 +20,7 @@
 // dV are rounded to bf16 once, from TMEM.
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "host.h"
 #include "sm103_ptx.cuh"
@@ -161,6 +162,40 @@ __device__ __forceinline__ void store32_bf16(__nv_bfloat16* out, const uint32_t 
       h[e] = pack_bf16x2(__uint_as_float(a[8 * q + 2 * e]) * scale, __uint_as_float(a[8 * q + 2 * e + 1]) * scale);
     st_global_v4(out + q * 8, h[0], h[1], h[2], h[3]);
   }
+}
+
+// Products issued by a whole converged warp, from which one lane is elected
+// inside the instruction sequence: addresses and descriptors then stay in
+// uniform registers.  Eight products of 128 x 128 x 16 from an idle pipe are
+// seen complete after 705 cycles, 841 when a thread of its own issues them
+// behind a branch (512 of them are the products).  The election is the same
+// every time, so commits cover the same thread's products.
+__device__ __forceinline__ void umma_one(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // ================================================================= forward
@@ -320,61 +355,57 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ S issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);  // Q (TMEM) x K (smem, K-major)
-      // S(j) once K(j) has landed and the softmax warps have read S(j - 1);
-      // a tile's first one also wants its Q in TMEM.
-      bool ok = true;
-      int it = 0;
-      for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
-        const int n_kv = QuerySpan(block_of(t), p).count();
-        if (!(ok = mbar_spin(bar(B_Q_TMEM), n & 1, w))) break;
-        for (int j = 0; j < n_kv; ++j, ++it) {
-          const int s = it % kStages;
-          if (!(ok = mbar_spin(bar(B_K_FULL + s), (it / kStages) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_S_READ), (it & 1) ^ 1, w))) break;
-          tc_fence_after();
-          const uint32_t ka = sb + OFF_K + s * kTile;
+    constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);  // Q (TMEM) x K (smem, K-major)
+    // S(j) once K(j) has landed and the softmax warps have read S(j - 1);
+    // a tile's first one also wants its Q in TMEM.
+    bool ok = true;
+    int it = 0;
+    for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
+      const int n_kv = QuerySpan(block_of(t), p).count();
+      if (!(ok = warp_wait(bar(B_Q_TMEM), n & 1, w))) break;
+      for (int j = 0; j < n_kv; ++j, ++it) {
+        const int s = it % kStages;
+        if (!(ok = warp_wait(bar(B_K_FULL + s), (it / kStages) & 1, w))) break;
+        if (!(ok = warp_wait(bar(B_S_READ), (it & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t ka = sb + OFF_K + s * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            umma_bf16_ts(tmem + TM_S, tmem + TM_Q + kk * 8,
-                         sdesc_sw128(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(bar(B_S_FULL));
-          umma_commit(bar(B_K_EMPTY + s));
+        for (int kk = 0; kk < 8; ++kk) {
+          umma_ts_one(tmem + TM_S, tmem + TM_Q + kk * 8,
+                       sdesc_sw128(ka + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024), id_s, kk > 0 ? 1u : 0u);
         }
+        commit_one(bar(B_S_FULL));
+        commit_one(bar(B_K_EMPTY + s));
       }
-      umma_commit(bar(B_DRAIN));
-      mbar_wait_drain(bar(B_DRAIN), 0, p.status);
     }
+    commit_one(bar(B_DRAIN));
+    mbar_wait_drain(bar(B_DRAIN), 0, p.status);
   } else if (warp == 6) {
     // ----------------------------------------------------------- PV issuer
-    if (lane == 0) {
-      constexpr uint32_t id_o = idesc_bf16(128, 128, 0, 1);  // P (TMEM) x V (smem, MN-major)
-      bool ok = true;
-      int it = 0;
-      for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
-        const int n_kv = QuerySpan(block_of(t), p).count();
-        for (int j = 0; j < n_kv; ++j, ++it) {
-          const int b = it & 1;
-          const int s = it % kStages;
-          // a tile's first P is written after the last tile's O has been read
-          if (!(ok = mbar_spin(bar(B_P_FULL + b), (it >> 1) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_V_FULL + s), (it / kStages) & 1, w))) break;
-          tc_fence_after();
-          const uint32_t va = sb + OFF_V + s * kTile;
+    constexpr uint32_t id_o = idesc_bf16(128, 128, 0, 1);  // P (TMEM) x V (smem, MN-major)
+    bool ok = true;
+    int it = 0;
+    for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
+      const int n_kv = QuerySpan(block_of(t), p).count();
+      for (int j = 0; j < n_kv; ++j, ++it) {
+        const int b = it & 1;
+        const int s = it % kStages;
+        // a tile's first P is written after the last tile's O has been read
+        if (!(ok = warp_wait(bar(B_P_FULL + b), (it >> 1) & 1, w))) break;
+        if (!(ok = warp_wait(bar(B_V_FULL + s), (it / kStages) & 1, w))) break;
+        tc_fence_after();
+        const uint32_t va = sb + OFF_V + s * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            umma_bf16_ts(tmem + TM_O, tmem + TM_P + b * 64 + kk * 8, sdesc_sw128(va + kk * 2048, kHalf, 1024), id_o,
-                         (j > 0 || kk > 0) ? 1u : 0u);
-          }
-          umma_commit(bar(B_P_EMPTY + b));
-          umma_commit(bar(B_V_EMPTY + s));
+        for (int kk = 0; kk < 8; ++kk) {
+          umma_ts_one(tmem + TM_O, tmem + TM_P + b * 64 + kk * 8, sdesc_sw128(va + kk * 2048, kHalf, 1024), id_o,
+                       (j > 0 || kk > 0) ? 1u : 0u);
         }
+        commit_one(bar(B_P_EMPTY + b));
+        commit_one(bar(B_V_EMPTY + s));
       }
-      umma_commit(bar(B_DRAIN_PV));
-      mbar_wait_drain(bar(B_DRAIN_PV), 0, p.status);
     }
+    commit_one(bar(B_DRAIN_PV));
+    mbar_wait_drain(bar(B_DRAIN_PV), 0, p.status);
   } else {
     // ------------------------------------------------------------- softmax
     const int r = warp * 32 + lane;  // query row in the tile = TMEM lane
@@ -881,104 +912,98 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      // S = Q K^T into buffer it & 1 once K has landed and the dQ product
-      // two blocks ago has released the buffer.
-      constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
-      bool ok = true;
-      int it = 0;
-      for (int n = 0; ok; ++n) {
-        if (!(ok = mbar_wait(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
-        const int t = tiles[n % kTileSlots];
-        if (t >= n_tiles) break;
-        const int n_kv = QuerySpan(block_of(t), p).count();
-        if (!(ok = mbar_spin(bar(B_Q_FULL), n & 1, w))) break;
-        for (int j = 0; j < n_kv; ++j, ++it) {
-          const int s = it % kKStages;
-          if (!(ok = mbar_spin(bar(B_K_FULL + s), (it / kKStages) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_S_FREE + (it & 1)), ((it >> 1) & 1) ^ 1, w))) break;
-          tc_fence_after();
-          const uint32_t ka = sb + OFF_K + s * kTile;
+    // S = Q K^T into buffer it & 1 once K has landed and the dQ product
+    // two blocks ago has released the buffer.
+    constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
+    bool ok = true;
+    int it = 0;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = warp_wait<false, true>(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
+      const int t = tiles[n % kTileSlots];
+      if (t >= n_tiles) break;
+      const int n_kv = QuerySpan(block_of(t), p).count();
+      if (!(ok = warp_wait(bar(B_Q_FULL), n & 1, w))) break;
+      for (int j = 0; j < n_kv; ++j, ++it) {
+        const int s = it % kKStages;
+        if (!(ok = warp_wait(bar(B_K_FULL + s), (it / kKStages) & 1, w))) break;
+        if (!(ok = warp_wait(bar(B_S_FREE + (it & 1)), ((it >> 1) & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t ka = sb + OFF_K + s * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_bf16(tmem + TM_S + (it & 1) * 128, sdesc_sw128(sb + OFF_Q + off, 16, 1024),
-                      sdesc_sw128(ka + off, 16, 1024), id_kk, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(bar(B_S_FULL + (it & 1)));
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_one(tmem + TM_S + (it & 1) * 128, sdesc_sw128(sb + OFF_Q + off, 16, 1024),
+                    sdesc_sw128(ka + off, 16, 1024), id_kk, kk > 0 ? 1u : 0u);
         }
-        if (ok) umma_commit(bar(B_Q_EMPTY));
+        commit_one(bar(B_S_FULL + (it & 1)));
       }
-      umma_commit(bar(B_DRAIN));
-      mbar_wait_drain(bar(B_DRAIN), 0, p.status);
+      if (ok) commit_one(bar(B_Q_EMPTY));
     }
+    commit_one(bar(B_DRAIN));
+    mbar_wait_drain(bar(B_DRAIN), 0, p.status);
   } else if (warp == kDpWarp) {
-    if (lane == 0) {
-      // dP = dO V^T once V has landed and the last block's dP has been read.
-      constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
-      bool ok = true;
-      int it = 0;
-      for (int n = 0; ok; ++n) {
-        if (!(ok = mbar_wait(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
-        const int t = tiles[n % kTileSlots];
-        if (t >= n_tiles) break;
-        const int n_kv = QuerySpan(block_of(t), p).count();
-        if (!(ok = mbar_spin(bar(B_DO_FULL), n & 1, w))) break;
-        for (int j = 0; j < n_kv; ++j, ++it) {
-          const int s = it % kVStages;
-          if (!(ok = mbar_spin(bar(B_V_FULL + s), (it / kVStages) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_DP_EMPTY), (it & 1) ^ 1, w))) break;
-          tc_fence_after();
-          const uint32_t va = sb + OFF_V + s * kTile;
+    // dP = dO V^T once V has landed and the last block's dP has been read.
+    constexpr uint32_t id_kk = idesc_bf16(128, 128, 0, 0);
+    bool ok = true;
+    int it = 0;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = warp_wait<false, true>(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
+      const int t = tiles[n % kTileSlots];
+      if (t >= n_tiles) break;
+      const int n_kv = QuerySpan(block_of(t), p).count();
+      if (!(ok = warp_wait(bar(B_DO_FULL), n & 1, w))) break;
+      for (int j = 0; j < n_kv; ++j, ++it) {
+        const int s = it % kVStages;
+        if (!(ok = warp_wait(bar(B_V_FULL + s), (it / kVStages) & 1, w))) break;
+        if (!(ok = warp_wait(bar(B_DP_EMPTY), (it & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t va = sb + OFF_V + s * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_bf16(tmem + TM_DP, sdesc_sw128(sb + OFF_DO + off, 16, 1024), sdesc_sw128(va + off, 16, 1024), id_kk,
-                      kk > 0 ? 1u : 0u);
-          }
-          umma_commit(bar(B_DP_FULL));
-          umma_commit(bar(B_V_EMPTY + s));
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_one(tmem + TM_DP, sdesc_sw128(sb + OFF_DO + off, 16, 1024), sdesc_sw128(va + off, 16, 1024), id_kk,
+                    kk > 0 ? 1u : 0u);
         }
-        if (ok) umma_commit(bar(B_DO_EMPTY));
+        commit_one(bar(B_DP_FULL));
+        commit_one(bar(B_V_EMPTY + s));
       }
-      umma_commit(bar(B_DRAIN_P));
-      mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
+      if (ok) commit_one(bar(B_DO_EMPTY));
     }
+    commit_one(bar(B_DRAIN_P));
+    mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
   } else if (warp == kGradWarp) {
-    if (lane == 0) {
-      // dQ += dS K once dS is written; then its S buffer and K stage are free
-      // (S had completed before dS existed).  A tile's first dS is written
-      // after the compute warps have read the last tile's dQ.
-      constexpr uint32_t id_q = idesc_bf16(128, 128, 0, 1);  // dS from TMEM, K MN-major
-      bool ok = true;
-      int it = 0;
-      for (int n = 0; ok; ++n) {
-        if (!(ok = mbar_wait(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
-        const int t = tiles[n % kTileSlots];
-        if (t >= n_tiles) break;
-        const int n_kv = QuerySpan(block_of(t), p).count();
-        for (int j = 0; j < n_kv; ++j, ++it) {
-          const int b = it & 1;
-          const int s = it % kKStages;
-          if (!(ok = mbar_spin(bar(B_DS_FULL + b), (it >> 1) & 1, w))) break;
-          tc_fence_after();
-          const uint32_t ka = sb + OFF_K + s * kTile;
+    // dQ += dS K once dS is written; then its S buffer and K stage are free
+    // (S had completed before dS existed).  A tile's first dS is written
+    // after the compute warps have read the last tile's dQ.
+    constexpr uint32_t id_q = idesc_bf16(128, 128, 0, 1);  // dS from TMEM, K MN-major
+    bool ok = true;
+    int it = 0;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = warp_wait<false, true>(bar(B_TILE + n % kTileSlots), (n / kTileSlots) & 1, w))) break;
+      const int t = tiles[n % kTileSlots];
+      if (t >= n_tiles) break;
+      const int n_kv = QuerySpan(block_of(t), p).count();
+      for (int j = 0; j < n_kv; ++j, ++it) {
+        const int b = it & 1;
+        const int s = it % kKStages;
+        if (!(ok = warp_wait(bar(B_DS_FULL + b), (it >> 1) & 1, w))) break;
+        tc_fence_after();
+        const uint32_t ka = sb + OFF_K + s * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            // keys 16 kk .. 16 kk + 15: compute half kk / 4 wrote them at its own
-            // 64-column slice of the S buffer
-            const uint32_t a = tmem + TM_S + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8;
-            umma_bf16_ts(tmem + TM_DQ, a, sdesc_sw128(ka + kk * 2048, kHalf, 1024), id_q,
-                         (j > 0 || kk > 0) ? 1u : 0u);
-          }
-          umma_commit(bar(B_S_FREE + b));
-          umma_commit(bar(B_K_EMPTY + s));
+        for (int kk = 0; kk < 8; ++kk) {
+          // keys 16 kk .. 16 kk + 15: compute half kk / 4 wrote them at its own
+          // 64-column slice of the S buffer
+          const uint32_t a = tmem + TM_S + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8;
+          umma_ts_one(tmem + TM_DQ, a, sdesc_sw128(ka + kk * 2048, kHalf, 1024), id_q,
+                       (j > 0 || kk > 0) ? 1u : 0u);
         }
-        if (ok) umma_commit(bar(B_DQ_DONE));
+        commit_one(bar(B_S_FREE + b));
+        commit_one(bar(B_K_EMPTY + s));
       }
-      umma_commit(bar(B_DRAIN_G));
-      mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
+      if (ok) commit_one(bar(B_DQ_DONE));
     }
+    commit_one(bar(B_DRAIN_G));
+    mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
   } else {
     // Compute warps: quadrant (warp & 3) of the TMEM lanes = query rows,
     // half (warp >> 2) of the 128 key columns of each block.
@@ -1278,123 +1303,119 @@ __global__ void __launch_bounds__(wkv::kThreadsKv, 1)
       }
     }
   } else if (warp == kMma) {
-    if (lane == 0) {
-      // S^T = K Q^T, and -LSE sqrt(d) of each query by the records' step, into
-      // region it & 1 once Q has landed and the last tile's dP^T, which was
-      // there, has been read.
-      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
-      bool ok = true;
-      int it = 0;
-      for (int n = 0; ok; ++n) {
-        if (!(ok = mbar_wait(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
-        const int i = items[n % kItemSlots];
-        if (i >= n_items) break;
-        const int n_it = KeyItem(i, p).tiles() * p.g;
-        if (!(ok = mbar_spin(bar(B_K_FULL), n & 1, w))) break;
-        for (const int end = it + n_it; it < end; ++it) {
-          const int qs = it % kQStages;
-          if (!(ok = mbar_spin(bar(B_Q_FULL + qs), (it / kQStages) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_DP_READ), (it & 1) ^ 1, w))) break;
-          tc_fence_after();
-          const uint32_t bq = sb + OFF_Q + qs * kTile;
+    // S^T = K Q^T, and -LSE sqrt(d) of each query by the records' step, into
+    // region it & 1 once Q has landed and the last tile's dP^T, which was
+    // there, has been read.
+    constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
+    bool ok = true;
+    int it = 0;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = warp_wait<false, true>(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
+      const int i = items[n % kItemSlots];
+      if (i >= n_items) break;
+      const int n_it = KeyItem(i, p).tiles() * p.g;
+      if (!(ok = warp_wait(bar(B_K_FULL), n & 1, w))) break;
+      for (const int end = it + n_it; it < end; ++it) {
+        const int qs = it % kQStages;
+        if (!(ok = warp_wait(bar(B_Q_FULL + qs), (it / kQStages) & 1, w))) break;
+        if (!(ok = warp_wait(bar(B_DP_READ), (it & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t bq = sb + OFF_Q + qs * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_bf16(tmem + TM_R + (it & 1) * 128, sdesc_sw128(sb + OFF_K + off, 16, 1024),
-                      sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-          }
-          umma_bf16(tmem + TM_R + (it & 1) * 128, sdesc_sw32(sb + OFF_ONES), sdesc_sw32(sb + OFF_REC + qs * kRec), id_s,
-                    1u);
-          umma_commit(bar(B_S_FULL));
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_one(tmem + TM_R + (it & 1) * 128, sdesc_sw128(sb + OFF_K + off, 16, 1024),
+                    sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
         }
-        if (ok) umma_commit(bar(B_K_EMPTY));
+        umma_one(tmem + TM_R + (it & 1) * 128, sdesc_sw32(sb + OFF_ONES), sdesc_sw32(sb + OFF_REC + qs * kRec), id_s,
+                  1u);
+        commit_one(bar(B_S_FULL));
       }
-      umma_commit(bar(B_DRAIN));
-      mbar_wait_drain(bar(B_DRAIN), 0, p.status);
+      if (ok) commit_one(bar(B_K_EMPTY));
     }
+    commit_one(bar(B_DRAIN));
+    mbar_wait_drain(bar(B_DRAIN), 0, p.status);
   } else if (warp == kDpMma) {
-    if (lane == 0) {
-      // dP^T = V dO^T, and -Delta of each query by the records' step, into the
-      // other region once dO (and Q, with the records) has landed and the last
-      // tile's dV and dK, whose P^T and dS^T were there, are done.
-      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
-      bool ok = true;
-      int it = 0;
-      for (int n = 0; ok; ++n) {
-        if (!(ok = mbar_wait(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
-        const int i = items[n % kItemSlots];
-        if (i >= n_items) break;
-        const int n_it = KeyItem(i, p).tiles() * p.g;
-        if (!(ok = mbar_spin(bar(B_V_FULL), n & 1, w))) break;
-        for (const int end = it + n_it; it < end; ++it) {
-          const int qs = it % kDoStages;
-          if (!(ok = mbar_spin(bar(B_DO_FULL + qs), (it / kDoStages) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_Q_FULL + it % kQStages), (it / kQStages) & 1, w))) break;
-          if (!(ok = mbar_spin(bar(B_R_FREE), (it & 1) ^ 1, w))) break;
-          tc_fence_after();
-          const uint32_t bq = sb + OFF_DO + qs * kTile;
+    // dP^T = V dO^T, and -Delta of each query by the records' step, into the
+    // other region once dO (and Q, with the records) has landed and the last
+    // tile's dV and dK, whose P^T and dS^T were there, are done.
+    constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0);
+    bool ok = true;
+    int it = 0;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = warp_wait<false, true>(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
+      const int i = items[n % kItemSlots];
+      if (i >= n_items) break;
+      const int n_it = KeyItem(i, p).tiles() * p.g;
+      if (!(ok = warp_wait(bar(B_V_FULL), n & 1, w))) break;
+      for (const int end = it + n_it; it < end; ++it) {
+        const int qs = it % kDoStages;
+        if (!(ok = warp_wait(bar(B_DO_FULL + qs), (it / kDoStages) & 1, w))) break;
+        if (!(ok = warp_wait(bar(B_Q_FULL + it % kQStages), (it / kQStages) & 1, w))) break;
+        if (!(ok = warp_wait(bar(B_R_FREE), (it & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint32_t bq = sb + OFF_DO + qs * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_bf16(tmem + TM_R + (~it & 1) * 128, sdesc_sw128(sb + OFF_V + off, 16, 1024),
-                      sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-          }
-          umma_bf16(tmem + TM_R + (~it & 1) * 128, sdesc_sw32(sb + OFF_ONES + kRec),
-                    sdesc_sw32(sb + OFF_REC + it % kQStages * kRec), id_s, 1u);
-          umma_commit(bar(B_DP_FULL));
-          umma_commit(bar(B_DO_EMPTY + qs));
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_one(tmem + TM_R + (~it & 1) * 128, sdesc_sw128(sb + OFF_V + off, 16, 1024),
+                    sdesc_sw128(bq + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
         }
-        if (ok) umma_commit(bar(B_V_EMPTY));
+        umma_one(tmem + TM_R + (~it & 1) * 128, sdesc_sw32(sb + OFF_ONES + kRec),
+                  sdesc_sw32(sb + OFF_REC + it % kQStages * kRec), id_s, 1u);
+        commit_one(bar(B_DP_FULL));
+        commit_one(bar(B_DO_EMPTY + qs));
       }
-      umma_commit(bar(B_DRAIN_P));
-      mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
+      if (ok) commit_one(bar(B_V_EMPTY));
     }
+    commit_one(bar(B_DRAIN_P));
+    mbar_wait_drain(bar(B_DRAIN_P), 0, p.status);
   } else if (warp == kGrad) {
-    if (lane == 0) {
-      // dV += P^T dO half by half as each half's P^T is written, then dK +=
-      // dS^T Q; both operands lie in region it & 1, free once both are done.
-      // (P^T of the next tile may be written before this thread has seen this
-      // one's, hence a barrier per region: the tile after next needs R_FREE.)
-      constexpr uint32_t id_g = idesc_bf16(128, 128, 0, 1);  // A from TMEM, B MN-major
-      auto issue_grad = [&](int it, bool more, int tm_a, uint32_t b, int tm_d, int kk0, int kk1) {
-        for (int kk = kk0; kk < kk1; ++kk) {
-          // queries 16 kk .. 16 kk + 15: compute group kk / 2 wrote them at
-          // its own 32-column slice
-          const uint32_t a = tmem + TM_R + (it & 1) * 128 + tm_a + (kk >> 1) * 32 + (kk & 1) * 8;
-          umma_bf16_ts(tmem + tm_d, a, sdesc_sw128(b + kk * 2048, kHalf, 1024), id_g, (more || kk > 0) ? 1u : 0u);
-        }
-      };
-      // An item's first product waits until all compute warps have read the
-      // last item's sums (P^T of a half comes from half of them).
-      bool ok = true;
-      int it = 0;
-      for (int n = 0; ok; ++n) {
-        if (!(ok = mbar_wait(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
-        const int i = items[n % kItemSlots];
-        if (i >= n_items) break;
-        const int n_it = KeyItem(i, p).tiles() * p.g;
-        const int begin = it;
-        if (!(ok = mbar_spin(bar(B_DKV_READ), (n & 1) ^ 1, w))) break;
-        for (const int end = it + n_it; ok && it < end; ++it) {
-          const uint32_t bdo = sb + OFF_DO + it % kDoStages * kTile;
-          for (int hf = 0; hf < 2; ++hf) {
-            if (!(ok = mbar_spin(bar(B_P_FULL + 2 * (it & 1) + hf), (it >> 1) & 1, w))) break;
-            tc_fence_after();
-            issue_grad(it, it > begin, TM_P, bdo, TM_DV, 4 * hf, 4 * hf + 4);
-          }
-          if (!ok) break;
-          umma_commit(bar(B_DO_EMPTY + it % kDoStages));
-          if (!(ok = mbar_spin(bar(B_DS_FULL), it & 1, w))) break;
-          tc_fence_after();
-          issue_grad(it, it > begin, TM_DS, sb + OFF_Q + it % kQStages * kTile, TM_DK, 0, 8);
-          umma_commit(bar(B_R_FREE));
-          umma_commit(bar(B_Q_EMPTY + it % kQStages));
-        }
-        if (ok) umma_commit(bar(B_DKV_DONE));
+    // dV += P^T dO half by half as each half's P^T is written, then dK +=
+    // dS^T Q; both operands lie in region it & 1, free once both are done.
+    // (P^T of the next tile may be written before this thread has seen this
+    // one's, hence a barrier per region: the tile after next needs R_FREE.)
+    constexpr uint32_t id_g = idesc_bf16(128, 128, 0, 1);  // A from TMEM, B MN-major
+    auto issue_grad = [&](int it, bool more, int tm_a, uint32_t b, int tm_d, int kk0, int kk1) {
+      for (int kk = kk0; kk < kk1; ++kk) {
+        // queries 16 kk .. 16 kk + 15: compute group kk / 2 wrote them at
+        // its own 32-column slice
+        const uint32_t a = tmem + TM_R + (it & 1) * 128 + tm_a + (kk >> 1) * 32 + (kk & 1) * 8;
+        umma_ts_one(tmem + tm_d, a, sdesc_sw128(b + kk * 2048, kHalf, 1024), id_g, (more || kk > 0) ? 1u : 0u);
       }
-      umma_commit(bar(B_DRAIN_G));
-      mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
+    };
+    // An item's first product waits until all compute warps have read the
+    // last item's sums (P^T of a half comes from half of them).
+    bool ok = true;
+    int it = 0;
+    for (int n = 0; ok; ++n) {
+      if (!(ok = warp_wait<false, true>(bar(B_ITEM + n % kItemSlots), (n / kItemSlots) & 1, w))) break;
+      const int i = items[n % kItemSlots];
+      if (i >= n_items) break;
+      const int n_it = KeyItem(i, p).tiles() * p.g;
+      const int begin = it;
+      if (!(ok = warp_wait(bar(B_DKV_READ), (n & 1) ^ 1, w))) break;
+      for (const int end = it + n_it; ok && it < end; ++it) {
+        // (P^T says nothing of dO, which dV reads from shared memory.)
+        if (!(ok = warp_wait(bar(B_DO_FULL + it % kDoStages), (it / kDoStages) & 1, w))) break;
+        const uint32_t bdo = sb + OFF_DO + it % kDoStages * kTile;
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!(ok = warp_wait(bar(B_P_FULL + 2 * (it & 1) + hf), (it >> 1) & 1, w))) break;
+          tc_fence_after();
+          issue_grad(it, it > begin, TM_P, bdo, TM_DV, 4 * hf, 4 * hf + 4);
+        }
+        if (!ok) break;
+        commit_one(bar(B_DO_EMPTY + it % kDoStages));
+        if (!(ok = warp_wait(bar(B_DS_FULL), it & 1, w))) break;
+        tc_fence_after();
+        issue_grad(it, it > begin, TM_DS, sb + OFF_Q + it % kQStages * kTile, TM_DK, 0, 8);
+        commit_one(bar(B_R_FREE));
+        commit_one(bar(B_Q_EMPTY + it % kQStages));
+      }
+      if (ok) commit_one(bar(B_DKV_DONE));
     }
+    commit_one(bar(B_DRAIN_G));
+    mbar_wait_drain(bar(B_DRAIN_G), 0, p.status);
   } else {
     // Compute warps: quadrant (warp & 3) of the key rows, group (warp >> 2)
     // of 32 query columns of each tile.
