@@ -55,7 +55,8 @@ cudaError_t counted(int kind, cudaStream_t st, F&& launch) {
 
 // Runs two launches that read nothing of each other's at once: `side` on the
 // device's second stream (greatest priority, forked from `st` and joined back
-// by events), `own` on `st`.  Both are counted.  UPIPE_OK or an error code.
+// by events), `own` on `st`; both on `st`, one after the other, while another
+// capture holds the second stream.  Both are counted.  UPIPE_OK or an error code.
 using LaunchFn = cudaError_t (*)(void* job, cudaStream_t on);
 int launch_beside(int side_kind, LaunchFn side, int own_kind, LaunchFn own, void* job, cudaStream_t st);
 

@@ -174,6 +174,14 @@ int device_ready(int** status) {
     }
   }
   if (g_dev_state[dev].load(std::memory_order_acquire) < 0) return UPIPE_ERR_UNSUPPORTED_DEVICE;
+  // A thread that has made no runtime call that needs the device (a
+  // framework's autograd thread) has no current context yet, and the driver
+  // call that encodes the tensor maps does not make one.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return UPIPE_ERR_CUDA;
+    bound = dev;
+  }
   *status = g_status_ptr[dev];
   return UPIPE_OK;
 }
@@ -300,6 +308,18 @@ int launch_beside(int side_kind, LaunchFn side, int own_kind, LaunchFn own, void
   std::lock_guard<std::mutex> lock(g_side_mu);
   Side* sd = nullptr;
   if (int e = side_stream(&sd)) return e;
+  // Between the fork of a capturing call and the end of that capture the
+  // second stream belongs to the capture: a call outside it then runs both
+  // launches on its own stream.
+  cudaStreamCaptureStatus mine = cudaStreamCaptureStatusNone, its = cudaStreamCaptureStatusNone;
+  unsigned long long my_id = 0, its_id = 0;
+  UPIPE_CU(cudaStreamGetCaptureInfo(st, &mine, &my_id));
+  UPIPE_CU(cudaStreamGetCaptureInfo(sd->s, &its, &its_id));
+  if (its != cudaStreamCaptureStatusNone && (mine != its || my_id != its_id)) {
+    UPIPE_CU(counted(side_kind, st, [&] { return side(job, st); }));
+    UPIPE_CU(counted(own_kind, st, [&] { return own(job, st); }));
+    return UPIPE_OK;
+  }
   UPIPE_CU(cudaEventRecord(sd->fork, st));
   UPIPE_CU(cudaStreamWaitEvent(sd->s, sd->fork, 0));
   UPIPE_CU(counted(side_kind, sd->s, [&] { return side(job, sd->s); }));

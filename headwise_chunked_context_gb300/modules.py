@@ -1,7 +1,9 @@
 """PyTorch autograd front end of the library: the head-chunked attention
 layer, the sequence-tiled SwiGLU MLP and the tiled LM-head loss as
 ``torch.autograd.Function`` s and ``nn.Module`` s, so that a training loop
-can use them in place of its own attention, MLP and loss.
+can use them in place of its own attention, MLP and loss; and, for a layer
+with projections of its own, what stands between them: rotary positions, the
+norms of queries and keys, and attention with a sliding window and sinks.
 
 Every forward and backward runs the library's kernels through the binding
 (``upipe.py``); nothing here computes.  Weights are held as fp32 master
@@ -124,4 +126,86 @@ class TiledCrossEntropy(torch.nn.Module):
         return _CeFn.apply(h, self.w, labels, self.T)
 
 
-__all__ = ["HeadChunkedAttention", "TiledSwiGLU", "TiledCrossEntropy"]
+# ------------------- rotary positions, query/key norms, windowed attention
+
+def _heads(t):
+    """t, or a copy of it where its heads do not start on 16-byte boundaries
+    or its rows overlap."""
+    t = t.to(torch.bfloat16)
+    row, head, one = t.stride()
+    return t if one == 1 and row > 0 and head > 0 and not ((row | head) & 7 or t.data_ptr() & 15) else t.contiguous()
+
+
+class _RopeFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, rope, pos0, positions):
+        ctx.rope, ctx.pos0, ctx.positions = rope, pos0, positions
+        return upipe.rope_forward(rope, _heads(q), _heads(k), pos0, positions)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        dq, dk = upipe.rope_backward(ctx.rope, _heads(dq), _heads(dk), ctx.pos0, ctx.positions)
+        return dq, dk, None, None, None
+
+
+def rotate(q, k, rope, pos0: int = 0, positions=None):
+    """q [L, H, d] and k [L, Hkv, d] rotated by `rope` (upipe.Rope) to the
+    positions pos0, pos0 + 1, ... or `positions` [L] int32, differentiable."""
+    return _RopeFn.apply(q, k, rope, pos0, positions)
+
+
+class _QKNormRopeFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, rope, eps, pos0, positions):
+        q, k = _heads(q), _heads(k)
+        ctx.save_for_backward(q, k, wq, wk)
+        ctx.args = rope, eps, pos0, positions
+        return upipe.qk_norm_rope_forward(rope, q, k, wq, wk, eps, pos0, positions)
+
+    @staticmethod
+    def backward(ctx, dqo, dko):
+        q, k, wq, wk = ctx.saved_tensors
+        rope, eps, pos0, positions = ctx.args
+        dq, dk, dwq, dwk = upipe.qk_norm_rope_backward(rope, q, k, wq, wk, _heads(dqo), _heads(dko), eps, pos0,
+                                                       positions)
+        return dq, dk, dwq, dwk, None, None, None, None
+
+
+class QKNormRope(torch.nn.Module):
+    """RMS norm of each query and key head (weights wq, wk [d] fp32) and the
+    rotation by `rope` in one pass: (q [L, H, d], k [L, Hkv, d]) bf16 ->
+    (q, k)."""
+
+    def __init__(self, rope, eps: float = 1e-6, device="cuda"):
+        super().__init__()
+        self.rope, self.eps = rope, eps
+        self.wq = torch.nn.Parameter(torch.ones(rope.d, device=device))
+        self.wk = torch.nn.Parameter(torch.ones(rope.d, device=device))
+
+    def forward(self, q, k, pos0: int = 0, positions=None):
+        return _QKNormRopeFn.apply(q, k, self.wq, self.wk, self.rope, self.eps, pos0, positions)
+
+
+class _WindowFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks):
+        q, k, v = (t.to(torch.bfloat16).contiguous() for t in (q, k, v))
+        ctx.cfg = upipe.WindowConfig(L=q.shape[0], H=q.shape[1], Hkv=k.shape[1], window=window, sinks=sinks)
+        o, lse = upipe.window_forward(ctx.cfg, q, k, v)
+        ctx.save_for_backward(q, k, v, o, lse)
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        dq, dk, dv = upipe.window_backward(ctx.cfg, *ctx.saved_tensors, do.to(torch.bfloat16).contiguous())
+        return dq, dk, dv, None, None
+
+
+def window_attention(q, k, v, window: int, sinks: int = 0):
+    """Causal attention in which query i sees key j iff j <= i and (i - j <
+    window or j < sinks): q [L, H, 128], k, v [L, Hkv, 128] -> [L, H, 128],
+    bf16, differentiable."""
+    return _WindowFn.apply(q, k, v, window, sinks)
+
+
+__all__ = ["HeadChunkedAttention", "TiledSwiGLU", "TiledCrossEntropy", "QKNormRope", "rotate", "window_attention"]

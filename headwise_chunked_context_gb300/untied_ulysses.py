@@ -206,20 +206,31 @@ def backward(q, k, v, o, lse, do, H, Hkv, U, core_bwd, group=None):
     return dq, dk, dv
 
 
-def gpu_core():
+def gpu_core(window=None, sinks=0):
     """The attention core of this library as (core_fwd, core_bwd) for
     forward / backward: each call runs upipe_attn_core_fwd / _bwd on the
-    current CUDA device over all the heads it is given (one chunk)."""
+    current CUDA device over all the heads it is given (one chunk), or, with
+    a `window` (and `sinks` first tokens that stay visible), upipe_window_fwd
+    / _bwd: a rank holds whole sequences of its heads, so the mask needs no
+    other rank."""
     from headwise_chunked_context_gb300 import upipe
+
+    if window is None and sinks:
+        raise ValueError("sinks: they need a window")
 
     def cfg(q, k):
         L, h, _ = q.shape
+        if window is not None:
+            return upipe.WindowConfig(L=L, H=h, Hkv=k.shape[1], window=window, sinks=sinks)
         return upipe.Config(L=L, H=h, Hkv=k.shape[1], U=h)
 
+    fwd, bwd = (upipe.core_forward, upipe.core_backward) if window is None else (upipe.window_forward,
+                                                                               upipe.window_backward)
+
     def core_fwd(q, k, v):
-        return upipe.core_forward(cfg(q, k), q, k, v)
+        return fwd(cfg(q, k), q, k, v)
 
     def core_bwd(q, k, v, o, lse, do):
-        return upipe.core_backward(cfg(q, k), q, k, v, o, lse, do)
+        return bwd(cfg(q, k), q, k, v, o, lse, do)
 
     return core_fwd, core_bwd

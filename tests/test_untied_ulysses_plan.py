@@ -158,3 +158,9 @@ def test_plan_and_shards_reject_bad_shapes():
     for H, Hkv, U, P in ((64, 8, 8, 8), (32, 8, 1, 4), (16, 16, 2, 2)):
         owned = [h for c in uu.plan(H, Hkv, U, P) for hs in c.q_heads for h in hs]
         assert sorted(owned) == list(range(H))
+
+
+def test_gpu_core_refuses_sinks_without_a_window():
+    from headwise_chunked_context_gb300 import untied_ulysses
+    with pytest.raises(ValueError, match="window"):
+        untied_ulysses.gpu_core(sinks=4)
