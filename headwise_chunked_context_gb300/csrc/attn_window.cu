@@ -200,14 +200,22 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
 
 // ================================================================= forward
 //
-// One CTA per (head, query tile).  Warp 4 streams Q once and K/V blocks of
-// 128 keys through 3-stage TMA rings; the softmax warps copy Q into TMEM
-// once.  Warp 5 issues S(j) = Q K^T (Q from TMEM) into the TMEM score buffer,
-// warp 6 O += P V (P from TMEM); one thread issues a tcgen05.mma only about
-// every 100 cycles, hence two.  Warps 0-3 own one query row per thread: row
-// maximum and sum are thread-local, P goes to one of two TMEM buffers as
-// packed bf16, and O is rescaled in TMEM only when a row's maximum grows by
-// more than 2^8, which bounds every exponent.
+// One CTA per SM walks (head, query tile) pairs.  Warp 4 streams each tile's Q
+// and the K/V blocks of 128 keys through 3-stage TMA rings; the softmax warps
+// copy Q into TMEM, the next tile's as soon as this one's last scores have
+// been formed.  Warp 5 issues S = Q K^T (Q from TMEM) into the TMEM score
+// buffer, free again as soon as it has been read, warp 6 O += P V (P from one
+// of two TMEM buffers).  Warps 0-3 own one query row per thread, so that row
+// maximum and sum are thread-local; O is rescaled in TMEM only when a row's
+// maximum grows by more than 2^8, which bounds every exponent.
+//
+// Measured (burst clocks): 32768 tokens, 32 heads, window 4096: 1.46 ms, 870
+// ns per 128 x 128 block (1024 cycles of products at 2 GHz are 512), the same
+// as the full causal kernel's 800 plus the masked blocks and the tiles' seams;
+// products and copies alone take 540 ns.  What bounds it is the chain scores
+// -> softmax -> P of the one warp per scheduler: two softmax groups that take
+// the blocks in turn were 1 to 4 % faster with long windows and 3 to 20 %
+// slower with short ones, because they share one running maximum and one P.
 
 namespace wf {
 constexpr int kTile = 128 * 128 * 2;  // [128][128] bf16, stored as two 64-column halves
@@ -647,29 +655,34 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
 // ================================================================ backward
 //
 // Two kernels, in which every sum has one order: dQ by query tiles and dK/dV
-// by key tiles, each recomputing S and dP.
+// by key tiles, each recomputing S and dP (7 products for the gradient's 5: one
+// kernel would need atomic or ordered sums of dQ and more TMEM than there is).
+// Both keep one CTA per SM and take tiles from a counter, so that whichever
+// runs on what the other one leaves idle finishes evenly; which CTA computes a
+// tile changes nothing in its sums.
 
 // The queries' records, and the counters' zeros.  16 lanes per (query, head),
-// 16 bytes of O and of dO each; four such items per group are in flight.
+// 16 bytes of O and of dO each.  A CTA takes 32 queries of one head, so that
+// their records and LSE are runs of memory (97 us for 32768 x 32 heads, 570
+// MB; 111 us with neighbouring heads side by side, whose records lie L * 32
+// bytes apart).
 __global__ void __launch_bounds__(256) window_records_kernel(const __grid_constant__ WinParams p,
                                                              __nv_bfloat16* __restrict__ rec) {
-  constexpr int U = 4;
-  const int64_t items = static_cast<int64_t>(p.L) * p.H;
+  constexpr int U = 2;
   const int sub = threadIdx.x & 15;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * 16 * U + (threadIdx.x >> 4);
+  const int h = static_cast<int>(blockIdx.x) % p.H;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.H) * 16 * U + (threadIdx.x >> 4);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.next_tile = *p.next_item = 0;
   uint4 o[U], g[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t i = base + u * 16;
+    const int64_t i = (row0 + u * 16) * p.H + h;
     o[u] = g[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (i < items) {
+    if (row0 + u * 16 < p.L) {
       o[u] = ld_global_nc_v4(p.o + i * kHeadDim + sub * 8);
       g[u] = ld_global_nc_v4(p.dout + i * kHeadDim + sub * 8);
     }
   }
-  int64_t row = base / p.H;
-  int h = static_cast<int>(base - row * p.H);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t ov[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, gv[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
@@ -681,6 +694,7 @@ __global__ void __launch_bounds__(256) window_records_kernel(const __grid_consta
     }
 #pragma unroll
     for (int x = 8; x > 0; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
+    const int64_t row = row0 + u * 16;
     if (sub < 2 && row < p.L) {
       const int64_t at = static_cast<int64_t>(h) * p.L + row;
       uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -701,14 +715,17 @@ __global__ void __launch_bounds__(256) window_records_kernel(const __grid_consta
       }
       st_global_v4(rec + at * 16 + sub * 8, w[0], w[1], w[2], w[3]);
     }
-    h += 16;
-    while (h >= p.H) {
-      h -= p.H;
-      ++row;
-    }
   }
 }
 
+// dQ: S = Q K^T into one of two TMEM buffers, dP = dO V^T into one that is free
+// once read; the compute warps write dS, packed bf16, over the S columns they
+// have read, and dQ += dS K takes it from there.  K is held until dQ (three
+// stages), V until dP (two).  The next tile's Q and dO are loaded, and its
+// first products formed, under this tile's last dQ product and epilogue.
+// 32768 tokens, 32 heads, window 4096: 1.7 ms, 1.0 us per block, 79 % of the
+// tensor rate; S and dP read both operands from shared memory, which alone
+// takes 107 cycles per 64-cycle product step.
 namespace wq {
 constexpr int kComputeWarps = 8;
 constexpr int kProducerWarp = 8;
@@ -1095,6 +1112,22 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
 }
 
 
+// dK and dV: a key tile's K and V stay in shared memory while the query tiles
+// of the heads that read it stream by.  TMEM holds dV, dK and two regions of
+// 128 columns that swap roles every tile:
+//   region i & 1:  S^T(i), then P^T(i) and dS^T(i), packed side by side
+//   the other one: dP^T(i), then, once that has been read, S^T(i + 1)
+// so that the next S^T is formed under this tile's dS^T, dV and dK, and only
+// dS^T -> dK -> next dP^T is a chain.  The scores come with -LSE sqrt(d)
+// already added and dP^T with -Delta: a K = 16 product step of ones with the
+// queries' records, in which each fp32 value is the sum of three bf16 (exact
+// to 2^-24 of it); the keys are the rows here, and each warp would otherwise
+// have to broadcast every query's two values by shuffle.
+// 32768 tokens, 32 heads, window 4096: 2.8 to 2.9 ms, 1.7 us per tile, 69 %
+// of the tensor rate (2.95 with one region for each of S^T and dP^T and the
+// shuffles).  Leaving out 7 of 8 steps of one product takes 15 % (S^T), 10 %
+// (dK), 7 % (dV) or 3 % (dP^T) off, the exponentials 1 %: the products' queue
+// bounds it.
 namespace wkv {
 constexpr int kTile = 128 * 128 * 2;  // K, V, Q or dO tile: [128 rows][128 d]
 constexpr int kHalf = kTile / 2;
@@ -1664,8 +1697,7 @@ cudaError_t launch_window_dkdv(const CUtensorMap& q, const CUtensorMap& k, const
 }
 
 cudaError_t launch_window_records(const WinParams& p, __nv_bfloat16* rec, cudaStream_t st) {
-  const int64_t items = static_cast<int64_t>(p.L) * p.H;
-  window_records_kernel<<<static_cast<unsigned>((items + 63) / 64), 256, 0, st>>>(p, rec);
+  window_records_kernel<<<static_cast<unsigned>((static_cast<int64_t>(p.L) + 31) / 32 * p.H), 256, 0, st>>>(p, rec);
   return cudaGetLastError();
 }
 
