@@ -107,9 +107,10 @@ struct KeyItem {
       q1 = q0 + p.far_chunk;
     } else {
       kb = item - far_items;
-      slot = kb < p.sink_tiles && p.far_slots ? 0 : -1;
+      slot = kb < p.sink_tiles ? 0 : -1;
       q0 = kb;
-      q1 = kb + p.near_tiles;
+      // unless other CTAs have them, a sink tile's later queries are its own
+      q1 = slot < 0 && kb * 128 < p.sinks ? tiles : kb + p.near_tiles;
     }
     q1 = q1 < tiles ? q1 : tiles;
   }
@@ -1638,7 +1639,11 @@ SinkPlan sink_plan(const WinShape& s) {
   if (f.tiles > far) f.tiles = static_cast<int>(far);  // key tiles that have queries past their window
   const int64_t all = static_cast<int64_t>(s.Hkv) * (static_cast<int64_t>(s.m_tiles) * f.near + far * f.tiles);
   const int64_t chunk = (all + 2 * 152 - 1) / (2 * 152);
-  f.chunk = static_cast<int>(chunk < far ? chunk : far);
+  if (chunk >= far) {  // one CTA has them done in time
+    f.tiles = 0;
+    return f;
+  }
+  f.chunk = static_cast<int>(chunk);
   f.slots = static_cast<int>((far + f.chunk - 1) / f.chunk);
   f.bytes = static_cast<size_t>(s.Hkv) * f.tiles * (f.slots + 1) * 2 * f.rows * kHeadDim * sizeof(float);
   return f;

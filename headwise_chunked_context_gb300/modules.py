@@ -15,6 +15,7 @@ sums.  Activations are bf16 CUDA tensors.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from headwise_chunked_context_gb300 import upipe
 
@@ -143,6 +144,7 @@ class _RopeFn(torch.autograd.Function):
         return upipe.rope_forward(rope, _heads(q), _heads(k), pos0, positions)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         dq, dk = upipe.rope_backward(ctx.rope, _heads(dq), _heads(dk), ctx.pos0, ctx.positions)
         return dq, dk, None, None, None
@@ -163,6 +165,7 @@ class _QKNormRopeFn(torch.autograd.Function):
         return upipe.qk_norm_rope_forward(rope, q, k, wq, wk, eps, pos0, positions)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dqo, dko):
         q, k, wq, wk = ctx.saved_tensors
         rope, eps, pos0, positions = ctx.args
@@ -196,6 +199,7 @@ class _WindowFn(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         dq, dk, dv = upipe.window_backward(ctx.cfg, *ctx.saved_tensors, do.to(torch.bfloat16).contiguous())
         return dq, dk, dv, None, None

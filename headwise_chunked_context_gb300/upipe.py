@@ -160,7 +160,13 @@ class WindowConfig:
     d: int = 128
 
     def __post_init__(self):
+        for n in ("L", "window", "sinks"):
+            if not -(1 << 63) <= getattr(self, n) < 1 << 63:
+                raise ValueError(f"{n}: {getattr(self, n)} is past 64 bits")
         object.__setattr__(self, "ref", ctypes.byref(self.c()))
+
+    def __reduce__(self):  # copies and pickles by value: `ref` is an address
+        return WindowConfig, (self.L, self.H, self.Hkv, self.window, self.sinks, self.d)
 
     def c(self) -> WinCfg:
         return WinCfg(self.L, self.window, self.sinks, self.H, self.Hkv, self.d)
@@ -756,6 +762,13 @@ class Rope:
                "upipe_rope_init")
         self._ref = ctypes.byref(self.table)
 
+    def __reduce__(self):  # copies and pickles by value: `_ref` is an address
+        return _rope_of, (self.d, self.rot, self.layout, self.magnitude, self.freqs)
+
+
+def _rope_of(d, rot, layout, magnitude, freqs):
+    return Rope(d, rot, layout, magnitude=magnitude, freqs=freqs)
+
 
 def _rows(t, L, heads, d, name, device):
     """A bf16 [L, heads, d] tensor, its rows and heads at any stride that
@@ -798,6 +811,8 @@ def _qk_call(q, k, pos0, positions, eps):
             raise ValueError("k: expected a [L, heads, d] tensor")
         Hkv = k.shape[1]
     at = None
+    if not -(1 << 62) < pos0 < 1 << 62:
+        raise ValueError(f"pos0: {pos0} is past 62 bits")
     if positions is not None:
         if pos0:
             raise ValueError("pos0 and positions: give one of them")

@@ -94,6 +94,18 @@ def test_functions_equal_the_binding():
     status_ok()
 
 
+def test_module_copies_and_second_derivatives_are_refused():
+    import copy
+    m = QKNormRope(upipe.Rope(D128, rot=64))
+    qkv = _qkv(40, 2, 1, 8)
+    a, b = m(qkv[:, :2], qkv[:, 2:3]), copy.deepcopy(m)(qkv[:, :2], qkv[:, 2:3])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    q, k, v = (t.contiguous().requires_grad_() for t in (qkv[:, :2], qkv[:, 2:3], qkv[:, 3:]))
+    g = torch.autograd.grad(window_attention(q, k, v, 9, 1).float().square().sum(), q, create_graph=True)[0]
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.float().sum().backward()
+
+
 def test_calls_from_a_thread_that_has_touched_no_device():
     """A fresh host thread has no current context; the library makes it
     current (autograd runs backwards on such threads)."""

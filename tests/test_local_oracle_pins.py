@@ -266,3 +266,37 @@ def test_window_binding_refuses_before_any_launch(lib):
     with pytest.raises(ValueError, match="CUDA"):
         upipe.window_fwd(cfg, q, k, k, q, lse)
     assert upipe.launch_count() == n0
+
+
+def test_copies_and_pickles_keep_the_tables(lib):
+    import copy
+    import pickle
+    r = upipe.Rope(128, rot=64, layout="interleaved", scaling=("bands", 8.0, 1.0, 4.0, 8192), magnitude=1.25)
+    c = upipe.WindowConfig(L=64, H=4, Hkv=2, window=9, sinks=1)
+    for f in (copy.deepcopy, copy.copy, lambda x: pickle.loads(pickle.dumps(x))):
+        q = f(r)
+        assert bytes(q.table) == bytes(r.table) and q.freqs == r.freqs and q.layout == r.layout
+        assert f(c) == c and upipe.window_workspace_bytes(f(c)) == upipe.window_workspace_bytes(c)
+
+
+def test_numbers_past_the_librarys_integers_are_refused(lib):
+    q = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
+    for bad in (1 << 62, -(1 << 62), 1 << 70):
+        with pytest.raises(ValueError, match="pos0"):
+            upipe.rope_apply(upipe.Rope(128), q, None, q, None, pos0=bad)
+    with pytest.raises(ValueError, match="window"):
+        upipe.WindowConfig(L=64, H=4, Hkv=2, window=1 << 63)
+    with pytest.raises(ValueError, match="sinks"):
+        upipe.WindowConfig(L=64, H=4, Hkv=2, window=4, sinks=1 << 64)
+
+
+def test_window_workspace_shares_of_sinks(lib):
+    """32 bytes per query and head, 128 of counters, and fp32 shares of the
+    sinks' dK and dV only where later queries are cut into chunks."""
+    need = lambda **kw: upipe.window_workspace_bytes(upipe.WindowConfig(**kw))  # noqa: E731
+    assert need(L=32768, H=32, Hkv=8, window=4096) == 128 + 32768 * 32 * 32
+    # the first tile's 223 later query tiles are less than half of what an SM gets: no cut
+    assert need(L=32768, H=32, Hkv=8, window=4096, sinks=4) == 128 + 32768 * 32 * 32
+    # 1015 later tiles; (1024 * 9 + 1015) / 304 -> chunks of 34, 30 shares and the tile's own, 16 rows each
+    assert need(L=131072, H=8, Hkv=1, window=1024, sinks=16) == 128 + 131072 * 8 * 32 + 31 * 2 * 16 * 128 * 4
+    assert need(L=131072, H=8, Hkv=1, window=131072, sinks=16) == 128 + 131072 * 8 * 32
