@@ -63,7 +63,8 @@
  *    kernel runs on `stream`.  All of a call's work is still ordered after
  *    the work enqueued on `stream` before it, and work enqueued on `stream`
  *    after it waits for all of it.  Make the first backward call on each
- *    device outside stream capture.
+ *    device outside stream capture.  (While a capture holds that stream, a
+ *    call outside the capture runs both kernels on `stream`.)
  *  - The activation-offload calls below use two more library-owned streams
  *    per device (copies to and from the host), created on their first use.
  *  - Entry points may be called from several host threads (calls that share
@@ -473,7 +474,9 @@ int upipe_qk_norm_rope_bwd(const upipe_rope* r, const upipe_qk_cfg* c, const upi
  *   L, H, Hkv, d   as upipe_cfg          window >= 1 (>= L: the full causal
  *   mask)                                sinks  >= 0
  * Work and time grow with L (window + sinks), not with L^2.  q, k, v and
- * dout_o have to be finite: a tile multiplies hidden keys by zero.         */
+ * dout_o have to be finite: a tile multiplies hidden keys by zero, and an
+ * infinity or NaN in one of them reaches every row of the tiles that read it.
+ * Outputs must not overlap inputs or each other.                           */
 typedef struct upipe_window_cfg {
   int64_t L;
   int64_t window;
