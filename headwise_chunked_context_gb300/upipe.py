@@ -164,6 +164,7 @@ class WindowConfig:
             if not -(1 << 63) <= getattr(self, n) < 1 << 63:
                 raise ValueError(f"{n}: {getattr(self, n)} is past 64 bits")
         object.__setattr__(self, "ref", ctypes.byref(self.c()))
+        object.__setattr__(self, "need", None)  # workspace bytes, once asked for
 
     def __reduce__(self):  # copies and pickles by value: `ref` is an address
         return WindowConfig, (self.L, self.H, self.Hkv, self.window, self.sinks, self.d)
@@ -756,11 +757,16 @@ class Rope:
             if len(freqs) != n:
                 raise ValueError(f"freqs: expected {n}, got {len(freqs)}")
             f[:n] = freqs
-        self.freqs = tuple(f[:n])
+        self._f = f
         self.table = RopeTable()
         _check(lib().upipe_rope_init(ctypes.byref(self.table), d, self.rot, ROPE_LAYOUTS[layout], self.magnitude, f),
                "upipe_rope_init")
         self._ref = ctypes.byref(self.table)
+
+    @property
+    def freqs(self):
+        """Radians per position of each pair."""
+        return tuple(self._f[:self.rot // 2])
 
     def __reduce__(self):  # copies and pickles by value: `_ref` is an address
         return _rope_of, (self.d, self.rot, self.layout, self.magnitude, self.freqs)
@@ -926,40 +932,45 @@ def qk_norm_rope_backward(rope: Rope, q, k, wq, wk, dqo, dko, eps: float = 1e-6,
 # ---------------------------------- attention with a window and sink tokens
 
 def window_workspace_bytes(cfg: WindowConfig) -> int:
-    return int(lib().upipe_window_workspace_bytes(cfg.ref))
+    if cfg.need is None:
+        object.__setattr__(cfg, "need", int(lib().upipe_window_workspace_bytes(cfg.ref)))
+    return cfg.need
 
 
 def window_fwd(cfg: WindowConfig, q, k, v, o, lse, stream=None):
     """upipe_window_fwd: tensors as attn_core_fwd."""
-    p = _window_tensors(cfg, (("q", q, cfg.H), ("k", k, cfg.Hkv), ("v", v, cfg.Hkv), ("o", o, cfg.H)), lse)
-    _check(lib().upipe_window_fwd(cfg.ref, *p, _raw(stream, q.get_device())), "upipe_window_fwd")
+    H, Hkv = cfg.H, cfg.Hkv
+    dev = _window_tensors(cfg, lse, (q, H, "q"), (k, Hkv, "k"), (v, Hkv, "v"), (o, H, "o"))
+    _check(lib().upipe_window_fwd(cfg.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                  _raw(stream, dev)), "upipe_window_fwd")
 
 
 def window_bwd(cfg: WindowConfig, q, k, v, o, lse, do, dq, dk, dv, ws=None, stream=None):
     """upipe_window_bwd: tensors as attn_core_bwd."""
     H, Hkv = cfg.H, cfg.Hkv
-    *p, l = _window_tensors(cfg, (("q", q, H), ("k", k, Hkv), ("v", v, Hkv), ("o", o, H), ("dout_o", do, H),
-                                  ("dq", dq, H), ("dk", dk, Hkv), ("dv", dv, Hkv)), lse)
-    f = lib()
-    ws, nbytes = _call_ws(f.upipe_window_workspace_bytes(cfg.ref), ws, q.device, stream)
-    _check(f.upipe_window_bwd(cfg.ref, *p[:4], l, *p[4:], ws.data_ptr(), nbytes, _raw(stream, q.get_device())),
-           "upipe_window_bwd")
+    dev = _window_tensors(cfg, lse, (q, H, "q"), (k, Hkv, "k"), (v, Hkv, "v"), (o, H, "o"), (do, H, "dout_o"),
+                          (dq, H, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv"))
+    ws, nbytes = _call_ws(window_workspace_bytes(cfg), ws, q.device, stream)
+    _check(lib().upipe_window_bwd(cfg.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                  do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), nbytes,
+                                  _raw(stream, dev)), "upipe_window_bwd")
 
 
-def _window_tensors(cfg, heads, lse):
-    """Addresses of the [L, n, 128] bf16 tensors of one call, then of lse,
-    checked as _core_tensors and _on_device do."""
-    L, got = cfg.L, []
-    for name, t, n in heads:
-        if t is None or t.dtype != torch.bfloat16 or t.shape != (L, n, 128):
-            _expect(t, (L, n, 128), torch.bfloat16, name)
-        got.append(t.data_ptr())
-    _expect(lse, (cfg.H, L), torch.float32, "lse")
-    dev = _here(heads[0][1], heads[0][0])
-    for name, t, _ in (*heads, ("lse", lse, 0)):
-        if t.get_device() != dev or not t.is_contiguous():
-            _on_device(**{name: t})
-    return *got, lse.data_ptr()
+def _window_tensors(cfg, lse, *heads):
+    """Checks the [L, n, 128] bf16 tensors of one call and lse; their device."""
+    L, bf16 = cfg.L, torch.bfloat16
+    dev = heads[0][0].get_device() if heads[0][0] is not None else -1
+    ok = dev >= 0 and dev == torch.cuda.current_device()
+    for t, n, _ in heads:
+        ok = (ok and t is not None and t.dtype == bf16 and t.shape == (L, n, 128) and t.get_device() == dev
+              and t.is_contiguous())
+    if not (ok and lse is not None and lse.dtype == torch.float32 and lse.shape == (cfg.H, L)
+            and lse.get_device() == dev and lse.is_contiguous()):
+        for t, n, name in heads:  # says which one, shapes first, as the core's calls do
+            _expect(t, (L, n, 128), bf16, name)
+        _expect(lse, (cfg.H, L), torch.float32, "lse")
+        _on_device(**{name: t for t, _, name in heads}, lse=lse)
+    return dev
 
 
 def window_forward(cfg: WindowConfig, q, k, v):
