@@ -130,23 +130,31 @@ class TiledCrossEntropy(torch.nn.Module):
 # ------------------- rotary positions, query/key norms, windowed attention
 
 def _heads(t):
-    """t, or a copy of it where its heads do not start on 16-byte boundaries
-    or its rows overlap."""
+    """t in bf16, copied where its heads do not start on 16-byte boundaries or
+    its rows are one (a broadcast)."""
     t = t.to(torch.bfloat16)
-    row, head, one = t.stride()
-    return t if one == 1 and row > 0 and head > 0 and not ((row | head) & 7 or t.data_ptr() & 15) else t.contiguous()
+    *outer, one = t.stride()
+    fits = one == 1 and t.data_ptr() % 16 == 0 and all(n == 1 or s > 0 and s % 8 == 0 for n, s in zip(t.shape, outer))
+    return t if fits else t.clone(memory_format=torch.contiguous_format)
+
+
+def _dense(t):
+    """t in bf16, copied where it is not dense from a 16-byte boundary on."""
+    t = t.to(torch.bfloat16)
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
 class _RopeFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, rope, pos0, positions):
-        ctx.rope, ctx.pos0, ctx.positions = rope, pos0, positions
+        ctx.save_for_backward(positions)  # which also sees to it that they are the forward's
+        ctx.rope, ctx.pos0 = rope, pos0
         return upipe.rope_forward(rope, _heads(q), _heads(k), pos0, positions)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
-        dq, dk = upipe.rope_backward(ctx.rope, _heads(dq), _heads(dk), ctx.pos0, ctx.positions)
+        dq, dk = upipe.rope_backward(ctx.rope, _heads(dq), _heads(dk), ctx.pos0, *ctx.saved_tensors)
         return dq, dk, None, None, None
 
 
@@ -160,15 +168,15 @@ class _QKNormRopeFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, wq, wk, rope, eps, pos0, positions):
         q, k = _heads(q), _heads(k)
-        ctx.save_for_backward(q, k, wq, wk)
-        ctx.args = rope, eps, pos0, positions
+        ctx.save_for_backward(q, k, wq, wk, positions)
+        ctx.args = rope, eps, pos0
         return upipe.qk_norm_rope_forward(rope, q, k, wq, wk, eps, pos0, positions)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dqo, dko):
-        q, k, wq, wk = ctx.saved_tensors
-        rope, eps, pos0, positions = ctx.args
+        q, k, wq, wk, positions = ctx.saved_tensors
+        rope, eps, pos0 = ctx.args
         dq, dk, dwq, dwk = upipe.qk_norm_rope_backward(rope, q, k, wq, wk, _heads(dqo), _heads(dko), eps, pos0,
                                                        positions)
         return dq, dk, dwq, dwk, None, None, None, None
@@ -192,7 +200,7 @@ class QKNormRope(torch.nn.Module):
 class _WindowFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, window, sinks):
-        q, k, v = (t.to(torch.bfloat16).contiguous() for t in (q, k, v))
+        q, k, v = _dense(q), _dense(k), _dense(v)
         ctx.cfg = upipe.WindowConfig(L=q.shape[0], H=q.shape[1], Hkv=k.shape[1], window=window, sinks=sinks)
         o, lse = upipe.window_forward(ctx.cfg, q, k, v)
         ctx.save_for_backward(q, k, v, o, lse)
@@ -201,7 +209,7 @@ class _WindowFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, do):
-        dq, dk, dv = upipe.window_backward(ctx.cfg, *ctx.saved_tensors, do.to(torch.bfloat16).contiguous())
+        dq, dk, dv = upipe.window_backward(ctx.cfg, *ctx.saved_tensors, _dense(do))
         return dq, dk, dv, None, None
 
 

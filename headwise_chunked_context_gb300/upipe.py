@@ -163,6 +163,9 @@ class WindowConfig:
         for n in ("L", "window", "sinks"):
             if not -(1 << 63) <= getattr(self, n) < 1 << 63:
                 raise ValueError(f"{n}: {getattr(self, n)} is past 64 bits")
+        for n in ("H", "Hkv", "d"):
+            if not -(1 << 31) <= getattr(self, n) < 1 << 31:
+                raise ValueError(f"{n}: {getattr(self, n)} is past 32 bits")
         object.__setattr__(self, "ref", ctypes.byref(self.c()))
         object.__setattr__(self, "need", None)  # workspace bytes, once asked for
 
@@ -783,6 +786,10 @@ def _rows(t, L, heads, d, name, device):
         _expect(t, (L, heads, d), torch.bfloat16, name)
     row, head, one = t.stride()
     p = t.data_ptr()
+    if L == 1:  # the stride of an axis of one says nothing
+        row = 0
+    if heads == 1:
+        head = 0
     if one != 1 or (row | head) & 7 or p & 15:
         raise ValueError(f"{name}: expected heads of contiguous elements on 16-byte boundaries, got strides "
                          f"{(row, head, one)} at {p:#x}")
@@ -817,6 +824,8 @@ def _qk_call(q, k, pos0, positions, eps):
             raise ValueError("k: expected a [L, heads, d] tensor")
         Hkv = k.shape[1]
     at = None
+    if H > 65536 or Hkv > 65536:
+        raise ValueError(f"q, k: at most 65536 heads, got {H} and {Hkv}")
     if not -(1 << 62) < pos0 < 1 << 62:
         raise ValueError(f"pos0: {pos0} is past 62 bits")
     if positions is not None:

@@ -94,6 +94,50 @@ def test_functions_equal_the_binding():
     status_ok()
 
 
+def test_tensors_off_16_byte_boundaries_are_copied():
+    """Dense, but one element into their storage, as gradients that come out
+    of a concatenation are; and one token of rows whose length is no multiple
+    of 8."""
+    L, H, Hkv = 130, 4, 2
+
+    def off(t):
+        x = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        return x.copy_(t)
+
+    rope, qkv, do = upipe.Rope(D128), _qkv(L, H, Hkv, 4), _qkv(L, H, 0, 5)
+    parts = [t.contiguous() for t in (qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:])]
+    results = []
+    for place in (torch.clone, off):
+        q, k, v = (place(t).requires_grad_() for t in parts)
+        m = QKNormRope(rope)
+        a, b = m(q, k)
+        o = window_attention(*(place(t) for t in rotate(a, b, rope, pos0=2)), place(v), 50, 3)
+        o.backward(place(do))
+        a, b = m(q, k)
+        torch.autograd.backward(rotate(a, b, rope), (place(do), place(parts[1])))
+        results.append((o, q.grad, k.grad, v.grad, m.wq.grad, m.wk.grad))
+    assert off(parts[0]).data_ptr() % 16 and off(parts[0]).is_contiguous()
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+    row = _qkv(1, 2, 0, 6).view(1, 256)
+    x = torch.cat([row, row[:, :4]], 1).as_strided((1, 2, D128), (260, D128, 1))
+    assert x.stride(0) % 8
+    y, z = rotate(x, x, rope, pos0=7)
+    assert torch.equal(y, rotate(row.view(1, 2, D128), row.view(1, 2, D128), rope, pos0=7)[0]) and torch.equal(y, z)
+    status_ok()
+
+
+def test_positions_changed_between_forward_and_backward_are_noticed():
+    q, k = _qkv(8, 2, 0).requires_grad_(), _qkv(8, 1, 0).requires_grad_()
+    rope = upipe.Rope(D128)
+    for f in (lambda pos: rotate(q, k, rope, positions=pos), lambda pos: QKNormRope(rope)(q, k, positions=pos)):
+        pos = torch.arange(8, dtype=torch.int32, device="cuda")
+        y, _ = f(pos)
+        pos += 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.float().sum().backward()
+    status_ok()
+
+
 def test_module_copies_and_second_derivatives_are_refused():
     import copy
     m = QKNormRope(upipe.Rope(D128, rot=64))

@@ -300,3 +300,26 @@ def test_window_workspace_shares_of_sinks(lib):
     # 1015 later tiles; (1024 * 9 + 1015) / 304 -> chunks of 34, 30 shares and the tile's own, 16 rows each
     assert need(L=131072, H=8, Hkv=1, window=1024, sinks=16) == 128 + 131072 * 8 * 32 + 31 * 2 * 16 * 128 * 4
     assert need(L=131072, H=8, Hkv=1, window=131072, sinks=16) == 128 + 131072 * 8 * 32
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """A C int of (1 << 32) + n is n."""
+    for kw in (dict(H=(1 << 32) + 4), dict(Hkv=(1 << 32) + 2), dict(d=(1 << 32) + 128)):
+        with pytest.raises(ValueError, match="32 bits"):
+            upipe.WindowConfig(**{**dict(L=64, H=4, Hkv=2, window=4), **kw})
+    q = torch.zeros(1, 1, 8, dtype=torch.bfloat16)
+    for bad in (q.expand(1, (1 << 32) + 1, 8), q.expand(1, 65537, 8)):
+        with pytest.raises(ValueError, match="heads"):
+            upipe.rope_apply(upipe.Rope(8), bad, None, bad, None)
+
+
+def test_strides_of_axes_of_one_say_nothing(lib):
+    """One token of rows of 100 elements, one head of such rows: what would be
+    the strides of a second token or head are no multiples of 8."""
+    x = torch.zeros(1, 108, dtype=torch.bfloat16)
+    for t, L in ((x[:, :72].unsqueeze(1), 1), (torch.zeros(3, 72, dtype=torch.bfloat16).as_strided((3, 1, 72), (72, 100, 1)), 3)):
+        assert max(t.stride()) % 8
+        rows = upipe._rows(t, L, 1, 72, "q", -1)._obj
+        assert rows.p == t.data_ptr() and rows.row % 8 == 0 and rows.head % 8 == 0
+    with pytest.raises(ValueError, match="16-byte"):
+        upipe._rows(torch.zeros(2, 108, dtype=torch.bfloat16)[:, :72].unsqueeze(1), 2, 1, 72, "q", -1)
