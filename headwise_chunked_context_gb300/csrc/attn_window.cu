@@ -218,9 +218,12 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
 // ns per 128 x 128 block (1024 cycles of products at 2 GHz are 512), the same
 // as the full causal kernel's 800 plus the masked blocks and the tiles' seams;
 // products and copies alone take 540 ns.  What bounds it is the chain scores
-// -> softmax -> P of the one warp per scheduler: two softmax groups that take
-// the blocks in turn were 1 to 4 % faster with long windows and 3 to 20 %
-// slower with short ones, because they share one running maximum and one P.
+// -> softmax -> P of the one warp per scheduler; hence barriers are probed
+// ahead, under arithmetic and stores (4 % of the time).  Two softmax groups
+// that take the blocks in turn were 1 to 4 % faster with long windows and 3 to
+// 20 % slower with short ones, because they share one running maximum and one
+// P; eight warps with half a block's columns each were 7 % slower: the products'
+// issue holds up the warps of its sub-partition, and the maxima are swapped.
 
 namespace wf {
 constexpr int kTile = 128 * 128 * 2;  // [128][128] bf16, stored as two 64-column halves
@@ -447,6 +450,7 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
       return true;
     };
     bool ok = take_q(0);
+    bool s_there = false;  // the next scores, by a probe made ahead
     int it = 0;
     for (int n = 0, t = tile_of(0); ok && t < n_tiles; t = tile_of(++n)) {
       const int h = head_of(t), qb = block_of(t);
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
       float l = 0.f;
       for (int j = 0; j < n_kv; ++j, ++it) {
         const int b = it & 1;  // P buffer
-        if (!(ok = warp_wait(bar(B_S_FULL), it & 1, w))) break;
+        if (!__all_sync(0xffffffffu, s_there) && !(ok = warp_wait(bar(B_S_FULL), it & 1, w))) break;
         tc_fence_after();
         const uint32_t tsb = trow + TM_S;
         uint32_t v0[32], v1[32], v2[32], v3[32];
@@ -516,6 +520,8 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
         }
         if (need) m_use = m_new;
 
+        // P buffer b held P(it - 2) until PV(it - 2) completed, long ago as a rule.
+        const bool p_free = it < 2 || mbar_test(bar(B_P_EMPTY + b), ((it >> 1) & 1) ^ 1);
         uint32_t pk0[32], pk1[32];
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
         const uint64_t nmx2 = f2_pack(-m_use, -m_use);
@@ -532,6 +538,13 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
           pk0[c >> 1] = pack_bf16x2(p0, p1);
           pk1[c >> 1] = pack_bf16x2(p2, p3);
         }
+        if (!__all_sync(0xffffffffu, p_free) &&
+            !(ok = warp_wait(bar(B_P_EMPTY + b), ((it >> 1) & 1) ^ 1, w)))
+          break;
+        tc_fence_after();
+        tmem_st32(trow + TM_P + b * 64 + 0, pk0);
+        tmem_st32(trow + TM_P + b * 64 + 32, pk1);
+        // under the stores: the row's sum, and a look at the next scores
         float rs = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -540,13 +553,7 @@ __global__ void __launch_bounds__(wf::kThreads, 1)
           rs += a + b;
         }
         l += rs;
-        // P buffer b held P(it - 2) until PV(it - 2) completed.
-        if (it >= 2) {
-          if (!(ok = warp_wait(bar(B_P_EMPTY + b), ((it >> 1) & 1) ^ 1, w))) break;
-          tc_fence_after();
-        }
-        tmem_st32(trow + TM_P + b * 64 + 0, pk0);
-        tmem_st32(trow + TM_P + b * 64 + 32, pk1);
+        s_there = mbar_test(bar(B_S_FULL), (it & 1) ^ 1);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
