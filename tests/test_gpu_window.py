@@ -196,3 +196,29 @@ def test_window_workspace_refusal():
     with pytest.raises(ValueError, match="ws"):
         upipe.window_bwd(cfg, q, k, v, o, lse, do, q.clone(), k.clone(), v.clone(),
                          ws=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
+
+
+def test_window_outputs_on_16_byte_boundaries_have_the_same_bits():
+    """Outputs 16 bytes past a 32-byte boundary are stored in halves of it;
+    the 16 bytes before and after them stay as they were."""
+    L, H, Hkv = 300, 4, 2
+    q, k, v, do = dev(*synth.core_inputs(L, H, Hkv))
+    cfg = upipe.WindowConfig(L=L, H=H, Hkv=Hkv, window=90, sinks=5)
+    o, lse = upipe.window_forward(cfg, q, k, v)
+    grads = upipe.window_backward(cfg, q, k, v, o, lse, do)
+
+    def off(heads):
+        room = torch.full((L * heads * 128 + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        return room, room[8:-8].view(L, heads, 128)
+
+    rooms, (o2, dq, dk, dv) = zip(*(off(n) for n in (H, H, Hkv, Hkv)))
+    assert all(t.data_ptr() % 32 == 16 for t in (o2, dq, dk, dv))
+    lse2 = torch.empty_like(lse)
+    upipe.window_fwd(cfg, q, k, v, o2, lse2)
+    upipe.window_bwd(cfg, q, k, v, o2, lse2, do, dq, dk, dv)
+    status_ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for a, b in zip(grads, (dq, dk, dv)):
+        assert torch.equal(a, b)
+    for room in rooms:
+        assert (room[:8] == 7).all() and (room[-8:] == 7).all()
