@@ -229,10 +229,10 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
 // maximum and sum are thread-local; O is rescaled in TMEM only when a row's
 // maximum grows by more than 2^8, which bounds every exponent.
 //
-// Measured (burst clocks): 32768 tokens, 32 heads, window 4096: 1.46 ms, 870
-// ns per 128 x 128 block (1024 cycles of products at 2 GHz are 512), the same
-// as the full causal kernel's 800 plus the masked blocks and the tiles' seams;
-// products and copies alone take 540 ns.  What bounds it is the chain scores
+// Measured (burst clocks): 32768 tokens, 32 heads, window 4096: 1.36 ms, 817
+// ns per 128 x 128 block (1024 cycles of products at 2 GHz are 512), 760 with
+// the full causal mask, the rest masked blocks and the tiles' seams; products
+// and copies alone take 540 ns.  What bounds it is the chain scores
 // -> softmax -> P of the one warp per scheduler; hence barriers are probed
 // ahead, under arithmetic and stores (4 % of the time).  Two softmax groups
 // that take the blocks in turn were 1 to 4 % faster with long windows and 3 to
@@ -741,9 +741,10 @@ __global__ void __launch_bounds__(256) window_records_kernel(const __grid_consta
 // have read, and dQ += dS K takes it from there.  K is held until dQ (three
 // stages), V until dP (two).  The next tile's Q and dO are loaded, and its
 // first products formed, under this tile's last dQ product and epilogue.
-// 32768 tokens, 32 heads, window 4096: 1.7 ms, 1.0 us per block, 79 % of the
-// tensor rate; S and dP read both operands from shared memory, which alone
-// takes 107 cycles per 64-cycle product step.
+// 32768 tokens, 32 heads, window 4096: 1.7 ms alone, 1.03 us per block, of
+// which the products by themselves take 0.97 (1536 cycles at 2 GHz are 0.77):
+// S and dP read both operands from shared memory, which alone takes 107 cycles
+// per 64-cycle product step, and TMEM has no room for Q and dO.
 namespace wq {
 constexpr int kComputeWarps = 8;
 constexpr int kProducerWarp = 8;
@@ -1141,11 +1142,10 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
 // queries' records, in which each fp32 value is the sum of three bf16 (exact
 // to 2^-24 of it); the keys are the rows here, and each warp would otherwise
 // have to broadcast every query's two values by shuffle.
-// 32768 tokens, 32 heads, window 4096: 2.8 to 2.9 ms, 1.7 us per tile, 69 %
-// of the tensor rate (2.95 with one region for each of S^T and dP^T and the
-// shuffles).  Leaving out 7 of 8 steps of one product takes 15 % (S^T), 10 %
-// (dK), 7 % (dV) or 3 % (dP^T) off, the exponentials 1 %: the products' queue
-// bounds it.
+// 32768 tokens, 32 heads, window 4096: 2.7 ms alone, 1.62 us per tile, of
+// which the products by themselves take 1.33 (2048 cycles at 2 GHz are 1.02;
+// S^T and dP^T read both operands from shared memory).  With one region for
+// each of S^T and dP^T and the values by shuffles it takes a tenth more.
 namespace wkv {
 constexpr int kTile = 128 * 128 * 2;  // K, V, Q or dO tile: [128 rows][128 d]
 constexpr int kHalf = kTile / 2;
