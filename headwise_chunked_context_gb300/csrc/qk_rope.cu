@@ -157,7 +157,9 @@ struct Raw {
 // shared memory: what is in flight then costs no registers, and one warp
 // keeps S steps of loads open (in registers there was room for one, and a
 // backward of 16 warps per SM ran at 4.4 TB/s).  A lane reads back only what
-// it copied itself, so there is nothing to synchronise.  The scalar path
+// it copied itself, so there is nothing to synchronise but the lane's own
+// copies: two into one slot have no order unless the first has been waited for,
+// so a pipe is drained before the next one takes its ring.  The scalar path
 // holds one step in registers (a copy is four bytes at least).
 template <int PATH, int T, int S>
 struct Pipe {
@@ -190,6 +192,10 @@ struct Pipe {
       asm volatile("cp.async.commit_group;" ::: "memory");
       at = at + 1 == S ? 0 : at + 1;
     }
+  }
+  // Waits for the copies in flight (at the end: zeros for the steps past it).
+  static __device__ __forceinline__ void drain() {
+    if constexpr (PATH != kScalar) asm volatile("cp.async.wait_all;" ::: "memory");
   }
   static constexpr int kAhead = PATH == kScalar ? 1 : S - 1;  // steps to start before the first turn
   // Starts one more step and takes the oldest.
@@ -523,6 +529,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const 
       if (h < nh && ln.live) store<PATH>(p.y[t].p + at.token * p.y[t].row + h * p.y[t].head, ln, a, b);
       at = after(at);
     }
+    pipe.drain();  // the next weight's pipe starts over in the same slots
     // The lanes that hold the same elements of different heads, then the warps.
 #pragma unroll
     for (int i = 0; i < M; ++i) {

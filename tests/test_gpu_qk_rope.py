@@ -257,3 +257,23 @@ def test_workspace_refusals():
     empty = torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
     with pytest.raises((upipe.UpipeError, ValueError)):
         upipe.rope_forward(r, empty)
+
+
+@pytest.mark.parametrize("L,H,Hkv,d,rot,layout", [(1, 1, 1, 128, 128, "half"), (1, 3, 2, 128, 128, "interleaved"),
+                                                  (40, 2, 5, 72, 40, "half"), (700, 1, 9, 128, 64, "half"),
+                                                  (5000, 2, 2, 64, 64, "interleaved"), (30, 3, 3, 128, 34, "half")])
+def test_keys_after_queries_equal_keys_alone(L, H, Hkv, d, rot, layout):
+    """The keys take the copies' ring over from the queries: their gradients
+    have the bits that they have as the queries of a call of their own."""
+    q, k, dq, dk = _randn(21, L, H, d), _randn(22, L, Hkv, d), _randn(23, L, H, d), _randn(24, L, Hkv, d)
+    w = torch.linspace(0.5, 1.5, d, device="cuda")
+    r = upipe.Rope(d, rot=rot, layout=layout)
+    want = upipe.qk_norm_rope_backward(r, k, None, w, None, dk, None, pos0=3)
+    x, dy, f = f64(k), f64(dk), np.array(r.freqs)
+    _, want_w, size = loc.norm_rope_bwd(x, f64(w), 1e-6, dy, np.arange(L) + 3, f, rot, layout)
+    rr = 1 / np.sqrt(np.mean(x * x, -1, keepdims=True) + 1e-6)
+    slack = WEIGHT * (size + np.sum(_pair_size(dy, rot, layout) * np.abs(x) * rr, (0, 1)))
+    for _ in range(20):
+        got = upipe.qk_norm_rope_backward(r, q, k, w, w, dq, dk, pos0=3)
+        assert torch.equal(got[1], want[0])
+        assert np.all(np.abs(f64(got[3]) - want_w) <= slack)

@@ -42,3 +42,19 @@ def test_no_device_trap_or_assert():
         code = re.sub(r"//[^\n]*", "", text)
         assert "__trap" not in code, name
         assert re.search(r"(?<!static_)\bassert\s*\(", code) is None, name
+
+
+def test_a_copy_ring_is_drained_before_it_is_filled_anew():
+    """Two asynchronous copies of one thread into the same shared-memory slot
+    have no order unless the first is waited for.  The backward of the norm
+    walks the queries and then the keys over one ring, and the queries' last
+    steps (zeros past the end) are still open when its loop ends: between that
+    loop and the keys' first copies stands a wait for all of them."""
+    text = _sources()["qk_rope.cu"]
+    body = text[text.index("void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel"):]
+    body = body[:body.index("\n}\n")]
+    assert body.count("Loads pipe(") == 1 and body.index("for (int t = 0; t < 2; ++t)") < body.index("Loads pipe(")
+    turns, ends = body.index("while (at.unit < units)"), body.index("__shfl_xor_sync(0xffffffffu, gu[i]")
+    assert re.search(r"\n    }\n    pipe\.drain\(\);", body[turns:ends])
+    drain = re.search(r"void drain\(\) \{(.*?)\n  \}", text, re.S).group(1)
+    assert "cp.async.wait_all;" in drain
