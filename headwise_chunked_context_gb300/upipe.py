@@ -357,12 +357,23 @@ def choose_u(cfg: Config, budget_bytes: int, pass_: int = 2, core_only: bool = F
     return r
 
 
-def _ws(cfg, pass_, core_only, o_mode, ws, device):
-    need = workspace_bytes(cfg, pass_, core_only, o_mode)
+def _call_ws(need, ws, device, stream):
+    """The caller's workspace, checked, or one made for this call.  That one
+    comes from the memory of the stream that the call runs on: a block of
+    another stream's may have work of that stream still pending on it."""
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if stream is None:
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return ws, ws.numel()
     _expect_ws(ws, need)
     return ws, ws.numel() * ws.element_size()
+
+
+def _ws(cfg, pass_, core_only, o_mode, ws, device, stream):
+    return _call_ws(workspace_bytes(cfg, pass_, core_only, o_mode), ws, device, stream)
 
 
 def _layer_tensors(cfg: Config, x, Wqkv, Wo, lse, o_saved):
@@ -396,7 +407,7 @@ def attn_fwd(cfg: Config, x, Wqkv, Wo, out, lse, o_saved=None, ws=None, stream=N
     _layer_tensors(cfg, x, Wqkv, Wo, lse, o_saved)
     _expect(out, (cfg.L, cfg.D), torch.bfloat16, "out")
     _on_device(x=x, Wqkv=Wqkv, Wo=Wo, out=out, lse=lse, o_saved=o_saved)
-    ws, nbytes = _ws(cfg, 0, False, O_DEVICE if o_saved is not None else O_RECOMPUTE, ws, x.device)
+    ws, nbytes = _ws(cfg, 0, False, O_DEVICE if o_saved is not None else O_RECOMPUTE, ws, x.device, stream)
     c = cfg.c()
     _check(lib().upipe_attn_fwd(ctypes.byref(c), _ptr(x), _ptr(Wqkv), _ptr(Wo), _ptr(out), _ptr(lse),
                                 _ptr(o_saved), _ptr(ws), nbytes, _stream(stream)), "upipe_attn_fwd")
@@ -410,7 +421,7 @@ def attn_bwd(cfg: Config, x, Wqkv, Wo, dout, lse, dx, dWqkv, dWo, o_saved=None, 
     _expect(dWqkv, ((H + 2 * Hkv) * 128, D), torch.float32, "dWqkv")
     _expect(dWo, (D, H * 128), torch.float32, "dWo")
     _on_device(x=x, Wqkv=Wqkv, Wo=Wo, dout=dout, lse=lse, o_saved=o_saved, dx=dx, dWqkv=dWqkv, dWo=dWo)
-    ws, nbytes = _ws(cfg, 1, False, O_DEVICE if o_saved is not None else O_RECOMPUTE, ws, x.device)
+    ws, nbytes = _ws(cfg, 1, False, O_DEVICE if o_saved is not None else O_RECOMPUTE, ws, x.device, stream)
     c = cfg.c()
     _check(lib().upipe_attn_bwd(ctypes.byref(c), _ptr(x), _ptr(Wqkv), _ptr(Wo), _ptr(dout), _ptr(lse),
                                 _ptr(o_saved), _ptr(dx), _ptr(dWqkv), _ptr(dWo), _ptr(ws), nbytes,
@@ -440,7 +451,7 @@ def attn_fwd_host_o(cfg: Config, x, Wqkv, Wo, out, lse, o_host, ws=None, stream=
     _expect(out, (cfg.L, cfg.D), torch.bfloat16, "out")
     oh = _host_o(cfg, o_host)
     _on_device(x=x, Wqkv=Wqkv, Wo=Wo, out=out, lse=lse)
-    ws, nbytes = _ws(cfg, 0, False, O_HOST, ws, x.device)
+    ws, nbytes = _ws(cfg, 0, False, O_HOST, ws, x.device, stream)
     c = cfg.c()
     _check(lib().upipe_attn_fwd_host_o(ctypes.byref(c), _ptr(x), _ptr(Wqkv), _ptr(Wo), _ptr(out), _ptr(lse),
                                        oh, _ptr(ws), nbytes, _stream(stream)), "upipe_attn_fwd_host_o")
@@ -455,7 +466,7 @@ def attn_bwd_host_o(cfg: Config, x, Wqkv, Wo, dout, lse, o_host, dx, dWqkv, dWo,
     _expect(dWo, (D, H * 128), torch.float32, "dWo")
     oh = _host_o(cfg, o_host)
     _on_device(x=x, Wqkv=Wqkv, Wo=Wo, dout=dout, lse=lse, dx=dx, dWqkv=dWqkv, dWo=dWo)
-    ws, nbytes = _ws(cfg, 1, False, O_HOST, ws, x.device)
+    ws, nbytes = _ws(cfg, 1, False, O_HOST, ws, x.device, stream)
     c = cfg.c()
     _check(lib().upipe_attn_bwd_host_o(ctypes.byref(c), _ptr(x), _ptr(Wqkv), _ptr(Wo), _ptr(dout), _ptr(lse),
                                        oh, _ptr(dx), _ptr(dWqkv), _ptr(dWo), _ptr(ws), nbytes,
@@ -468,7 +479,7 @@ def attn_core_fwd(cfg: Config, q, k, v, o, lse, ws=None, stream=None):
     need = workspace_bytes(cfg, 0, True)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     if need and ws is None:
-        ws, nbytes = _ws(cfg, 0, True, False, None, q.device)
+        ws, nbytes = _ws(cfg, 0, True, False, None, q.device, stream)
     _expect_ws(ws, need)
     c = cfg.c()
     _check(lib().upipe_attn_core_fwd(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
@@ -479,7 +490,7 @@ def attn_core_bwd(cfg: Config, q, k, v, o, lse, do, dq, dk, dv, ws=None, stream=
     _core_tensors(cfg, q, k, v, lse, o)
     _core_grads(cfg, do, dq, dk, dv)
     _on_device(q=q, k=k, v=v, o=o, lse=lse, dout_o=do, dq=dq, dk=dk, dv=dv)
-    ws, nbytes = _ws(cfg, 1, True, False, ws, q.device)
+    ws, nbytes = _ws(cfg, 1, True, False, ws, q.device, stream)
     c = cfg.c()
     _check(lib().upipe_attn_core_bwd(ctypes.byref(c), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do),
                                      _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), nbytes, _stream(stream)),
@@ -639,13 +650,6 @@ def ce_workspace_bytes(L: int, D: int, V: int, T: int) -> int:
     return int(lib().upipe_ce_workspace_bytes(ctypes.byref(c)))
 
 
-def _tile_ws(need, ws, device):
-    if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    _expect_ws(ws, need)
-    return ws, ws.numel() * ws.element_size()
-
-
 def mlp_fwd(x, Wgu, Wd, y, T, ws=None, stream=None):
     """upipe_mlp_fwd: x [L, D], Wgu [2F, D] (gate rows, then up rows),
     Wd [D, F], y [L, D] (written), all bf16; T rows per tile."""
@@ -656,7 +660,7 @@ def mlp_fwd(x, Wgu, Wd, y, T, ws=None, stream=None):
     _expect(Wd, (D, F), torch.bfloat16, "Wd")
     _expect(y, (L, D), torch.bfloat16, "y")
     _on_device(x=x, Wgu=Wgu, Wd=Wd, y=y)
-    ws, nbytes = _tile_ws(mlp_workspace_bytes(L, D, F, T, 0), ws, x.device)
+    ws, nbytes = _call_ws(mlp_workspace_bytes(L, D, F, T, 0), ws, x.device, stream)
     c = MlpCfg(L, D, F, T)
     _check(lib().upipe_mlp_fwd(ctypes.byref(c), _ptr(x), _ptr(Wgu), _ptr(Wd), _ptr(y), _ptr(ws), nbytes,
                                _stream(stream)), "upipe_mlp_fwd")
@@ -674,7 +678,7 @@ def mlp_bwd(x, Wgu, Wd, dy, dx, dWgu, dWd, T, ws=None, stream=None):
     _expect(dWgu, (2 * F, D), torch.float32, "dWgu")
     _expect(dWd, (D, F), torch.float32, "dWd")
     _on_device(x=x, Wgu=Wgu, Wd=Wd, dy=dy, dx=dx, dWgu=dWgu, dWd=dWd)
-    ws, nbytes = _tile_ws(mlp_workspace_bytes(L, D, F, T, 1), ws, x.device)
+    ws, nbytes = _call_ws(mlp_workspace_bytes(L, D, F, T, 1), ws, x.device, stream)
     c = MlpCfg(L, D, F, T)
     _check(lib().upipe_mlp_bwd(ctypes.byref(c), _ptr(x), _ptr(Wgu), _ptr(Wd), _ptr(dy), _ptr(dx), _ptr(dWgu),
                                _ptr(dWd), _ptr(ws), nbytes, _stream(stream)), "upipe_mlp_bwd")
@@ -692,7 +696,7 @@ def ce_fwd_bwd(h, W, labels, scale, loss, dh, dW, T, ws=None, stream=None):
     _expect(dh, (L, D), torch.bfloat16, "dh")
     _expect(dW, (V, D), torch.float32, "dW")
     _on_device(h=h, W=W, labels=labels, loss=loss, dh=dh, dW=dW)
-    ws, nbytes = _tile_ws(ce_workspace_bytes(L, D, V, T), ws, h.device)
+    ws, nbytes = _call_ws(ce_workspace_bytes(L, D, V, T), ws, h.device, stream)
     c = CeCfg(L, D, V, T)
     _check(lib().upipe_ce_fwd_bwd(ctypes.byref(c), _ptr(h), _ptr(W), _ptr(labels), float(scale), _ptr(loss),
                                   _ptr(dh), _ptr(dW), _ptr(ws), nbytes, _stream(stream)), "upipe_ce_fwd_bwd")
@@ -891,18 +895,6 @@ def qk_norm_rope_bwd(rope: Rope, q, k, wq, wk, dqo, dko, dq, dk, dwq, dwk, eps: 
     ws, nbytes = _call_ws(f.upipe_qk_norm_rope_workspace_bytes(rope._ref, c), ws, q.device, stream)
     _check(f.upipe_qk_norm_rope_bwd(rope._ref, c, tq[0], tk[0], pq, pk, at, tq[1], tk[1], tq[2], tk[2], gq, gk,
                                     ws.data_ptr(), nbytes, _raw(stream, here)), "upipe_qk_norm_rope_bwd")
-
-
-def _call_ws(need, ws, device, stream):
-    """The caller's workspace, checked, or one made for this call: it belongs
-    to the current stream's memory, so it is told of the stream it is used on."""
-    if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        if stream is not None:
-            ws.record_stream(stream)
-        return ws, ws.numel()
-    _expect_ws(ws, need)
-    return ws, ws.numel() * ws.element_size()
 
 
 def _like(t):
