@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const 
           qs += q2;
           ds += d2;
         }
-      const float r = rsqrtf(qs * inv_d + p.eps);
+      // lanes without a head hold zeros, whose inverse root is infinite if eps is 0
+      const float r = rsqrtf(qs * inv_d + (h < nh ? p.eps : 1.f));
       const float k = -(r * r) * (r * ds) * inv_d;  // dx = r dn - x r^3 mean(dn x)
       const uint64_t rr = f2_pack(r, r), kk = f2_pack(k, k);
 #pragma unroll

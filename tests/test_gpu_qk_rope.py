@@ -277,3 +277,36 @@ def test_keys_after_queries_equal_keys_alone(L, H, Hkv, d, rot, layout):
         got = upipe.qk_norm_rope_backward(r, q, k, w, w, dq, dk, pos0=3)
         assert torch.equal(got[1], want[0])
         assert np.all(np.abs(f64(got[3]) - want_w) <= slack)
+
+
+def _check_norm_backward(q, k, wq, wk, dq, dk, rope, eps, got, name=""):
+    """(dq, dk, dwq, dwk) of one call at positions 0, 1, ... against the oracle."""
+    pos, f = np.arange(q.shape[0]), np.array(rope.freqs)
+    for x, w, dy, dx, dw, n in ((q, wq, dq, got[0], got[2], "q"), (k, wk, dk, got[1], got[3], "k")):
+        x, w, dy = f64(x), f64(w), f64(dy)
+        want, want_w, size_w = loc.norm_rope_bwd(x, w, eps, dy, pos, f, rope.rot, rope.layout)
+        rr = 1 / np.sqrt(np.mean(x * x, -1, keepdims=True) + eps)
+        pair = _pair_size(dy, rope.rot, rope.layout)
+        dn = np.abs(w) * pair
+        _near(dx, want, NORM * rr * (dn + np.abs(x) * rr * np.mean(dn * np.abs(x) * rr, -1, keepdims=True)),
+              f"{name} d{n}")
+        assert np.all(np.abs(f64(dw) - want_w) <= WEIGHT * (size_w + np.sum(pair * np.abs(x) * rr, (0, 1)))), \
+            f"{name} dw{n}"
+
+
+@pytest.mark.parametrize("d,rot,layout", [(128, 128, "half"), (128, 64, "interleaved"), (64, 64, "half"),
+                                          (72, 40, "half"), (24, 8, "interleaved"), (128, 34, "half")])
+@pytest.mark.parametrize("H,Hkv", [(1, 2), (6, 3), (5, 7), (16, 1)])
+def test_norm_without_eps(d, rot, layout, H, Hkv):
+    """eps = 0 with head counts that leave lanes of a step without a head:
+    those hold zeros, whose inverse root is infinite, and add nothing."""
+    L = 37
+    q, k, dq, dk = _randn(25, L, H, d), _randn(26, L, Hkv, d), _randn(27, L, H, d), _randn(28, L, Hkv, d)
+    wq, wk = torch.linspace(0.5, 1.5, d, device="cuda"), torch.linspace(1.5, 0.5, d, device="cuda")
+    r = upipe.Rope(d, rot=rot, layout=layout)
+    f, pos = np.array(r.freqs), np.arange(L)
+    for x, w, y in zip((q, k), (wq, wk), upipe.qk_norm_rope_forward(r, q, k, wq, wk, eps=0.0)):
+        z = loc.norm_rope(f64(x), f64(w), 0.0, pos, np.zeros(rot // 2), rot, layout)  # unrotated
+        _near(y, loc.norm_rope(f64(x), f64(w), 0.0, pos, f, rot, layout), (ANGLE + NORM) * _pair_size(z, rot, layout),
+              "forward")
+    _check_norm_backward(q, k, wq, wk, dq, dk, r, 0.0, upipe.qk_norm_rope_backward(r, q, k, wq, wk, dq, dk, eps=0.0))
