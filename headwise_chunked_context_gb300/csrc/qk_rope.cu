@@ -110,6 +110,9 @@ struct Lane {
   }
   __device__ __forceinline__ bool holds(int e) const { return PATH == kScalar ? 2 * pair(e) < d : live; }
   __device__ __forceinline__ bool turns(int e) const { return 2 * pair(e) < rot; }
+  // Whether word j of the lane's vectors (Raw::w) belongs to pairs that turn:
+  // a pair each, or, in the half layout, parts of pairs that all do or all do not.
+  __device__ __forceinline__ bool turns_word(int j) const { return turns(is_half(PATH) ? 0 : j); }
   __device__ __forceinline__ int first(int e) const {
     if (is_half(PATH)) return off_a + e;
     return PATH == kScalar && turns(e) && !interleaved ? pair(e) : 2 * pair(e);
@@ -225,19 +228,48 @@ struct Pipe {
   }
 };
 
-// Rounds the lane's pairs to bf16, the only rounding of the pass, and stores them.
-template <int PATH>
+// Pairs 2 i and 2 i + 1 of a lane turned by their angles.  Those past rot (WHOLE:
+// there are none) stay as they are: times 1 and 0 an infinity of one member
+// would make the other NaN.
+template <int PATH, bool WHOLE>
+__device__ __forceinline__ void turn_pairs(const Lane<PATH>& ln, int i, uint64_t c, uint64_t s, uint64_t& u,
+                                           uint64_t& v) {
+  const uint64_t a = f2_sub(f2_mul(u, c), f2_mul(v, s));
+  const uint64_t b = f2_fma(u, s, f2_mul(v, c));
+  if (WHOLE) {
+    u = a;
+    v = b;
+    return;
+  }
+  const bool t0 = ln.turns(2 * i), t1 = ln.turns(2 * i + 1);
+  float a0, a1, b0, b1, u0, u1, v0, v1;
+  f2_unpack(a, a0, a1);
+  f2_unpack(b, b0, b1);
+  f2_unpack(u, u0, u1);
+  f2_unpack(v, v0, v1);
+  u = f2_pack(t0 ? a0 : u0, t1 ? a1 : u1);
+  v = f2_pack(t0 ? b0 : v0, t1 ? b1 : v1);
+}
+
+// Rounds the lane's pairs to bf16, the only rounding of the pass, and stores
+// them.  COPY: pairs that do not turn hold bf16 values as they were read, whose
+// bits (a NaN's too) are the upper half of the fp32's.
+template <int PATH, bool COPY>
 __device__ __forceinline__ void store(bf16* head, const Lane<PATH>& ln, const uint64_t (&u)[Lane<PATH>::M],
                                       const uint64_t (&v)[Lane<PATH>::M]) {
   constexpr int M = Lane<PATH>::M;
   uint32_t w[2 * M];
+  auto word = [&](int j, float lo, float hi) {
+    w[j] = pack_bf16x2(lo, hi);
+    if (COPY && !ln.turns_word(j)) w[j] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+  };
 #pragma unroll
   for (int i = 0; i < M; ++i) {
     float a0, a1, b0, b1;
     f2_unpack(u[i], a0, a1);
     f2_unpack(v[i], b0, b1);
-    w[is_half(PATH) ? i : 2 * i] = is_half(PATH) ? pack_bf16x2(a0, a1) : pack_bf16x2(a0, b0);
-    w[is_half(PATH) ? M + i : 2 * i + 1] = is_half(PATH) ? pack_bf16x2(b0, b1) : pack_bf16x2(a1, b1);
+    word(is_half(PATH) ? i : 2 * i, a0, is_half(PATH) ? a1 : b0);
+    word(is_half(PATH) ? M + i : 2 * i + 1, is_half(PATH) ? b0 : a1, b1);
   }
   if constexpr (PATH == kScalar) {
     uint16_t* h = reinterpret_cast<uint16_t*>(head);
@@ -339,7 +371,7 @@ struct Steps {
 
 constexpr int kFwdSteps = 4, kBwdSteps = 4;  // steps in flight per warp
 
-template <int MODE, int PATH>
+template <int MODE, int PATH, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32, 3) qk_rope_kernel(const __grid_constant__ QkParams p) {
   constexpr int M = Lane<PATH>::M;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -403,12 +435,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_rope_kernel(const __grid_co
       }
     }
 #pragma unroll
-    for (int e = 0; e < M; ++e) {
-      const uint64_t a = f2_sub(f2_mul(u[e], c[e]), f2_mul(v[e], s[e]));
-      v[e] = f2_fma(u[e], s[e], f2_mul(v[e], c[e]));
-      u[e] = a;
-    }
-    if (h < p.nheads[t] && ln.live) store<PATH>(t ? yk + h * p.y[1].head : yq + h * p.y[0].head, ln, u, v);
+    for (int e = 0; e < M; ++e) turn_pairs<PATH, WHOLE>(ln, e, c[e], s[e], u[e], v[e]);
+    if (h < p.nheads[t] && ln.live)
+      store<PATH, MODE == kTurn>(t ? yk + h * p.y[1].head : yq + h * p.y[0].head, ln, u, v);
   }
 }
 
@@ -416,7 +445,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_rope_kernel(const __grid_co
 // tokens) a grid apart, the queries of all of them first, then the keys, and
 // keeps its lanes' shares of dw in registers; a CTA adds its warps' shares in
 // a fixed order and writes one row per weight, which norm_sum_kernel adds up.
-template <int PATH>
+template <int PATH, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const __grid_constant__ QkParams p) {
   constexpr int M = Lane<PATH>::M;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -499,14 +528,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const 
       uint64_t gx[M], gy[M];  // dz x, the terms of dw before the norm's factor
 #pragma unroll
       for (int e = 0; e < M; ++e) {
-        const uint64_t za = f2_sub(f2_mul(a[e], c[e]), f2_mul(b[e], s[e]));  // dz: s holds -sin here
-        const uint64_t zb = f2_fma(a[e], s[e], f2_mul(b[e], c[e]));
+        turn_pairs<PATH, WHOLE>(ln, e, c[e], s[e], a[e], b[e]);  // dz: s holds -sin here
         q = f2_fma(u[e], u[e], f2_fma(v[e], v[e], q));
-        gx[e] = f2_mul(za, u[e]);
-        gy[e] = f2_mul(zb, v[e]);
+        gx[e] = f2_mul(a[e], u[e]);
+        gy[e] = f2_mul(b[e], v[e]);
         dot = f2_fma(gx[e], wu[e], f2_fma(gy[e], wv[e], dot));
-        a[e] = f2_mul(za, wu[e]);  // dn
-        b[e] = f2_mul(zb, wv[e]);
+        a[e] = f2_mul(a[e], wu[e]);  // dn
+        b[e] = f2_mul(b[e], wv[e]);
       }
       float qs = f2_sum(q), ds = f2_sum(dot);
 #pragma unroll
@@ -527,7 +555,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const 
         a[e] = f2_fma(u[e], kk, f2_mul(a[e], rr));
         b[e] = f2_fma(v[e], kk, f2_mul(b[e], rr));
       }
-      if (h < nh && ln.live) store<PATH>(p.y[t].p + at.token * p.y[t].row + h * p.y[t].head, ln, a, b);
+      if (h < nh && ln.live) store<PATH, false>(p.y[t].p + at.token * p.y[t].row + h * p.y[t].head, ln, a, b);
       at = after(at);
     }
     pipe.drain();  // the next weight's pipe starts over in the same slots
@@ -658,11 +686,21 @@ int path_of(const upipe_rope* r) {
   return kScalar;
 }
 
+// Heads that turn whole have kernels of the norm's own: 32768 tokens of 40 such
+// heads, 103 us forward and 178 backward, 110 and 189 with the choice per pair.
+// The rotation alone takes the same time with and without the choice; single
+// elements hold parts of heads only.
+constexpr bool whole_kernel(int mode, int path) { return mode != kTurn && path != kScalar; }
+
 template <int MODE, int PATH>
 cudaError_t launch_fwd_path(const QkParams& p, cudaStream_t st) {
   const int64_t units = p.L * p.parts;
   const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
-  qk_rope_kernel<MODE, PATH><<<grid, kWarps * 32, kWarps * Pipe<PATH, 1, kFwdSteps>::kBytes, st>>>(p);
+  constexpr int kRing = kWarps * Pipe<PATH, 1, kFwdSteps>::kBytes;
+  if (whole_kernel(MODE, PATH) && p.rot == p.d)
+    qk_rope_kernel<MODE, PATH, whole_kernel(MODE, PATH)><<<grid, kWarps * 32, kRing, st>>>(p);
+  else
+    qk_rope_kernel<MODE, PATH, false><<<grid, kWarps * 32, kRing, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -685,10 +723,12 @@ int bwd_ctas(const QkParams& p) {
 template <int PATH>
 cudaError_t launch_bwd_path(const QkParams& p, cudaStream_t st) {
   constexpr int kRing = kWarps * Pipe<PATH, 2, kBwdSteps>::kBytes;
-  const cudaError_t e =
-      cudaFuncSetAttribute(qk_norm_rope_bwd_kernel<PATH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+  constexpr bool kWhole = whole_kernel(kNormTurnBwd, PATH);
+  const auto kernel =
+      kWhole && p.rot == p.d ? qk_norm_rope_bwd_kernel<PATH, kWhole> : qk_norm_rope_bwd_kernel<PATH, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
   if (e != cudaSuccess) return e;
-  qk_norm_rope_bwd_kernel<PATH><<<bwd_ctas(p), kWarps * 32, kRing, st>>>(p);
+  kernel<<<bwd_ctas(p), kWarps * 32, kRing, st>>>(p);
   return cudaGetLastError();
 }
 

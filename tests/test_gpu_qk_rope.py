@@ -310,3 +310,56 @@ def test_norm_without_eps(d, rot, layout, H, Hkv):
         _near(y, loc.norm_rope(f64(x), f64(w), 0.0, pos, f, rot, layout), (ANGLE + NORM) * _pair_size(z, rot, layout),
               "forward")
     _check_norm_backward(q, k, wq, wk, dq, dk, r, 0.0, upipe.qk_norm_rope_backward(r, q, k, wq, wk, dq, dk, eps=0.0))
+
+
+# d, rot, layout: vectors of 8 and of 4 elements in both layouts, single elements; nothing rotated
+PARTIAL = [(128, 64, "half"), (128, 34, "interleaved"), (72, 40, "half"), (72, 10, "interleaved"), (128, 34, "half"),
+           (16, 2, "half"), (128, 0, "half"), (72, 0, "interleaved"), (256, 48, "half")]
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16)
+
+
+@pytest.mark.parametrize("d,rot,layout", PARTIAL)
+@pytest.mark.parametrize("transpose", [False, True])
+def test_elements_past_rot_are_copied_bit_for_bit(d, rot, layout, transpose):
+    """Infinities, NaN of several payloads and zeros of both signs among the
+    elements that do not turn stay what they are and reach nothing else."""
+    L, H, Hkv = 29, 5, 2
+    r = upipe.Rope(d, rot=rot, layout=layout, magnitude=1.25)
+    x = [_randn(29, L, H, d), _randn(30, L, Hkv, d)]
+    clean = [upipe.rope_forward, upipe.rope_backward][transpose](r, *x, pos0=11)
+    g = torch.Generator().manual_seed(31)
+    odd = torch.tensor([0x7F80, -0x80, 0x7FC0, 0x7F81, -0x3F, -0x8000, 0, 0x0001], dtype=torch.int16)
+    for t in x:
+        at = torch.rand(t.shape, generator=g) < 0.3
+        at[..., :rot] = False
+        _bits(t)[at.cuda()] = odd[torch.randint(0, len(odd), (int(at.sum()),), generator=g)].cuda()
+    assert not torch.isfinite(x[0]).all()
+    for place in ("apart", "in place"):
+        y = [torch.full_like(t, 7.0) for t in x] if place == "apart" else [t.clone() for t in x]
+        upipe.rope_apply(r, *(x if place == "apart" else y), *y, pos0=11, transpose=transpose)
+        for a, b, c in zip(y, x, clean):
+            assert torch.equal(_bits(a)[..., rot:], _bits(b)[..., rot:]), place
+            assert torch.equal(_bits(a)[..., :rot], _bits(c)[..., :rot]), place
+
+
+@pytest.mark.parametrize("d,rot,layout", [p for p in PARTIAL if p[1]])
+def test_norm_keeps_elements_past_rot_apart(d, rot, layout):
+    """An infinite weight of an element that does not turn makes that element's
+    output infinite, and an infinite gradient of it that weight's gradient: no
+    other element's, which have the bits that they have without it."""
+    L, H, e = 9, 3, d - 3
+    r = upipe.Rope(d, rot=rot, layout=layout)
+    q, dq, w = _randn(32, L, H, d), _randn(33, L, H, d), torch.linspace(0.5, 1.5, d, device="cuda")
+    rest = torch.arange(d, device="cuda") != e
+    want, _ = upipe.qk_norm_rope_forward(r, q, None, w, None)
+    _, _, want_w, _ = upipe.qk_norm_rope_backward(r, q, None, w, None, dq, None)
+    big = w.clone()
+    big[e] = math.inf
+    y, _ = upipe.qk_norm_rope_forward(r, q, None, big, None)
+    assert torch.isinf(y[..., e]).all() and torch.equal(y[..., rest], want[..., rest])
+    dq[0, 0, e] = math.inf
+    _, _, dw, _ = upipe.qk_norm_rope_backward(r, q, None, w, None, dq, None)
+    assert torch.isinf(dw[e]) and torch.equal(dw[rest], want_w[rest])
