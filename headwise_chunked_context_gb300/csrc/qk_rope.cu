@@ -640,6 +640,9 @@ bool rows_ok(const upipe_rows* t, int64_t L, int n, int d, bool written) {
   return row_major || head_major;
 }
 
+// A weight or its gradient, which the kernels read and write by single floats.
+bool weight_ok(const float* w) { return w && reinterpret_cast<uintptr_t>(w) % sizeof(float) == 0; }
+
 bool call_ok(const upipe_rope* r, const upipe_qk_cfg* c) {
   return rope_ok(r) && c && c->L >= 1 && c->L <= 0x7fffffffLL && c->H >= 1 && c->H <= 65536 && c->Hkv >= 0 &&
          c->Hkv <= 65536 && c->pos0 > -(int64_t(1) << 62) && c->pos0 < (int64_t(1) << 62);
@@ -826,10 +829,10 @@ int upipe_qk_norm_rope_fwd(const upipe_rope* r, const upipe_qk_cfg* c, const upi
                            const float* wq, const float* wk, const int32_t* positions, const upipe_rows* qo,
                            const upipe_rows* ko, void* stream) {
   if (!call_ok(r, c) || !(c->eps >= 0.f) || !std::isfinite(c->eps)) return UPIPE_ERR_INVALID_ARG;
-  if (!rows_ok(q, c->L, c->H, r->d, false) || !rows_ok(qo, c->L, c->H, r->d, true) || !wq || !aligned16(wq))
+  if (!rows_ok(q, c->L, c->H, r->d, false) || !rows_ok(qo, c->L, c->H, r->d, true) || !weight_ok(wq))
     return UPIPE_ERR_INVALID_ARG;
-  if (c->Hkv && (!rows_ok(k, c->L, c->Hkv, r->d, false) || !rows_ok(ko, c->L, c->Hkv, r->d, true) || !wk ||
-                 !aligned16(wk)))
+  if (c->Hkv && (!rows_ok(k, c->L, c->Hkv, r->d, false) || !rows_ok(ko, c->L, c->Hkv, r->d, true) ||
+                 !weight_ok(wk)))
     return UPIPE_ERR_INVALID_ARG;
   int* status = nullptr;
   if (int e = device_ready(&status)) return e;
@@ -861,10 +864,10 @@ int upipe_qk_norm_rope_bwd(const upipe_rope* r, const upipe_qk_cfg* c, const upi
                            void* ws, size_t ws_bytes, void* stream) {
   if (!call_ok(r, c) || !(c->eps >= 0.f) || !std::isfinite(c->eps)) return UPIPE_ERR_INVALID_ARG;
   if (!rows_ok(q, c->L, c->H, r->d, false) || !rows_ok(dqo, c->L, c->H, r->d, false) ||
-      !rows_ok(dq, c->L, c->H, r->d, true) || !wq || !aligned16(wq) || !dwq || !aligned16(dwq))
+      !rows_ok(dq, c->L, c->H, r->d, true) || !weight_ok(wq) || !weight_ok(dwq))
     return UPIPE_ERR_INVALID_ARG;
   if (c->Hkv && (!rows_ok(k, c->L, c->Hkv, r->d, false) || !rows_ok(dko, c->L, c->Hkv, r->d, false) ||
-                 !rows_ok(dk, c->L, c->Hkv, r->d, true) || !wk || !aligned16(wk) || !dwk || !aligned16(dwk)))
+                 !rows_ok(dk, c->L, c->Hkv, r->d, true) || !weight_ok(wk) || !weight_ok(dwk)))
     return UPIPE_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws)) return UPIPE_ERR_INVALID_ARG;
   if (ws_bytes < upipe_qk_norm_rope_workspace_bytes(r, c)) return UPIPE_ERR_WS_TOO_SMALL;

@@ -52,7 +52,8 @@
  *    MLP / loss variants), except the host buffers the activation-offload
  *    calls name as such.  The library allocates no device memory.
  *  - bf16 tensors are passed as `uint16_t*` holding bfloat16 bit patterns.
- *  - Every pointer must be 16-byte aligned; tensors are dense row-major.
+ *  - Every pointer must be 16-byte aligned; tensors are dense row-major
+ *    (where an entry point says otherwise, as it says).
  *  - Work is enqueued on `stream` (a cudaStream_t, 0 = legacy default) and
  *    the call returns without waiting.  Calls that share a workspace must be
  *    ordered on the GPU (for example, issued on one stream).
@@ -449,7 +450,8 @@ int upipe_rope_apply(const upipe_rope* r, const upipe_qk_cfg* c, const upipe_row
                      void* stream);
 
 /* RMS norm of each query and key head and the rotation in one pass:
- * z = w x / sqrt(mean(x^2) + eps), then as above.  wq, wk [d] fp32.
+ * z = w x / sqrt(mean(x^2) + eps), then as above.  wq, wk [d] fp32, at any
+ * 4-byte boundary (a parameter inside a flat buffer), as their gradients.
  * In-place and overlap rules as upipe_rope_apply.                          */
 int upipe_qk_norm_rope_fwd(const upipe_rope* r, const upipe_qk_cfg* c, const upipe_rows* q, const upipe_rows* k,
                            const float* wq, const float* wk, const int32_t* positions, const upipe_rows* qo,

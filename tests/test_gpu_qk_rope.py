@@ -363,3 +363,24 @@ def test_norm_keeps_elements_past_rot_apart(d, rot, layout):
     dq[0, 0, e] = math.inf
     _, _, dw, _ = upipe.qk_norm_rope_backward(r, q, None, w, None, dq, None)
     assert torch.isinf(dw[e]) and torch.equal(dw[rest], want_w[rest])
+
+
+@pytest.mark.parametrize("d,rot,layout", [(128, 128, "half"), (72, 40, "interleaved"), (128, 34, "half")])
+def test_weights_at_any_place_of_a_flat_buffer(d, rot, layout):
+    """Weights and their gradients are read and written element by element:
+    views into a flat buffer need no alignment but their own."""
+    q, k, dq, dk = _randn(34, 50, 3, d), _randn(35, 50, 2, d), _randn(36, 50, 3, d), _randn(37, 50, 2, d)
+    flat = torch.linspace(0.5, 1.5, 2 * d + 4, device="cuda")
+    wq, wk = flat[1:d + 1], flat[d + 2:2 * d + 2]
+    assert wq.data_ptr() % 16 == 4 and wk.data_ptr() % 16 == 8
+    r = upipe.Rope(d, rot=rot, layout=layout)
+    for a, b in zip(upipe.qk_norm_rope_forward(r, q, k, wq, wk),
+                    upipe.qk_norm_rope_forward(r, q, k, wq.clone(), wk.clone())):
+        assert torch.equal(a, b)
+    want = upipe.qk_norm_rope_backward(r, q, k, wq.clone(), wk.clone(), dq, dk)
+    grads = torch.full((2 * d + 4,), 7.0, device="cuda")
+    gq, gk = torch.empty_like(q), torch.empty_like(k)
+    upipe.qk_norm_rope_bwd(r, q, k, wq, wk, dq, dk, gq, gk, grads[1:d + 1], grads[d + 2:2 * d + 2])
+    for a, b in zip((gq, gk, grads[1:d + 1], grads[d + 2:2 * d + 2]), want):
+        assert torch.equal(a, b)
+    assert (grads[[0, d + 1, 2 * d + 2, 2 * d + 3]] == 7).all()

@@ -220,6 +220,25 @@ def test_rope_entry_refuses_bad_shapes_pointers_and_strides(lib):
     assert upipe.qk_norm_rope_workspace_bytes(r, 0, 32, 8) == 0
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would launch on made-up addresses")
+def test_norm_entries_take_weights_at_any_float(lib):
+    import ctypes
+    r, c = upipe.Rope(128), ctypes.byref(upipe.QkCfg(4, 2, 1, 0, 1e-6))
+    q, k = ctypes.byref(upipe.Rows(1 << 20, 256, 128)), ctypes.byref(upipe.Rows(1 << 21, 128, 128))
+    fwd = lambda wq, wk: lib.upipe_qk_norm_rope_fwd(r._ref, c, q, k, wq, wk, None, q, k, None)  # noqa: E731
+    bwd = lambda *w: lib.upipe_qk_norm_rope_bwd(r._ref, c, q, k, w[0], w[1], None, q, k, q, k, w[2], w[3],  # noqa: E731
+                                                1 << 24, 1 << 20, None)
+    at = 1 << 23
+    for entry, n in ((fwd, 2), (bwd, 4)):
+        for off in (0, 4, 8, 12):
+            assert entry(*[at + off] * n) in (upipe.UPIPE_ERR_CUDA, upipe.UPIPE_ERR_UNSUPPORTED_DEVICE), off
+        for i in range(n):
+            for bad in (None, at + 2):
+                w = [at] * n
+                w[i] = bad
+                assert entry(*w) == upipe.UPIPE_ERR_INVALID_ARG, (i, bad)
+
+
 @pytest.mark.parametrize("kw", [dict(window=0), dict(window=-3), dict(sinks=-1), dict(L=0), dict(L=1 << 31), dict(d=64),
                                 dict(H=6, Hkv=4), dict(H=96, Hkv=8), dict(Hkv=0)])
 def test_window_refuses_bad_configurations(lib, kw):
