@@ -895,6 +895,9 @@ def qk_norm_rope_bwd(rope: Rope, q, k, wq, wk, dqo, dko, dq, dk, dwq, dwk, eps: 
     ws, nbytes = _call_ws(f.upipe_qk_norm_rope_workspace_bytes(rope._ref, c), ws, q.device, stream)
     _check(f.upipe_qk_norm_rope_bwd(rope._ref, c, tq[0], tk[0], pq, pk, at, tq[1], tk[1], tq[2], tk[2], gq, gk,
                                     ws.data_ptr(), nbytes, _raw(stream, here)), "upipe_qk_norm_rope_bwd")
+    if keys and not Hkv:  # the library takes keys of no heads for none; the sum over them is 0
+        with torch.cuda.stream(stream):
+            dwk.zero_()
 
 
 def _like(t):

@@ -384,3 +384,23 @@ def test_weights_at_any_place_of_a_flat_buffer(d, rot, layout):
     for a, b in zip((gq, gk, grads[1:d + 1], grads[d + 2:2 * d + 2]), want):
         assert torch.equal(a, b)
     assert (grads[[0, d + 1, 2 * d + 2, 2 * d + 3]] == 7).all()
+
+
+def test_keys_without_heads():
+    """k of no heads is no keys: its weight's gradient, a sum of nothing, is
+    written like any other."""
+    q, dq, w = _randn(38, 20, 2, 128), _randn(39, 20, 2, 128), torch.ones(128, device="cuda")
+    none = q[:, :0]
+    r = upipe.Rope(128)
+    want = upipe.qk_norm_rope_backward(r, q, None, w, None, dq, None)
+    gq, gwq, gwk = torch.empty_like(q), torch.empty_like(w), torch.full_like(w, 7.0)
+    upipe.qk_norm_rope_bwd(r, q, none, w, w, dq, none, gq, none, gwq, gwk)
+    assert torch.equal(gq, want[0]) and torch.equal(gwq, want[2]) and not gwk.any()
+    st = torch.cuda.Stream()
+    gwk.fill_(7.0)
+    torch.cuda.synchronize()
+    upipe.qk_norm_rope_bwd(r, q, none, w, w, dq, none, gq, none, gwq, gwk, stream=st)
+    st.synchronize()
+    assert not gwk.any()
+    y, z = upipe.qk_norm_rope_forward(r, q, none, w, w)
+    assert z.shape == none.shape and torch.equal(y, upipe.qk_norm_rope_forward(r, q, None, w, None)[0])
