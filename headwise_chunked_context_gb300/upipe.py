@@ -877,6 +877,9 @@ def _weight(w, d, name, device):
 
 
 def qk_norm_rope_workspace_bytes(rope: Rope, L: int, H: int, Hkv: int = 0) -> int:
+    """Workspace of qk_norm_rope_bwd; 0 for sizes that it refuses."""
+    if not all(0 <= n < 1 << 31 for n in (L, H, Hkv)):  # a C int of (1 << 32) + n is n
+        return 0
     return int(lib().upipe_qk_norm_rope_workspace_bytes(rope._ref, ctypes.byref(QkCfg(L, H, Hkv, 0, 0.0))))
 
 

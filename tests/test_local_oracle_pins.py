@@ -332,6 +332,15 @@ def test_sizes_past_32_bits_are_refused(lib):
             upipe.rope_apply(upipe.Rope(8), bad, None, bad, None)
 
 
+def test_no_workspace_for_sizes_past_the_librarys_integers(lib):
+    r = upipe.Rope(128)
+    need = upipe.qk_norm_rope_workspace_bytes
+    assert need(r, 100, 8, 2) > 0
+    for kw in (dict(L=(1 << 64) + 100), dict(L=1 << 31), dict(H=(1 << 32) + 8), dict(Hkv=(1 << 32) + 2),
+               dict(H=8 - (1 << 32))):
+        assert need(r, **{**dict(L=100, H=8, Hkv=2), **kw}) == 0, kw
+
+
 def test_strides_of_axes_of_one_say_nothing(lib):
     """One token of rows of 100 elements, one head of such rows: what would be
     the strides of a second token or head are no multiples of 8."""
