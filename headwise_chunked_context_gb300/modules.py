@@ -167,7 +167,7 @@ def rotate(q, k, rope, pos0: int = 0, positions=None):
 class _QKNormRopeFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, wq, wk, rope, eps, pos0, positions):
-        q, k = _heads(q), _heads(k)
+        q, k, wq, wk = _heads(q), _heads(k), wq.float(), wk.float()
         ctx.save_for_backward(q, k, wq, wk, positions)
         ctx.args = rope, eps, pos0
         return upipe.qk_norm_rope_forward(rope, q, k, wq, wk, eps, pos0, positions)

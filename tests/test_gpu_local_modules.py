@@ -297,3 +297,23 @@ def test_chunk_loop_with_a_window_on_one_nccl_rank(L, H, Hkv, U):
             assert_close(f64(dv), f64(rdv), "dv (chunk partials summed in fp32)")
     finally:
         dist.destroy_process_group()
+
+
+def test_norm_module_with_weights_of_another_type():
+    """QKNormRope after .bfloat16(), as the package's other modules run:
+    computed with the fp32 value of each weight, gradients in the weight's type."""
+    rope, qkv = upipe.Rope(D128), _qkv(60, 3, 2, 9)
+    q, k = qkv[:, :3], qkv[:, 3:5]
+    m = QKNormRope(rope).bfloat16()
+    with torch.no_grad():
+        m.wq.copy_(torch.linspace(0.5, 1.5, D128))
+    y = m(q, k)
+    w = (m.wq.detach().float(), m.wk.detach().float())
+    for a, b in zip(y, upipe.qk_norm_rope_forward(rope, q, k, *w)):
+        assert torch.equal(a, b)
+    dq, dk = _qkv(60, 3, 0, 10), _qkv(60, 2, 0, 11)
+    torch.autograd.backward(y, (dq, dk))
+    want = upipe.qk_norm_rope_backward(rope, q, k, *w, dq, dk)[2:]
+    assert m.wq.dtype == m.wq.grad.dtype == torch.bfloat16
+    assert torch.equal(m.wq.grad, want[0].bfloat16()) and torch.equal(m.wk.grad, want[1].bfloat16())
+    status_ok()
