@@ -322,10 +322,13 @@ int launch_beside(int side_kind, LaunchFn side, int own_kind, LaunchFn own, void
   }
   UPIPE_CU(cudaEventRecord(sd->fork, st));
   UPIPE_CU(cudaStreamWaitEvent(sd->s, sd->fork, 0));
-  UPIPE_CU(counted(side_kind, sd->s, [&] { return side(job, sd->s); }));
-  UPIPE_CU(counted(own_kind, st, [&] { return own(job, st); }));
+  // Joined whatever becomes of the launches: a caller that gets an error may
+  // release what the side's kernel still uses, and a capture wants it back.
+  cudaError_t e = counted(side_kind, sd->s, [&] { return side(job, sd->s); });
+  if (e == cudaSuccess) e = counted(own_kind, st, [&] { return own(job, st); });
   UPIPE_CU(cudaEventRecord(sd->join, sd->s));
   UPIPE_CU(cudaStreamWaitEvent(st, sd->join, 0));
+  UPIPE_CU(e);
   return UPIPE_OK;
 }
 
