@@ -42,7 +42,7 @@ constexpr int kWarps = 8;  // per CTA
 
 enum Mode { kTurn = 0, kNormTurn = 1, kNormTurnBwd = 2 };
 // How a lane holds its pairs: vectors of 8 or 4 elements in either layout, or
-// single elements.
+// single elements (half layout; interleaved pairs always lie in vectors).
 enum Path { kHalf8 = 0, kInter8 = 1, kHalf4 = 2, kInter4 = 3, kScalar = 4 };
 __host__ __device__ constexpr bool is_half(int path) { return path == kHalf8 || path == kHalf4; }
 __host__ __device__ constexpr int vec_of(int path) { return path == kHalf8 || path == kInter8 ? 8 : 4; }
@@ -59,7 +59,6 @@ struct QkParams {
   int d, rot;
   int lanes;      // lanes of a warp that share a head (a power of two)
   int parts;      // shares that a token's heads are split into
-  int interleaved;  // pair layout (read by the scalar path; the vector paths have it as a parameter)
   float magnitude, eps, sign;  // sign: -1 turns by the transpose
   Rows x[2];   // the input (the norm's, or what is turned)
   Rows dy[2];  // backward: gradient of the output
@@ -81,12 +80,11 @@ struct Lane {
   int off_a;  // vector paths: first elements of the lane's two vectors
   int off_b;
   bool live;
-  int d, rot, interleaved;
+  int d, rot;
 
   __device__ __forceinline__ Lane(const QkParams& p, int lane) {
     d = p.d;
     rot = p.rot;
-    interleaved = p.interleaved;
     sub = lane % p.lanes;
     live = PATH == kScalar || sub * 2 * N < d;
     // Neighbouring lanes hold neighbouring vectors, so that each access of a
@@ -115,11 +113,11 @@ struct Lane {
   __device__ __forceinline__ bool turns_word(int j) const { return turns(is_half(PATH) ? 0 : j); }
   __device__ __forceinline__ int first(int e) const {
     if (is_half(PATH)) return off_a + e;
-    return PATH == kScalar && turns(e) && !interleaved ? pair(e) : 2 * pair(e);
+    return PATH == kScalar && turns(e) ? pair(e) : 2 * pair(e);
   }
   __device__ __forceinline__ int second(int e) const {
     if (is_half(PATH)) return off_b + e;
-    return PATH == kScalar && turns(e) && !interleaved ? pair(e) + rot / 2 : 2 * pair(e) + 1;
+    return PATH == kScalar && turns(e) ? pair(e) + rot / 2 : 2 * pair(e) + 1;
   }
 };
 
@@ -662,7 +660,6 @@ QkParams base_params(const upipe_rope* r, const upipe_qk_cfg* c, const int32_t* 
   p.d = r->d;
   p.rot = r->rot;
   p.lanes = lanes_of(r->d, path);
-  p.interleaved = r->layout == UPIPE_ROPE_INTERLEAVED;
   p.magnitude = static_cast<float>(r->magnitude);
   p.sign = 1.f;
   p.positions = positions;
