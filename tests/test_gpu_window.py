@@ -222,3 +222,57 @@ def test_window_outputs_on_16_byte_boundaries_have_the_same_bits():
         assert torch.equal(a, b)
     for room in rooms:
         assert (room[:8] == 7).all() and (room[-8:] == 7).all()
+
+
+@pytest.mark.parametrize("L,H,Hkv,W,S,loud", [(520, 2, 1, 150, 2, 1), (520, 2, 1, 150, 2, 8), (1100, 4, 2, 64, 130, 8),
+                                              (300, 4, 1, 300, 0, 8), (700, 2, 2, 1, 3, 8)])
+def test_window_gradients_at_large_scores(L, H, Hkv, W, S, loud):
+    """Scores of tens to hundreds against the plain definition (with the given
+    o in Delta, see test_window_matches_oracle), and hidden keys, before the
+    window and after the query, whose exponentials overflow.  Element by
+    element, with b = 2^-8 for each rounding to bf16:
+    S: sums of 128 products and -LSE in fp32, each of 10 steps off by at most
+    2^-23 of the largest partial sum; LSE comes from such scores too, so P is
+    off by e_i = 20 2^-23 (max_j sum_c |q_c k_c| / sqrt(d) + |LSE_i|) + 4e-6 of
+    itself (the last for exp2 and log2 in fp32).
+    dP - Delta: off by n_ij = 12 2^-23 sum_c |dO_c| (|v_c| + |o_c|).
+    dS enters its products with an error of P (|dP - Delta| (e + b) + n), P
+    with P (e + b); the products' sums over at most 70 steps add 70 2^-23 of
+    their terms' sizes, and each output is rounded to bf16 once."""
+    q, k, v, do = synth.core_inputs(L, H, Hkv)
+    q, k = (q.float() * 16).bfloat16(), k.clone()
+    k[13::97] *= loud
+    cfg = upipe.WindowConfig(L=L, H=H, Hkv=Hkv, window=W, sinks=S)
+    qd, kd, vd, dod = dev(q, k, v, do)
+    o, lse = upipe.window_forward(cfg, qd, kd, vd)
+    got = [f64(t) for t in (o, *upipe.window_backward(cfg, qd, kd, vd, o, lse, dod))]
+    status_ok()
+    q, k, v, do = (f64(t) for t in (q, k, v, do))
+    seen, g, rt = loc.visible(np.arange(L), np.arange(L), W, S), H // Hkv, 128 ** 0.5
+    b, add = 2.0 ** -8, 70 * 2.0 ** -23
+    want = [np.zeros_like(x) for x in got]
+    slack = [np.zeros_like(x) for x in got]
+    above = 0.0
+    for h in range(H):
+        kv = h // g
+        s = q[:, h] @ k[:, kv].T / rt
+        m = np.where(seen, s, -np.inf).max(1)
+        ref = m + np.log(np.exp(np.where(seen, s, -np.inf) - m[:, None]).sum(1))
+        above = max(above, np.max(np.where(seen, -np.inf, s) - ref[:, None]))
+        size = (np.abs(q[:, h]) @ np.abs(k[:, kv]).T / rt * seen).max(1)
+        e = (20 * 2.0 ** -23 * (size + np.abs(ref)) + 4e-6)[:, None]
+        assert np.all(np.abs(f64(lse)[h] - ref) <= e[:, 0])
+        p = np.where(seen, np.exp(np.where(seen, s, -np.inf) - ref[:, None]), 0.0)
+        d = do[:, h] @ v[:, kv].T - np.sum(do[:, h] * got[0][:, h], 1, keepdims=True)
+        n = 12 * 2.0 ** -23 * (np.abs(do[:, h]) @ np.abs(v[:, kv]).T +
+                               np.sum(np.abs(do[:, h] * got[0][:, h]), 1, keepdims=True))
+        ds, dserr, perr = p * d, p * (np.abs(d) * (e + b + add) + n), p * (e + b + add)
+        for i, head, value, err, x, scale in ((0, h, p, perr, v[:, kv], 1.0), (1, h, ds, dserr, k[:, kv], rt),
+                                              (2, kv, ds.T, dserr.T, q[:, h], rt), (3, kv, p.T, perr.T, do[:, h], 1.0)):
+            want[i][:, head] += value @ x / scale
+            slack[i][:, head] += err @ np.abs(x) / scale
+    assert loud == 1 or above > 100  # exp of it is past fp32
+    for a, w, t, name in zip(got, want, slack, ("o", "dq", "dk", "dv")):
+        over = np.abs(a - w) - (t * (1 + b) + b * np.abs(w) + 1e-30)
+        at = np.unravel_index(over.argmax(), over.shape)
+        assert np.isfinite(a).all() and over.max() <= 0, f"{name}: {over.max():.3e} over at {at}"
