@@ -404,3 +404,33 @@ def test_keys_without_heads():
     assert not gwk.any()
     y, z = upipe.qk_norm_rope_forward(r, q, none, w, w)
     assert z.shape == none.shape and torch.equal(y, upipe.qk_norm_rope_forward(r, q, None, w, None)[0])
+
+
+@pytest.mark.parametrize("d,rot,layout", [(128, 128, "interleaved"), (128, 34, "interleaved"), (72, 72, "interleaved"),
+                                          (72, 10, "interleaved"), (128, 34, "half"), (24, 18, "half")])
+def test_strided_and_in_place_calls_on_the_other_paths(d, rot, layout):
+    """The interleaved layouts' vectors of 8 and of 4, and single elements: out
+    of and into slices of a fused buffer, head-major outputs, in place."""
+    L, H, Hkv = 61, 5, 3
+    qkv, dqkv = _fused(40, L, H, Hkv, d), _fused(41, L, H, Hkv, d)
+    parts = lambda t: (t[:, :H], t[:, H:H + Hkv])  # noqa: E731
+    w = (torch.linspace(0.5, 1.5, d, device="cuda"), torch.linspace(1.5, 0.5, d, device="cuda"))
+    r = upipe.Rope(d, rot=rot, layout=layout)
+    dense, ddense = ([t.contiguous() for t in parts(x)] for x in (qkv, dqkv))
+    runs = [(upipe.rope_forward(r, *dense, pos0=5), lambda x, y: upipe.rope_apply(r, *x, *y, pos0=5)),
+            (upipe.rope_backward(r, *dense, pos0=5), lambda x, y: upipe.rope_apply(r, *x, *y, pos0=5, transpose=True)),
+            (upipe.qk_norm_rope_forward(r, *dense, *w), lambda x, y: upipe.qk_norm_rope_fwd(r, *x, *w, *y))]
+    for want, call in runs:
+        buf, hm = qkv.clone(), torch.full((H + Hkv, L, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        for src, out in ((qkv, torch.full_like(qkv, 7.0)), (buf, buf)):
+            call(parts(src), parts(out))
+            assert all(torch.equal(a, b) for a, b in zip(parts(out), want))
+        assert torch.equal(buf[:, H + Hkv:], qkv[:, H + Hkv:])
+        call(parts(qkv), (hm[:H].transpose(0, 1), hm[H:].transpose(0, 1)))
+        assert all(torch.equal(a.transpose(0, 1), b) for a, b in zip((hm[:H], hm[H:]), want))
+    want = upipe.qk_norm_rope_backward(r, *dense, *w, *ddense)
+    for over in ("gradients", "inputs"):
+        x, dy = qkv.clone(), dqkv.clone()
+        out, dw = parts(dy if over == "gradients" else x), [torch.empty_like(t) for t in w]
+        upipe.qk_norm_rope_bwd(r, *parts(x), *w, *parts(dy), *out, *dw)
+        assert all(torch.equal(a, b) for a, b in zip((*out, *dw), want)), over
