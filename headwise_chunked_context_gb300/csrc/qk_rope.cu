@@ -81,6 +81,7 @@ struct Lane {
   int off_b;
   bool live;
   int d, rot;
+  int turn_a, turn_b;  // interleaved: how many pairs of each vector's start turn
 
   __device__ __forceinline__ Lane(const QkParams& p, int lane) {
     d = p.d;
@@ -100,6 +101,8 @@ struct Lane {
       off_a = from + N * (sub - turned);
       off_b = off_a + (d - from) / 2;
     }
+    turn_a = (rot - off_a) / 2;
+    turn_b = (rot - off_b) / 2;
   }
   __device__ __forceinline__ int pair(int e) const {
     if (PATH == kScalar) return sub + 32 * e;
@@ -107,10 +110,14 @@ struct Lane {
     return e < M ? off_a / 2 + e : off_b / 2 + e - M;
   }
   __device__ __forceinline__ bool holds(int e) const { return PATH == kScalar ? 2 * pair(e) < d : live; }
-  __device__ __forceinline__ bool turns(int e) const { return 2 * pair(e) < rot; }
-  // Whether word j of the lane's vectors (Raw::w) belongs to pairs that turn:
-  // a pair each, or, in the half layout, parts of pairs that all do or all do not.
-  __device__ __forceinline__ bool turns_word(int j) const { return turns(is_half(PATH) ? 0 : j); }
+  // Whether pair e turns, and word e of the lane's vectors (Raw::w) with it: a
+  // word is a pair, or, in the half layout, part of two of a lane's pairs, which
+  // all turn or all do not.  (The counts spare the interleaved layout a sum per
+  // pair: 142 to 124 us for the norm's backward of 20011 tokens, 64 of 128.)
+  __device__ __forceinline__ bool turns(int e) const {
+    if (PATH == kScalar || is_half(PATH)) return 2 * pair(is_half(PATH) ? 0 : e) < rot;
+    return e < M ? e < turn_a : e - M < turn_b;
+  }
   __device__ __forceinline__ int first(int e) const {
     if (is_half(PATH)) return off_a + e;
     return PATH == kScalar && turns(e) ? pair(e) : 2 * pair(e);
@@ -226,15 +233,15 @@ struct Pipe {
   }
 };
 
-// Pairs 2 i and 2 i + 1 of a lane turned by their angles.  Those past rot (WHOLE:
-// there are none) stay as they are: times 1 and 0 an infinity of one member
-// would make the other NaN.
-template <int PATH, bool WHOLE>
+// Pairs 2 i and 2 i + 1 of a lane turned by their angles.  KEEP: those past rot
+// stay as they are; times 1 and 0 an infinity of one member would make the other
+// NaN.
+template <int PATH, bool KEEP>
 __device__ __forceinline__ void turn_pairs(const Lane<PATH>& ln, int i, uint64_t c, uint64_t s, uint64_t& u,
                                            uint64_t& v) {
   const uint64_t a = f2_sub(f2_mul(u, c), f2_mul(v, s));
   const uint64_t b = f2_fma(u, s, f2_mul(v, c));
-  if (WHOLE) {
+  if (!KEEP) {
     u = a;
     v = b;
     return;
@@ -250,24 +257,24 @@ __device__ __forceinline__ void turn_pairs(const Lane<PATH>& ln, int i, uint64_t
 }
 
 // Rounds the lane's pairs to bf16, the only rounding of the pass, and stores
-// them.  COPY: pairs that do not turn hold bf16 values as they were read, whose
-// bits (a NaN's too) are the upper half of the fp32's.
+// them.  COPY: pairs that do not turn are stored bit for bit as they were read.
 template <int PATH, bool COPY>
 __device__ __forceinline__ void store(bf16* head, const Lane<PATH>& ln, const uint64_t (&u)[Lane<PATH>::M],
-                                      const uint64_t (&v)[Lane<PATH>::M]) {
+                                      const uint64_t (&v)[Lane<PATH>::M], const Raw<PATH>& as_read) {
   constexpr int M = Lane<PATH>::M;
   uint32_t w[2 * M];
-  auto word = [&](int j, float lo, float hi) {
-    w[j] = pack_bf16x2(lo, hi);
-    if (COPY && !ln.turns_word(j)) w[j] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-  };
 #pragma unroll
   for (int i = 0; i < M; ++i) {
     float a0, a1, b0, b1;
     f2_unpack(u[i], a0, a1);
     f2_unpack(v[i], b0, b1);
-    word(is_half(PATH) ? i : 2 * i, a0, is_half(PATH) ? a1 : b0);
-    word(is_half(PATH) ? M + i : 2 * i + 1, is_half(PATH) ? b0 : a1, b1);
+    w[is_half(PATH) ? i : 2 * i] = is_half(PATH) ? pack_bf16x2(a0, a1) : pack_bf16x2(a0, b0);
+    w[is_half(PATH) ? M + i : 2 * i + 1] = is_half(PATH) ? pack_bf16x2(b0, b1) : pack_bf16x2(a1, b1);
+  }
+  if (COPY) {
+#pragma unroll
+    for (int j = 0; j < 2 * M; ++j)
+      if (!ln.turns(j)) w[j] = as_read.w[j];
   }
   if constexpr (PATH == kScalar) {
     uint16_t* h = reinterpret_cast<uint16_t*>(head);
@@ -369,8 +376,13 @@ struct Steps {
 
 constexpr int kFwdSteps = 4, kBwdSteps = 4;  // steps in flight per warp
 
+// CTAs per SM of the forward: the rotation by single elements, which has one
+// step in flight, hides its loads behind other warps (262 us with four, 298 with
+// three, of halves of 17 in 32768 tokens of 40 heads).
+constexpr int fwd_ctas(int mode, int path) { return mode == kTurn && path == kScalar ? 4 : 3; }
+
 template <int MODE, int PATH, bool WHOLE>
-__global__ void __launch_bounds__(kWarps * 32, 3) qk_rope_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kWarps * 32, fwd_ctas(MODE, PATH)) qk_rope_kernel(const __grid_constant__ QkParams p) {
   constexpr int M = Lane<PATH>::M;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 tables[kWarps][kMaxPairs];
@@ -433,9 +445,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_rope_kernel(const __grid_co
       }
     }
 #pragma unroll
-    for (int e = 0; e < M; ++e) turn_pairs<PATH, WHOLE>(ln, e, c[e], s[e], u[e], v[e]);
+    for (int e = 0; e < M; ++e) turn_pairs<PATH, !WHOLE && MODE != kTurn>(ln, e, c[e], s[e], u[e], v[e]);
     if (h < p.nheads[t] && ln.live)
-      store<PATH, MODE == kTurn>(t ? yk + h * p.y[1].head : yq + h * p.y[0].head, ln, u, v);
+      store<PATH, !WHOLE && MODE == kTurn>(t ? yk + h * p.y[1].head : yq + h * p.y[0].head, ln, u, v, raw[0]);
   }
 }
 
@@ -526,7 +538,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const 
       uint64_t gx[M], gy[M];  // dz x, the terms of dw before the norm's factor
 #pragma unroll
       for (int e = 0; e < M; ++e) {
-        turn_pairs<PATH, WHOLE>(ln, e, c[e], s[e], a[e], b[e]);  // dz: s holds -sin here
+        turn_pairs<PATH, !WHOLE>(ln, e, c[e], s[e], a[e], b[e]);  // dz: s holds -sin here
         q = f2_fma(u[e], u[e], f2_fma(v[e], v[e], q));
         gx[e] = f2_mul(a[e], u[e]);
         gy[e] = f2_mul(b[e], v[e]);
@@ -553,7 +565,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qk_norm_rope_bwd_kernel(const 
         a[e] = f2_fma(u[e], kk, f2_mul(a[e], rr));
         b[e] = f2_fma(v[e], kk, f2_mul(b[e], rr));
       }
-      if (h < nh && ln.live) store<PATH, false>(p.y[t].p + at.token * p.y[t].row + h * p.y[t].head, ln, a, b);
+      if (h < nh && ln.live) store<PATH, false>(p.y[t].p + at.token * p.y[t].row + h * p.y[t].head, ln, a, b, raw[0]);
       at = after(at);
     }
     pipe.drain();  // the next weight's pipe starts over in the same slots
@@ -675,9 +687,10 @@ QkParams base_params(const upipe_rope* r, const upipe_qk_cfg* c, const int32_t* 
 }
 
 // The widest vectors that hold whole pairs (interleaved) or whose partners are
-// vectors too (half), rotated and passing part alike.  32768 tokens of 40
-// heads of 128: 102 us with 8 elements; heads of 72, 4 elements, 154 us; 34 of
-// 128 rotated in halves, whose partners sit at odd elements, 256 us.
+// vectors too (half), rotated and passing part alike.  The rotation of 32768
+// tokens of 40 heads of 128: 102 us with 8 elements, 262 us of halves of 17,
+// whose partners sit at odd elements; as many bytes in heads of 72 (58254
+// tokens), 4 elements: 153 us.
 int path_of(const upipe_rope* r) {
   const bool half = r->layout == UPIPE_ROPE_HALF;
   const int whole = half ? r->rot | r->d : r->d;
@@ -686,19 +699,19 @@ int path_of(const upipe_rope* r) {
   return kScalar;
 }
 
-// Heads that turn whole have kernels of the norm's own: 32768 tokens of 40 such
-// heads, 103 us forward and 178 backward, 110 and 189 with the choice per pair.
-// The rotation alone takes the same time with and without the choice; single
-// elements hold parts of heads only.
-constexpr bool whole_kernel(int mode, int path) { return mode != kTurn && path != kScalar; }
+// Heads that turn whole have kernels of their own, which choose nothing per pair
+// (single elements hold heads that turn in part only).  With the choice 32768
+// tokens of 40 such heads take 105 us for 102 in the norm's forward and 184 for
+// 180 in its backward, the rotation of 131072 tokens of 9 heads 128 for 113.
+constexpr bool whole_kernel(int path) { return path != kScalar; }
 
 template <int MODE, int PATH>
 cudaError_t launch_fwd_path(const QkParams& p, cudaStream_t st) {
   const int64_t units = p.L * p.parts;
   const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
   constexpr int kRing = kWarps * Pipe<PATH, 1, kFwdSteps>::kBytes;
-  if (whole_kernel(MODE, PATH) && p.rot == p.d)
-    qk_rope_kernel<MODE, PATH, whole_kernel(MODE, PATH)><<<grid, kWarps * 32, kRing, st>>>(p);
+  if (whole_kernel(PATH) && p.rot == p.d)
+    qk_rope_kernel<MODE, PATH, whole_kernel(PATH)><<<grid, kWarps * 32, kRing, st>>>(p);
   else
     qk_rope_kernel<MODE, PATH, false><<<grid, kWarps * 32, kRing, st>>>(p);
   return cudaGetLastError();
@@ -723,7 +736,7 @@ int bwd_ctas(const QkParams& p) {
 template <int PATH>
 cudaError_t launch_bwd_path(const QkParams& p, cudaStream_t st) {
   constexpr int kRing = kWarps * Pipe<PATH, 2, kBwdSteps>::kBytes;
-  constexpr bool kWhole = whole_kernel(kNormTurnBwd, PATH);
+  constexpr bool kWhole = whole_kernel(PATH);
   const auto kernel =
       kWhole && p.rot == p.d ? qk_norm_rope_bwd_kernel<PATH, kWhole> : qk_norm_rope_bwd_kernel<PATH, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
