@@ -10,6 +10,10 @@ Every forward and backward runs the library's kernels through the binding
 parameters: each call hands their bf16 rounding to the kernels and returns
 the kernels' fp32 weight gradients, so no precision is lost in the gradient
 sums.  Activations are bf16 CUDA tensors.
+
+Before a backward is captured into a CUDA graph, drop the eager graphs of the
+same leaves: PyTorch accumulates a leaf's gradient on the stream of its first
+use for as long as such a graph lives, and a capture cannot wait for that stream.
 """
 
 from __future__ import annotations

@@ -317,3 +317,38 @@ def test_norm_module_with_weights_of_another_type():
     assert m.wq.dtype == m.wq.grad.dtype == torch.bfloat16
     assert torch.equal(m.wq.grad, want[0].bfloat16()) and torch.equal(m.wk.grad, want[1].bfloat16())
     status_ok()
+
+
+def test_captured_training_step_of_the_modules():
+    """Forward and backward of norm, rotation and window through autograd,
+    captured after a warm-up on a side stream and replayed on new inputs."""
+    L, H, Hkv = 260, 4, 2
+    m, rope = QKNormRope(upipe.Rope(D128, rot=64)), upipe.Rope(D128, layout="interleaved")
+    with torch.no_grad():
+        m.wk.copy_(torch.linspace(0.5, 1.5, D128))
+    qkv, do = _qkv(L, H, Hkv, 12).requires_grad_(), _qkv(L, H, 0, 13)
+    leaves = (qkv, m.wq, m.wk)
+
+    def step():
+        q, k = m(qkv[:, :H], qkv[:, H:H + Hkv])
+        o = window_attention(*rotate(q, k, rope, pos0=3), qkv[:, H + Hkv:], 60, 2)
+        return (o, *torch.autograd.grad(o, leaves, do))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (14, 15):
+        with torch.no_grad():
+            qkv.copy_(_qkv(L, H, Hkv, seed))
+        do.copy_(_qkv(L, H, 0, seed + 10))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    status_ok()
