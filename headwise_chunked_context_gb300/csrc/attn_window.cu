@@ -188,8 +188,8 @@ __device__ __forceinline__ void store32_bf16(__nv_bfloat16* out, const uint32_t 
 // every time, so commits cover the same thread's products.
 // Between products these warps wait suspended: probes in a loop take issue
 // slots from the row warps of the same sub-partition, whose serial time per
-// block is what every role waits for (the backward of 32768 x 32 heads, window
-// 4096, takes 5.04 ms with such loops and 4.71 without, the forward 2 % more).
+// block is what every role waits for (with such loops the backward of 32768 x 32
+// heads, window 4096, took 7 % longer, the forward 2 %).
 __device__ __forceinline__ void umma_one(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -229,8 +229,9 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
 // maximum and sum are thread-local; O is rescaled in TMEM only when a row's
 // maximum grows by more than 2^8, which bounds every exponent.
 //
-// Measured (burst clocks): 32768 tokens, 32 heads, window 4096: 1.36 ms, 817
-// ns per 128 x 128 block (1024 cycles of products at 2 GHz are 512), 760 with
+// Measured: 32768 tokens, 32 heads, window 4096: 1.37 ms from rest, 1.49 call
+// upon call, when the power limit holds the SMs at 1830 MHz.  From rest that is
+// 820 ns per 128 x 128 block (1024 cycles of products at 2 GHz are 512), 765 with
 // the full causal mask, the rest masked blocks and the tiles' seams; products
 // and copies alone take 540 ns.  What bounds it is the chain scores
 // -> softmax -> P of the one warp per scheduler; hence barriers are probed
@@ -675,9 +676,9 @@ __device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
 // Two kernels, in which every sum has one order: dQ by query tiles and dK/dV
 // by key tiles, each recomputing S and dP (7 products for the gradient's 5: one
 // kernel would need atomic or ordered sums of dQ and more TMEM than there is).
-// Both keep one CTA per SM and take tiles from a counter, so that whichever
-// runs on what the other one leaves idle finishes evenly; which CTA computes a
-// tile changes nothing in its sums.
+// Both keep one CTA per SM and take tiles from a counter, so that the one whose
+// CTAs start as the other's end finishes evenly; which CTA computes a tile
+// changes nothing in its sums.
 
 // The queries' records, and the counters' zeros.  16 lanes per (query, head),
 // 16 bytes of O and of dO each.  A CTA takes 32 queries of one head, so that
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(256) window_records_kernel(const __grid_consta
 // have read, and dQ += dS K takes it from there.  K is held until dQ (three
 // stages), V until dP (two).  The next tile's Q and dO are loaded, and its
 // first products formed, under this tile's last dQ product and epilogue.
-// 32768 tokens, 32 heads, window 4096: 1.7 ms alone, 1.03 us per block, of
+// 32768 tokens, 32 heads, window 4096, alone and from rest: 1.7 ms, 1.03 us per block, of
 // which the products by themselves take 0.97 (1536 cycles at 2 GHz are 0.77):
 // S and dP read both operands from shared memory, which alone takes 107 cycles
 // per 64-cycle product step, and TMEM has no room for Q and dO.
@@ -1142,7 +1143,7 @@ __global__ void __launch_bounds__(wq::kThreadsDq, 1)
 // queries' records, in which each fp32 value is the sum of three bf16 (exact
 // to 2^-24 of it); the keys are the rows here, and each warp would otherwise
 // have to broadcast every query's two values by shuffle.
-// 32768 tokens, 32 heads, window 4096: 2.7 ms alone, 1.62 us per tile, of
+// 32768 tokens, 32 heads, window 4096, alone and from rest: 2.7 ms, 1.62 us per tile, of
 // which the products by themselves take 1.33 (2048 cycles at 2 GHz are 1.02;
 // S^T and dP^T read both operands from shared memory).  With one region for
 // each of S^T and dP^T and the values by shuffles it takes a tenth more.
@@ -1808,8 +1809,9 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
   p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
   p.sectors = on_sectors(dq) && on_sectors(dk) && on_sectors(dv);
   UPIPE_LAUNCH(UPIPE_KIND_WINDOW_RECORDS, launch_window_records(p, rec, st));
-  // Neither reads what the other writes: dQ's CTAs, with the shorter tiles,
-  // take the SMs that the last of dK/dV's items leave idle.
+  // Neither reads what the other writes.  dQ is launched first and on the stream
+  // of greatest priority: a CTA of dK/dV starts where one of dQ has run out of
+  // tiles, and its counter evens out the different starts.
   struct Job {
     const CUtensorMap &q, &k, &v, &dO, &rec;
     const WinParams& p;

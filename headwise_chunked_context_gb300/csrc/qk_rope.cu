@@ -382,7 +382,8 @@ constexpr int kFwdSteps = 4, kBwdSteps = 4;  // steps in flight per warp
 constexpr int fwd_ctas(int mode, int path) { return mode == kTurn && path == kScalar ? 4 : 3; }
 
 template <int MODE, int PATH, bool WHOLE>
-__global__ void __launch_bounds__(kWarps * 32, fwd_ctas(MODE, PATH)) qk_rope_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kWarps * 32, fwd_ctas(MODE, PATH))
+    qk_rope_kernel(const __grid_constant__ QkParams p) {
   constexpr int M = Lane<PATH>::M;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 tables[kWarps][kMaxPairs];

@@ -382,7 +382,8 @@ int upipe_ce_fwd_bwd(const upipe_ce_cfg* cfg, const uint16_t* h, const uint16_t*
  *   y_a = c (x_a cos(p f_i) - x_b sin(p f_i)),
  *   y_b = c (x_a sin(p f_i) + x_b cos(p f_i)),
  * (a, b) = (i, i + rot/2) in the half layout, (2i, 2i + 1) in the
- * interleaved one; elements from rot on are copied.
+ * interleaved one; elements from rot on are copied (bit for bit, and nothing
+ * that they hold reaches another element).
  *
  * upipe_rope_freqs writes f_0 .. f_{rot/2-1} = theta^(-2i/rot) to `freqs`:
  *   UPIPE_ROPE_UNSCALED  as they are
@@ -452,6 +453,8 @@ int upipe_rope_apply(const upipe_rope* r, const upipe_qk_cfg* c, const upipe_row
 /* RMS norm of each query and key head and the rotation in one pass:
  * z = w x / sqrt(mean(x^2) + eps), then as above.  wq, wk [d] fp32, at any
  * 4-byte boundary (a parameter inside a flat buffer), as their gradients.
+ * The squares are fp32: a head with elements past 1.8e19 has an infinite mean
+ * and comes out as zeros, as 1 / sqrt(infinity) says.
  * In-place and overlap rules as upipe_rope_apply.                          */
 int upipe_qk_norm_rope_fwd(const upipe_rope* r, const upipe_qk_cfg* c, const upipe_rows* q, const upipe_rows* k,
                            const float* wq, const float* wk, const int32_t* positions, const upipe_rows* qo,
@@ -500,7 +503,8 @@ int upipe_window_fwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
 /* Gradients of sum(o * dout_o): dq [L, H, 128], dk, dv [L, Hkv, 128] bf16
  * (written), from o and lse of the forward.  Sums have one order: the same
  * inputs give the same bits.  Uses the library's second stream as the other
- * backward entries do (first backward call on a device outside capture).    */
+ * backward entries do, dQ on it (first backward call on a device outside
+ * capture).                                                                 */
 int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                      const uint16_t* o, const float* lse, const uint16_t* dout_o, uint16_t* dq, uint16_t* dk,
                      uint16_t* dv, void* ws, size_t ws_bytes, void* stream);
