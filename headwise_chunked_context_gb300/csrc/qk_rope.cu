@@ -40,7 +40,7 @@ using bf16 = __nv_bfloat16;
 constexpr int kMaxPairs = UPIPE_ROPE_MAX_D / 2;
 constexpr int kWarps = 8;  // per CTA
 
-enum Mode { kTurn = 0, kNormTurn = 1, kNormTurnBwd = 2 };
+enum Mode { kTurn = 0, kNormTurn = 1 };  // of the forward kernel
 // How a lane holds its pairs: vectors of 8 or 4 elements in either layout, or
 // single elements (half layout; interleaved pairs always lie in vectors).
 enum Path { kHalf8 = 0, kInter8 = 1, kHalf4 = 2, kInter4 = 3, kScalar = 4 };
