@@ -1,5 +1,6 @@
 // Host-side helpers shared by the entry-point files (upipe.cu for the
-// attention layer, alst.cu for the sequence-tiled MLP and loss): argument
+// attention layer, alst.cu for the sequence-tiled MLP and loss, qk_rope.cu,
+// attn_window.cu, embed.cu and residual.cu for what stands around them): argument
 // checks, device readiness, TMA tensor maps and launch accounting.  Defined
 // in upipe.cu.
 #pragma once
@@ -14,6 +15,13 @@
 namespace upipe {
 
 bool aligned16(const void* p);
+// A bf16 tensor [L, D] given as rows (its head stride says nothing): 16-byte
+// alignment of every row, and for a written tensor no element at two places.
+inline bool matrix_ok(const upipe_rows* t, int64_t L, int64_t D, bool written) {
+  constexpr int64_t kMost = int64_t(1) << 60;  // keeps offsets from overflowing
+  if (!t || !t->p || !aligned16(t->p) || t->row < 0 || t->row % 8 != 0) return false;
+  return L == 1 || (t->row <= kMost / L && (!written || t->row >= D));
+}
 // Bound of every device-side wait (UPIPE_SPIN_LIMIT_NS, default 2 s).
 uint64_t spin_limit_ns();
 // Checks that the current device is an sm_103 part and returns the address

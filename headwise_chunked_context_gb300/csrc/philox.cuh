@@ -1,0 +1,75 @@
+// Random bits of dropout masks: Philox 4x32 with ten rounds (Salmon, Moraes,
+// Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011), a
+// function of a counter and a key.  Nothing is stored: element e of a tensor
+// takes word e % 4 of the block whose counter is (e / 4, call) under the key
+// `seed`, whichever kernel asks, and however it splits the tensor.
+#pragma once
+
+#include <cstdint>
+
+#include "upipe.h"
+
+namespace upipe {
+
+// A mask as the kernels take it (upipe_dropout after its checks).
+struct Drop {
+  uint64_t seed, call, first;
+  const uint64_t* step;  // device: added to call, or null
+  uint32_t cut;          // kept iff the element's word >= cut: p = cut 2^-32
+  float factor;          // 1 / (1 - p)
+};
+
+// False: p or first out of range.  cut is p in whole steps of 2^-32, and the
+// factor is that of the steps, so that the mean is kept exactly.
+inline bool drop_of(const upipe_dropout* u, Drop* d) {
+  if (!(u->p >= 0.0) || !(u->p < 1.0) || u->first % 8 != 0) return false;
+  const double cut = static_cast<double>(static_cast<uint64_t>(u->p * 4294967296.0 + 0.5));
+  if (cut > 4294967295.0) return false;
+  if (reinterpret_cast<uintptr_t>(u->step) % sizeof(uint64_t) != 0) return false;
+  d->seed = u->seed;
+  d->call = u->call;
+  d->first = u->first;
+  d->step = u->step;
+  d->cut = static_cast<uint32_t>(cut);
+  d->factor = static_cast<float>(4294967296.0 / (4294967296.0 - cut));
+  return true;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void philox(uint64_t block, uint64_t call, uint64_t seed, uint32_t (&w)[4]) {
+  uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
+  uint32_t c2 = static_cast<uint32_t>(call), c3 = static_cast<uint32_t>(call >> 32);
+  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
+}
+
+// The call that a mask is drawn for.
+__device__ __forceinline__ uint64_t drop_call(const Drop& d) { return d.call + (d.step ? *d.step : 0); }
+
+// v[0..7], elements e .. e + 7 of the tensor (e a multiple of 8), behind the
+// mask.  A dropped element is 0 whatever it held.  One rounding per kept
+// element, and no contraction with a sum that follows: the sum of a mask with
+// p = 0 is the plain sum.
+__device__ __forceinline__ void drop8(const Drop& d, uint64_t call, uint64_t e, float (&v)[8]) {
+  const uint64_t block = (d.first + e) >> 2;
+  uint32_t w[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    philox(block + h, call, d.seed, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i] >= d.cut ? __fmul_rn(v[4 * h + i], d.factor) : 0.f;
+  }
+}
+#endif
+
+}  // namespace upipe

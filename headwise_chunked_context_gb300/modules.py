@@ -1,9 +1,11 @@
 """PyTorch autograd front end of the library: the head-chunked attention
 layer, the sequence-tiled SwiGLU MLP and the tiled LM-head loss as
 ``torch.autograd.Function`` s and ``nn.Module`` s, so that a training loop
-can use them in place of its own attention, MLP and loss; and, for a layer
-with projections of its own, what stands between them: rotary positions, the
-norms of queries and keys, and attention with a sliding window and sinks.
+can use them in place of its own attention, MLP and loss; for a layer with
+projections of its own, what stands between them: rotary positions, the norms
+of queries and keys, and attention with a sliding window and sinks; and what
+carries the residual stream between the sublayers: token embedding, dropout,
+and layer or RMS norm with the residual sum.
 
 Every forward and backward runs the library's kernels through the binding
 (``upipe.py``); nothing here computes.  Weights are held as fp32 master
@@ -224,4 +226,111 @@ def window_attention(q, k, v, window: int, sinks: int = 0):
     return _WindowFn.apply(q, k, v, window, sinks)
 
 
-__all__ = ["HeadChunkedAttention", "TiledSwiGLU", "TiledCrossEntropy", "QKNormRope", "rotate", "window_attention"]
+# ------------------------------------------------------ the residual stream
+
+class _EmbedFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, w, tokens, scale):
+        ctx.save_for_backward(tokens)
+        ctx.V, ctx.scale = w.shape[0], scale
+        return upipe.embed_forward(tokens, w, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        return upipe.embed_backward(*ctx.saved_tensors, _heads(dy), ctx.V, ctx.scale), None, None
+
+
+class TokenEmbedding(torch.nn.Module):
+    """Rows of a table, ``scale * w[tokens]`` rounded to bf16 (upipe_embed_fwd
+    / _bwd): tokens [L] int32 or int64 -> [L, D].  A negative token (padding)
+    gives zeros and has no gradient, one past the table a row of NaN.  The
+    table is read as the fp32 master parameter that it is."""
+
+    def __init__(self, V: int, D: int, scale: float = 1.0, device="cuda", init_std: float = 0.02):
+        super().__init__()
+        self.scale = scale
+        self.w = torch.nn.Parameter(torch.randn(V, D, device=device) * init_std)
+
+    def forward(self, tokens):
+        w = self.w if self.w.dtype in (torch.float32, torch.bfloat16) else self.w.float()
+        return _EmbedFn.apply(w.contiguous(), tokens.contiguous(), self.scale)
+
+
+def _step(drop):
+    return None if drop is None else drop.step
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, drop):
+        ctx.save_for_backward(drop.step)  # which also sees to it that it is the forward's
+        ctx.drop = drop
+        return upipe.dropout_forward(drop, _heads(x), None if residual is None else _heads(residual))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        ctx.saved_tensors  # raises if the step has changed
+        dx = upipe.dropout_backward(ctx.drop, _heads(dy)) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None
+
+
+def dropout(x, drop, residual=None):
+    """``residual + drop(x)`` (or ``drop(x)``) for x [L, D] bf16 and the mask
+    `drop` (upipe.Dropout; None: nothing is dropped), differentiable.  The
+    mask is a function of drop's numbers: give each call of a run numbers of
+    its own, and a recomputation the same."""
+    if drop is None:
+        if residual is None:
+            return x
+        drop = upipe.Dropout(0.0)
+    return _DropoutFn.apply(x, residual, drop)
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, w, b, eps, rms, drop):
+        ctx.set_materialize_grads(False)
+        x, w = _heads(x), w.float()
+        residual, b = None if residual is None else _heads(residual), None if b is None else b.float()
+        y, s = upipe.layer_norm_forward(x, w, b, eps, rms, residual, drop)
+        ctx.save_for_backward(s, w, _step(drop))
+        ctx.args, ctx.bias = (eps, rms, drop), b is not None
+        return y if s is x else (y, s)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, w, _ = ctx.saved_tensors
+        eps, rms, drop = ctx.args
+        if dy is None:  # nothing came through the norm
+            if ds is None:
+                return (None,) * 7
+            dx = ds if drop is None else upipe.dropout_backward(drop, _heads(ds))
+            return dx, ds, torch.zeros_like(w), torch.zeros_like(w) if ctx.bias else None, None, None, None
+        dx, dres, dw, db = upipe.layer_norm_backward(s, w, _heads(dy), None if ds is None else _heads(ds), eps, rms,
+                                                     ctx.bias, drop)
+        return dx, dres, dw, db, None, None, None
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm (rms: RMS norm) over the model width, w and b [D] fp32:
+    ``y = norm(x)`` for x [L, D] bf16, or with a residual or a mask
+    (upipe.Dropout) ``s = residual + drop(x); y = norm(s)`` in one pass, which
+    returns (y, s): s is the residual stream behind the sum.  bias None: one
+    for layer norm, none for RMS norm."""
+
+    def __init__(self, D: int, eps: float = 1e-5, rms: bool = False, bias=None, device="cuda"):
+        super().__init__()
+        self.eps, self.rms = eps, rms
+        self.w = torch.nn.Parameter(torch.ones(D, device=device))
+        bias = not rms if bias is None else bias
+        self.register_parameter("b", torch.nn.Parameter(torch.zeros(D, device=device)) if bias else None)
+
+    def forward(self, x, residual=None, dropout=None):
+        return _LayerNormFn.apply(x, residual, self.w, self.b, self.eps, self.rms, dropout)
+
+
+__all__ = ["HeadChunkedAttention", "TiledSwiGLU", "TiledCrossEntropy", "QKNormRope", "rotate", "window_attention",
+           "TokenEmbedding", "LayerNorm", "dropout"]

@@ -55,6 +55,13 @@ EXPORTS = (
     "upipe_window_workspace_bytes",
     "upipe_window_fwd",
     "upipe_window_bwd",
+    "upipe_embed_fwd",
+    "upipe_embed_workspace_bytes",
+    "upipe_embed_bwd",
+    "upipe_dropout_apply",
+    "upipe_layer_norm_fwd",
+    "upipe_layer_norm_workspace_bytes",
+    "upipe_layer_norm_bwd",
     "upipe_offload_async",
     "upipe_prefetch_async",
     "upipe_copies_join",
@@ -69,7 +76,8 @@ EXPORTS = (
 KINDS = ("rope_table", "qkv_gemm", "attn_fwd", "oproj_gemm", "do_gemm", "dwo_gemm", "attn_bwd_dq",
          "attn_bwd_dkdv", "dwqkv_gemm", "dx_gemm", "delta", "zero_rows", "alst_gu", "alst_gemm", "alst_wgrad",
          "ce_rows", "qk_rope", "norm_sum", "window_fwd", "window_dq", "window_dkdv",
-         "window_sinks", "window_records")
+         "window_sinks", "window_records", "embed_fwd", "embed_sort", "embed_bwd", "dropout", "layer_norm_fwd",
+         "layer_norm_bwd")
 
 
 class UpipeError(RuntimeError):
@@ -130,6 +138,26 @@ class QkCfg(ctypes.Structure):
 
     _fields_ = [("L", ctypes.c_int64), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("pos0", ctypes.c_int64),
                 ("eps", ctypes.c_float)]
+
+
+class EmbedCfg(ctypes.Structure):
+    """Mirror of ``upipe_embed_cfg``."""
+
+    _fields_ = [("L", ctypes.c_int64), ("V", ctypes.c_int32), ("D", ctypes.c_int32), ("wide", ctypes.c_int32),
+                ("master", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class DropoutCfg(ctypes.Structure):
+    """Mirror of ``upipe_dropout``."""
+
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("call", ctypes.c_uint64),
+                ("first", ctypes.c_uint64), ("step", ctypes.c_void_p)]
+
+
+class NormCfg(ctypes.Structure):
+    """Mirror of ``upipe_norm_cfg``."""
+
+    _fields_ = [("L", ctypes.c_int64), ("D", ctypes.c_int32), ("rms", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 @dataclass(frozen=True)
@@ -248,6 +276,21 @@ def lib() -> ctypes.CDLL:
         L.upipe_window_fwd.argtypes = [win, P, P, P, P, P, P]
         L.upipe_window_bwd.restype = ctypes.c_int
         L.upipe_window_bwd.argtypes = [win, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        emb, drop, norm = ctypes.POINTER(EmbedCfg), ctypes.POINTER(DropoutCfg), ctypes.POINTER(NormCfg)
+        L.upipe_embed_fwd.restype = ctypes.c_int
+        L.upipe_embed_fwd.argtypes = [emb, P, P, rows, P]
+        L.upipe_embed_workspace_bytes.restype = ctypes.c_size_t
+        L.upipe_embed_workspace_bytes.argtypes = [emb]
+        L.upipe_embed_bwd.restype = ctypes.c_int
+        L.upipe_embed_bwd.argtypes = [emb, P, rows, P, ctypes.c_int, P, ctypes.c_size_t, P]
+        L.upipe_dropout_apply.restype = ctypes.c_int
+        L.upipe_dropout_apply.argtypes = [drop, ctypes.c_int64, ctypes.c_int32, rows, rows, rows, P]
+        L.upipe_layer_norm_fwd.restype = ctypes.c_int
+        L.upipe_layer_norm_fwd.argtypes = [norm, drop, rows, rows, P, P, rows, rows, P]
+        L.upipe_layer_norm_workspace_bytes.restype = ctypes.c_size_t
+        L.upipe_layer_norm_workspace_bytes.argtypes = [norm]
+        L.upipe_layer_norm_bwd.restype = ctypes.c_int
+        L.upipe_layer_norm_bwd.argtypes = [norm, drop, rows, P, rows, rows, rows, rows, P, P, P, ctypes.c_size_t, P]
         L.upipe_offload_async.restype = ctypes.c_int
         L.upipe_offload_async.argtypes = [P, P, ctypes.c_size_t, P]
         L.upipe_prefetch_async.restype = ctypes.c_int
@@ -992,3 +1035,257 @@ def window_backward(cfg: WindowConfig, q, k, v, o, lse, do):
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     window_bwd(cfg, q, k, v, o, lse, do, dq, dk, dv)
     return dq, dk, dv
+
+
+# ------------------------------------------------------- the residual stream
+
+EMBED_MAX_D, NORM_MAX_D = 65536, 16384
+
+
+def _matrix(t, L, D, name, device):
+    """A bf16 [L, D] tensor, its rows at any stride that keeps them 16-byte
+    aligned, as the library's description of it; None for none."""
+    if t is None:
+        return None
+    if t.dtype != torch.bfloat16 or t.shape != (L, D):
+        _expect(t, (L, D), torch.bfloat16, name)
+    row, one = t.stride()
+    p = t.data_ptr()
+    if L == 1:  # the stride of an axis of one says nothing
+        row = 0
+    if one != 1 or row & 7 or p & 15:
+        raise ValueError(f"{name}: expected rows of contiguous elements on 16-byte boundaries, got strides "
+                         f"{(row, one)} at {p:#x}")
+    if t.get_device() != device:
+        _here(t, name)
+    return ctypes.byref(Rows(p, row, 0))
+
+
+def _two(t, name):
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name}: expected a [L, D] tensor")
+    return t.shape
+
+
+class Dropout:
+    """A dropout mask, given by numbers (upipe_dropout): the same numbers draw
+    the same mask, so a backward or a recomputation takes the forward's object.
+
+    p: chance of an element to be dropped, 0 <= p < 1.
+    seed, call: 64-bit numbers; `call` tells the masks of a run apart.
+    first: index of the first element of a tensor that is a part of a larger
+    one, a multiple of 8 (a rank's first row times D).
+    step: int64 CUDA tensor of one element that is added to `call` when the
+    kernels run, or None (a captured graph draws a new mask per replay)."""
+
+    __slots__ = ("p", "seed", "call", "first", "step", "ref", "_c")
+
+    def __init__(self, p: float, seed: int = 0, call: int = 0, first: int = 0, step=None):
+        p = float(p)
+        if not 0.0 <= p < 1.0 - 2.0 ** -33:
+            raise ValueError(f"p: expected 0 <= p < 1, got {p}")
+        for n, v in (("seed", seed), ("call", call), ("first", first)):
+            if not 0 <= v < 1 << 64:
+                raise ValueError(f"{n}: expected a number of 64 bits, got {v}")
+        if first % 8:
+            raise ValueError(f"first: expected a multiple of 8, got {first}")
+        at = None
+        if step is not None:
+            if not step.is_cuda or step.dtype != torch.int64 or step.numel() != 1:
+                raise ValueError(f"step: expected one int64 element on a CUDA device, got {tuple(step.shape)} "
+                                 f"{step.dtype} on {step.device}")
+            at = step.data_ptr()
+        self.p, self.seed, self.call, self.first, self.step = p, int(seed), int(call), int(first), step
+        self._c = DropoutCfg(p, self.seed, self.call, self.first, at)
+        self.ref = ctypes.byref(self._c)
+
+    def __reduce__(self):  # copies and pickles by value: `ref` is an address
+        return Dropout, (self.p, self.seed, self.call, self.first, self.step)
+
+    def __repr__(self):
+        return f"Dropout(p={self.p}, seed={self.seed}, call={self.call}, first={self.first}, step={self.step})"
+
+
+def _drop(drop, device):
+    """The mask's description; its `step` has to be on the call's device."""
+    if drop is None:
+        return None
+    if drop.step is not None and drop.step.get_device() != device:
+        raise ValueError(f"dropout: step is on {drop.step.device}, the call's tensors on cuda:{device}")
+    return drop.ref
+
+
+def dropout_apply(drop: Dropout, x, res, y, stream=None):
+    """upipe_dropout_apply: y = res + drop(x), or drop(x) where res is None; x,
+    res, y [L, D] bf16.  y may be x or res."""
+    if drop is None:
+        raise ValueError("drop: missing")
+    L, D = _two(x, "x")
+    if y is None:
+        raise ValueError("y: missing")
+    dev = _here(x, "x")
+    _check(lib().upipe_dropout_apply(_drop(drop, dev), L, _int32(D, "D"), _matrix(x, L, D, "x", dev),
+                                     _matrix(res, L, D, "res", dev), _matrix(y, L, D, "y", dev),
+                                     _raw(stream, dev)), "upipe_dropout_apply")
+
+
+def _int32(n, name):
+    if not -(1 << 31) <= n < 1 << 31:  # a C int of (1 << 32) + n is n
+        raise ValueError(f"{name}: {n} is past 32 bits")
+    return n
+
+
+def _given(t, D, name, device):
+    return None if t is None else _weight(t, D, name, device)
+
+
+def layer_norm_fwd(x, w, b, y, s=None, eps: float = 1e-5, rms: bool = False, residual=None, dropout=None, stream=None):
+    """upipe_layer_norm_fwd: y = norm(s) with weights w and b (or None) [D]
+    fp32, s = residual + drop(x) (written; given iff residual or dropout is)."""
+    L, D = _two(x, "x")
+    dev = _here(x, "x")
+    if (s is None) != (residual is None and dropout is None):
+        raise ValueError("s: given iff residual or dropout is")
+    if y is None:
+        raise ValueError("y: missing")
+    c = NormCfg(L, _int32(D, "D"), int(bool(rms)), eps)
+    _check(lib().upipe_layer_norm_fwd(ctypes.byref(c), _drop(dropout, dev), _matrix(x, L, D, "x", dev),
+                                      _matrix(residual, L, D, "residual", dev), _weight(w, D, "w", dev),
+                                      _given(b, D, "b", dev), _matrix(s, L, D, "s", dev), _matrix(y, L, D, "y", dev),
+                                      _raw(stream, dev)), "upipe_layer_norm_fwd")
+
+
+def layer_norm_workspace_bytes(L: int, D: int) -> int:
+    """Workspace of layer_norm_bwd; 0 for sizes that it refuses."""
+    if not all(0 <= n < 1 << 31 for n in (L, D)):
+        return 0
+    return int(lib().upipe_layer_norm_workspace_bytes(ctypes.byref(NormCfg(L, D, 0, 0.0))))
+
+
+def layer_norm_bwd(s, w, dy, ds, dres, dx, dw, db, eps: float = 1e-5, rms: bool = False, dropout=None, ws=None,
+                   stream=None):
+    """upipe_layer_norm_bwd: from s, dy and ds (or None) to dres (the gradient
+    of s), dx (behind the mask; given iff dropout is), dw and db (or None)."""
+    L, D = _two(s, "s")
+    dev = _here(s, "s")
+    for t, n in ((dy, "dy"), (dres, "dres")):
+        if t is None:
+            raise ValueError(f"{n}: missing")
+    if (dx is None) != (dropout is None):
+        raise ValueError("dx: given iff dropout is")
+    c = ctypes.byref(NormCfg(L, _int32(D, "D"), int(bool(rms)), eps))
+    args = (c, _drop(dropout, dev), _matrix(s, L, D, "s", dev), _weight(w, D, "w", dev), _matrix(dy, L, D, "dy", dev),
+            _matrix(ds, L, D, "ds", dev), _matrix(dres, L, D, "dres", dev), _matrix(dx, L, D, "dx", dev),
+            _weight(dw, D, "dw", dev), _given(db, D, "db", dev))
+    f = lib()
+    ws, nbytes = _call_ws(f.upipe_layer_norm_workspace_bytes(c), ws, s.device, stream)
+    _check(f.upipe_layer_norm_bwd(*args, ws.data_ptr(), nbytes, _raw(stream, dev)), "upipe_layer_norm_bwd")
+
+
+def _embed_call(tokens, V, D, master, scale, device):
+    """(upipe_embed_cfg, address of the tokens) of one call."""
+    if tokens is None or tokens.dim() != 1 or tokens.dtype not in (torch.int32, torch.int64):
+        raise ValueError("tokens: expected a [L] tensor of int32 or int64")
+    if tokens.get_device() != device or not tokens.is_contiguous():
+        _on_device(tokens=tokens)
+    c = EmbedCfg(tokens.shape[0], _int32(V, "V"), _int32(D, "D"), int(tokens.dtype == torch.int64), int(master), scale)
+    return ctypes.byref(c), tokens.data_ptr()
+
+
+def embed_fwd(tokens, W, y, scale: float = 1.0, stream=None):
+    """upipe_embed_fwd: y = bf16(scale W[tokens]), tokens [L] int32 or int64, W
+    [V, D] fp32 or bf16, y [L, D] bf16."""
+    V, D = _two(W, "W")
+    if W.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"W: expected fp32 or bf16, got {W.dtype}")
+    _on_device(W=W)
+    dev = W.get_device()
+    c, at = _embed_call(tokens, V, D, W.dtype == torch.float32, scale, dev)
+    if y is None:
+        raise ValueError("y: missing")
+    _check(lib().upipe_embed_fwd(c, at, W.data_ptr(), _matrix(y, tokens.shape[0], D, "y", dev), _raw(stream, dev)),
+           "upipe_embed_fwd")
+
+
+def embed_workspace_bytes(L: int, V: int, D: int) -> int:
+    """Workspace of embed_bwd; 0 for sizes that it refuses."""
+    if not all(0 <= n < 1 << 31 for n in (L, V, D)):
+        return 0
+    return int(lib().upipe_embed_workspace_bytes(ctypes.byref(EmbedCfg(L, V, D, 0, 0, 1.0))))
+
+
+def embed_bwd(tokens, dy, dW, scale: float = 1.0, add: bool = False, ws=None, stream=None):
+    """upipe_embed_bwd: dy [L, D] bf16 to dW [V, D] fp32, written or (add)
+    added to."""
+    V, D = _two(dW, "dW")
+    _expect(dW, (V, D), torch.float32, "dW")
+    _on_device(dW=dW)
+    dev = dW.get_device()
+    c, at = _embed_call(tokens, V, D, False, scale, dev)
+    if dy is None:
+        raise ValueError("dy: missing")
+    m = _matrix(dy, tokens.shape[0], D, "dy", dev)
+    f = lib()
+    ws, nbytes = _call_ws(f.upipe_embed_workspace_bytes(c), ws, dW.device, stream)
+    _check(f.upipe_embed_bwd(c, at, m, dW.data_ptr(), int(bool(add)), ws.data_ptr(), nbytes, _raw(stream, dev)),
+           "upipe_embed_bwd")
+
+
+def _new(like):
+    """A dense tensor of like's shape (empty_like keeps a broadcast's strides)."""
+    return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+
+
+def embed_forward(tokens, W, scale: float = 1.0):
+    """Allocates and returns y [L, D] bf16."""
+    _two(W, "W")
+    if tokens is None or tokens.dim() != 1:
+        raise ValueError("tokens: expected a [L] tensor of int32 or int64")
+    y = torch.empty((tokens.shape[0], W.shape[1]), dtype=torch.bfloat16, device=W.device)
+    embed_fwd(tokens, W, y, scale)
+    return y
+
+
+def embed_backward(tokens, dy, V: int, scale: float = 1.0):
+    """Allocates and returns the table's gradient dW [V, D] fp32."""
+    _two(dy, "dy")
+    dW = torch.empty((V, dy.shape[1]), dtype=torch.float32, device=dy.device)
+    embed_bwd(tokens, dy, dW, scale)
+    return dW
+
+
+def dropout_forward(drop: Dropout, x, residual=None):
+    """Allocates and returns residual + drop(x) (residual None: drop(x))."""
+    _two(x, "x")
+    y = _new(x)
+    dropout_apply(drop, x, residual, y)
+    return y
+
+
+def dropout_backward(drop: Dropout, dy):
+    """Gradient of dropout_forward's x from that of its output (the
+    residual's is dy itself)."""
+    return dropout_forward(drop, dy)
+
+
+def layer_norm_forward(x, w, b=None, eps: float = 1e-5, rms: bool = False, residual=None, dropout=None):
+    """Allocates and returns (y, s): the norm and what it is of, x itself
+    where neither residual nor dropout is given."""
+    _two(x, "x")
+    s = None if residual is None and dropout is None else _new(x)
+    y = _new(x)
+    layer_norm_fwd(x, w, b, y, s, eps, rms, residual, dropout)
+    return y, x if s is None else s
+
+
+def layer_norm_backward(s, w, dy, ds=None, eps: float = 1e-5, rms: bool = False, bias: bool = True, dropout=None):
+    """Allocates and returns (dx, dres, dw, db) of layer_norm_forward, from
+    the gradients dy of y and ds of s (or None); dx is dres without dropout,
+    db None without bias."""
+    _two(s, "s")
+    dres = _new(s)
+    dx = None if dropout is None else _new(s)
+    dw = torch.empty(s.shape[1], dtype=torch.float32, device=s.device)
+    db = torch.empty_like(dw) if bias else None
+    layer_norm_bwd(s, w, dy, ds, dres, dx, dw, db, eps, rms, dropout)
+    return dres if dx is None else dx, dres, dw, db

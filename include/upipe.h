@@ -31,7 +31,10 @@
  * upipe_ce_*, below).  For callers of the attention core it computes what
  * stands before it, rotary positions and the norms of queries and keys
  * (upipe_rope_*, upipe_qk_norm_rope_*), and the core with a sliding window
- * and sink tokens in place of the full causal mask (upipe_window_*).
+ * and sink tokens in place of the full causal mask (upipe_window_*).  Between
+ * the sublayers it computes what carries the residual stream: the token
+ * embedding (upipe_embed_*), dropout (upipe_dropout_apply), and layer or RMS
+ * norm with the residual sum and dropout in one pass (upipe_layer_norm_*).
  *
  * Conventions (readings of points the pages leave open)
  * -----------------------------------------------------
@@ -509,6 +512,115 @@ int upipe_window_bwd(const upipe_window_cfg* cfg, const uint16_t* q, const uint1
                      const uint16_t* o, const float* lse, const uint16_t* dout_o, uint16_t* dq, uint16_t* dk,
                      uint16_t* dv, void* ws, size_t ws_bytes, void* stream);
 
+/* Token embedding: y_i = bf16(scale W[t_i]).  A negative token reads zeros
+ * and leaves no gradient (padding; as a negative label of the loss), a token
+ * >= V reads NaN and leaves none (as a label >= V).
+ *   L       tokens (1 .. 2^31-1)
+ *   V       rows of the table (1 .. 2^31-1)
+ *   D       elements of a row, a multiple of 8, 8 .. UPIPE_EMBED_MAX_D
+ *   wide    1: tokens are int64_t, 0: int32_t (aligned as such)
+ *   master  1: the table is fp32 (no bf16 copy of a master weight is needed:
+ *           only the rows of the tokens are read), 0: bf16; forward only
+ *   scale   finite, e.g. 1 or sqrt(D)                                      */
+#define UPIPE_EMBED_MAX_D 65536
+typedef struct upipe_embed_cfg {
+  int64_t L;
+  int32_t V;
+  int32_t D;
+  int32_t wide;
+  int32_t master;
+  float scale;
+} upipe_embed_cfg;
+
+/*   tokens [L]   W [V, D] dense
+ *   y      [L, D] bf16 (written): rows at any stride (upipe_rows above; its
+ *          head stride says nothing)                                       */
+int upipe_embed_fwd(const upipe_embed_cfg* cfg, const void* tokens, const void* W, const upipe_rows* y, void* stream);
+
+/* Gradient of the table, dW[v] = scale (sum of the dy_i with t_i = v), by
+ * sorted tokens: the sums are fp32 and have one order, fixed by the tokens
+ * and the sizes.
+ *   dy   [L, D] bf16, rows at any stride
+ *   dW   [V, D] fp32, dense: written (add = 0; rows without a token get
+ *        zeros), or added to (add = 1: rows without a token are neither read
+ *        nor written; a head's gradient of a tied table, earlier batches')
+ *   ws   at least upipe_embed_workspace_bytes (0: invalid)                 */
+size_t upipe_embed_workspace_bytes(const upipe_embed_cfg* cfg);
+int upipe_embed_bwd(const upipe_embed_cfg* cfg, const void* tokens, const upipe_rows* dy, float* dW, int add, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* A dropout mask, given by numbers: nothing is stored, and every call with
+ * the same numbers draws the same mask.  Element e of a tensor [L, D] in
+ * row-major order (whatever its strides) is kept iff a 32-bit word is at least
+ * p 2^32, p rounded to whole steps of 2^-32, and then multiplied by 1/(1-p):
+ * word e' % 4 of Philox 4x32-10 (Salmon et al., 2011) with the counter
+ * (e' / 4, call) and the key `seed`, e' = first + e.  A dropped element is 0
+ * whatever it held.
+ *   p      0 <= p < 1 - 2^-33
+ *   call   tells the masks of one run apart (layer and step, say)
+ *   first  index of the tensor's first element, a multiple of 8: the first
+ *          row of a rank's rows times D, so that ranks draw the whole
+ *          tensor's mask
+ *   step   device address (8-byte aligned) of a number that is added to
+ *          `call` when the kernel runs, or NULL: a captured graph draws a new
+ *          mask per replay.  The backward must find the forward's number.   */
+typedef struct upipe_dropout {
+  double p;
+  uint64_t seed;
+  uint64_t call;
+  uint64_t first;
+  const uint64_t* step;
+} upipe_dropout;
+
+/* y = res + drop(x) (res NULL: drop(x)), rounded to bf16 once.  The gradient
+ * of x is the same call on that of y without res.  x, res, y [L, D] bf16, rows
+ * at any stride, D a multiple of 8, 8 or more; y may be x or res (same p and
+ * row) and must not overlap them in any other way.                         */
+int upipe_dropout_apply(const upipe_dropout* drop, int64_t L, int32_t D, const upipe_rows* x, const upipe_rows* res,
+                        const upipe_rows* y, void* stream);
+
+/* Layer norm over the model width, with the residual sum and dropout before
+ * it in the same pass:
+ *   s = bf16(res + drop(x)),  m = mean(s),  r = 1 / sqrt(mean((s - m)^2) + eps),
+ *   y = w (s - m) r + b
+ * (drop NULL: no dropout; res NULL: no sum; both NULL: s is x).
+ *   L    rows (1 .. 2^31-1)
+ *   D    row length, a multiple of 8, 8 .. UPIPE_NORM_MAX_D
+ *   rms  1: RMS norm, m = 0
+ *   eps  >= 0, finite (0: a row without spread gives NaN)
+ * Sums are fp32: elements are best below 1e19 / D in size, an infinite sum of
+ * squares gives a row of b (or NaN).                                       */
+#define UPIPE_NORM_MAX_D 16384
+typedef struct upipe_norm_cfg {
+  int64_t L;
+  int32_t D;
+  int32_t rms;
+  float eps;
+} upipe_norm_cfg;
+
+/*   x, res, s, y  [L, D] bf16, rows at any stride (s and y written); s is
+ *          given iff res or drop is, and the norm is of s as it is stored.  s
+ *          and y may each be x or res (same p and row), not both the same one
+ *   w, b   [D] fp32 at any 4-byte boundary, as their gradients; b may be NULL */
+int upipe_layer_norm_fwd(const upipe_norm_cfg* cfg, const upipe_dropout* drop, const upipe_rows* x,
+                         const upipe_rows* res, const float* w, const float* b, const upipe_rows* s,
+                         const upipe_rows* y, void* stream);
+
+/* Its gradients, from s (x without res and drop; the statistics are computed
+ * again), the gradient dy of y and, where s is used behind the norm too, the
+ * gradient ds that reaches it from there (NULL: none):
+ *   dres  gradient of s, of res, and without drop of x (written)
+ *   dx    with drop: gradient of x, dres behind the mask (written); without
+ *         it NULL.  dres and dx may each be s, dy or ds (same p and row), not
+ *         both the same one
+ *   dw    [D] fp32 (written, not accumulated), db likewise or NULL: sums over
+ *         the rows in an order fixed by the sizes
+ *   ws    at least upipe_layer_norm_workspace_bytes (0: invalid)           */
+size_t upipe_layer_norm_workspace_bytes(const upipe_norm_cfg* cfg);
+int upipe_layer_norm_bwd(const upipe_norm_cfg* cfg, const upipe_dropout* drop, const upipe_rows* s, const float* w,
+                         const upipe_rows* dy, const upipe_rows* ds, const upipe_rows* dres, const upipe_rows* dx,
+                         float* dw, float* db, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads and clears the device status word of
  * the current device.  Returns UPIPE_OK, UPIPE_ERR_DEVICE_TIMEOUT if a
  * bounded wait of any earlier call ran out, or UPIPE_ERR_CUDA.              */
@@ -550,7 +662,13 @@ int upipe_debug_wait_timeout(uint64_t limit_ns, void* stream);
 #define UPIPE_KIND_WINDOW_DKDV 20
 #define UPIPE_KIND_WINDOW_SINKS 21
 #define UPIPE_KIND_WINDOW_RECORDS 22  /* its row statistics, for the backward */
-#define UPIPE_KIND_COUNT 23
+#define UPIPE_KIND_EMBED_FWD 23
+#define UPIPE_KIND_EMBED_SORT 24  /* sort of the tokens for the table's gradient */
+#define UPIPE_KIND_EMBED_BWD 25
+#define UPIPE_KIND_DROPOUT 26
+#define UPIPE_KIND_LAYER_NORM_FWD 27
+#define UPIPE_KIND_LAYER_NORM_BWD 28
+#define UPIPE_KIND_COUNT 29
 int64_t upipe_launch_count(void);
 void upipe_profile_enable(int on);
 int upipe_profile_read(double* ms, int64_t* launches, int n);
