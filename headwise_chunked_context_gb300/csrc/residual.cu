@@ -39,8 +39,8 @@ struct NormParams {
   Mat x, res, s, y;      // forward; backward: s is read
   Mat dy, ds, dres, dx;  // backward
   const float *w, *b;
-  int team;        // threads of a row in one CTA
-  float* partial;  // backward: [row walks][2][D] shares of dw and db
+  int warps;       // of a row
+  float* partial;  // backward: [gridDim.x][2][D] shares of dw and db
 };
 
 __device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
@@ -83,108 +83,100 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
 
 // ------------------------------------------------------------------- norm
 //
-// A team of threads holds a row, two 16-byte vectors a thread, and walks rows
-// a grid apart; short rows share a CTA, long ones are split over the CTAs of a
-// cluster, so that a CTA never has more than kMaxTeam threads and two of the
-// largest fit an SM with the registers that the backward's column sums take.
-// Copies run S - 1 rows ahead, asynchronously, into slots of shared memory that
-// only the copying thread reads: there is nothing to wait for but its own
-// copies.  What the team waits for are its sums: one barrier for the mean and
-// one for the sums that need it.
-constexpr int kMaxTeam = 320;
-constexpr int kVecs = 2;  // per thread
-constexpr int kMaxSlots = 40;  // warps of a team over its cluster: 4 x 10
+// A warp holds 1024 columns of a row, a lane four 16-byte vectors of it, 512
+// bytes apart; the warps of a row are a team.  One CTA per SM holds as many
+// teams as 16 warps make, each on its own way over rows a grid apart.  Copies
+// run ahead of the arithmetic, asynchronously, into slots of shared memory that
+// only the copying lane reads: there is nothing to wait for but its own copies.
+// What a team waits for are its sums: one barrier for the mean and one for the
+// sums that need it.
+constexpr int kVecs = 4;                // per lane
+constexpr int kWarpCols = 256 * kVecs;  // columns of a warp
+constexpr int kNormWarps = 16;          // per SM
+constexpr int kMaxWarps = UPIPE_NORM_MAX_D / kWarpCols;
+static_assert(kMaxWarps <= kNormWarps, "the longest row fits a CTA");
 
 struct Team {
-  int size, teams;  // threads of a row in this CTA, rows at once
-  int id, at;       // this thread's team, its place there
-  int warps;        // of a row in this CTA
-  int lane, warp;
+  int warps;       // of a row
+  int id, teams;   // this thread's team, teams in the CTA
+  int warp, lane;  // this thread's place in its team
+  int col;         // first column of its first vector
+  bool live[kVecs];
 };
 
-__device__ __forceinline__ Team team_of(int size) {
+__device__ __forceinline__ Team team_of(const NormParams& p) {
   Team t;
-  t.size = size;
-  t.teams = blockDim.x / size;
-  t.id = threadIdx.x / size;
-  t.at = threadIdx.x - t.id * size;
-  t.warps = size / 32;
+  t.warps = p.warps;
+  t.teams = blockDim.x / (32 * p.warps);
+  t.id = (threadIdx.x >> 5) / p.warps;
+  t.warp = (threadIdx.x >> 5) - t.id * p.warps;
   t.lane = threadIdx.x & 31;
-  t.warp = t.at >> 5;
+  t.col = t.warp * kWarpCols + t.lane * 8;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) t.live[j] = t.col + j * 256 < p.D;
   return t;
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Slots of the warps' sums: two kinds of sums, each kind's by turns of two, so
+// that a set is used again two sums later at the earliest, when every thread
+// has passed the barrier between.  A row of slots belongs to a team of two warps
+// at least and is as long as the team, rounded up to four, with zeros behind.
+template <int N>
+struct Slots {
+  float f[2][N][kNormWarps * 2];
+};
+template <int N>
+__device__ __forceinline__ void clear(Slots<N>& s) {
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(s) / 4); i += blockDim.x) (&s.f[0][0][0])[i] = 0.f;
 }
 
-// Sums of N numbers over the row's team (and the other CTAs of its cluster),
-// added in one order.  slots [N][kMaxSlots], zeros behind the warps' sums: a
-// set of slots is used again two sums later at the earliest, when every thread
-// has passed the barrier between.
-template <int N, int CL>
-__device__ __forceinline__ void team_sum(float (&v)[N], float (*slots)[kMaxSlots], const Team& t) {
+// Sums of N numbers over the row's team, added in one order.
+template <int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& s, int turn, const Team& t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (CL == 1 && t.warps == 1) return;
-  if (CL == 1) {
-    if (t.lane == 0)
+  if (t.warps == 1) return;
+  const int quads = (t.warps + 3) >> 2;
+  float* slot = &s.f[turn][0][t.id * quads * 4];
+  if (t.lane == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) slots[i][t.warp] = v[i];
-    asm volatile("bar.sync %0, %1;" ::"r"(t.id + 1), "r"(t.size) : "memory");
-  } else {
-    if (t.lane < CL) {
-      const int at = static_cast<int>(cluster_rank()) * t.warps + t.warp;
-#pragma unroll
-      for (int i = 0; i < N; ++i) st_cluster(mapa_shared(smem_u32(&slots[i][at]), t.lane), v[i]);
-    }
-    __syncwarp();
-    cluster_sync();
-  }
+    for (int i = 0; i < N; ++i) slot[i * kNormWarps * 2 + t.warp] = v[i];
+  asm volatile("bar.sync %0, %1;" ::"r"(t.id + 1), "r"(t.warps * 32) : "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int k = 0; k < CL * t.warps; k += 4)
+  for (int k = 0; k < quads; ++k)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float4 f = *reinterpret_cast<const float4*>(&slots[i][k]);
+      const float4 f = *reinterpret_cast<const float4*>(slot + i * kNormWarps * 2 + k * 4);
       v[i] += (f.x + f.y) + (f.z + f.w);
     }
 }
 
-// T rows in flight, S deep; slots of this thread alone.
-template <int T, int S>
-struct Rows {
-  static constexpr int kBytes = S * T * kVecs * 16;  // per thread
-  uint32_t slot;
-  uint32_t pitch;  // from one vector's slot to the next
-  int at;
-  __device__ __forceinline__ explicit Rows(const uint8_t* ring)
-      : slot(smem_u32(ring) + threadIdx.x * 16), pitch(blockDim.x * 16), at(0) {}
-  // Starts the copies of one row: vectors at columns col[j] of row[t]; off:
-  // zeros, and nothing is read.
-  __device__ __forceinline__ void start(const bf16* const (&row)[T], const int (&col)[kVecs],
-                                        const bool (&on)[kVecs]) {
+// This lane's slots in the ring: blocks of a row's part, 2 KB of a warp each.
+constexpr int kBlock = kVecs * 512;
+__device__ __forceinline__ void copy_row(uint32_t block, const bf16* from, const Team& t) {
 #pragma unroll
-    for (int t = 0; t < T; ++t)
+  for (int j = 0; j < kVecs; ++j)
+    if (t.live[j])
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(block + j * 512), "l"(from + j * 256) : "memory");
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Dead vectors are never copied: their slots are zeros from the start.
+template <int BLOCKS>
+__device__ __forceinline__ uint32_t ring_of(const uint8_t* ring, const Team& t) {
+  const uint32_t at = smem_u32(ring) + (threadIdx.x >> 5) * (BLOCKS * kBlock) + t.lane * 16;
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const uint32_t to = slot + ((at * T + t) * kVecs + j) * pitch;
-        const bf16* from = on[j] ? row[t] + col[j] : row[t];
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on[j] ? 16 : 0)
-                     : "memory");
-      }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    at = at + 1 == S ? 0 : at + 1;
-  }
-  // The oldest row has arrived: it stands in the slot after the newest one's.
-  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory"); }
-  __device__ __forceinline__ uint4 take(int t, int j) const {
-    return ld_shared_v4(slot + ((at * T + t) * kVecs + j) * pitch);
-  }
-  static __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-};
+  for (int j = 0; j < kVecs; ++j)
+    if (!t.live[j])
+      for (int i = 0; i < BLOCKS; ++i) st_shared_v4(at + i * kBlock + j * 512, 0, 0, 0, 0);
+  return at;
+}
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
   v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
@@ -206,280 +198,284 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
   return a + b;
 }
 
-// This thread's part of a row: columns of its vectors, and whether they exist.
-template <int CL>
-__device__ __forceinline__ void my_columns(const Team& t, int D, int (&col)[kVecs], bool (&live)[kVecs]) {
-  const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
+// Vector j of a weight (at any float) as four pairs; none or dead: zeros.
+__device__ __forceinline__ void weight4(const float* w, const Team& t, int j, uint64_t (&v)[4]) {
+  const float* at = w + t.col + j * 256;
+  const bool on = t.live[j] && w != nullptr;
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    col[j] = (rank * kVecs * t.size + j * t.size + t.at) * 8;
-    live[j] = col[j] < D;
-  }
+  for (int e = 0; e < 4; ++e) v[e] = on ? f2_pack(__ldg(at + 2 * e), __ldg(at + 2 * e + 1)) : 0;
 }
 
-// A vector of a weight as four pairs; dead: zeros.
-__device__ __forceinline__ void weight4(const float* w, int col, bool live, uint64_t (&v)[4]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    v[e] = live && w ? f2_pack(__ldg(w + col + 2 * e), __ldg(w + col + 2 * e + 1)) : 0;
-}
+// Blocks of the ring per warp: rows of x (and of res), one of them being worked
+// on and the others on their way.
+__host__ __device__ constexpr int fwd_blocks(bool res) { return res ? 4 : 3; }
 
-constexpr int kFwdDepth = 4;
-__host__ __device__ constexpr int bwd_depth(bool ds) { return ds ? 3 : 4; }
-
-template <bool RES, bool DROP, int CL>
-__global__ void __launch_bounds__(kMaxTeam, 2) layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
-  constexpr int T = RES ? 2 : 1;
+template <bool RES, bool DROP>
+__global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
+  constexpr int T = RES ? 2 : 1, S = fwd_blocks(RES) / T;  // tensors, rows
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ __align__(16) float slots[4][4][1][kMaxSlots];  // of each team: two sums, each by turns of two
-  const Team t = team_of(p.team);
-  int col[kVecs];
-  bool live[kVecs];
-  my_columns<CL>(t, p.D, col, live);
-  if (CL > 1 || t.warps > 1) {
-    for (int i = threadIdx.x; i < 16 * kMaxSlots; i += blockDim.x) (&slots[0][0][0][0])[i] = 0.f;
-    if (CL > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+  __shared__ __align__(16) Slots<1> means, squares;
+  const Team t = team_of(p);
+  if (t.warps > 1) {
+    clear(means);
+    clear(squares);
+    __syncthreads();
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x / CL) * t.teams;
-  int64_t row = static_cast<int64_t>(blockIdx.x / CL) * t.teams + t.id, ahead = row;
-  Rows<T, kFwdDepth> rows(ring);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * t.teams;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * t.teams + t.id, ahead = row;
+  const uint32_t base = ring_of<T * S>(ring, t);
+  uint32_t at = base;
+  const bf16 *x = p.x.p + row * p.x.row + t.col, *res = RES ? p.res.p + row * p.res.row + t.col : nullptr;
+  bf16 *s_to = RES || DROP ? p.s.p + row * p.s.row + t.col : nullptr, *y_to = p.y.p + row * p.y.row + t.col;
   auto start = [&] {
-    const bool in = ahead < p.L;
-    const bf16* from[T];
-    from[0] = in ? p.x.p + ahead * p.x.row : p.x.p;
-    if (RES) from[T - 1] = in ? p.res.p + ahead * p.res.row : p.res.p;
-    bool on[kVecs];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) on[j] = in && live[j];
-    rows.start(from, col, on);
+    if (ahead < p.L) {
+      copy_row(at, x, t);
+      if (RES) copy_row(at + kBlock, res, t);
+      x += step * p.x.row;
+      if (RES) res += step * p.res.row;
+    }
+    commit();
+    at = at == base + (S - 1) * T * kBlock ? base : at + T * kBlock;
     ahead += step;
   };
 #pragma unroll
-  for (int i = 0; i + 1 < kFwdDepth; ++i) start();
+  for (int i = 0; i + 1 < S; ++i) start();
   uint64_t w[kVecs][4], b[kVecs][4];
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
-    weight4(p.w, col[j], live[j], w[j]);
-    weight4(p.b, col[j], live[j], b[j]);
+    weight4(p.w, t, j, w[j]);
+    weight4(p.b, t, j, b[j]);
   }
   const uint64_t call = DROP ? drop_call(p.drop) : 0;
   const float inv = 1.f / p.D;
   for (int turn = 0; row < p.L; row += step, turn ^= 1) {
     start();
-    rows.wait();
+    wait<S - 1>();  // the oldest row has arrived: it stands behind the newest one
     uint64_t s[kVecs][4];
     uint64_t sum = 0;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const uint4 x = rows.take(0, j);
+      const uint4 u = ld_shared_v4(at + j * 512);
       if (!RES && !DROP) {
-        unpack4(x, s[j]);
+        unpack4(u, s[j]);
       } else {
         float v[8];
-        unpack8(x, v);
-        if (DROP) drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + col[j], v);
+        unpack8(u, v);
+        if (DROP) drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, v);
         if (RES) {
           float r[8];
-          unpack8(rows.take(T - 1, j), r);
+          unpack8(ld_shared_v4(at + kBlock + j * 512), r);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(r[e], v[e]);
         }
-        const uint4 u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+        const uint4 z = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                    pack_bf16x2(v[6], v[7]));
-        if (live[j]) st_global_v4(p.s.p + row * p.s.row + col[j], u.x, u.y, u.z, u.w);
-        unpack4(u, s[j]);  // the norm is of s as it is stored
+        if (t.live[j]) st_global_v4(s_to + j * 256, z.x, z.y, z.z, z.w);
+        unpack4(z, s[j]);  // the norm is of s as it is stored
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum = f2_add(sum, s[j][e]);
     }
     if (!p.rms) {
       float m[1] = {f2_sum(sum)};
-      team_sum<1, CL>(m, slots[t.id & 3][turn], t);
-      const uint64_t mm = f2_both(m[0] * inv);
+      team_sum<1>(m, means, turn, t);
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j)
+      for (int j = 0; j < kVecs; ++j) {
+        const uint64_t mm = f2_both(t.live[j] ? m[0] * inv : 0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = f2_sub(s[j][e], mm);
+      }
     }
     uint64_t sq = 0;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
-      if (live[j])
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sq = f2_fma(s[j][e], s[j][e], sq);
+      for (int e = 0; e < 4; ++e) sq = f2_fma(s[j][e], s[j][e], sq);
     float q[1] = {f2_sum(sq)};
-    team_sum<1, CL>(q, slots[t.id & 3][2 + turn], t);
+    team_sum<1>(q, squares, turn, t);
     const uint64_t r = f2_both(rsqrtf(q[0] * inv + p.eps));
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       uint32_t y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = round2(f2_fma(f2_mul(s[j][e], r), w[j][e], b[j][e]));
-      if (live[j]) st_global_v4(p.y.p + row * p.y.row + col[j], y[0], y[1], y[2], y[3]);
+      if (t.live[j]) st_global_v4(y_to + j * 256, y[0], y[1], y[2], y[3]);
     }
+    if (RES || DROP) s_to += step * p.s.row;
+    y_to += step * p.y.row;
   }
-  rows.drain();
-  if (CL > 1) cluster_sync();  // nobody leaves while a peer may still write to it
+  wait<0>();
 }
 
-// Each CTA keeps its columns' sums of dw and db in registers over all of its
-// rows and writes one share of each (the teams' shares added in order), which
-// weight_sum_kernel adds up.
-template <bool DS, bool DROP, int CL>
-__global__ void __launch_bounds__(kMaxTeam, 2) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
-  constexpr int T = DS ? 3 : 2;
-  constexpr int S = bwd_depth(DS);
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ __align__(16) float slots_m[4][2][1][kMaxSlots], slots_g[4][2][3][kMaxSlots];
-  const Team t = team_of(p.team);
-  int col[kVecs];
-  bool live[kVecs];
-  my_columns<CL>(t, p.D, col, live);
-  if (CL > 1 || t.warps > 1) {
-    for (int i = threadIdx.x; i < 8 * kMaxSlots; i += blockDim.x) (&slots_m[0][0][0][0])[i] = 0.f;
-    for (int i = threadIdx.x; i < 24 * kMaxSlots; i += blockDim.x) (&slots_g[0][0][0][0])[i] = 0.f;
-    if (CL > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-  }
-  const int64_t step = static_cast<int64_t>(gridDim.x / CL) * t.teams;
-  int64_t row = static_cast<int64_t>(blockIdx.x / CL) * t.teams + t.id, ahead = row;
-  Rows<T, S> rows(ring);
+// Blocks of the ring per warp: two rows of s and dy, and one of ds, which is
+// read last: its next row is on its way from then on.  The weight stands in
+// shared memory in front of the ring, where all teams read it, once per row.
+__host__ __device__ constexpr int bwd_blocks(bool ds) { return ds ? 5 : 4; }
+
+// Each lane keeps its columns' sums of dw and db in registers over all of its
+// rows; a CTA writes one share of each (its teams' shares added in order),
+// which weight_sum_kernel adds up.
+template <bool DS, bool DROP, bool BIAS>
+__global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t shared[];
+  __shared__ __align__(16) Slots<1> means;
+  __shared__ __align__(16) Slots<3> sums;
+  const Team t = team_of(p);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * t.teams;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * t.teams + t.id, ahead = row;
+  uint8_t* ring = shared + t.warps * kWarpCols * sizeof(float);
+  const uint32_t base = ring_of<bwd_blocks(DS)>(ring, t);
+  const uint32_t weight = smem_u32(shared) + t.warp * kWarpCols * sizeof(float) + t.lane * 16;
+  const uint32_t ds_at = base + 4 * kBlock;
+  uint32_t at = 0;  // of the pair of blocks that is filled next: 0 or 2 kBlock
+  const bf16 *s = p.s.p + row * p.s.row + t.col, *dy = p.dy.p + row * p.dy.row + t.col;
+  const bf16* ds = DS ? p.ds.p + row * p.ds.row + t.col : nullptr;
+  bf16 *dres = p.dres.p + row * p.dres.row + t.col, *dx = DROP ? p.dx.p + row * p.dx.row + t.col : nullptr;
   auto start = [&] {
-    const bool in = ahead < p.L;
-    const bf16* from[T];
-    from[0] = in ? p.s.p + ahead * p.s.row : p.s.p;
-    from[1] = in ? p.dy.p + ahead * p.dy.row : p.dy.p;
-    if (DS) from[T - 1] = in ? p.ds.p + ahead * p.ds.row : p.ds.p;
-    bool on[kVecs];
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) on[j] = in && live[j];
-    rows.start(from, col, on);
+    if (ahead < p.L) {
+      copy_row(base + at, s, t);
+      copy_row(base + at + kBlock, dy, t);
+      s += step * p.s.row;
+      dy += step * p.dy.row;
+    }
+    commit();
+    at ^= 2 * kBlock;
     ahead += step;
   };
+  auto start_ds = [&](int64_t of) {
+    if (of < p.L) copy_row(ds_at, ds, t);
+    ds += step * p.ds.row;
+    commit();
+  };
+  start();
+  if (DS) start_ds(row);
+  clear(means);
+  clear(sums);
+  if (t.id == 0)  // the weight, in two planes of 16 bytes a lane
 #pragma unroll
-  for (int i = 0; i + 1 < S; ++i) start();
-  uint64_t w[kVecs][4], dw[kVecs][4], db[kVecs][4];
+    for (int j = 0; j < kVecs; ++j) {
+      uint64_t v[4];
+      weight4(p.w, t, j, v);
+      float f[8];
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    weight4(p.w, col[j], live[j], w[j]);
+      for (int e = 0; e < 4; ++e) f2_unpack(v[e], f[2 * e], f[2 * e + 1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        st_shared_v4(weight + (2 * j + h) * 512, __float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
+                     __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3]));
+    }
+  __syncthreads();
+  uint64_t dw[kVecs][4], db[kVecs][4];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw[j][e] = db[j][e] = 0;
-  }
   const uint64_t call = DROP ? drop_call(p.drop) : 0;
   const float inv = 1.f / p.D;
   for (int turn = 0; row < p.L; row += step, turn ^= 1) {
     start();
-    rows.wait();
-    uint4 su[kVecs], gu[kVecs];
-    uint64_t mm = 0;
+    wait<DS ? 2 : 1>();  // this row's s and dy
+    const uint32_t mine = base + at;
+    // Held, or read again where db's sums have the registers.
+    uint4 su[BIAS ? 1 : kVecs];
+    if (!BIAS)
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      su[j] = rows.take(0, j);
-      gu[j] = rows.take(1, j);
-    }
+      for (int j = 0; j < kVecs; ++j) su[j] = ld_shared_v4(mine + j * 512);
+    float m = 0.f;
     if (!p.rms) {
       uint64_t sum = 0;
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         uint64_t a[4];
-        unpack4(su[j], a);
+        unpack4(BIAS ? ld_shared_v4(mine + j * 512) : su[j], a);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum = f2_add(sum, a[e]);
       }
-      float m[1] = {f2_sum(sum)};
-      team_sum<1, CL>(m, slots_m[t.id & 3][turn], t);
-      mm = f2_both(m[0] * inv);
+      float v[1] = {f2_sum(sum)};
+      team_sum<1>(v, means, turn, t);
+      m = v[0] * inv;
     }
+    uint64_t g[kVecs][4];
     uint64_t sq = 0, sg = 0, sd = 0;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-      if (live[j]) {
-        uint64_t a[4], g[4];
-        unpack4(su[j], a);
-        unpack4(gu[j], g);
+    for (int j = 0; j < kVecs; ++j) {
+      const uint64_t mm = f2_both(t.live[j] ? m : 0.f);
+      const uint4 w0 = ld_shared_v4(weight + 2 * j * 512), w1 = ld_shared_v4(weight + (2 * j + 1) * 512);
+      const uint64_t w[4] = {f2_pack(__uint_as_float(w0.x), __uint_as_float(w0.y)),
+                             f2_pack(__uint_as_float(w0.z), __uint_as_float(w0.w)),
+                             f2_pack(__uint_as_float(w1.x), __uint_as_float(w1.y)),
+                             f2_pack(__uint_as_float(w1.z), __uint_as_float(w1.w))};
+      uint64_t a[4];
+      unpack4(BIAS ? ld_shared_v4(mine + j * 512) : su[j], a);
+      unpack4(ld_shared_v4(mine + kBlock + j * 512), g[j]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] = f2_sub(a[e], mm);
-          g[e] = f2_mul(g[e], w[j][e]);
-          sq = f2_fma(a[e], a[e], sq);
-          sg = f2_add(sg, g[e]);
-          sd = f2_fma(g[e], a[e], sd);
-        }
+      for (int e = 0; e < 4; ++e) {
+        a[e] = f2_sub(a[e], mm);
+        g[j][e] = f2_mul(g[j][e], w[e]);
+        sq = f2_fma(a[e], a[e], sq);
+        sg = f2_add(sg, g[j][e]);
+        sd = f2_fma(g[j][e], a[e], sd);
       }
+    }
     float v[3] = {f2_sum(sq), f2_sum(sg), f2_sum(sd)};
-    team_sum<3, CL>(v, slots_g[t.id & 3][turn], t);
+    team_sum<3>(v, sums, turn, t);
     const float r = rsqrtf(v[0] * inv + p.eps);
-    const uint64_t rr = f2_both(r);
+    const uint64_t rr = f2_both(r), mr = f2_both(-m * r);
     const uint64_t c0 = f2_both(p.rms ? 0.f : -r * (v[1] * inv));  // -r mean(g)
     const uint64_t c1 = f2_both(-r * (r * (v[2] * inv)));          // -r mean(g n)
+    if (DS) wait<1>();                                             // this row's ds
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      if (!live[j]) continue;
-      uint64_t a[4], g[4];
-      unpack4(su[j], a);
-      unpack4(gu[j], g);
+      uint64_t a[4], d[4];
+      unpack4(BIAS ? ld_shared_v4(mine + j * 512) : su[j], a);
+      unpack4(ld_shared_v4(mine + kBlock + j * 512), d);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint64_t n = f2_mul(f2_sub(a[e], mm), rr);
-        dw[j][e] = f2_fma(g[e], n, dw[j][e]);
-        db[j][e] = f2_add(db[j][e], g[e]);
-        a[e] = f2_fma(n, c1, f2_fma(f2_mul(g[e], w[j][e]), rr, c0));
+        const uint64_t n = f2_fma(a[e], rr, mr);
+        dw[j][e] = f2_fma(d[e], n, dw[j][e]);
+        if (BIAS) db[j][e] = f2_add(db[j][e], d[e]);
+        a[e] = f2_fma(n, c1, f2_fma(g[j][e], rr, c0));
       }
       if (DS) {
-        unpack4(rows.take(T - 1, j), g);
+        unpack4(ld_shared_v4(ds_at + j * 512), d);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[e] = f2_add(a[e], g[e]);
+        for (int e = 0; e < 4; ++e) a[e] = f2_add(a[e], d[e]);
       }
-      st_global_v4(p.dres.p + row * p.dres.row + col[j], round2(a[0]), round2(a[1]), round2(a[2]), round2(a[3]));
+      if (t.live[j]) st_global_v4(dres + j * 256, round2(a[0]), round2(a[1]), round2(a[2]), round2(a[3]));
       if (DROP) {
-        float d[8];
+        float f[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f2_unpack(a[e], d[2 * e], d[2 * e + 1]);
-        drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + col[j], d);
-        store8(p.dx.p + row * p.dx.row + col[j], d);
+        for (int e = 0; e < 4; ++e) f2_unpack(a[e], f[2 * e], f[2 * e + 1]);
+        drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, f);
+        if (t.live[j]) store8(dx + j * 256, f);
       }
     }
+    if (DS) start_ds(row + step);
+    dres += step * p.dres.row;
+    if (DROP) dx += step * p.dx.row;
   }
-  rows.drain();
-  float* out = p.partial + static_cast<int64_t>(blockIdx.x / CL) * 2 * p.D;
-  if (CL > 1 || t.teams == 1) {
+  wait<0>();
+  // Shares [dw][db] of the CTA; of several teams by way of the ring's memory,
+  // one half of them at a time.
+  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+#pragma unroll
+  for (int half = 0; half < (BIAS ? 2 : 1); ++half, out += p.D) {
+    float* share = t.teams == 1 ? out : reinterpret_cast<float*>(ring) + t.id * p.D;
+    __syncthreads();  // every team's copies, and the half before, have been read
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
-      if (live[j]) {
-        uint64_t* to = reinterpret_cast<uint64_t*>(out + col[j]);
-        uint64_t* to_b = reinterpret_cast<uint64_t*>(out + p.D + col[j]);
+      if (t.live[j]) {
+        uint64_t* to = reinterpret_cast<uint64_t*>(share + t.col + j * 256);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          to[e] = dw[j][e];
-          to_b[e] = db[j][e];
-        }
+        for (int e = 0; e < 4; ++e) to[e] = half ? db[j][e] : dw[j][e];
       }
-    if (CL > 1) cluster_sync();  // nobody leaves while a peer may still write to it
-    return;
-  }
-  // The teams' shares, [team][2][D], in the ring's memory.
-  float* share = reinterpret_cast<float*>(ring);
-  __syncthreads();  // every team's copies have arrived and been read
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j)
-    if (live[j]) {
-      uint64_t* to = reinterpret_cast<uint64_t*>(share + t.id * 2 * p.D + col[j]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        to[e] = dw[j][e];
-        to[p.D / 2 + e] = db[j][e];
-      }
+    if (t.teams == 1) continue;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.D; i += blockDim.x) {
+      float f = 0.f;
+      for (int k = 0; k < t.teams; ++k) f += reinterpret_cast<float*>(ring)[k * p.D + i];
+      out[i] = f;
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * p.D; i += blockDim.x) {
-    float g = 0.f;
-    for (int k = 0; k < t.teams; ++k) g += share[k * 2 * p.D + i];
-    out[i] = g;
   }
 }
 
@@ -505,8 +501,6 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const float* __restric
 
 // ------------------------------------------------------------------- host
 
-constexpr int kThreadsPerSm = 2 * kMaxTeam;
-
 bool norm_ok(const upipe_norm_cfg* c) {
   return c && c->L >= 1 && c->L <= 0x7fffffffLL && c->D >= 8 && c->D <= UPIPE_NORM_MAX_D && c->D % 8 == 0 &&
          (c->rms == 0 || c->rms == 1) && c->eps >= 0.f && std::isfinite(c->eps);
@@ -516,67 +510,52 @@ bool weight_ok(const float* w) { return w && reinterpret_cast<uintptr_t>(w) % si
 
 Mat mat_of(const upipe_rows* t) { return t ? Mat{reinterpret_cast<bf16*>(t->p), t->row} : Mat{nullptr, 0}; }
 
-// How rows of D elements lie: CTAs per row, threads of a row in one CTA, rows
-// at once in one CTA, and how many CTAs (or clusters) walk the rows.
+// How rows of D elements lie: warps of a row, rows at once in one CTA (no more
+// than it takes to give every SM one), and CTAs that walk the rows.
 struct Layout {
-  int cluster, team, teams, walks;
+  int warps, teams, ctas;
 };
 Layout layout_of(int64_t L, int D) {
   Layout y;
-  const int most = kMaxTeam * kVecs * 8;  // elements of a CTA
-  y.cluster = D <= most ? 1 : D <= 2 * most ? 2 : 4;
-  const int lanes = (D / 8 + kVecs * y.cluster - 1) / (kVecs * y.cluster);
-  y.team = (lanes + 31) / 32 * 32;
-  y.teams = y.cluster > 1 || y.team > 128 ? 1 : 256 / y.team;
+  y.warps = (D + kWarpCols - 1) / kWarpCols;
+  const int64_t want = (L + 151) / 152;
+  const int most = kNormWarps / y.warps;
+  y.teams = static_cast<int>(want < most ? want : most);
   const int64_t need = (L + y.teams - 1) / y.teams;
-  const int room = 152 * (kThreadsPerSm / (y.team * y.teams)) / y.cluster;
-  y.walks = static_cast<int>(need < room ? need : room);
+  y.ctas = static_cast<int>(need < 152 ? need : 152);
   return y;
 }
 
 template <class K>
-cudaError_t launch_rows(K kernel, const Layout& y, int bytes_per_thread, const NormParams& p, cudaStream_t st) {
-  const int threads = y.team * y.teams;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxTeam * bytes_per_thread);
+cudaError_t launch_rows(K kernel, int blocks, int weights, NormParams& p, cudaStream_t st) {
+  const Layout y = layout_of(p.L, p.D);
+  const int warps = y.warps * y.teams;
+  const int row = weights * kWarpCols * static_cast<int>(sizeof(float));  // of a warp's weights
+  const int bytes = warps * blocks * kBlock + y.warps * row;
+  // the same for every call: two threads' calls may set it in any order
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kNormWarps * blocks * kBlock + kMaxWarps * row);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(y.walks * y.cluster));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(threads) * bytes_per_thread;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(y.cluster);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = y.cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  p.warps = y.warps;
+  kernel<<<static_cast<unsigned>(y.ctas), 32 * warps, bytes, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <bool RES, bool DROP>
-cudaError_t launch_fwd(const Layout& y, const NormParams& p, cudaStream_t st) {
-  constexpr int kBytes = Rows<RES ? 2 : 1, kFwdDepth>::kBytes;
-  switch (y.cluster) {
-    case 1: return launch_rows(layer_norm_fwd_kernel<RES, DROP, 1>, y, kBytes, p, st);
-    case 2: return launch_rows(layer_norm_fwd_kernel<RES, DROP, 2>, y, kBytes, p, st);
-  }
-  return launch_rows(layer_norm_fwd_kernel<RES, DROP, 4>, y, kBytes, p, st);
+cudaError_t launch_fwd(NormParams& p, cudaStream_t st) {
+  return launch_rows(layer_norm_fwd_kernel<RES, DROP>, fwd_blocks(RES), 0, p, st);
 }
 
 template <bool DS, bool DROP>
-cudaError_t launch_bwd(const Layout& y, const NormParams& p, cudaStream_t st) {
-  constexpr int kBytes = Rows<DS ? 3 : 2, bwd_depth(DS)>::kBytes;
-  switch (y.cluster) {
-    case 1: return launch_rows(layer_norm_bwd_kernel<DS, DROP, 1>, y, kBytes, p, st);
-    case 2: return launch_rows(layer_norm_bwd_kernel<DS, DROP, 2>, y, kBytes, p, st);
-  }
-  return launch_rows(layer_norm_bwd_kernel<DS, DROP, 4>, y, kBytes, p, st);
+cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
+  return bias ? launch_rows(layer_norm_bwd_kernel<DS, DROP, true>, bwd_blocks(DS), 1, p, st)
+              : launch_rows(layer_norm_bwd_kernel<DS, DROP, false>, bwd_blocks(DS), 1, p, st);
 }
 
-cudaError_t launch_weight_sum(const NormParams& p, int walks, float* dw, float* db, cudaStream_t st) {
+cudaError_t launch_weight_sum(const NormParams& p, float* dw, float* db, cudaStream_t st) {
+  const int n = layout_of(p.L, p.D).ctas;
   const unsigned cols = static_cast<unsigned>(db ? 2 * p.D : p.D);
-  weight_sum_kernel<<<(cols + 31) / 32, dim3(32, 32), 0, st>>>(p.partial, walks, p.D, dw, db);
+  weight_sum_kernel<<<(cols + 31) / 32, dim3(32, 32), 0, st>>>(p.partial, n, p.D, dw, db);
   return cudaGetLastError();
 }
 
@@ -639,15 +618,13 @@ int upipe_layer_norm_fwd(const upipe_norm_cfg* c, const upipe_dropout* drop, con
   int* status = nullptr;
   if (int e = device_ready(&status)) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Layout lay = layout_of(c->L, c->D);
-  p.team = lay.team;
-  UPIPE_LAUNCH(UPIPE_KIND_LAYER_NORM_FWD, res ? (drop ? launch_fwd<true, true>(lay, p, st) : launch_fwd<true, false>(lay, p, st))
-                                              : (drop ? launch_fwd<false, true>(lay, p, st) : launch_fwd<false, false>(lay, p, st)));
+  UPIPE_LAUNCH(UPIPE_KIND_LAYER_NORM_FWD, res ? (drop ? launch_fwd<true, true>(p, st) : launch_fwd<true, false>(p, st))
+                                              : (drop ? launch_fwd<false, true>(p, st) : launch_fwd<false, false>(p, st)));
   return UPIPE_OK;
 }
 
 size_t upipe_layer_norm_workspace_bytes(const upipe_norm_cfg* c) {
-  return norm_ok(c) ? static_cast<size_t>(layout_of(c->L, c->D).walks) * 2 * c->D * sizeof(float) : 0;
+  return norm_ok(c) ? static_cast<size_t>(layout_of(c->L, c->D).ctas) * 2 * c->D * sizeof(float) : 0;
 }
 
 int upipe_layer_norm_bwd(const upipe_norm_cfg* c, const upipe_dropout* drop, const upipe_rows* s, const float* w,
@@ -672,12 +649,11 @@ int upipe_layer_norm_bwd(const upipe_norm_cfg* c, const upipe_dropout* drop, con
   int* status = nullptr;
   if (int e = device_ready(&status)) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Layout lay = layout_of(c->L, c->D);
-  p.team = lay.team;
+  const bool bias = db != nullptr;
   UPIPE_LAUNCH(UPIPE_KIND_LAYER_NORM_BWD,
-               ds ? (drop ? launch_bwd<true, true>(lay, p, st) : launch_bwd<true, false>(lay, p, st))
-                  : (drop ? launch_bwd<false, true>(lay, p, st) : launch_bwd<false, false>(lay, p, st)));
-  UPIPE_LAUNCH(UPIPE_KIND_NORM_SUM, launch_weight_sum(p, lay.walks, dw, db, st));
+               ds ? (drop ? launch_bwd<true, true>(p, bias, st) : launch_bwd<true, false>(p, bias, st))
+                  : (drop ? launch_bwd<false, true>(p, bias, st) : launch_bwd<false, false>(p, bias, st)));
+  UPIPE_LAUNCH(UPIPE_KIND_NORM_SUM, launch_weight_sum(p, dw, db, st));
   return UPIPE_OK;
 }
 
