@@ -13,7 +13,8 @@ namespace upipe {
 
 // A mask as the kernels take it (upipe_dropout after its checks).
 struct Drop {
-  uint64_t seed, call, first;
+  uint32_t key[20];  // of the ten rounds, which read them as operands out of constant memory
+  uint64_t call, first;
   const uint64_t* step;  // device: added to call, or null
   uint32_t cut;          // kept iff the element's word >= cut: p = cut 2^-32
   float factor;          // 1 / (1 - p)
@@ -26,7 +27,10 @@ inline bool drop_of(const upipe_dropout* u, Drop* d) {
   const double cut = static_cast<double>(static_cast<uint64_t>(u->p * 4294967296.0 + 0.5));
   if (cut > 4294967295.0) return false;
   if (reinterpret_cast<uintptr_t>(u->step) % sizeof(uint64_t) != 0) return false;
-  d->seed = u->seed;
+  for (uint32_t r = 0; r < 10; ++r) {
+    d->key[2 * r] = static_cast<uint32_t>(u->seed) + r * 0x9E3779B9u;
+    d->key[2 * r + 1] = static_cast<uint32_t>(u->seed >> 32) + r * 0xBB67AE85u;
+  }
   d->call = u->call;
   d->first = u->first;
   d->step = u->step;
@@ -36,19 +40,16 @@ inline bool drop_of(const upipe_dropout* u, Drop* d) {
 }
 
 #ifdef __CUDACC__
-__device__ __forceinline__ void philox(uint64_t block, uint64_t call, uint64_t seed, uint32_t (&w)[4]) {
+__device__ __forceinline__ void philox(uint64_t block, uint64_t call, const uint32_t (&key)[20], uint32_t (&w)[4]) {
   uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
   uint32_t c2 = static_cast<uint32_t>(call), c3 = static_cast<uint32_t>(call >> 32);
-  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ key[2 * r];
     c1 = static_cast<uint32_t>(b);
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ key[2 * r + 1];
     c3 = static_cast<uint32_t>(a);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
 }
@@ -65,7 +66,7 @@ __device__ __forceinline__ void drop8(const Drop& d, uint64_t call, uint64_t e, 
   uint32_t w[4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    philox(block + h, call, d.seed, w);
+    philox(block + h, call, d.key, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i] >= d.cut ? __fmul_rn(v[4 * h + i], d.factor) : 0.f;
   }

@@ -83,47 +83,43 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
 
 // ------------------------------------------------------------------- norm
 //
-// A warp holds 1024 columns of a row, a lane four 16-byte vectors of it, 512
-// bytes apart; the warps of a row are a team.  One CTA per SM holds as many
-// teams as 16 warps make, each on its own way over rows a grid apart.  Copies
-// run ahead of the arithmetic, asynchronously, into slots of shared memory that
-// only the copying lane reads: there is nothing to wait for but its own copies.
-// What a team waits for are its sums: one barrier for the mean and one for the
-// sums that need it.
-constexpr int kVecs = 4;                // per lane
-constexpr int kWarpCols = 256 * kVecs;  // columns of a warp
-constexpr int kNormWarps = 16;          // per SM
-constexpr int kMaxWarps = UPIPE_NORM_MAX_D / kWarpCols;
-static_assert(kMaxWarps <= kNormWarps, "the longest row fits a CTA");
+// A lane holds NV 16-byte vectors of a row, 512 bytes apart, a warp so 256 NV
+// columns; the warps of a row are a team.  One CTA per SM holds as many teams as
+// its warps make, each on its own way over rows a grid apart.  Copies run ahead
+// of the arithmetic, asynchronously, into slots of shared memory that only the
+// copying lane reads: there is nothing to wait for but its own copies.  What a
+// team waits for are its sums: one barrier for the mean and one for the sums
+// that need it.
+//
+// LEAN: RMS norm without bias; otherwise either norm, with or without one.
+__host__ __device__ constexpr int warps_of(int nv) { return nv == 4 ? 16 : nv == 2 ? 24 : 32; }  // per SM: by registers
+constexpr int kMostWarps = 32;
 
+template <int NV>
 struct Team {
   int warps;       // of a row
   int id, teams;   // this thread's team, teams in the CTA
   int warp, lane;  // this thread's place in its team
   int col;         // first column of its first vector
-  bool live[kVecs];
+  bool live[NV];
+  __device__ __forceinline__ explicit Team(const NormParams& p) {
+    warps = p.warps;
+    teams = blockDim.x / (32 * p.warps);
+    id = (threadIdx.x >> 5) / p.warps;
+    warp = (threadIdx.x >> 5) - id * p.warps;
+    lane = threadIdx.x & 31;
+    col = warp * NV * 256 + lane * 8;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) live[j] = col + j * 256 < p.D;
+  }
 };
 
-__device__ __forceinline__ Team team_of(const NormParams& p) {
-  Team t;
-  t.warps = p.warps;
-  t.teams = blockDim.x / (32 * p.warps);
-  t.id = (threadIdx.x >> 5) / p.warps;
-  t.warp = (threadIdx.x >> 5) - t.id * p.warps;
-  t.lane = threadIdx.x & 31;
-  t.col = t.warp * kWarpCols + t.lane * 8;
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j) t.live[j] = t.col + j * 256 < p.D;
-  return t;
-}
-
-// Slots of the warps' sums: two kinds of sums, each kind's by turns of two, so
-// that a set is used again two sums later at the earliest, when every thread
-// has passed the barrier between.  A row of slots belongs to a team of two warps
-// at least and is as long as the team, rounded up to four, with zeros behind.
+// Slots of the warps' sums, by turns of two: a set is used again two sums later
+// at the earliest, when every thread has passed the barrier between.  A team's
+// row of slots is as long as the team, rounded up to four, with zeros behind.
 template <int N>
 struct Slots {
-  float f[2][N][kNormWarps * 2];
+  float f[2][N][kMostWarps];
 };
 template <int N>
 __device__ __forceinline__ void clear(Slots<N>& s) {
@@ -131,34 +127,34 @@ __device__ __forceinline__ void clear(Slots<N>& s) {
 }
 
 // Sums of N numbers over the row's team, added in one order.
-template <int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& s, int turn, const Team& t) {
+template <int N, int NV>
+__device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& s, int turn, const Team<NV>& t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (t.warps == 1) return;
+  if (NV == 1 || t.warps == 1) return;  // NV = 1 holds rows of one warp only
   const int quads = (t.warps + 3) >> 2;
   float* slot = &s.f[turn][0][t.id * quads * 4];
   if (t.lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) slot[i * kNormWarps * 2 + t.warp] = v[i];
+    for (int i = 0; i < N; ++i) slot[i * kMostWarps + t.warp] = v[i];
   asm volatile("bar.sync %0, %1;" ::"r"(t.id + 1), "r"(t.warps * 32) : "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
   for (int k = 0; k < quads; ++k)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float4 f = *reinterpret_cast<const float4*>(slot + i * kNormWarps * 2 + k * 4);
+      const float4 f = *reinterpret_cast<const float4*>(slot + i * kMostWarps + k * 4);
       v[i] += (f.x + f.y) + (f.z + f.w);
     }
 }
 
-// This lane's slots in the ring: blocks of a row's part, 2 KB of a warp each.
-constexpr int kBlock = kVecs * 512;
-__device__ __forceinline__ void copy_row(uint32_t block, const bf16* from, const Team& t) {
+// This lane's slots in the ring: blocks of a row's part, 512 NV bytes of a warp.
+template <int NV>
+__device__ __forceinline__ void copy_row(uint32_t block, const bf16* from, const Team<NV>& t) {
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j)
+  for (int j = 0; j < NV; ++j)
     if (t.live[j])
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(block + j * 512), "l"(from + j * 256) : "memory");
 }
@@ -168,13 +164,13 @@ __device__ __forceinline__ void wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // Dead vectors are never copied: their slots are zeros from the start.
-template <int BLOCKS>
-__device__ __forceinline__ uint32_t ring_of(const uint8_t* ring, const Team& t) {
-  const uint32_t at = smem_u32(ring) + (threadIdx.x >> 5) * (BLOCKS * kBlock) + t.lane * 16;
+template <int BLOCKS, int NV>
+__device__ __forceinline__ uint32_t ring_of(const uint8_t* ring, const Team<NV>& t) {
+  const uint32_t at = smem_u32(ring) + (threadIdx.x >> 5) * (BLOCKS * NV * 512) + t.lane * 16;
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j)
+  for (int j = 0; j < NV; ++j)
     if (!t.live[j])
-      for (int i = 0; i < BLOCKS; ++i) st_shared_v4(at + i * kBlock + j * 512, 0, 0, 0, 0);
+      for (int i = 0; i < BLOCKS; ++i) st_shared_v4(at + (i * NV + j) * 512, 0, 0, 0, 0);
   return at;
 }
 
@@ -192,31 +188,36 @@ __device__ __forceinline__ uint32_t round2(uint64_t v) {
   return pack_bf16x2(a, b);
 }
 __device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
-__device__ __forceinline__ float f2_sum(uint64_t v) {
+template <int N>
+__device__ __forceinline__ float f2_sum(const uint64_t (&v)[N]) {
+  uint64_t s = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) s = f2_add(s, v[i]);
   float a, b;
-  f2_unpack(v, a, b);
+  f2_unpack(s, a, b);
   return a + b;
 }
 
 // Vector j of a weight (at any float) as four pairs; none or dead: zeros.
-__device__ __forceinline__ void weight4(const float* w, const Team& t, int j, uint64_t (&v)[4]) {
+template <int NV>
+__device__ __forceinline__ void weight4(const float* w, const Team<NV>& t, int j, uint64_t (&v)[4]) {
   const float* at = w + t.col + j * 256;
   const bool on = t.live[j] && w != nullptr;
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = on ? f2_pack(__ldg(at + 2 * e), __ldg(at + 2 * e + 1)) : 0;
 }
 
-// Blocks of the ring per warp: rows of x (and of res), one of them being worked
-// on and the others on their way.
-__host__ __device__ constexpr int fwd_blocks(bool res) { return res ? 4 : 3; }
+// Rows of x in the ring, or of x and res: the row being worked on, and others
+// on their way.
+__host__ __device__ constexpr int fwd_rows(bool res) { return res ? 2 : 3; }
 
-template <bool RES, bool DROP>
-__global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
-  constexpr int T = RES ? 2 : 1, S = fwd_blocks(RES) / T;  // tensors, rows
+template <int NV, bool RES, bool DROP, bool LEAN>
+__global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
+  constexpr int T = RES ? 2 : 1, S = fwd_rows(RES), kBlock = NV * 512;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) Slots<1> means, squares;
-  const Team t = team_of(p);
-  if (t.warps > 1) {
+  const Team<NV> t(p);
+  if (NV > 1) {
     clear(means);
     clear(squares);
     __syncthreads();
@@ -240,65 +241,65 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_fwd_kernel(cons
   };
 #pragma unroll
   for (int i = 0; i + 1 < S; ++i) start();
-  uint64_t w[kVecs][4], b[kVecs][4];
+  uint64_t w[NV][4], b[LEAN ? 1 : NV][4];
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
+  for (int j = 0; j < NV; ++j) {
     weight4(p.w, t, j, w[j]);
-    weight4(p.b, t, j, b[j]);
+    if (!LEAN) weight4(p.b, t, j, b[j]);
   }
   const uint64_t call = DROP ? drop_call(p.drop) : 0;
   const float inv = 1.f / p.D;
   for (int turn = 0; row < p.L; row += step, turn ^= 1) {
     start();
     wait<S - 1>();  // the oldest row has arrived: it stands behind the newest one
-    uint64_t s[kVecs][4];
-    uint64_t sum = 0;
+    uint64_t s[NV][4], sum[NV];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const uint4 u = ld_shared_v4(at + j * 512);
-      if (!RES && !DROP) {
-        unpack4(u, s[j]);
-      } else {
+    for (int j = 0; j < NV; ++j) {
+      uint4 u = ld_shared_v4(at + j * 512);
+      if (RES || DROP) {
         float v[8];
         unpack8(u, v);
-        if (DROP) drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, v);
+        if (DROP && t.live[j]) drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, v);
         if (RES) {
           float r[8];
           unpack8(ld_shared_v4(at + kBlock + j * 512), r);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(r[e], v[e]);
         }
-        const uint4 z = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                   pack_bf16x2(v[6], v[7]));
-        if (t.live[j]) st_global_v4(s_to + j * 256, z.x, z.y, z.z, z.w);
-        unpack4(z, s[j]);  // the norm is of s as it is stored
+        u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+        if (t.live[j]) st_global_v4(s_to + j * 256, u.x, u.y, u.z, u.w);
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum = f2_add(sum, s[j][e]);
+      unpack4(u, s[j]);  // the norm is of s as it is stored
+      if (!LEAN) sum[j] = f2_add(f2_add(s[j][0], s[j][1]), f2_add(s[j][2], s[j][3]));
     }
-    if (!p.rms) {
+    if (!LEAN) {
       float m[1] = {f2_sum(sum)};
-      team_sum<1>(m, means, turn, t);
+      team_sum(m, means, turn, t);
+      m[0] = p.rms ? 0.f : m[0] * inv;
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const uint64_t mm = f2_both(t.live[j] ? m[0] * inv : 0.f);
+      for (int j = 0; j < NV; ++j) {
+        const uint64_t mm = f2_both(t.live[j] ? m[0] : 0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = f2_sub(s[j][e], mm);
       }
     }
-    uint64_t sq = 0;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sq = f2_fma(s[j][e], s[j][e], sq);
-    float q[1] = {f2_sum(sq)};
-    team_sum<1>(q, squares, turn, t);
+    for (int j = 0; j < NV; ++j) {
+      sum[j] = f2_fma(s[j][0], s[j][0], f2_mul(s[j][1], s[j][1]));
+      sum[j] = f2_fma(s[j][2], s[j][2], f2_fma(s[j][3], s[j][3], sum[j]));
+    }
+    float q[1] = {f2_sum(sum)};
+    team_sum(q, squares, turn, t);
     const uint64_t r = f2_both(rsqrtf(q[0] * inv + p.eps));
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
+    for (int j = 0; j < NV; ++j) {
       uint32_t y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = round2(f2_fma(f2_mul(s[j][e], r), w[j][e], b[j][e]));
+      for (int e = 0; e < 4; ++e) {
+        s[j][e] = f2_mul(s[j][e], r);
+        y[e] = round2(LEAN ? f2_mul(s[j][e], w[j][e]) : f2_fma(s[j][e], w[j][e], b[j][e]));
+      }
       if (t.live[j]) st_global_v4(y_to + j * 256, y[0], y[1], y[2], y[3]);
     }
     if (RES || DROP) s_to += step * p.s.row;
@@ -315,17 +316,18 @@ __host__ __device__ constexpr int bwd_blocks(bool ds) { return ds ? 5 : 4; }
 // Each lane keeps its columns' sums of dw and db in registers over all of its
 // rows; a CTA writes one share of each (its teams' shares added in order),
 // which weight_sum_kernel adds up.
-template <bool DS, bool DROP, bool BIAS>
-__global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+template <int NV, bool DS, bool DROP, bool LEAN>
+__global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  constexpr int kBlock = NV * 512;
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) Slots<1> means;
-  __shared__ __align__(16) Slots<3> sums;
-  const Team t = team_of(p);
+  __shared__ __align__(16) Slots<LEAN ? 2 : 3> sums;
+  const Team<NV> t(p);
   const int64_t step = static_cast<int64_t>(gridDim.x) * t.teams;
   int64_t row = static_cast<int64_t>(blockIdx.x) * t.teams + t.id, ahead = row;
-  uint8_t* ring = shared + t.warps * kWarpCols * sizeof(float);
+  uint8_t* ring = shared + t.warps * NV * 1024;
   const uint32_t base = ring_of<bwd_blocks(DS)>(ring, t);
-  const uint32_t weight = smem_u32(shared) + t.warp * kWarpCols * sizeof(float) + t.lane * 16;
+  const uint32_t weight = smem_u32(shared) + t.warp * NV * 1024 + t.lane * 16;
   const uint32_t ds_at = base + 4 * kBlock;
   uint32_t at = 0;  // of the pair of blocks that is filled next: 0 or 2 kBlock
   const bf16 *s = p.s.p + row * p.s.row + t.col, *dy = p.dy.p + row * p.dy.row + t.col;
@@ -343,8 +345,10 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_bwd_kernel(cons
     ahead += step;
   };
   auto start_ds = [&](int64_t of) {
-    if (of < p.L) copy_row(ds_at, ds, t);
-    ds += step * p.ds.row;
+    if (of < p.L) {
+      copy_row(ds_at, ds, t);
+      ds += step * p.ds.row;
+    }
     commit();
   };
   start();
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_bwd_kernel(cons
   clear(sums);
   if (t.id == 0)  // the weight, in two planes of 16 bytes a lane
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
+    for (int j = 0; j < NV; ++j) {
       uint64_t v[4];
       weight4(p.w, t, j, v);
       float f[8];
@@ -365,9 +369,9 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_bwd_kernel(cons
                      __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3]));
     }
   __syncthreads();
-  uint64_t dw[kVecs][4], db[kVecs][4];
+  uint64_t dw[NV][4], db[NV][4];
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j)
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw[j][e] = db[j][e] = 0;
   const uint64_t call = DROP ? drop_call(p.drop) : 0;
@@ -376,78 +380,86 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_bwd_kernel(cons
     start();
     wait<DS ? 2 : 1>();  // this row's s and dy
     const uint32_t mine = base + at;
-    // Held, or read again where db's sums have the registers.
-    uint4 su[BIAS ? 1 : kVecs];
-    if (!BIAS)
+    // s is held, or read again where db's sums have the registers.
+    uint4 su[LEAN ? NV : 1];
+    if (LEAN)
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) su[j] = ld_shared_v4(mine + j * 512);
+      for (int j = 0; j < NV; ++j) su[j] = ld_shared_v4(mine + j * 512);
     float m = 0.f;
-    if (!p.rms) {
-      uint64_t sum = 0;
+    if (!LEAN) {
+      uint64_t sum[NV];
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
+      for (int j = 0; j < NV; ++j) {
         uint64_t a[4];
-        unpack4(BIAS ? ld_shared_v4(mine + j * 512) : su[j], a);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum = f2_add(sum, a[e]);
+        unpack4(ld_shared_v4(mine + j * 512), a);
+        sum[j] = f2_add(f2_add(a[0], a[1]), f2_add(a[2], a[3]));
       }
       float v[1] = {f2_sum(sum)};
-      team_sum<1>(v, means, turn, t);
-      m = v[0] * inv;
+      team_sum(v, means, turn, t);
+      m = p.rms ? 0.f : v[0] * inv;
     }
-    uint64_t g[kVecs][4];
-    uint64_t sq = 0, sg = 0, sd = 0;
+    uint64_t g[NV][4];
+    uint64_t sq[2] = {0, 0}, sg[2] = {0, 0}, sd[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const uint64_t mm = f2_both(t.live[j] ? m : 0.f);
+    for (int j = 0; j < NV; ++j) {
       const uint4 w0 = ld_shared_v4(weight + 2 * j * 512), w1 = ld_shared_v4(weight + (2 * j + 1) * 512);
       const uint64_t w[4] = {f2_pack(__uint_as_float(w0.x), __uint_as_float(w0.y)),
                              f2_pack(__uint_as_float(w0.z), __uint_as_float(w0.w)),
                              f2_pack(__uint_as_float(w1.x), __uint_as_float(w1.y)),
                              f2_pack(__uint_as_float(w1.z), __uint_as_float(w1.w))};
       uint64_t a[4];
-      unpack4(BIAS ? ld_shared_v4(mine + j * 512) : su[j], a);
+      unpack4(LEAN ? su[j] : ld_shared_v4(mine + j * 512), a);
       unpack4(ld_shared_v4(mine + kBlock + j * 512), g[j]);
+      if (!LEAN) {
+        const uint64_t mm = f2_both(t.live[j] ? m : 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = f2_sub(a[e], mm);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        a[e] = f2_sub(a[e], mm);
         g[j][e] = f2_mul(g[j][e], w[e]);
-        sq = f2_fma(a[e], a[e], sq);
-        sg = f2_add(sg, g[j][e]);
-        sd = f2_fma(g[j][e], a[e], sd);
+        sq[e & 1] = f2_fma(a[e], a[e], sq[e & 1]);
+        if (!LEAN) sg[e & 1] = f2_add(sg[e & 1], g[j][e]);
+        sd[e & 1] = f2_fma(g[j][e], a[e], sd[e & 1]);
       }
     }
-    float v[3] = {f2_sum(sq), f2_sum(sg), f2_sum(sd)};
-    team_sum<3>(v, sums, turn, t);
+    float v[LEAN ? 2 : 3];
+    v[0] = f2_sum(sq);
+    v[1] = f2_sum(sd);
+    if constexpr (!LEAN) v[2] = f2_sum(sg);
+    team_sum(v, sums, turn, t);
     const float r = rsqrtf(v[0] * inv + p.eps);
     const uint64_t rr = f2_both(r), mr = f2_both(-m * r);
-    const uint64_t c0 = f2_both(p.rms ? 0.f : -r * (v[1] * inv));  // -r mean(g)
-    const uint64_t c1 = f2_both(-r * (r * (v[2] * inv)));          // -r mean(g n)
-    if (DS) wait<1>();                                             // this row's ds
+    uint64_t c0 = 0;  // -r mean(g)
+    if constexpr (!LEAN) c0 = f2_both(p.rms ? 0.f : -r * (v[2] * inv));
+    const uint64_t c1 = f2_both(-r * (r * (v[1] * inv)));  // -r mean(g n)
+    if (DS) wait<1>();                                     // this row's ds
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
+    for (int j = 0; j < NV; ++j) {
       uint64_t a[4], d[4];
-      unpack4(BIAS ? ld_shared_v4(mine + j * 512) : su[j], a);
+      unpack4(LEAN ? su[j] : ld_shared_v4(mine + j * 512), a);
       unpack4(ld_shared_v4(mine + kBlock + j * 512), d);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint64_t n = f2_fma(a[e], rr, mr);
+        const uint64_t n = LEAN ? f2_mul(a[e], rr) : f2_fma(a[e], rr, mr);
         dw[j][e] = f2_fma(d[e], n, dw[j][e]);
-        if (BIAS) db[j][e] = f2_add(db[j][e], d[e]);
-        a[e] = f2_fma(n, c1, f2_fma(g[j][e], rr, c0));
+        if (!LEAN) db[j][e] = f2_add(db[j][e], d[e]);
+        a[e] = f2_fma(n, c1, LEAN ? f2_mul(g[j][e], rr) : f2_fma(g[j][e], rr, c0));
       }
       if (DS) {
         unpack4(ld_shared_v4(ds_at + j * 512), d);
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[e] = f2_add(a[e], d[e]);
       }
-      if (t.live[j]) st_global_v4(dres + j * 256, round2(a[0]), round2(a[1]), round2(a[2]), round2(a[3]));
-      if (DROP) {
-        float f[8];
+      if (t.live[j]) {
+        st_global_v4(dres + j * 256, round2(a[0]), round2(a[1]), round2(a[2]), round2(a[3]));
+        if (DROP) {
+          float f[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f2_unpack(a[e], f[2 * e], f[2 * e + 1]);
-        drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, f);
-        if (t.live[j]) store8(dx + j * 256, f);
+          for (int e = 0; e < 4; ++e) f2_unpack(a[e], f[2 * e], f[2 * e + 1]);
+          drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, f);
+          store8(dx + j * 256, f);
+        }
       }
     }
     if (DS) start_ds(row + step);
@@ -459,11 +471,11 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) layer_norm_bwd_kernel(cons
   // one half of them at a time.
   float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
 #pragma unroll
-  for (int half = 0; half < (BIAS ? 2 : 1); ++half, out += p.D) {
+  for (int half = 0; half < (LEAN ? 1 : 2); ++half, out += p.D) {
     float* share = t.teams == 1 ? out : reinterpret_cast<float*>(ring) + t.id * p.D;
     __syncthreads();  // every team's copies, and the half before, have been read
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
+    for (int j = 0; j < NV; ++j)
       if (t.live[j]) {
         uint64_t* to = reinterpret_cast<uint64_t*>(share + t.col + j * 256);
 #pragma unroll
@@ -510,46 +522,73 @@ bool weight_ok(const float* w) { return w && reinterpret_cast<uintptr_t>(w) % si
 
 Mat mat_of(const upipe_rows* t) { return t ? Mat{reinterpret_cast<bf16*>(t->p), t->row} : Mat{nullptr, 0}; }
 
-// How rows of D elements lie: warps of a row, rows at once in one CTA (no more
-// than it takes to give every SM one), and CTAs that walk the rows.
+// How rows of D elements lie: vectors of a lane, warps of a row, rows at once in
+// one CTA (no more than it takes to give every SM one), and CTAs that walk the
+// rows.  Four vectors a lane make the least of the sums over lanes and warps;
+// fewer, with more warps, where four would stand half empty: forward of 131072
+// rows of 256 24, 27 and 34 us with one, two and four, of 65536 rows of 1536 67,
+// 72 and 73, with the mean and the bias 105, 75 and 75, of 2048 132, 99 and 93.
 struct Layout {
-  int warps, teams, ctas;
+  int nv, warps, teams, ctas;
 };
 Layout layout_of(int64_t L, int D) {
   Layout y;
-  y.warps = (D + kWarpCols - 1) / kWarpCols;
+  y.nv = D <= 256 ? 1 : D <= 512 || (D > 1024 && D <= 1536) ? 2 : 4;
+  y.warps = (D + y.nv * 256 - 1) / (y.nv * 256);
   const int64_t want = (L + 151) / 152;
-  const int most = kNormWarps / y.warps;
+  const int most = warps_of(y.nv) / y.warps;
   y.teams = static_cast<int>(want < most ? want : most);
   const int64_t need = (L + y.teams - 1) / y.teams;
   y.ctas = static_cast<int>(need < 152 ? need : 152);
   return y;
 }
+static_assert(UPIPE_NORM_MAX_D <= 1024 * warps_of(4), "the longest row fits a CTA");
 
+// blocks: of the ring per warp; weights: whether the weight stands before it.
 template <class K>
-cudaError_t launch_rows(K kernel, int blocks, int weights, NormParams& p, cudaStream_t st) {
-  const Layout y = layout_of(p.L, p.D);
-  const int warps = y.warps * y.teams;
-  const int row = weights * kWarpCols * static_cast<int>(sizeof(float));  // of a warp's weights
-  const int bytes = warps * blocks * kBlock + y.warps * row;
+cudaError_t launch_rows(K kernel, const Layout& y, int blocks, bool weights, NormParams& p, cudaStream_t st) {
+  const int block = y.nv * 512, warps = y.warps * y.teams;
+  const int bytes = warps * blocks * block + (weights ? 2 * y.warps * block : 0);
   // the same for every call: two threads' calls may set it in any order
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kNormWarps * blocks * kBlock + kMaxWarps * row);
+                                             warps_of(y.nv) * (blocks + (weights ? 2 : 0)) * block);
   if (e != cudaSuccess) return e;
   p.warps = y.warps;
   kernel<<<static_cast<unsigned>(y.ctas), 32 * warps, bytes, st>>>(p);
   return cudaGetLastError();
 }
 
+template <int NV, bool RES, bool DROP>
+cudaError_t launch_fwd_nv(const Layout& y, NormParams& p, cudaStream_t st) {
+  constexpr int kBlocks = fwd_rows(RES) * (RES ? 2 : 1);
+  return p.rms && !p.b ? launch_rows(layer_norm_fwd_kernel<NV, RES, DROP, true>, y, kBlocks, false, p, st)
+                       : launch_rows(layer_norm_fwd_kernel<NV, RES, DROP, false>, y, kBlocks, false, p, st);
+}
+template <int NV, bool DS, bool DROP>
+cudaError_t launch_bwd_nv(const Layout& y, NormParams& p, bool bias, cudaStream_t st) {
+  constexpr int kBlocks = bwd_blocks(DS);
+  return p.rms && !bias ? launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, true>, y, kBlocks, true, p, st)
+                        : launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, false>, y, kBlocks, true, p, st);
+}
+
 template <bool RES, bool DROP>
 cudaError_t launch_fwd(NormParams& p, cudaStream_t st) {
-  return launch_rows(layer_norm_fwd_kernel<RES, DROP>, fwd_blocks(RES), 0, p, st);
+  const Layout y = layout_of(p.L, p.D);
+  switch (y.nv) {
+    case 1: return launch_fwd_nv<1, RES, DROP>(y, p, st);
+    case 2: return launch_fwd_nv<2, RES, DROP>(y, p, st);
+  }
+  return launch_fwd_nv<4, RES, DROP>(y, p, st);
 }
 
 template <bool DS, bool DROP>
 cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
-  return bias ? launch_rows(layer_norm_bwd_kernel<DS, DROP, true>, bwd_blocks(DS), 1, p, st)
-              : launch_rows(layer_norm_bwd_kernel<DS, DROP, false>, bwd_blocks(DS), 1, p, st);
+  const Layout y = layout_of(p.L, p.D);
+  switch (y.nv) {
+    case 1: return launch_bwd_nv<1, DS, DROP>(y, p, bias, st);
+    case 2: return launch_bwd_nv<2, DS, DROP>(y, p, bias, st);
+  }
+  return launch_bwd_nv<4, DS, DROP>(y, p, bias, st);
 }
 
 cudaError_t launch_weight_sum(const NormParams& p, float* dw, float* db, cudaStream_t st) {
