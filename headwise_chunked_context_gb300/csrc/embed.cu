@@ -4,9 +4,18 @@
 // leaves no gradient, a token >= V reads NaN and leaves none.  The gradient is
 // dW[v] = scale (sum over i with t_i = v of dy_i), in fp32.
 //
-// The gradient's sums have one order whatever runs when: the tokens are sorted
-// by a stable radix sort (9 bits a pass), so that a row's positions stand
-// behind one another in ascending order.
+// The gradient's sums have one order whatever runs when.  The tokens are sorted
+// by a stable radix sort (9 bits a pass; up to kSmall tokens in one CTA's shared
+// memory), so that a row's positions stand behind one another in ascending
+// order, and cut into chunks of equal length.  A CTA adds up a chunk's runs of
+// equal tokens: runs inside the chunk are a row of dW, the others leave shares,
+// which are added in the chunks' order.  Rows without a token are zeros, written
+// beside the sums by CTAs of their own, which look their rows up in the sorted
+// tokens.
+//
+// What bounds it: HBM.  The gradient reads dy once and writes V rows, most of
+// them zeros at a real vocabulary; the sort, of 4 to 12 bytes a token, is its
+// launches.
 #include <cmath>
 #include <cstring>
 
@@ -24,51 +33,67 @@ constexpr int kBins = 1 << kDigit;
 constexpr int kSortThreads = kBins;  // a thread per bin
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxTiles = 304;
+constexpr int kSmall = 8192;         // tokens that one CTA sorts alone
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr int kSlice = 2048;         // columns of a CTA of the gradient: a vector of 8 per thread
+constexpr int kMaxChunk = 64;        // positions of a chunk
+constexpr int kZeroRows = 32;        // rows of a CTA that writes zeros
+constexpr int kShort = 16;           // chunks behind its first that a short run reaches at most
+constexpr int kShortCols = 4 * kThreads;       // columns of a CTA that adds a short run's shares
+constexpr int kLongCols = 128, kLongRows = 8;  // of one that adds a long run's: columns, shares at once
 
 struct EmbedParams {
   int64_t L;
   int V, D;
-  int wide, master;  // 64-bit tokens, fp32 table
+  int wide;  // 64-bit tokens
   float scale;
   const void* tokens;
   const void* table;
   const bf16* dy;
   int64_t row;  // row stride of y or dy
   bf16* y;
-  float* dW;
-  int add;
 };
 
 __device__ __forceinline__ int64_t token_at(const void* tokens, int wide, int64_t i) {
   return wide ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
 }
 
+// A warp copies 1024 columns of a row, all of its loads open at once.
+template <bool MASTER>
 __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const __grid_constant__ EmbedParams p) {
-  for (int64_t i = blockIdx.x; i < p.L; i += gridDim.x) {
-    const int64_t t = token_at(p.tokens, p.wide, i);
-    bf16* y = p.y + i * p.row;
-    const float fill = t < 0 ? 0.f : __int_as_float(0x7fc00000);
-    const bool real = t >= 0 && t < p.V;
-    for (int c = threadIdx.x * 8; c < p.D; c += kThreads * 8) {
-      float v[8];
-      if (!real) {
+  constexpr int kVec = MASTER ? 4 : 8;  // elements of a 16-byte load
+  constexpr int kLoads = 32 / kVec;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  if (i >= p.L) return;
+  const int64_t t = token_at(p.tokens, p.wide, i);
+  const int col = blockIdx.y * 1024 + lane * kVec;
+  bf16* y = p.y + i * p.row + col;
+  const bool real = t >= 0 && t < p.V;
+  uint4 u[kLoads];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fill;
-      } else if (p.master) {
-        const float4* w = reinterpret_cast<const float4*>(static_cast<const float*>(p.table) + t * p.D + c);
-        const float4 a = w[0], b = w[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-      } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.table) + t * p.D + c);
-        v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-        v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-      }
-      if (real) {
+  for (int j = 0; j < kLoads; ++j)
+    if (real && col + j * 32 * kVec < p.D)
+      u[j] = MASTER ? ld_global_nc_v4(static_cast<const float*>(p.table) + t * p.D + col + j * 32 * kVec)
+                    : ld_global_nc_v4(static_cast<const bf16*>(p.table) + t * p.D + col + j * 32 * kVec);
+    else
+      u[j] = make_uint4(0, 0, 0, 0);
+  const uint32_t fill = t < 0 ? 0u : 0x7fc07fc0u;  // zeros or NaN
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= p.scale;
-      }
-      st_global_v4(y + c, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                   pack_bf16x2(v[6], v[7]));
+  for (int j = 0; j < kLoads; ++j) {
+    if (col + j * 32 * kVec >= p.D) continue;
+    if (MASTER) {
+      const uint32_t a = pack_bf16x2(__uint_as_float(u[j].x) * p.scale, __uint_as_float(u[j].y) * p.scale);
+      const uint32_t b = pack_bf16x2(__uint_as_float(u[j].z) * p.scale, __uint_as_float(u[j].w) * p.scale);
+      *reinterpret_cast<uint2*>(y + j * 32 * kVec) = real ? make_uint2(a, b) : make_uint2(fill, fill);
+    } else {
+      const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = real ? pack_bf16x2(bf16_lo(w[e]) * p.scale, bf16_hi(w[e]) * p.scale) : fill;
+      st_global_v4(y + j * 32 * kVec, v[0], v[1], v[2], v[3]);
     }
   }
 }
@@ -85,6 +110,7 @@ struct SortParams {
   const int2* in;
   int2* out;
   int32_t* counts;  // [tiles][kBins]
+  int* joins;       // [2], set to 0 on the way
 };
 
 __device__ __forceinline__ int2 sort_item(const SortParams& p, int64_t i) {
@@ -107,6 +133,7 @@ __device__ __forceinline__ void count_digits(const SortParams& p, int (*hist)[kB
 
 __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_constant__ SortParams p) {
   __shared__ int hist[kSortWarps][kBins];
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.joins[threadIdx.x] = 0;
   count_digits(p, hist);
   int n = 0;
 #pragma unroll
@@ -160,14 +187,103 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
   }
 }
 
+// All passes for up to kSmall tokens, in one CTA: pairs in shared memory, a part
+// of them to each warp, per pass as above.
+struct SmallSortParams {
+  int L, V, wide, passes;
+  const void* tokens;
+  int2* out;
+  int* joins;
+};
+constexpr int kSmallBytes = 2 * kSmall * sizeof(int2) + kSmallWarps * kBins * sizeof(int);
+
+__global__ void __launch_bounds__(kSmallThreads) embed_small_sort_kernel(const __grid_constant__ SmallSortParams p) {
+  extern __shared__ __align__(16) uint8_t mem[];
+  __shared__ int warp_total[kSmallWarps];
+  int2 *from = reinterpret_cast<int2*>(mem), *to = from + kSmall;
+  int(*hist)[kBins] = reinterpret_cast<int(*)[kBins]>(mem + 2 * kSmall * sizeof(int2));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < 2) p.joins[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < p.L; i += kSmallThreads) {
+    const int64_t t = token_at(p.tokens, p.wide, i);
+    from[i] = make_int2(t >= 0 && t < p.V ? static_cast<int>(t) : p.V, i);
+  }
+  const int part = (p.L + kSmallThreads - 1) / kSmallThreads * 32, first = warp * part;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * kDigit;
+    for (int i = threadIdx.x; i < kSmallWarps * kBins; i += kSmallThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+    for (int i = first + lane; i < first + part && i < p.L; i += 32)
+      atomicAdd(&hist[warp][(from[i].x >> shift) & (kBins - 1)], 1);
+    __syncthreads();
+    int all = 0, scan = 0;
+    if (threadIdx.x < kBins) {
+#pragma unroll 8
+      for (int w = 0; w < kSmallWarps; ++w) all += hist[w][threadIdx.x];
+      scan = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += up;
+      }
+      if (lane == 31) warp_total[warp] = scan;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBins) {
+      int at = scan - all;
+      for (int w = 0; w < warp; ++w) at += warp_total[w];
+#pragma unroll 8
+      for (int w = 0; w < kSmallWarps; ++w) {
+        const int n = hist[w][threadIdx.x];
+        hist[w][threadIdx.x] = at;
+        at += n;
+      }
+    }
+    __syncthreads();
+    for (int i = first + lane; i - lane < first + part && i - lane < p.L; i += 32) {
+      const bool on = i < p.L;
+      const int2 item = on ? from[i] : make_int2(0, 0);
+      const int digit = on ? (item.x >> shift) & (kBins - 1) : kBins;
+      const unsigned same = __match_any_sync(0xffffffffu, digit);
+      const int rank = __popc(same & ((1u << lane) - 1));
+      int place = 0;
+      if (on) place = hist[warp][digit] + rank;
+      __syncwarp();
+      if (on && rank == 0) hist[warp][digit] += __popc(same);
+      __syncwarp();
+      if (on) to[place] = item;
+    }
+    __syncthreads();
+    int2* swap = from;
+    from = to;
+    to = swap;
+  }
+  for (int i = threadIdx.x; i < p.L; i += kSmallThreads) p.out[i] = from[i];
+}
+
 // --------------------------------------------------------------- gradient
 
-// First of the n sorted items whose key is at least v.
-__device__ __forceinline__ int64_t lower_bound(const int2* items, int64_t n, int v) {
+struct GradParams {
+  int64_t L;
+  int V, D;
+  int chunk, chunks;  // positions of a chunk, chunks
+  int add;
+  float scale;
+  const bf16* dy;
+  int64_t row;
+  float* dW;
+  const int2* items;  // sorted (token, position)
+  float* share;       // [chunks][2][D]: of the run that began before the chunk, of the one that goes on behind it
+  int* joins;         // counters: short runs that span chunks, long ones
+  int* join;          // [2][chunks]: the chunks that they begin in
+};
+
+// First of the n sorted items whose token is at least v.
+__device__ __forceinline__ int64_t lower_bound(const int2* items, int64_t n, int64_t v) {
   int64_t lo = 0, hi = n;
   while (lo < hi) {
     const int64_t mid = (lo + hi) >> 1;
-    if (items[mid].x < v)
+    if (__ldg(&items[mid].x) < v)
       lo = mid + 1;
     else
       hi = mid;
@@ -175,21 +291,149 @@ __device__ __forceinline__ int64_t lower_bound(const int2* items, int64_t n, int
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_constant__ EmbedParams p,
-                                                             const int2* __restrict__ items) {
-  const int v = blockIdx.x;
-  const int64_t from = lower_bound(items, p.L, v), to = lower_bound(items, p.L, v + 1);
-  if (p.add && from == to) return;
-  for (int c = threadIdx.x * 8; c < p.D; c += kThreads * 8) {
-    float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int64_t i = from; i < to; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p.dy + items[i].y * p.row + c);
-      g[0] += bf16_lo(u.x), g[1] += bf16_hi(u.x), g[2] += bf16_lo(u.y), g[3] += bf16_hi(u.y);
-      g[4] += bf16_lo(u.z), g[5] += bf16_hi(u.z), g[6] += bf16_lo(u.w), g[7] += bf16_hi(u.w);
+__device__ __forceinline__ void write_row8(float* w, const float (&g)[8], float scale, int add) {
+  float4 a = make_float4(g[0] * scale, g[1] * scale, g[2] * scale, g[3] * scale);
+  float4 b = make_float4(g[4] * scale, g[5] * scale, g[6] * scale, g[7] * scale);
+  float4* to = reinterpret_cast<float4*>(w);
+  if (add) {
+    const float4 x = to[0], y = to[1];
+    a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+  }
+  to[0] = a;
+  to[1] = b;
+}
+
+// Chunks first, slice by slice, then rows to fill with zeros.
+__global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_constant__ GradParams p) {
+  const int slices = (p.D + kSlice - 1) / kSlice;
+  const int64_t block = blockIdx.x;
+  if (block >= static_cast<int64_t>(p.chunks) * slices) {
+    // Which of the CTA's rows have no token: a lane looks one up.
+    __shared__ unsigned empty;
+    const int64_t first = (block - static_cast<int64_t>(p.chunks) * slices) * kZeroRows;
+    if (threadIdx.x < 32) {
+      const int64_t v = first + threadIdx.x;
+      bool none = v < p.V;
+      if (none) {
+        const int64_t at = lower_bound(p.items, p.L, v);
+        none = at == p.L || __ldg(&p.items[at].x) != v;
+      }
+      const unsigned mask = __ballot_sync(0xffffffffu, none);
+      if (threadIdx.x == 0) empty = mask;
     }
-    float* w = p.dW + static_cast<int64_t>(v) * p.D + c;
+    __syncthreads();
+    for (unsigned left = empty; left; left &= left - 1) {
+      float4* to = reinterpret_cast<float4*>(p.dW + (first + __ffs(left) - 1) * p.D);
+      for (int c = threadIdx.x; c < p.D / 4; c += kThreads) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  __shared__ int2 items[kMaxChunk + 2];  // with the one before and the one behind
+  const int chunk = static_cast<int>(block / slices);
+  const int col = static_cast<int>(block - static_cast<int64_t>(chunk) * slices) * kSlice + threadIdx.x * 8;
+  const int64_t first = static_cast<int64_t>(chunk) * p.chunk;
+  for (int i = threadIdx.x; i < p.chunk + 2; i += kThreads) {
+    const int64_t at = first + i - 1;
+    items[i] = at >= 0 && at < p.L ? p.items[at] : make_int2(-1, 0);
+  }
+  __syncthreads();
+  const int before = items[0].x, behind = items[p.chunk + 1].x;
+  // The chunk's tokens that are rows: those without one stand at the end of all.
+  const int mine = threadIdx.x < p.chunk ? items[threadIdx.x + 1].x : -1;
+  const int n = __syncthreads_count(mine >= 0 && mine < p.V);
+  if (col == 0 && n == p.chunk && items[n].x == behind && !(items[1].x == behind && before == behind)) {
+    // A run begins here and goes on; the order of the lists says nothing.
+    const int64_t far = first + static_cast<int64_t>(kShort + 1) * p.chunk;
+    const int kind = far < p.L && p.items[far].x == behind;
+    p.join[kind * p.chunks + atomicAdd(p.joins + kind, 1)] = chunk;
+  }
+  if (col >= p.D) return;
+  const bf16* dy = p.dy + col;
+  float g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  bool began = before != items[1].x;  // the current run began in this chunk
+  constexpr int kAhead = 8;
+  for (int i = 0; i < n; i += kAhead) {
+    uint4 u[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = p.add ? fmaf(g[e], p.scale, w[e]) : from == to ? 0.f : g[e] * p.scale;
+    for (int k = 0; k < kAhead; ++k)
+      if (i + k < n) u[k] = ld_global_nc_v4(dy + items[i + k + 1].y * p.row);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i + k >= n) break;
+      g[0] += bf16_lo(u[k].x), g[1] += bf16_hi(u[k].x), g[2] += bf16_lo(u[k].y), g[3] += bf16_hi(u[k].y);
+      g[4] += bf16_lo(u[k].z), g[5] += bf16_hi(u[k].z), g[6] += bf16_lo(u[k].w), g[7] += bf16_hi(u[k].w);
+      const int token = items[i + k + 1].x;
+      if (token == items[i + k + 2].x) {
+        if (i + k + 1 < n) continue;  // the run goes on in this chunk
+      } else if (began) {             // the whole run is in this chunk
+        write_row8(p.dW + static_cast<int64_t>(token) * p.D + col, g, p.scale, p.add);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = 0.f;
+        continue;
+      }
+      write_row8(p.share + (2 * static_cast<int64_t>(chunk) + began) * p.D + col, g, 1.f, 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = 0.f;
+      began = true;
+    }
+  }
+}
+
+// Rows whose runs span chunks: the share of the chunk that a run begins in, then
+// those of the chunks behind it.  A short run's are added one after another, a
+// long run's by kLongRows rows of threads, each taking every kLongRows-th.
+__device__ __forceinline__ void add4(float4& g, const float4& f) { g.x += f.x, g.y += f.y, g.z += f.z, g.w += f.w; }
+
+__device__ __forceinline__ void write_row4(const GradParams& p, int token, int col, float4 g) {
+  float4* to = reinterpret_cast<float4*>(p.dW + static_cast<int64_t>(token) * p.D + col);
+  g.x *= p.scale, g.y *= p.scale, g.z *= p.scale, g.w *= p.scale;
+  if (p.add) add4(g, *to);
+  *to = g;
+}
+
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ GradParams p) {
+  __shared__ float4 part[kLongRows][kLongCols / 4];
+  const float4* share = reinterpret_cast<const float4*>(p.share);
+  const int64_t pitch = p.D / 4;  // of a share
+  int slices = (p.D + kShortCols - 1) / kShortCols;
+  int64_t work = static_cast<int64_t>(p.joins[0]) * slices;
+  for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
+    const int chunk = p.join[i / slices];
+    const int quad = static_cast<int>(i % slices) * kThreads + threadIdx.x;
+    if (quad >= pitch) continue;
+    const int token = p.items[static_cast<int64_t>(chunk + 1) * p.chunk].x;
+    float4 g = share[(2 * static_cast<int64_t>(chunk) + 1) * pitch + quad];
+#pragma unroll 4
+    for (int k = chunk + 1; k <= chunk + kShort && k < p.chunks; ++k) {
+      if (p.items[static_cast<int64_t>(k) * p.chunk].x != token) break;
+      add4(g, share[2 * static_cast<int64_t>(k) * pitch + quad]);
+    }
+    write_row4(p, token, quad * 4, g);
+  }
+  slices = (p.D + kLongCols - 1) / kLongCols;
+  work = static_cast<int64_t>(p.joins[1]) * slices;
+  const int row = threadIdx.x / (kLongCols / 4), lane = threadIdx.x % (kLongCols / 4);
+  for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
+    const int chunk = p.join[p.chunks + i / slices];
+    const int quad = static_cast<int>(i % slices) * (kLongCols / 4) + lane;
+    const int token = p.items[static_cast<int64_t>(chunk + 1) * p.chunk].x;
+    const int64_t end = lower_bound(p.items, p.L, static_cast<int64_t>(token) + 1);
+    const int last = static_cast<int>((end - 1) / p.chunk);  // chunk of the run's end
+    float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (quad < pitch) {
+#pragma unroll 8
+      for (int k = chunk + row; k <= last; k += kLongRows)
+        add4(g, share[(2 * static_cast<int64_t>(k) + (k == chunk)) * pitch + quad]);
+    }
+    __syncthreads();  // the sums before have been read
+    part[row][lane] = g;
+    __syncthreads();
+    if (row == 0 && quad < pitch) {
+#pragma unroll
+      for (int j = 1; j < kLongRows; ++j) add4(g, part[j][lane]);
+      write_row4(p, token, quad * 4, g);
+    }
   }
 }
 
@@ -212,21 +456,21 @@ EmbedParams embed_params(const upipe_embed_cfg* c, const void* tokens) {
   p.V = c->V;
   p.D = c->D;
   p.wide = c->wide;
-  p.master = c->master;
   p.scale = c->scale;
   p.tokens = tokens;
   return p;
 }
 
-// The sort's plan: tiles of whole rounds, as few as kMaxTiles hold, and the
-// passes that the largest key, V, takes.
-struct SortPlan {
+// The plan of a gradient: the sort's tiles (whole rounds, as few as kMaxTiles
+// hold) and passes (what the largest key, V, takes), the chunks, and the places
+// of the workspace.
+struct GradPlan {
   int64_t tile;
-  int tiles, passes;
-  size_t pairs, bytes;
+  int tiles, passes, chunk, chunks;
+  size_t pairs[2], counts, share, join, bytes;
 };
-SortPlan sort_plan(const upipe_embed_cfg* c) {
-  SortPlan s;
+GradPlan grad_plan(const upipe_embed_cfg* c) {
+  GradPlan s;
   constexpr int64_t kRound = kSortThreads;
   s.tile = (c->L + kMaxTiles - 1) / kMaxTiles;
   s.tile = s.tile < 2048 ? 2048 : (s.tile + kRound - 1) / kRound * kRound;
@@ -234,9 +478,32 @@ SortPlan sort_plan(const upipe_embed_cfg* c) {
   int bits = 1;
   while (bits < 31 && (c->V >> bits) != 0) ++bits;
   s.passes = (bits + kDigit - 1) / kDigit;
-  s.pairs = (static_cast<size_t>(c->L) * sizeof(int2) + 15) / 16 * 16;
-  s.bytes = 2 * s.pairs + static_cast<size_t>(s.tiles) * kBins * sizeof(int32_t);
+  // Long chunks leave few shares, short ones give every SM some.
+  s.chunk = kMaxChunk;
+  while (s.chunk > 8 && c->L / s.chunk < 152 * 4) s.chunk /= 2;
+  s.chunks = static_cast<int>((c->L + s.chunk - 1) / s.chunk);
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t from = at;
+    at += (bytes + 15) / 16 * 16;
+    return from;
+  };
+  s.join = take((2 + 2 * static_cast<size_t>(s.chunks)) * sizeof(int));  // the counters, then the lists
+  s.pairs[0] = take(static_cast<size_t>(c->L) * sizeof(int2));
+  const bool small = c->L <= kSmall;
+  s.pairs[1] = small ? s.pairs[0] : take(static_cast<size_t>(c->L) * sizeof(int2));
+  s.counts = small ? 0 : take(static_cast<size_t>(s.tiles) * kBins * sizeof(int32_t));
+  s.share = take(2 * static_cast<size_t>(s.chunks) * c->D * sizeof(float));
+  s.bytes = at;
   return s;
+}
+
+cudaError_t launch_small_sort(const SmallSortParams& p, cudaStream_t st) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(embed_small_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
+  if (e != cudaSuccess) return e;
+  embed_small_sort_kernel<<<1, kSmallThreads, kSmallBytes, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -256,50 +523,75 @@ int upipe_embed_fwd(const upipe_embed_cfg* c, const void* tokens, const void* W,
   p.y = reinterpret_cast<bf16*>(y->p);
   p.row = y->row;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(c->L < 152 * 8 ? c->L : 152 * 8);
-  UPIPE_LAUNCH(UPIPE_KIND_EMBED_FWD, (embed_fwd_kernel<<<grid, kThreads, 0, st>>>(p), cudaGetLastError()));
+  constexpr int kWarps = kThreads / 32;
+  const dim3 grid(static_cast<unsigned>((c->L + kWarps - 1) / kWarps), static_cast<unsigned>((c->D + 1023) / 1024));
+  UPIPE_LAUNCH(UPIPE_KIND_EMBED_FWD, ((c->master ? embed_fwd_kernel<true> : embed_fwd_kernel<false>)<<<grid, kThreads, 0, st>>>(p),
+                                      cudaGetLastError()));
   return UPIPE_OK;
 }
 
-size_t upipe_embed_workspace_bytes(const upipe_embed_cfg* c) { return embed_ok(c) ? sort_plan(c).bytes : 0; }
+size_t upipe_embed_workspace_bytes(const upipe_embed_cfg* c) { return embed_ok(c) ? grad_plan(c).bytes : 0; }
 
 int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_rows* dy, float* dW, int add, void* ws,
                     size_t ws_bytes, void* stream) {
   if (!embed_ok(c) || !tokens_ok(c, tokens) || !matrix_ok(dy, c->L, c->D, false) || !dW || !aligned16(dW))
     return UPIPE_ERR_INVALID_ARG;
   if ((add != 0 && add != 1) || !ws || !aligned16(ws)) return UPIPE_ERR_INVALID_ARG;
-  const SortPlan plan = sort_plan(c);
+  const GradPlan plan = grad_plan(c);
   if (ws_bytes < plan.bytes) return UPIPE_ERR_WS_TOO_SMALL;
   int* status = nullptr;
   if (int e = device_ready(&status)) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* at = static_cast<uint8_t*>(ws);
-  SortParams s;
-  std::memset(&s, 0, sizeof(s));
-  s.L = c->L;
-  s.tile = plan.tile;
-  s.tiles = plan.tiles;
-  s.V = c->V;
-  s.wide = c->wide;
-  s.tokens = tokens;
-  s.bits = kDigit;
-  s.counts = reinterpret_cast<int32_t*>(at + 2 * plan.pairs);
-  for (int i = 0; i < plan.passes; ++i) {
-    s.first = i == 0;
-    s.shift = i * kDigit;
-    s.in = reinterpret_cast<const int2*>(at + (i & 1 ? 0 : plan.pairs));
-    s.out = reinterpret_cast<int2*>(at + (i & 1 ? plan.pairs : 0));
-    UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
-                 (embed_count_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError()));
-    UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
-                 (embed_scatter_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError()));
+  GradParams g;
+  std::memset(&g, 0, sizeof(g));
+  g.joins = reinterpret_cast<int*>(at + plan.join);
+  g.join = g.joins + 2;
+  if (c->L <= kSmall) {
+    const SmallSortParams s{static_cast<int>(c->L), c->V, c->wide, plan.passes, tokens,
+                            reinterpret_cast<int2*>(at + plan.pairs[0]), g.joins};
+    UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT, launch_small_sort(s, st));
+    g.items = s.out;
+  } else {
+    SortParams s;
+    std::memset(&s, 0, sizeof(s));
+    s.L = c->L;
+    s.tile = plan.tile;
+    s.tiles = plan.tiles;
+    s.V = c->V;
+    s.wide = c->wide;
+    s.tokens = tokens;
+    s.bits = kDigit;
+    s.joins = g.joins;
+    s.counts = reinterpret_cast<int32_t*>(at + plan.counts);
+    for (int i = 0; i < plan.passes; ++i) {
+      s.first = i == 0;
+      s.shift = i * kDigit;
+      s.in = reinterpret_cast<const int2*>(at + plan.pairs[(i & 1) ^ 1]);
+      s.out = reinterpret_cast<int2*>(at + plan.pairs[i & 1]);
+      UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
+                   (embed_count_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError()));
+      UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
+                   (embed_scatter_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError()));
+    }
+    g.items = s.out;
   }
-  EmbedParams p = embed_params(c, tokens);
-  p.dy = reinterpret_cast<const bf16*>(dy->p);
-  p.row = dy->row;
-  p.dW = dW;
-  p.add = add;
-  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_bwd_kernel<<<c->V, kThreads, 0, st>>>(p, s.out), cudaGetLastError()));
+  g.L = c->L;
+  g.V = c->V;
+  g.D = c->D;
+  g.chunk = plan.chunk;
+  g.chunks = plan.chunks;
+  g.add = add;
+  g.scale = c->scale;
+  g.dy = reinterpret_cast<const bf16*>(dy->p);
+  g.row = dy->row;
+  g.dW = dW;
+  g.share = reinterpret_cast<float*>(at + plan.share);
+  const int64_t sums = static_cast<int64_t>(plan.chunks) * ((c->D + kSlice - 1) / kSlice);
+  const int64_t zeros = add ? 0 : (static_cast<int64_t>(c->V) + kZeroRows - 1) / kZeroRows;
+  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_bwd_kernel<<<static_cast<unsigned>(sums + zeros), kThreads, 0, st>>>(g),
+                                      cudaGetLastError()));
+  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_join_kernel<<<152 * 4, kThreads, 0, st>>>(g), cudaGetLastError()));
   return UPIPE_OK;
 }
 
