@@ -41,7 +41,7 @@ constexpr int kMaxChunk = 64;        // positions of a chunk
 constexpr int kZeroRows = 32;        // rows of a CTA that writes zeros
 constexpr int kShort = 16;           // chunks behind its first that a short run reaches at most
 constexpr int kShortCols = 4 * kThreads;       // columns of a CTA that adds a short run's shares
-constexpr int kLongCols = 128, kLongRows = 8;  // of one that adds a long run's: columns, shares at once
+constexpr int kLongCols = 32, kLongRows = 32;  // of one that adds a long run's: columns, shares at once
 
 struct EmbedParams {
   int64_t L;
@@ -100,12 +100,12 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const __grid_consta
 
 // ------------------------------------------------------------------- sort
 
-// One pass of the sort: keys by `bits` bits from `shift` on.  The first pass
+// One pass of the sort: keys by kDigit bits from `shift` on.  The first pass
 // reads the tokens (those without a row get key V, behind all rows), later
 // passes the (key, position) pairs of the pass before.
 struct SortParams {
   int64_t L, tile;  // tokens per CTA, a multiple of 32 kSortWarps
-  int tiles, V, wide, first, shift, bits;
+  int tiles, V, wide, first, shift;
   const void* tokens;
   const int2* in;
   int2* out;
@@ -113,10 +113,37 @@ struct SortParams {
   int* joins;       // [2], set to 0 on the way
 };
 
-__device__ __forceinline__ int2 sort_item(const SortParams& p, int64_t i) {
-  if (!p.first) return p.in[i];
-  const int64_t t = token_at(p.tokens, p.wide, i);
-  return make_int2(t >= 0 && t < p.V ? static_cast<int>(t) : p.V, static_cast<int>(i));
+constexpr int kBatch = 4;  // items that a lane has open at once, 32 apart
+
+// Items i, i + 32, ... of a lane; behind the last one: a digit of its own.
+__device__ __forceinline__ void sort_items(const SortParams& p, int64_t i, int64_t end, int2 (&item)[kBatch],
+                                           int (&digit)[kBatch]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    item[k] = make_int2(p.V, 0);
+    if (i + 32 * k >= end) continue;
+    if (p.first) {
+      const int64_t t = token_at(p.tokens, p.wide, i + 32 * k);
+      item[k] = make_int2(t >= 0 && t < p.V ? static_cast<int>(t) : p.V, static_cast<int>(i + 32 * k));
+    } else {
+      item[k] = __ldg(p.in + i + 32 * k);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k)
+    digit[k] = i + 32 * k < end ? (item[k].x >> p.shift) & (kBins - 1) : kBins;
+}
+
+// Ranks an item among its warp's of the same digit and counts on.
+__device__ __forceinline__ int place_of(int digit, int lane, int* row) {
+  const bool on = digit < kBins;
+  const unsigned same = __match_any_sync(0xffffffffu, digit);
+  const int rank = __popc(same & ((1u << lane) - 1));
+  const int to = on ? row[digit] + rank : 0;
+  __syncwarp();
+  if (on && rank == 0) row[digit] += __popc(same);
+  __syncwarp();
+  return to;
 }
 
 // Each warp counts the digits of its own part of the tile into its own row.
@@ -125,8 +152,14 @@ __device__ __forceinline__ void count_digits(const SortParams& p, int (*hist)[kB
   for (int i = threadIdx.x; i < kSortWarps * kBins; i += kSortThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
   const int64_t part = p.tile / kSortWarps, from = blockIdx.x * p.tile + warp * part;
-  for (int64_t i = from + lane; i < from + part; i += 32) {
-    if (i < p.L) atomicAdd(&hist[warp][(sort_item(p, i).x >> p.shift) & ((1 << p.bits) - 1)], 1);
+  const int64_t end = from + part < p.L ? from + part : p.L;
+  for (int64_t i = from; i < end; i += 32 * kBatch) {
+    int2 item[kBatch];
+    int digit[kBatch];
+    sort_items(p, i + lane, end, item, digit);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (digit[k] < kBins) atomicAdd(&hist[warp][digit[k]], 1);
   }
   __syncthreads();
 }
@@ -149,6 +182,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   count_digits(p, hist);
   int before = 0, all = 0;
+#pragma unroll 16
   for (int t = 0; t < p.tiles; ++t) {
     const int n = p.counts[static_cast<int64_t>(t) * kBins + threadIdx.x];
     all += n;
@@ -172,18 +206,16 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
   }
   __syncthreads();
   const int64_t part = p.tile / kSortWarps, from = blockIdx.x * p.tile + warp * part;
-  for (int64_t i = from + lane; i - lane < from + part; i += 32) {
-    const bool on = i < p.L;
-    const int2 item = on ? sort_item(p, i) : make_int2(0, 0);
-    const int digit = on ? (item.x >> p.shift) & ((1 << p.bits) - 1) : kBins;
-    const unsigned same = __match_any_sync(0xffffffffu, digit);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    int to = 0;
-    if (on) to = hist[warp][digit] + rank;
-    __syncwarp();
-    if (on && rank == 0) hist[warp][digit] += __popc(same);
-    __syncwarp();
-    if (on) p.out[to] = item;
+  const int64_t end = from + part < p.L ? from + part : p.L;
+  for (int64_t i = from; i < end; i += 32 * kBatch) {
+    int2 item[kBatch];
+    int digit[kBatch];
+    sort_items(p, i + lane, end, item, digit);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int to = place_of(digit[k], lane, hist[warp]);
+      if (digit[k] < kBins) p.out[to] = item[k];
+    }
   }
 }
 
@@ -241,17 +273,10 @@ __global__ void __launch_bounds__(kSmallThreads) embed_small_sort_kernel(const _
     }
     __syncthreads();
     for (int i = first + lane; i - lane < first + part && i - lane < p.L; i += 32) {
-      const bool on = i < p.L;
-      const int2 item = on ? from[i] : make_int2(0, 0);
-      const int digit = on ? (item.x >> shift) & (kBins - 1) : kBins;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
-      const int rank = __popc(same & ((1u << lane) - 1));
-      int place = 0;
-      if (on) place = hist[warp][digit] + rank;
-      __syncwarp();
-      if (on && rank == 0) hist[warp][digit] += __popc(same);
-      __syncwarp();
-      if (on) to[place] = item;
+      const int2 item = i < p.L ? from[i] : make_int2(0, 0);
+      const int digit = i < p.L ? (item.x >> shift) & (kBins - 1) : kBins;
+      const int place = place_of(digit, lane, hist[warp]);
+      if (digit < kBins) to[place] = item;
     }
     __syncthreads();
     int2* swap = from;
@@ -275,7 +300,7 @@ struct GradParams {
   const int2* items;  // sorted (token, position)
   float* share;       // [chunks][2][D]: of the run that began before the chunk, of the one that goes on behind it
   int* joins;         // counters: short runs that span chunks, long ones
-  int* join;          // [2][chunks]: the chunks that they begin in
+  int4* join;         // [2][chunks]: first chunk, last chunk, token of each
 };
 
 // First of the n sorted items whose token is at least v.
@@ -343,10 +368,25 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_consta
   const int mine = threadIdx.x < p.chunk ? items[threadIdx.x + 1].x : -1;
   const int n = __syncthreads_count(mine >= 0 && mine < p.V);
   if (col == 0 && n == p.chunk && items[n].x == behind && !(items[1].x == behind && before == behind)) {
-    // A run begins here and goes on; the order of the lists says nothing.
-    const int64_t far = first + static_cast<int64_t>(kShort + 1) * p.chunk;
-    const int kind = far < p.L && p.items[far].x == behind;
-    p.join[kind * p.chunks + atomicAdd(p.joins + kind, 1)] = chunk;
+    // A run begins here and goes on: where it ends, by strides of 1, 2, 4, ...
+    // chunks and then between the last two; the order of the lists says nothing.
+    int in = chunk + 1, past = p.chunks;  // it reaches chunk `in`, and not `past`
+    for (int by = 1; in + by < past; by *= 2) {
+      if (__ldg(&p.items[static_cast<int64_t>(in + by) * p.chunk].x) != behind) {
+        past = in + by;
+        break;
+      }
+      in += by;
+    }
+    while (past - in > 1) {
+      const int mid = (in + past) / 2;
+      if (__ldg(&p.items[static_cast<int64_t>(mid) * p.chunk].x) == behind)
+        in = mid;
+      else
+        past = mid;
+    }
+    const int kind = in - chunk > kShort;
+    p.join[kind * p.chunks + atomicAdd(p.joins + kind, 1)] = make_int4(chunk, in, behind, 0);
   }
   if (col >= p.D) return;
   const bf16* dy = p.dy + col;
@@ -396,35 +436,30 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
   __shared__ float4 part[kLongRows][kLongCols / 4];
   const float4* share = reinterpret_cast<const float4*>(p.share);
   const int64_t pitch = p.D / 4;  // of a share
+  const int counts[2] = {p.joins[0], p.joins[1]};
   int slices = (p.D + kShortCols - 1) / kShortCols;
-  int64_t work = static_cast<int64_t>(p.joins[0]) * slices;
+  int64_t work = static_cast<int64_t>(counts[0]) * slices;
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int chunk = p.join[i / slices];
+    const int4 run = p.join[i / slices];
     const int quad = static_cast<int>(i % slices) * kThreads + threadIdx.x;
     if (quad >= pitch) continue;
-    const int token = p.items[static_cast<int64_t>(chunk + 1) * p.chunk].x;
-    float4 g = share[(2 * static_cast<int64_t>(chunk) + 1) * pitch + quad];
+    const float4* from = share + 2 * static_cast<int64_t>(run.x) * pitch + quad;
+    float4 g = from[pitch];
 #pragma unroll 4
-    for (int k = chunk + 1; k <= chunk + kShort && k < p.chunks; ++k) {
-      if (p.items[static_cast<int64_t>(k) * p.chunk].x != token) break;
-      add4(g, share[2 * static_cast<int64_t>(k) * pitch + quad]);
-    }
-    write_row4(p, token, quad * 4, g);
+    for (int k = run.x + 1; k <= run.y; ++k) add4(g, *(from += 2 * pitch));
+    write_row4(p, run.z, quad * 4, g);
   }
   slices = (p.D + kLongCols - 1) / kLongCols;
-  work = static_cast<int64_t>(p.joins[1]) * slices;
+  work = static_cast<int64_t>(counts[1]) * slices;
   const int row = threadIdx.x / (kLongCols / 4), lane = threadIdx.x % (kLongCols / 4);
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int chunk = p.join[p.chunks + i / slices];
+    const int4 run = p.join[p.chunks + i / slices];
     const int quad = static_cast<int>(i % slices) * (kLongCols / 4) + lane;
-    const int token = p.items[static_cast<int64_t>(chunk + 1) * p.chunk].x;
-    const int64_t end = lower_bound(p.items, p.L, static_cast<int64_t>(token) + 1);
-    const int last = static_cast<int>((end - 1) / p.chunk);  // chunk of the run's end
     float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
     if (quad < pitch) {
 #pragma unroll 8
-      for (int k = chunk + row; k <= last; k += kLongRows)
-        add4(g, share[(2 * static_cast<int64_t>(k) + (k == chunk)) * pitch + quad]);
+      for (int k = run.x + row; k <= run.y; k += kLongRows)
+        add4(g, share[(2 * static_cast<int64_t>(k) + (k == run.x)) * pitch + quad]);
     }
     __syncthreads();  // the sums before have been read
     part[row][lane] = g;
@@ -432,7 +467,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
     if (row == 0 && quad < pitch) {
 #pragma unroll
       for (int j = 1; j < kLongRows; ++j) add4(g, part[j][lane]);
-      write_row4(p, token, quad * 4, g);
+      write_row4(p, run.z, quad * 4, g);
     }
   }
 }
@@ -488,7 +523,7 @@ GradPlan grad_plan(const upipe_embed_cfg* c) {
     at += (bytes + 15) / 16 * 16;
     return from;
   };
-  s.join = take((2 + 2 * static_cast<size_t>(s.chunks)) * sizeof(int));  // the counters, then the lists
+  s.join = take((1 + 2 * static_cast<size_t>(s.chunks)) * sizeof(int4));  // the counters, then the lists
   s.pairs[0] = take(static_cast<size_t>(c->L) * sizeof(int2));
   const bool small = c->L <= kSmall;
   s.pairs[1] = small ? s.pairs[0] : take(static_cast<size_t>(c->L) * sizeof(int2));
@@ -546,7 +581,7 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   GradParams g;
   std::memset(&g, 0, sizeof(g));
   g.joins = reinterpret_cast<int*>(at + plan.join);
-  g.join = g.joins + 2;
+  g.join = reinterpret_cast<int4*>(g.joins) + 1;
   if (c->L <= kSmall) {
     const SmallSortParams s{static_cast<int>(c->L), c->V, c->wide, plan.passes, tokens,
                             reinterpret_cast<int2*>(at + plan.pairs[0]), g.joins};
@@ -561,7 +596,6 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
     s.V = c->V;
     s.wide = c->wide;
     s.tokens = tokens;
-    s.bits = kDigit;
     s.joins = g.joins;
     s.counts = reinterpret_cast<int32_t*>(at + plan.counts);
     for (int i = 0; i < plan.passes; ++i) {
@@ -591,7 +625,7 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   const int64_t zeros = add ? 0 : (static_cast<int64_t>(c->V) + kZeroRows - 1) / kZeroRows;
   UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_bwd_kernel<<<static_cast<unsigned>(sums + zeros), kThreads, 0, st>>>(g),
                                       cudaGetLastError()));
-  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_join_kernel<<<152 * 4, kThreads, 0, st>>>(g), cudaGetLastError()));
+  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_join_kernel<<<152 * 8, kThreads, 0, st>>>(g), cudaGetLastError()));
   return UPIPE_OK;
 }
 
