@@ -165,6 +165,8 @@ __device__ __forceinline__ void count_digits(const SortParams& p, int (*hist)[kB
 }
 
 __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_constant__ SortParams p) {
+  after_previous();
+  let_next_start();
   __shared__ int hist[kSortWarps][kBins];
   if (blockIdx.x == 0 && threadIdx.x < 2) p.joins[threadIdx.x] = 0;
   count_digits(p, hist);
@@ -177,6 +179,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_
 // Where the tile's tokens go: behind all smaller digits, behind the same digit
 // of earlier tiles, of earlier warps, of earlier lanes.
 __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __grid_constant__ SortParams p) {
+  after_previous();
+  let_next_start();
   __shared__ int hist[kSortWarps][kBins];
   __shared__ int warp_total[kSortWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,6 +234,7 @@ struct SmallSortParams {
 constexpr int kSmallBytes = 2 * kSmall * sizeof(int2) + kSmallWarps * kBins * sizeof(int);
 
 __global__ void __launch_bounds__(kSmallThreads) embed_small_sort_kernel(const __grid_constant__ SmallSortParams p) {
+  let_next_start();
   extern __shared__ __align__(16) uint8_t mem[];
   __shared__ int warp_total[kSmallWarps];
   int2 *from = reinterpret_cast<int2*>(mem), *to = from + kSmall;
@@ -331,6 +336,8 @@ __device__ __forceinline__ void write_row8(float* w, const float (&g)[8], float 
 
 // Chunks first, slice by slice, then rows to fill with zeros.
 __global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_constant__ GradParams p) {
+  after_previous();
+  let_next_start();
   const int slices = (p.D + kSlice - 1) / kSlice;
   const int64_t block = blockIdx.x;
   if (block >= static_cast<int64_t>(p.chunks) * slices) {
@@ -433,6 +440,7 @@ __device__ __forceinline__ void write_row4(const GradParams& p, int token, int c
 }
 
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ GradParams p) {
+  after_previous();
   __shared__ float4 part[kLongRows][kLongCols / 4];
   const float4* share = reinterpret_cast<const float4*>(p.share);
   const int64_t pitch = p.D / 4;  // of a share
@@ -604,9 +612,10 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
       s.in = reinterpret_cast<const int2*>(at + plan.pairs[(i & 1) ^ 1]);
       s.out = reinterpret_cast<int2*>(at + plan.pairs[i & 1]);
       UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
-                   (embed_count_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError()));
+                   (i ? launch_next(embed_count_kernel, plan.tiles, kSortThreads, 0, st, s)
+                      : (embed_count_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError())));
       UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
-                   (embed_scatter_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError()));
+                   launch_next(embed_scatter_kernel, plan.tiles, kSortThreads, 0, st, s));
     }
     g.items = s.out;
   }
@@ -623,9 +632,9 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   g.share = reinterpret_cast<float*>(at + plan.share);
   const int64_t sums = static_cast<int64_t>(plan.chunks) * ((c->D + kSlice - 1) / kSlice);
   const int64_t zeros = add ? 0 : (static_cast<int64_t>(c->V) + kZeroRows - 1) / kZeroRows;
-  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_bwd_kernel<<<static_cast<unsigned>(sums + zeros), kThreads, 0, st>>>(g),
-                                      cudaGetLastError()));
-  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, (embed_join_kernel<<<152 * 8, kThreads, 0, st>>>(g), cudaGetLastError()));
+  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD,
+               launch_next(embed_bwd_kernel, static_cast<unsigned>(sums + zeros), kThreads, 0, st, g));
+  UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, launch_next(embed_join_kernel, 152 * 8, kThreads, 0, st, g));
   return UPIPE_OK;
 }
 

@@ -61,6 +61,25 @@ cudaError_t counted(int kind, cudaStream_t st, F&& launch) {
   return e;
 }
 
+// Launches a kernel that may be made ready while the one before it on the stream
+// still runs.  Every thread of it begins with after_previous() (sm103_ptx.cuh),
+// so that it touches nothing before that one has ended; the one before allows it
+// by let_next_start().
+template <class P>
+cudaError_t launch_next(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Runs two launches that read nothing of each other's at once: `side` on the
 // device's second stream (greatest priority, forked from `st` and joined back
 // by events), `own` on `st`; both on `st`, one after the other, while another

@@ -499,6 +499,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// Between kernels launched behind one another (launch_next in host.h): the
+// earlier one lets the next be made ready; that one waits, at its beginning, for
+// the end of the earlier one and sees what it wrote.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Paired fp32 arithmetic (two lanes of fp32 in one 64-bit register pair),
 // which halves the issue slots of the softmax element-wise math.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
