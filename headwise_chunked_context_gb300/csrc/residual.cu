@@ -43,8 +43,7 @@ struct NormParams {
   float* partial;  // backward: [gridDim.x][2][D] shares of dw and db
 };
 
-__device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
   v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
   v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
 }
@@ -57,28 +56,62 @@ __device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
 struct DropParams {
   int64_t L;
   int D;
+  int across;  // threads of a row (rows at a stride)
   Drop drop;
   Mat x, res, y;
 };
 
+// Vectors of 8 elements; every load of a thread is open before the first mask is
+// drawn.  FLAT: dense tensors are one long row.
+constexpr int kDropVecs = 4;
+
+template <bool RES, bool FLAT>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropParams p) {
   const int per = p.D / 8;
-  const int64_t n = p.L * per, stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  const uint64_t call = drop_call(p.drop);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
-    const int64_t row = i / per;
-    const int col = static_cast<int>(i - row * per) * 8;
-    float v[8];
-    load8(p.x.p + row * p.x.row + col, v);
-    drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + col, v);
-    if (p.res.p) {
-      float r[8];
-      load8(p.res.p + row * p.res.row + col, r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(r[e], v[e]);
-    }
-    store8(p.y.p + row * p.y.row + col, v);
+  int64_t row = 0, at, end;
+  int step = kThreads;
+  if (FLAT) {
+    at = static_cast<int64_t>(blockIdx.x) * (kThreads * kDropVecs) + threadIdx.x;
+    end = p.L * per;
+  } else {
+    const int y = threadIdx.x / p.across;
+    row = static_cast<int64_t>(blockIdx.x) * (kThreads / p.across) + y;
+    if (row >= p.L) return;
+    step = p.across;
+    at = threadIdx.x - y * p.across;
+    end = per;
   }
+  const uint64_t call = drop_call(p.drop);
+  const bf16 *x = p.x.p + row * p.x.row, *res = RES ? p.res.p + row * p.res.row : nullptr;
+  bf16* y = p.y.p + row * p.y.row;
+  do {
+    uint4 u[kDropVecs], r[RES ? kDropVecs : 1];
+#pragma unroll
+    for (int j = 0; j < kDropVecs; ++j) {
+      const int64_t i = at + j * step;
+      if (i < end) {
+        u[j] = *reinterpret_cast<const uint4*>(x + i * 8);
+        if (RES) r[j] = *reinterpret_cast<const uint4*>(res + i * 8);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kDropVecs; ++j) {
+      const int64_t i = at + j * step;
+      if (i < end) {
+        float v[8];
+        unpack8(u[j], v);
+        drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + i * 8, v);
+        if (RES) {
+          float s[8];
+          unpack8(r[j], s);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(s[e], v[e]);
+        }
+        store8(y + i * 8, v);
+      }
+    }
+    at += kDropVecs * step;
+  } while (!FLAT && at < end);
 }
 
 // ------------------------------------------------------------------- norm
@@ -174,10 +207,6 @@ __device__ __forceinline__ uint32_t ring_of(const uint8_t* ring, const Team<NV>&
   return at;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-  v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-}
 __device__ __forceinline__ void unpack4(const uint4& u, uint64_t (&v)[4]) {
   v[0] = f2_pack(bf16_lo(u.x), bf16_hi(u.x)), v[1] = f2_pack(bf16_lo(u.y), bf16_hi(u.y));
   v[2] = f2_pack(bf16_lo(u.z), bf16_hi(u.z)), v[3] = f2_pack(bf16_lo(u.w), bf16_hi(u.w));
@@ -522,6 +551,24 @@ bool weight_ok(const float* w) { return w && reinterpret_cast<uintptr_t>(w) % si
 
 Mat mat_of(const upipe_rows* t) { return t ? Mat{reinterpret_cast<bf16*>(t->p), t->row} : Mat{nullptr, 0}; }
 
+template <bool RES>
+cudaError_t launch_dropout(DropParams& p, cudaStream_t st) {
+  const bool flat = p.L == 1 || (p.x.row == p.D && p.y.row == p.D && (!RES || p.res.row == p.D));
+  if (flat) {
+    constexpr int64_t kPer = static_cast<int64_t>(kThreads) * kDropVecs;
+    const int64_t grid = (p.L * (p.D / 8) + kPer - 1) / kPer;
+    if (grid <= 0x7fffffff) {
+      dropout_kernel<RES, true><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p);
+      return cudaGetLastError();
+    }
+  }
+  p.across = 8;  // rows of fewer vectors share a CTA
+  while (p.across < kThreads && p.across * 8 < p.D) p.across *= 2;
+  const int64_t rows = kThreads / p.across;
+  dropout_kernel<RES, false><<<static_cast<unsigned>((p.L + rows - 1) / rows), kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
 // How rows of D elements lie: vectors of a lane, warps of a row, rows at once in
 // one CTA (no more than it takes to give every SM one), and CTAs that walk the
 // rows.  Four vectors a lane make the least of the sums over lanes and warps;
@@ -632,9 +679,7 @@ int upipe_dropout_apply(const upipe_dropout* drop, int64_t L, int32_t D, const u
   int* status = nullptr;
   if (int e = device_ready(&status)) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t need = (L * (D / 8) + kThreads - 1) / kThreads;
-  const unsigned grid = static_cast<unsigned>(need < 152 * 8 ? need : 152 * 8);
-  UPIPE_LAUNCH(UPIPE_KIND_DROPOUT, (dropout_kernel<<<grid, kThreads, 0, st>>>(p), cudaGetLastError()));
+  UPIPE_LAUNCH(UPIPE_KIND_DROPOUT, res ? launch_dropout<true>(p, st) : launch_dropout<false>(p, st));
   return UPIPE_OK;
 }
 
