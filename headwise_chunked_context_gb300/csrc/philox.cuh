@@ -7,6 +7,7 @@
 
 #include <cstdint>
 
+#include "sm103_ptx.cuh"
 #include "upipe.h"
 
 namespace upipe {
@@ -40,37 +41,69 @@ inline bool drop_of(const upipe_dropout* u, Drop* d) {
 }
 
 #ifdef __CUDACC__
-__device__ __forceinline__ void philox(uint64_t block, uint64_t call, const uint32_t (&key)[20], uint32_t (&w)[4]) {
-  uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
-  uint32_t c2 = static_cast<uint32_t>(call), c3 = static_cast<uint32_t>(call >> 32);
-#pragma unroll
-  for (int r = 0; r < 10; ++r) {
-    const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ key[2 * r];
-    c1 = static_cast<uint32_t>(b);
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ key[2 * r + 1];
-    c3 = static_cast<uint32_t>(a);
-  }
-  w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
-}
-
 // The call that a mask is drawn for.
 __device__ __forceinline__ uint64_t drop_call(const Drop& d) { return d.call + (d.step ? *d.step : 0); }
 
-// v[0..7], elements e .. e + 7 of the tensor (e a multiple of 8), behind the
-// mask.  A dropped element is 0 whatever it held.  One rounding per kept
-// element, and no contraction with a sum that follows: the sum of a mask with
-// p = 0 is the plain sum.
-__device__ __forceinline__ void drop8(const Drop& d, uint64_t call, uint64_t e, float (&v)[8]) {
-  const uint64_t block = (d.first + e) >> 2;
-  uint32_t w[4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    philox(block + h, call, d.key, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i] >= d.cut ? __fmul_rn(v[4 * h + i], d.factor) : 0.f;
+// A mask being drawn.  With the call fixed, half of the first two rounds is the
+// same for all blocks whose counters agree in their upper 32 bits (2^34
+// elements): it is kept from one vector to the next.
+class Mask {
+ public:
+  __device__ __forceinline__ Mask(const Drop& d, uint64_t call) : d_(d), first_(d.first >> 2) {
+    c3_ = static_cast<uint32_t>(call >> 32);
+    b_ = static_cast<uint64_t>(static_cast<uint32_t>(call)) * kB;
+    enter(static_cast<uint32_t>(first_ >> 32));
   }
-}
+  // v[0..7], elements e .. e + 7 of the tensor (e a multiple of 8), behind the
+  // mask.  A dropped element is 0 whatever it held.  One rounding per kept
+  // element, and no contraction with a sum that follows: the sum of a mask with
+  // p = 0 is the plain sum.
+  __device__ __forceinline__ void apply(uint64_t e, float (&v)[8]) {
+    const uint64_t block = first_ + (e >> 2);  // even: the next one has the same upper half
+    if (static_cast<uint32_t>(block >> 32) != upper_) enter(static_cast<uint32_t>(block >> 32));
+    const uint64_t f = f2_pack(d_.factor, d_.factor);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), f), v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4];
+      draw(static_cast<uint32_t>(block) + h, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i] >= d_.cut ? v[4 * h + i] : 0.f;
+    }
+  }
+
+ private:
+  static constexpr uint32_t kA = 0xD2511F53u, kB = 0xCD9E8D57u;
+  const Drop& d_;
+  uint64_t first_, a_, b_;  // a_: product of the second round, b_: of the first
+  uint32_t c3_, upper_;
+
+  __device__ __forceinline__ void enter(uint32_t upper) {
+    upper_ = upper;
+    a_ = static_cast<uint64_t>(static_cast<uint32_t>(b_ >> 32) ^ upper ^ d_.key[0]) * kA;
+  }
+  // Words of the counter (lower, upper_, call).
+  __device__ __forceinline__ void draw(uint32_t lower, uint32_t (&w)[4]) const {
+    uint64_t a = static_cast<uint64_t>(lower) * kA;  // round 1
+    uint32_t c2 = static_cast<uint32_t>(a >> 32) ^ c3_ ^ d_.key[1], c3 = static_cast<uint32_t>(a);
+    uint64_t b = static_cast<uint64_t>(c2) * kB;     // round 2
+    uint32_t c0 = static_cast<uint32_t>(b >> 32) ^ static_cast<uint32_t>(b_) ^ d_.key[2];
+    uint32_t c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a_ >> 32) ^ c3 ^ d_.key[3];
+    c3 = static_cast<uint32_t>(a_);
+#pragma unroll
+    for (int r = 2; r < 10; ++r) {
+      a = static_cast<uint64_t>(c0) * kA;
+      b = static_cast<uint64_t>(c2) * kB;
+      c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ d_.key[2 * r];
+      c1 = static_cast<uint32_t>(b);
+      c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ d_.key[2 * r + 1];
+      c3 = static_cast<uint32_t>(a);
+    }
+    w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
+  }
+};
 #endif
 
 }  // namespace upipe

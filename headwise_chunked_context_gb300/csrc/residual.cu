@@ -12,6 +12,7 @@
 // The statistics are recomputed from s, which the backward reads in any case.
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "host.h"
 #include "philox.cuh"
@@ -40,6 +41,7 @@ struct NormParams {
   Mat dy, ds, dres, dx;  // backward
   const float *w, *b;
   int warps;       // of a row
+  int ctas;
   float* partial;  // backward: [gridDim.x][2][D] shares of dw and db
 };
 
@@ -81,35 +83,32 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
     at = threadIdx.x - y * p.across;
     end = per;
   }
-  const uint64_t call = drop_call(p.drop);
+  Mask mask(p.drop, drop_call(p.drop));
   const bf16 *x = p.x.p + row * p.x.row, *res = RES ? p.res.p + row * p.res.row : nullptr;
   bf16* y = p.y.p + row * p.y.row;
   do {
     uint4 u[kDropVecs], r[RES ? kDropVecs : 1];
+    const bool all = at + (kDropVecs - 1) * step < end;
 #pragma unroll
-    for (int j = 0; j < kDropVecs; ++j) {
-      const int64_t i = at + j * step;
-      if (i < end) {
-        u[j] = *reinterpret_cast<const uint4*>(x + i * 8);
-        if (RES) r[j] = *reinterpret_cast<const uint4*>(res + i * 8);
+    for (int j = 0; j < kDropVecs; ++j)
+      if (all || at + j * step < end) {
+        u[j] = *reinterpret_cast<const uint4*>(x + at * 8 + j * step * 8);
+        if (RES) r[j] = *reinterpret_cast<const uint4*>(res + at * 8 + j * step * 8);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kDropVecs; ++j) {
-      const int64_t i = at + j * step;
-      if (i < end) {
+    for (int j = 0; j < kDropVecs; ++j)
+      if (all || at + j * step < end) {
         float v[8];
         unpack8(u[j], v);
-        drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + i * 8, v);
+        mask.apply(static_cast<uint64_t>(row) * p.D + at * 8 + j * step * 8, v);
         if (RES) {
           float s[8];
           unpack8(r[j], s);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(s[e], v[e]);
         }
-        store8(y + i * 8, v);
+        store8(y + at * 8 + j * step * 8, v);
       }
-    }
     at += kDropVecs * step;
   } while (!FLAT && at < end);
 }
@@ -127,6 +126,11 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
 // LEAN: RMS norm without bias; otherwise either norm, with or without one.
 __host__ __device__ constexpr int warps_of(int nv) { return nv == 4 ? 16 : nv == 2 ? 24 : 32; }  // per SM: by registers
 constexpr int kMostWarps = 32;
+
+struct NoMask {
+  __device__ __forceinline__ NoMask(const Drop&, uint64_t) {}
+  __device__ __forceinline__ void apply(uint64_t, float (&)[8]) const {}
+};
 
 template <int NV>
 struct Team {
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_fwd_kernel(co
     weight4(p.w, t, j, w[j]);
     if (!LEAN) weight4(p.b, t, j, b[j]);
   }
-  const uint64_t call = DROP ? drop_call(p.drop) : 0;
+  std::conditional_t<DROP, Mask, NoMask> mask(p.drop, DROP ? drop_call(p.drop) : 0);
   const float inv = 1.f / p.D;
   for (int turn = 0; row < p.L; row += step, turn ^= 1) {
     start();
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_fwd_kernel(co
       if (RES || DROP) {
         float v[8];
         unpack8(u, v);
-        if (DROP && t.live[j]) drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, v);
+        if (DROP && t.live[j]) mask.apply(static_cast<uint64_t>(row) * p.D + t.col + j * 256, v);
         if (RES) {
           float r[8];
           unpack8(ld_shared_v4(at + kBlock + j * 512), r);
@@ -345,9 +349,16 @@ __host__ __device__ constexpr int bwd_blocks(bool ds) { return ds ? 5 : 4; }
 // Each lane keeps its columns' sums of dw and db in registers over all of its
 // rows; a CTA writes one share of each (its teams' shares added in order),
 // which weight_sum_kernel adds up.
-template <int NV, bool DS, bool DROP, bool LEAN>
-__global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+//
+// Registers decide: what spills costs more than what is read again.  Held from
+// one pass over the row to the next are s where nothing else needs the room, and
+// g = w dy but where db's sums do; with ds and db there are 12 warps, whose g is
+// held, for 16 that spill (32768 x 4096: 168 us for 215; 65536 x 5120: 433 for
+// 544), without ds 16 that read w twice (146 us for 155).
+template <int NV, bool DS, bool DROP, bool LEAN, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int kBlock = NV * 512;
+  constexpr bool kHoldS = LEAN && !DS && !DROP, kHoldG = LEAN || NV == 1 || WARPS == 12;
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) Slots<1> means;
   __shared__ __align__(16) Slots<LEAN ? 2 : 3> sums;
@@ -359,25 +370,17 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(co
   const uint32_t weight = smem_u32(shared) + t.warp * NV * 1024 + t.lane * 16;
   const uint32_t ds_at = base + 4 * kBlock;
   uint32_t at = 0;  // of the pair of blocks that is filled next: 0 or 2 kBlock
-  const bf16 *s = p.s.p + row * p.s.row + t.col, *dy = p.dy.p + row * p.dy.row + t.col;
-  const bf16* ds = DS ? p.ds.p + row * p.ds.row + t.col : nullptr;
-  bf16 *dres = p.dres.p + row * p.dres.row + t.col, *dx = DROP ? p.dx.p + row * p.dx.row + t.col : nullptr;
   auto start = [&] {
     if (ahead < p.L) {
-      copy_row(base + at, s, t);
-      copy_row(base + at + kBlock, dy, t);
-      s += step * p.s.row;
-      dy += step * p.dy.row;
+      copy_row(base + at, p.s.p + ahead * p.s.row + t.col, t);
+      copy_row(base + at + kBlock, p.dy.p + ahead * p.dy.row + t.col, t);
     }
     commit();
     at ^= 2 * kBlock;
     ahead += step;
   };
   auto start_ds = [&](int64_t of) {
-    if (of < p.L) {
-      copy_row(ds_at, ds, t);
-      ds += step * p.ds.row;
-    }
+    if (of < p.L) copy_row(ds_at, p.ds.p + of * p.ds.row + t.col, t);
     commit();
   };
   start();
@@ -398,6 +401,11 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(co
                      __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3]));
     }
   __syncthreads();
+  auto read_w = [&](int j, uint64_t (&w)[4]) {
+    const uint4 a = ld_shared_v4(weight + 2 * j * 512), b = ld_shared_v4(weight + (2 * j + 1) * 512);
+    w[0] = f2_pack(__uint_as_float(a.x), __uint_as_float(a.y)), w[1] = f2_pack(__uint_as_float(a.z), __uint_as_float(a.w));
+    w[2] = f2_pack(__uint_as_float(b.x), __uint_as_float(b.y)), w[3] = f2_pack(__uint_as_float(b.z), __uint_as_float(b.w));
+  };
   uint64_t dw[NV][4], db[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -409,9 +417,8 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(co
     start();
     wait<DS ? 2 : 1>();  // this row's s and dy
     const uint32_t mine = base + at;
-    // s is held, or read again where db's sums have the registers.
-    uint4 su[LEAN ? NV : 1];
-    if (LEAN)
+    uint4 su[kHoldS ? NV : 1];
+    if (kHoldS)
 #pragma unroll
       for (int j = 0; j < NV; ++j) su[j] = ld_shared_v4(mine + j * 512);
     float m = 0.f;
@@ -427,18 +434,15 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(co
       team_sum(v, means, turn, t);
       m = p.rms ? 0.f : v[0] * inv;
     }
-    uint64_t g[NV][4];
+    uint64_t gh[kHoldG ? NV : 1][4];
     uint64_t sq[2] = {0, 0}, sg[2] = {0, 0}, sd[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint4 w0 = ld_shared_v4(weight + 2 * j * 512), w1 = ld_shared_v4(weight + (2 * j + 1) * 512);
-      const uint64_t w[4] = {f2_pack(__uint_as_float(w0.x), __uint_as_float(w0.y)),
-                             f2_pack(__uint_as_float(w0.z), __uint_as_float(w0.w)),
-                             f2_pack(__uint_as_float(w1.x), __uint_as_float(w1.y)),
-                             f2_pack(__uint_as_float(w1.z), __uint_as_float(w1.w))};
-      uint64_t a[4];
-      unpack4(LEAN ? su[j] : ld_shared_v4(mine + j * 512), a);
-      unpack4(ld_shared_v4(mine + kBlock + j * 512), g[j]);
+      uint64_t a[4], w[4];
+      read_w(j, w);
+      unpack4(kHoldS ? su[j] : ld_shared_v4(mine + j * 512), a);
+      uint64_t (&g)[4] = gh[kHoldG ? j : 0];
+      unpack4(ld_shared_v4(mine + kBlock + j * 512), g);
       if (!LEAN) {
         const uint64_t mm = f2_both(t.live[j] ? m : 0.f);
 #pragma unroll
@@ -446,10 +450,10 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(co
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        g[j][e] = f2_mul(g[j][e], w[e]);
+        g[e] = f2_mul(g[e], w[e]);
         sq[e & 1] = f2_fma(a[e], a[e], sq[e & 1]);
-        if (!LEAN) sg[e & 1] = f2_add(sg[e & 1], g[j][e]);
-        sd[e & 1] = f2_fma(g[j][e], a[e], sd[e & 1]);
+        if (!LEAN) sg[e & 1] = f2_add(sg[e & 1], g[e]);
+        sd[e & 1] = f2_fma(g[e], a[e], sd[e & 1]);
       }
     }
     float v[LEAN ? 2 : 3];
@@ -462,18 +466,27 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(co
     uint64_t c0 = 0;  // -r mean(g)
     if constexpr (!LEAN) c0 = f2_both(p.rms ? 0.f : -r * (v[2] * inv));
     const uint64_t c1 = f2_both(-r * (r * (v[1] * inv)));  // -r mean(g n)
+    bf16* const dres = p.dres.p + row * p.dres.row + t.col;
+    bf16* const dx = DROP ? p.dx.p + row * p.dx.row + t.col : nullptr;
     if (DS) wait<1>();                                     // this row's ds
+    std::conditional_t<DROP, Mask, NoMask> mask(p.drop, call);  // made anew: the row's sums need the registers
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       uint64_t a[4], d[4];
-      unpack4(LEAN ? su[j] : ld_shared_v4(mine + j * 512), a);
+      unpack4(kHoldS ? su[j] : ld_shared_v4(mine + j * 512), a);
       unpack4(ld_shared_v4(mine + kBlock + j * 512), d);
+      uint64_t (&g)[4] = gh[kHoldG ? j : 0];
+      if (!kHoldG) {
+        read_w(j, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = f2_mul(g[e], d[e]);
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint64_t n = LEAN ? f2_mul(a[e], rr) : f2_fma(a[e], rr, mr);
         dw[j][e] = f2_fma(d[e], n, dw[j][e]);
         if (!LEAN) db[j][e] = f2_add(db[j][e], d[e]);
-        a[e] = f2_fma(n, c1, LEAN ? f2_mul(g[j][e], rr) : f2_fma(g[j][e], rr, c0));
+        a[e] = f2_fma(n, c1, LEAN ? f2_mul(g[e], rr) : f2_fma(g[e], rr, c0));
       }
       if (DS) {
         unpack4(ld_shared_v4(ds_at + j * 512), d);
@@ -486,14 +499,12 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_bwd_kernel(co
           float f[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) f2_unpack(a[e], f[2 * e], f[2 * e + 1]);
-          drop8(p.drop, call, static_cast<uint64_t>(row) * p.D + t.col + j * 256, f);
+          mask.apply(static_cast<uint64_t>(row) * p.D + t.col + j * 256, f);
           store8(dx + j * 256, f);
         }
       }
     }
     if (DS) start_ds(row + step);
-    dres += step * p.dres.row;
-    if (DROP) dx += step * p.dx.row;
   }
   wait<0>();
   // Shares [dw][db] of the CTA; of several teams by way of the ring's memory,
@@ -578,12 +589,13 @@ cudaError_t launch_dropout(DropParams& p, cudaStream_t st) {
 struct Layout {
   int nv, warps, teams, ctas;
 };
-Layout layout_of(int64_t L, int D) {
+Layout layout_of(int64_t L, int D, int most_warps = kMostWarps) {
   Layout y;
   y.nv = D <= 256 ? 1 : D <= 512 || (D > 1024 && D <= 1536) ? 2 : 4;
   y.warps = (D + y.nv * 256 - 1) / (y.nv * 256);
   const int64_t want = (L + 151) / 152;
-  const int most = warps_of(y.nv) / y.warps;
+  const int held = most_warps < warps_of(y.nv) ? most_warps : warps_of(y.nv);
+  const int most = held < y.warps ? 1 : held / y.warps;
   y.teams = static_cast<int>(want < most ? want : most);
   const int64_t need = (L + y.teams - 1) / y.teams;
   y.ctas = static_cast<int>(need < 152 ? need : 152);
@@ -601,6 +613,7 @@ cudaError_t launch_rows(K kernel, const Layout& y, int blocks, bool weights, Nor
                                              warps_of(y.nv) * (blocks + (weights ? 2 : 0)) * block);
   if (e != cudaSuccess) return e;
   p.warps = y.warps;
+  p.ctas = y.ctas;
   kernel<<<static_cast<unsigned>(y.ctas), 32 * warps, bytes, st>>>(p);
   return cudaGetLastError();
 }
@@ -613,9 +626,12 @@ cudaError_t launch_fwd_nv(const Layout& y, NormParams& p, cudaStream_t st) {
 }
 template <int NV, bool DS, bool DROP>
 cudaError_t launch_bwd_nv(const Layout& y, NormParams& p, bool bias, cudaStream_t st) {
-  constexpr int kBlocks = bwd_blocks(DS);
-  return p.rms && !bias ? launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, true>, y, kBlocks, true, p, st)
-                        : launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, false>, y, kBlocks, true, p, st);
+  constexpr int kBlocks = bwd_blocks(DS), kWarps = warps_of(NV);
+  if (p.rms && !bias) return launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, true, kWarps>, y, kBlocks, true, p, st);
+  if constexpr (NV == 4 && DS)
+    if (y.warps * y.teams <= 12)
+      return launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, false, 12>, y, kBlocks, true, p, st);
+  return launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, false, kWarps>, y, kBlocks, true, p, st);
 }
 
 template <bool RES, bool DROP>
@@ -630,7 +646,8 @@ cudaError_t launch_fwd(NormParams& p, cudaStream_t st) {
 
 template <bool DS, bool DROP>
 cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
-  const Layout y = layout_of(p.L, p.D);
+  const bool heavy = DS && (!p.rms || bias) && p.D > 1536;  // see the kernel on registers
+  const Layout y = layout_of(p.L, p.D, heavy ? 12 : kMostWarps);
   switch (y.nv) {
     case 1: return launch_bwd_nv<1, DS, DROP>(y, p, bias, st);
     case 2: return launch_bwd_nv<2, DS, DROP>(y, p, bias, st);
@@ -639,9 +656,8 @@ cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
 }
 
 cudaError_t launch_weight_sum(const NormParams& p, float* dw, float* db, cudaStream_t st) {
-  const int n = layout_of(p.L, p.D).ctas;
   const unsigned cols = static_cast<unsigned>(db ? 2 * p.D : p.D);
-  weight_sum_kernel<<<(cols + 31) / 32, dim3(32, 32), 0, st>>>(p.partial, n, p.D, dw, db);
+  weight_sum_kernel<<<(cols + 31) / 32, dim3(32, 32), 0, st>>>(p.partial, p.ctas, p.D, dw, db);
   return cudaGetLastError();
 }
 
@@ -708,7 +724,7 @@ int upipe_layer_norm_fwd(const upipe_norm_cfg* c, const upipe_dropout* drop, con
 }
 
 size_t upipe_layer_norm_workspace_bytes(const upipe_norm_cfg* c) {
-  return norm_ok(c) ? static_cast<size_t>(layout_of(c->L, c->D).ctas) * 2 * c->D * sizeof(float) : 0;
+  return norm_ok(c) ? static_cast<size_t>(c->L < 152 ? c->L : 152) * 2 * c->D * sizeof(float) : 0;
 }
 
 int upipe_layer_norm_bwd(const upipe_norm_cfg* c, const upipe_dropout* drop, const upipe_rows* s, const float* w,
