@@ -191,12 +191,24 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& s, int turn, c
 }
 
 // This lane's slots in the ring: blocks of a row's part, 512 NV bytes of a warp.
-template <int NV, bool FULL>
+// ONCE: the row leaves L2 first.  That helps where nothing else is read and the
+// arithmetic is short (RMS norm of 65536 x 5120: forward 210 to 206 us, backward 337
+// to 317) and costs as much with masks (backward 510 to 540).
+template <bool ONCE, int NV, bool FULL>
 __device__ __forceinline__ void copy_row(uint32_t block, const bf16* from, const Team<NV, FULL>& t) {
+  uint64_t first = 0;
+  if (ONCE) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (t.live(j))
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(block + j * 512), "l"(from + j * 256) : "memory");
+    if (t.live(j)) {
+      if (ONCE)
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(block + j * 512),
+                     "l"(from + j * 256), "l"(first)
+                     : "memory");
+      else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(block + j * 512), "l"(from + j * 256)
+                     : "memory");
+    }
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -243,13 +255,14 @@ __device__ __forceinline__ void weight4(const float* w, const Team<NV, FULL>& t,
   for (int e = 0; e < 4; ++e) v[e] = on ? f2_pack(__ldg(at + 2 * e), __ldg(at + 2 * e + 1)) : 0;
 }
 
-// Rows of x in the ring, or of x and res: the row being worked on, and others
-// on their way.
-__host__ __device__ constexpr int fwd_rows(bool res) { return res ? 2 : 3; }
+// Rows of x (and of res) in the ring: the one being worked on and the next.  With
+// two on their way the reads crowd out the writes: RMS norm of 65536 x 5120 takes
+// 227 us for 210, and as many bytes by copies with two rows' writes open 226.
+constexpr int kFwdRows = 2;
 
 template <int NV, bool RES, bool DROP, bool LEAN, bool FULL>
 __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_fwd_kernel(const __grid_constant__ NormParams p) {
-  constexpr int T = RES ? 2 : 1, S = fwd_rows(RES), kBlock = NV * 512;
+  constexpr int T = RES ? 2 : 1, S = kFwdRows, kBlock = NV * 512;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(16) Slots<1> means, squares;
   const Team<NV, FULL> t(p);
@@ -264,8 +277,8 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_fwd_kernel(co
   uint32_t at = base;
   auto start = [&] {
     if (ahead < rows) {
-      copy_row(at, p.x.p + ahead * p.x.row + t.col, t);
-      if (RES) copy_row(at + kBlock, p.res.p + ahead * p.res.row + t.col, t);
+      copy_row<LEAN && !RES && !DROP>(at, p.x.p + ahead * p.x.row + t.col, t);
+      if (RES) copy_row<false>(at + kBlock, p.res.p + ahead * p.res.row + t.col, t);
     }
     commit();
     at = at == base + (S - 1) * T * kBlock ? base : at + T * kBlock;
@@ -357,10 +370,11 @@ __host__ __device__ constexpr int bwd_blocks(bool ds) { return ds ? 5 : 4; }
 template <int NV, bool DS, bool DROP, bool LEAN, bool FULL, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int kBlock = NV * 512;
-  constexpr bool kHoldS = LEAN && !DS && !DROP, kHoldG = LEAN || NV == 1 || WARPS == 12;
+  constexpr bool kOnce = LEAN && !DS && !DROP, kHoldS = kOnce, kHoldG = LEAN || NV == 1 || WARPS == 12;
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) Slots<1> means;
   __shared__ __align__(16) Slots<LEAN ? 2 : 3> sums;
+  let_next_start();
   const Team<NV, FULL> t(p);
   const uint32_t rows = static_cast<uint32_t>(p.L), step = gridDim.x * t.teams;  // rows below 2^31
   uint32_t row = blockIdx.x * t.teams + t.id, ahead = row;
@@ -371,15 +385,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) layer_norm_bwd_kernel(const __g
   uint32_t at = 0;  // of the pair of blocks that is filled next: 0 or 2 kBlock
   auto start = [&] {
     if (ahead < rows) {
-      copy_row(base + at, p.s.p + ahead * p.s.row + t.col, t);
-      copy_row(base + at + kBlock, p.dy.p + ahead * p.dy.row + t.col, t);
+      copy_row<kOnce>(base + at, p.s.p + ahead * p.s.row + t.col, t);
+      copy_row<kOnce>(base + at + kBlock, p.dy.p + ahead * p.dy.row + t.col, t);
     }
     commit();
     at ^= 2 * kBlock;
     ahead += step;
   };
   auto start_ds = [&](uint32_t of) {
-    if (of < rows) copy_row(ds_at, p.ds.p + of * p.ds.row + t.col, t);
+    if (of < rows) copy_row<false>(ds_at, p.ds.p + of * p.ds.row + t.col, t);
     commit();
   };
   start();
@@ -530,24 +544,30 @@ __global__ void __launch_bounds__(WARPS * 32, 1) layer_norm_bwd_kernel(const __g
   }
 }
 
+struct SumParams {
+  const float* partial;
+  int n, D;
+  float *dw, *db;
+};
+
 // dw[i] and db[i], the sums over the n rows of partial [n][2][D], in a fixed
 // order: thread row j adds rows j, j + 32, ..., then the 32 shares are added.
-__global__ void __launch_bounds__(1024) weight_sum_kernel(const float* __restrict__ partial, int n, int D, float* dw,
-                                                          float* db) {
+__global__ void __launch_bounds__(1024) weight_sum_kernel(const __grid_constant__ SumParams p) {
+  after_previous();
   __shared__ float share[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D, or D without db
-  const int cols = db ? 2 * D : D;
+  const int cols = p.db ? 2 * p.D : p.D;
   float g = 0.f;
   if (col < cols)
-#pragma unroll 4
-    for (int r = threadIdx.y; r < n; r += 32) g += partial[static_cast<int64_t>(r) * 2 * D + col];
+#pragma unroll 5
+    for (int r = threadIdx.y; r < p.n; r += 32) g += p.partial[static_cast<int64_t>(r) * 2 * p.D + col];
   share[threadIdx.y][threadIdx.x] = g;
   __syncthreads();
   g = share[threadIdx.x][threadIdx.y];  // warp y adds column y
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) g += __shfl_xor_sync(0xffffffffu, g, o);
   const int out = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && out < cols) (out < D ? dw[out] : db[out - D]) = g;
+  if (threadIdx.x == 0 && out < cols) (out < p.D ? p.dw[out] : p.db[out - p.D]) = g;
 }
 
 // ------------------------------------------------------------------- host
@@ -621,7 +641,7 @@ cudaError_t launch_rows(K kernel, const Layout& y, int blocks, bool weights, Nor
 // without masks: 32768 x 4096 forward 89 us for 93, backward 132 for 146.
 template <int NV, bool RES, bool DROP>
 cudaError_t launch_fwd_nv(const Layout& y, NormParams& p, cudaStream_t st) {
-  constexpr int kBlocks = fwd_rows(RES) * (RES ? 2 : 1);
+  constexpr int kBlocks = kFwdRows * (RES ? 2 : 1);
   if (p.rms && !p.b) return launch_rows(layer_norm_fwd_kernel<NV, RES, DROP, true, false>, y, kBlocks, false, p, st);
   if constexpr (NV == 4 && !DROP)
     if (p.D % 1024 == 0)
@@ -668,9 +688,9 @@ cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
 }
 
 cudaError_t launch_weight_sum(const NormParams& p, float* dw, float* db, cudaStream_t st) {
+  const SumParams s{p.partial, p.ctas, p.D, dw, db};
   const unsigned cols = static_cast<unsigned>(db ? 2 * p.D : p.D);
-  weight_sum_kernel<<<(cols + 31) / 32, dim3(32, 32), 0, st>>>(p.partial, p.ctas, p.D, dw, db);
-  return cudaGetLastError();
+  return launch_next(weight_sum_kernel, (cols + 31) / 32, dim3(32, 32), 0, st, s);
 }
 
 // The part of a norm's parameters that both directions share.
