@@ -39,7 +39,8 @@ constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kFwdCols = 512;         // columns that a warp looks up
 constexpr int kSlice = 2048;         // columns of a CTA of the gradient: a vector of 8 per thread
 constexpr int kMaxChunk = 64;        // positions of a chunk
-constexpr int kZeroRows = 32;        // rows of a CTA that writes zeros
+constexpr int kZeroRows = 256;       // rows of a CTA that writes zeros, at most
+constexpr int64_t kSmallTable = int64_t(1) << 29;  // bytes of a table whose zeros are written beside the small sort
 constexpr int kShort = 16;           // chunks behind its first that a short run reaches at most
 constexpr int kShortCols = 4 * kThreads;       // columns of a CTA that adds a short run's shares
 constexpr int kLongCols = 32, kLongRows = 32;  // of one that adds a long run's: columns, shares at once
@@ -227,22 +228,59 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
   }
 }
 
-// All passes for up to kSmall tokens, in one CTA: pairs in shared memory, a part
-// of them to each warp, per pass as above.
-struct SmallSortParams {
-  int L, V, wide, passes;
+// Up to kSmall tokens: one CTA sorts them, pairs in shared memory, a part of them
+// to each warp, per pass as above.  Meanwhile, at tables below kSmallTable, the
+// others write the rows without a token, which they tell by looking through all
+// tokens (4099 tokens, 30011 x 1032: 38 us for 46 with the zeros beside the sums;
+// 1024 tokens, 128256 x 4096: 339 for 297, its few large CTAs write more slowly).
+struct SmallParams {
+  int L, V, D, wide, passes;
   const void* tokens;
   int2* out;
   int* joins;
+  float* dW;
 };
 constexpr int kSmallBytes = 2 * kSmall * sizeof(int2) + kSmallWarps * kBins * sizeof(int);
+constexpr int kGroups = 32;  // groups of 32 rows that a CTA looks for at once
 
-__global__ void __launch_bounds__(kSmallThreads) embed_small_sort_kernel(const __grid_constant__ SmallSortParams p) {
+// The CTAs take the groups in turns: together they write from one end of dW to
+// the other.
+__device__ __forceinline__ void zero_rows_without(const SmallParams& p, unsigned* has) {
+  const unsigned ctas = gridDim.x - 1, cta = blockIdx.x - 1;
+  int across = 2;  // threads of a row
+  while (across < 32 && across * 4 < p.D) across *= 2;
+  const int lane = threadIdx.x % across, quads = p.D / 4;
+  const int64_t stretch = static_cast<int64_t>(ctas) * 32 * kGroups;
+  for (int64_t from = 0; from < p.V; from += stretch) {
+    __syncthreads();
+    if (threadIdx.x < kGroups) has[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.L; i += kSmallThreads) {
+      const int64_t t = token_at(p.tokens, p.wide, i) - from;
+      const unsigned group = static_cast<unsigned>(t >> 5);
+      if (t >= 0 && t < stretch && group % ctas == cta) atomicOr(&has[group / ctas], 1u << (t & 31));
+    }
+    __syncthreads();
+    for (int k = threadIdx.x / across; k < 32 * kGroups; k += kSmallThreads / across) {
+      const int64_t v = from + static_cast<int64_t>(k / 32 * ctas + cta) * 32 + k % 32;
+      if (v >= p.V || ((has[k / 32] >> (k % 32)) & 1)) continue;
+      float4* to = reinterpret_cast<float4*>(p.dW + v * p.D);
+#pragma unroll 4
+      for (int c = lane; c < quads; c += across) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const __grid_constant__ SmallParams p) {
   let_next_start();
   extern __shared__ __align__(16) uint8_t mem[];
   __shared__ int warp_total[kSmallWarps];
   int2 *from = reinterpret_cast<int2*>(mem), *to = from + kSmall;
   int(*hist)[kBins] = reinterpret_cast<int(*)[kBins]>(mem + 2 * kSmall * sizeof(int2));
+  if (blockIdx.x > 0) {
+    zero_rows_without(p, reinterpret_cast<unsigned*>(mem));
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x < 2) p.joins[threadIdx.x] = 0;
   for (int i = threadIdx.x; i < p.L; i += kSmallThreads) {
@@ -302,6 +340,7 @@ struct GradParams {
   int V, D;
   int chunk, chunks;  // positions of a chunk, chunks
   int add;
+  int zero_rows;      // rows of a CTA that writes zeros, at least 32
   float scale;
   const bf16* dy;
   int64_t row;
@@ -346,23 +385,22 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_consta
   const int64_t block = blockIdx.x;
   if (block >= static_cast<int64_t>(p.chunks) * slices) {
     // Which of the CTA's rows have no token: a lane looks one up.
-    __shared__ unsigned empty;
-    const int64_t first = (block - static_cast<int64_t>(p.chunks) * slices) * kZeroRows;
-    if (threadIdx.x < 32) {
-      const int64_t v = first + threadIdx.x;
-      bool none = v < p.V;
-      if (none) {
-        const int64_t at = lower_bound(p.items, p.L, v);
-        none = at == p.L || __ldg(&p.items[at].x) != v;
-      }
-      const unsigned mask = __ballot_sync(0xffffffffu, none);
-      if (threadIdx.x == 0) empty = mask;
+    __shared__ unsigned empty[kZeroRows / 32];
+    const int64_t first = (block - static_cast<int64_t>(p.chunks) * slices) * p.zero_rows;
+    const int64_t v = first + threadIdx.x;
+    bool none = threadIdx.x < p.zero_rows && v < p.V;
+    if (none) {
+      const int64_t at = lower_bound(p.items, p.L, v);
+      none = at == p.L || __ldg(&p.items[at].x) != v;
     }
+    const unsigned mask = __ballot_sync(0xffffffffu, none);
+    if ((threadIdx.x & 31) == 0) empty[threadIdx.x >> 5] = mask;
     __syncthreads();
-    for (unsigned left = empty; left; left &= left - 1) {
-      float4* to = reinterpret_cast<float4*>(p.dW + (first + __ffs(left) - 1) * p.D);
-      for (int c = threadIdx.x; c < p.D / 4; c += kThreads) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    for (int k = 0; k < p.zero_rows / 32; ++k)
+      for (unsigned left = empty[k]; left; left &= left - 1) {
+        float4* to = reinterpret_cast<float4*>(p.dW + (first + 32 * k + __ffs(left) - 1) * p.D);
+        for (int c = threadIdx.x; c < p.D / 4; c += kThreads) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     return;
   }
   __shared__ int2 items[kMaxChunk + 2];  // with the one before and the one behind
@@ -545,11 +583,11 @@ GradPlan grad_plan(const upipe_embed_cfg* c) {
   return s;
 }
 
-cudaError_t launch_small_sort(const SmallSortParams& p, cudaStream_t st) {
+cudaError_t launch_small(const SmallParams& p, bool zeros, cudaStream_t st) {
   const cudaError_t e =
-      cudaFuncSetAttribute(embed_small_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
+      cudaFuncSetAttribute(embed_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
   if (e != cudaSuccess) return e;
-  embed_small_sort_kernel<<<1, kSmallThreads, kSmallBytes, st>>>(p);
+  embed_small_kernel<<<zeros ? 152 : 1, kSmallThreads, kSmallBytes, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -594,10 +632,13 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   std::memset(&g, 0, sizeof(g));
   g.joins = reinterpret_cast<int*>(at + plan.join);
   g.join = reinterpret_cast<int4*>(g.joins) + 1;
+  bool zeros = !add;  // beside the sums
+  const bool beside = zeros && static_cast<int64_t>(c->V) * c->D * 4 < kSmallTable;  // the small sort
   if (c->L <= kSmall) {
-    const SmallSortParams s{static_cast<int>(c->L), c->V, c->wide, plan.passes, tokens,
-                            reinterpret_cast<int2*>(at + plan.pairs[0]), g.joins};
-    UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT, launch_small_sort(s, st));
+    const SmallParams s{static_cast<int>(c->L), c->V, c->D, c->wide, plan.passes, tokens,
+                        reinterpret_cast<int2*>(at + plan.pairs[0]), g.joins, dW};
+    zeros = zeros && !beside;
+    UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT, launch_small(s, beside, st));
     g.items = s.out;
   } else {
     SortParams s;
@@ -635,9 +676,10 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   g.dW = dW;
   g.share = reinterpret_cast<float*>(at + plan.share);
   const int64_t sums = static_cast<int64_t>(plan.chunks) * ((c->D + kSlice - 1) / kSlice);
-  const int64_t zeros = add ? 0 : (static_cast<int64_t>(c->V) + kZeroRows - 1) / kZeroRows;
+  g.zero_rows = c->D < 1024 ? kZeroRows : 32;
+  const int64_t empty = zeros ? (static_cast<int64_t>(c->V) + g.zero_rows - 1) / g.zero_rows : 0;
   UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD,
-               launch_next(embed_bwd_kernel, static_cast<unsigned>(sums + zeros), kThreads, 0, st, g));
+               launch_next(embed_bwd_kernel, static_cast<unsigned>(sums + empty), kThreads, 0, st, g));
   UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, launch_next(embed_join_kernel, 152 * 8, kThreads, 0, st, g));
   return UPIPE_OK;
 }
