@@ -396,11 +396,13 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_consta
     const unsigned mask = __ballot_sync(0xffffffffu, none);
     if ((threadIdx.x & 31) == 0) empty[threadIdx.x >> 5] = mask;
     __syncthreads();
-    for (int k = 0; k < p.zero_rows / 32; ++k)
-      for (unsigned left = empty[k]; left; left &= left - 1) {
-        float4* to = reinterpret_cast<float4*>(p.dW + (first + 32 * k + __ffs(left) - 1) * p.D);
-        for (int c = threadIdx.x; c < p.D / 4; c += kThreads) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+    int across = 2;  // threads of a row
+    while (across < kThreads && across * 4 < p.D) across *= 2;
+    for (int k = threadIdx.x / across; k < p.zero_rows; k += kThreads / across) {
+      if (!((empty[k / 32] >> (k % 32)) & 1)) continue;
+      float4* to = reinterpret_cast<float4*>(p.dW + (first + k) * p.D);
+      for (int c = threadIdx.x % across; c < p.D / 4; c += across) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     return;
   }
   __shared__ int2 items[kMaxChunk + 2];  // with the one before and the one behind
