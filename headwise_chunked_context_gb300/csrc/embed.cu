@@ -131,7 +131,7 @@ __device__ __forceinline__ void sort_items(const SortParams& p, int64_t i, int64
       const int64_t t = token_at(p.tokens, p.wide, i + 32 * k);
       item[k] = make_int2(t >= 0 && t < p.V ? static_cast<int>(t) : p.V, static_cast<int>(i + 32 * k));
     } else {
-      item[k] = __ldg(p.in + i + 32 * k);
+      item[k] = __ldcg(p.in + i + 32 * k);
     }
   }
 #pragma unroll
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
   int before = 0, all = 0;
 #pragma unroll 16
   for (int t = 0; t < p.tiles; ++t) {
-    const int n = p.counts[static_cast<int64_t>(t) * kBins + threadIdx.x];
+    const int n = __ldcg(p.counts + static_cast<int64_t>(t) * kBins + threadIdx.x);
     all += n;
     before += t < static_cast<int>(blockIdx.x) ? n : 0;
   }
@@ -256,9 +256,10 @@ __device__ __forceinline__ void zero_rows_without(const SmallParams& p, unsigned
     if (threadIdx.x < kGroups) has[threadIdx.x] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.L; i += kSmallThreads) {
-      const int64_t t = token_at(p.tokens, p.wide, i) - from;
-      const unsigned group = static_cast<unsigned>(t >> 5);
-      if (t >= 0 && t < stretch && group % ctas == cta) atomicOr(&has[group / ctas], 1u << (t & 31));
+      const int64_t t = token_at(p.tokens, p.wide, i);
+      if (t < from || t >= from + stretch) continue;
+      const unsigned at = static_cast<unsigned>(t - from), group = at / 32;
+      if (group % ctas == cta) atomicOr(&has[group / ctas], 1u << (at % 32));
     }
     __syncthreads();
     for (int k = threadIdx.x / across; k < 32 * kGroups; k += kSmallThreads / across) {
@@ -351,15 +352,16 @@ struct GradParams {
   int4* join;         // [2][chunks]: first chunk, last chunk, token of each
 };
 
-// First of the n sorted items whose token is at least v.
-__device__ __forceinline__ int64_t lower_bound(const int2* items, int64_t n, int64_t v) {
-  int64_t lo = 0, hi = n;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (__ldg(&items[mid].x) < v)
-      lo = mid + 1;
-    else
-      hi = mid;
+// The same for a whole warp: the first of the n sorted items whose token is at
+// least v, by 32 probes at once.
+__device__ __forceinline__ int64_t warp_lower_bound(const int2* items, int64_t n, int64_t v) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, end = n;  // it is in [lo, end]
+  while (lo < end) {
+    const int64_t step = (end - lo + 31) / 32, at = lo + lane * step + step - 1;
+    const bool less = at < end && __ldcg(&items[at].x) < v;
+    lo += __popc(__ballot_sync(0xffffffffu, less)) * step;
+    if (lo + step - 1 < end) end = lo + step - 1;
   }
   return lo;
 }
@@ -377,21 +379,33 @@ __device__ __forceinline__ void write_row8(float* w, const float (&g)[8], float 
   to[1] = b;
 }
 
-// Chunks first, slice by slice, then rows to fill with zeros.
-__global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_constant__ GradParams p) {
+// Chunks first, slice by slice, then rows to fill with zeros.  A thread has the
+// loads of eight positions open; four CTAs per SM (131072 tokens, 152064 x 5120:
+// 687 us, with three 704, with five 722).
+__global__ void __launch_bounds__(kThreads, 4) embed_bwd_kernel(const __grid_constant__ GradParams p) {
   after_previous();
   let_next_start();
   const int slices = (p.D + kSlice - 1) / kSlice;
   const int64_t block = blockIdx.x;
   if (block >= static_cast<int64_t>(p.chunks) * slices) {
-    // Which of the CTA's rows have no token: a lane looks one up.
+    // Which of the CTA's rows have no token: a warp finds the tokens of 32 rows, a
+    // lane among them its own row's.
     __shared__ unsigned empty[kZeroRows / 32];
     const int64_t first = (block - static_cast<int64_t>(p.chunks) * slices) * p.zero_rows;
     const int64_t v = first + threadIdx.x;
-    bool none = threadIdx.x < p.zero_rows && v < p.V;
-    if (none) {
-      const int64_t at = lower_bound(p.items, p.L, v);
-      none = at == p.L || __ldg(&p.items[at].x) != v;
+    bool none = false;
+    if (threadIdx.x < p.zero_rows) {  // whole warps
+      int64_t lo = warp_lower_bound(p.items, p.L, v - (threadIdx.x & 31));
+      int64_t hi = warp_lower_bound(p.items, p.L, v - (threadIdx.x & 31) + 32);
+      const int64_t end = hi;
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (__ldcg(&p.items[mid].x) < v)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      none = v < p.V && (lo == end || __ldcg(&p.items[lo].x) != v);
     }
     const unsigned mask = __ballot_sync(0xffffffffu, none);
     if ((threadIdx.x & 31) == 0) empty[threadIdx.x >> 5] = mask;
@@ -407,37 +421,30 @@ __global__ void __launch_bounds__(kThreads) embed_bwd_kernel(const __grid_consta
   }
   __shared__ int2 items[kMaxChunk + 2];  // with the one before and the one behind
   const int chunk = static_cast<int>(block / slices);
-  const int col = static_cast<int>(block - static_cast<int64_t>(chunk) * slices) * kSlice + threadIdx.x * 8;
+  const int slice = static_cast<int>(block - static_cast<int64_t>(chunk) * slices);
+  const int col = slice * kSlice + threadIdx.x * 8;
   const int64_t first = static_cast<int64_t>(chunk) * p.chunk;
   for (int i = threadIdx.x; i < p.chunk + 2; i += kThreads) {
     const int64_t at = first + i - 1;
-    items[i] = at >= 0 && at < p.L ? p.items[at] : make_int2(-1, 0);
+    items[i] = at >= 0 && at < p.L ? __ldcg(p.items + at) : make_int2(-1, 0);
   }
   __syncthreads();
   const int before = items[0].x, behind = items[p.chunk + 1].x;
   // The chunk's tokens that are rows: those without one stand at the end of all.
   const int mine = threadIdx.x < p.chunk ? items[threadIdx.x + 1].x : -1;
   const int n = __syncthreads_count(mine >= 0 && mine < p.V);
-  if (col == 0 && n == p.chunk && items[n].x == behind && !(items[1].x == behind && before == behind)) {
-    // A run begins here and goes on: where it ends, by strides of 1, 2, 4, ...
-    // chunks and then between the last two; the order of the lists says nothing.
-    int in = chunk + 1, past = p.chunks;  // it reaches chunk `in`, and not `past`
-    for (int by = 1; in + by < past; by *= 2) {
-      if (__ldg(&p.items[static_cast<int64_t>(in + by) * p.chunk].x) != behind) {
-        past = in + by;
-        break;
-      }
-      in += by;
-    }
-    while (past - in > 1) {
-      const int mid = (in + past) / 2;
-      if (__ldg(&p.items[static_cast<int64_t>(mid) * p.chunk].x) == behind)
-        in = mid;
-      else
-        past = mid;
-    }
+  const bool goes_on = n == p.chunk && items[n].x == behind && !(items[1].x == behind && before == behind);
+  if (goes_on && slice == 0 && threadIdx.x < 32) {
+    // A run begins here and goes on to chunk `in`: in one of the next 31, which a
+    // warp looks at, or further; the order of the lists says nothing.
+    const int next = chunk + 1 + threadIdx.x;
+    const bool same = next < p.chunks && __ldcg(&p.items[static_cast<int64_t>(next) * p.chunk].x) == behind;
+    const unsigned others = ~__ballot_sync(0xffffffffu, same);
+    int in = chunk + __ffs(others) - 1;
+    if (others == 0)
+      in = static_cast<int>((warp_lower_bound(p.items, p.L, static_cast<int64_t>(behind) + 1) - 1) / p.chunk);
     const int kind = in - chunk > kShort;
-    p.join[kind * p.chunks + atomicAdd(p.joins + kind, 1)] = make_int4(chunk, in, behind, 0);
+    if (threadIdx.x == 0) p.join[kind * p.chunks + atomicAdd(p.joins + kind, 1)] = make_int4(chunk, in, behind, 0);
   }
   if (col >= p.D) return;
   const bf16* dy = p.dy + col;
@@ -488,30 +495,30 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_const
   __shared__ float4 part[kLongRows][kLongCols / 4];
   const float4* share = reinterpret_cast<const float4*>(p.share);
   const int64_t pitch = p.D / 4;  // of a share
-  const int counts[2] = {p.joins[0], p.joins[1]};
+  const int counts[2] = {__ldcg(p.joins), __ldcg(p.joins + 1)};
   int slices = (p.D + kShortCols - 1) / kShortCols;
   int64_t work = static_cast<int64_t>(counts[0]) * slices;
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int4 run = p.join[i / slices];
+    const int4 run = __ldcg(p.join + i / slices);
     const int quad = static_cast<int>(i % slices) * kThreads + threadIdx.x;
     if (quad >= pitch) continue;
     const float4* from = share + 2 * static_cast<int64_t>(run.x) * pitch + quad;
-    float4 g = from[pitch];
+    float4 g = __ldcg(from + pitch);
 #pragma unroll 4
-    for (int k = run.x + 1; k <= run.y; ++k) add4(g, *(from += 2 * pitch));
+    for (int k = run.x + 1; k <= run.y; ++k) add4(g, __ldcg(from += 2 * pitch));
     write_row4(p, run.z, quad * 4, g);
   }
   slices = (p.D + kLongCols - 1) / kLongCols;
   work = static_cast<int64_t>(counts[1]) * slices;
   const int row = threadIdx.x / (kLongCols / 4), lane = threadIdx.x % (kLongCols / 4);
   for (int64_t i = blockIdx.x; i < work; i += gridDim.x) {
-    const int4 run = p.join[p.chunks + i / slices];
+    const int4 run = __ldcg(p.join + p.chunks + i / slices);
     const int quad = static_cast<int>(i % slices) * (kLongCols / 4) + lane;
     float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
     if (quad < pitch) {
 #pragma unroll 8
       for (int k = run.x + row; k <= run.y; k += kLongRows)
-        add4(g, share[(2 * static_cast<int64_t>(k) + (k == run.x)) * pitch + quad]);
+        add4(g, __ldcg(share + (2 * static_cast<int64_t>(k) + (k == run.x)) * pitch + quad));
     }
     __syncthreads();  // the sums before have been read
     part[row][lane] = g;

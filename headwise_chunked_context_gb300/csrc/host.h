@@ -63,8 +63,9 @@ cudaError_t counted(int kind, cudaStream_t st, F&& launch) {
 
 // Launches a kernel that may be made ready while the one before it on the stream
 // still runs.  Every thread of it begins with after_previous() (sm103_ptx.cuh),
-// so that it touches nothing before that one has ended; the one before allows it
-// by let_next_start().
+// so that it touches nothing before that one has ended, and reads what kernels
+// before it wrote past L1 (__ldcg), which may have been filled earlier; the one
+// before allows it by let_next_start().
 template <class P>
 cudaError_t launch_next(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
   cudaLaunchConfig_t cfg = {};

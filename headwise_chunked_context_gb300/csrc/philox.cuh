@@ -24,7 +24,7 @@ struct Drop {
 // False: p or first out of range.  cut is p in whole steps of 2^-32, and the
 // factor is that of the steps, so that the mean is kept exactly.
 inline bool drop_of(const upipe_dropout* u, Drop* d) {
-  if (!(u->p >= 0.0) || !(u->p < 1.0) || u->first % 8 != 0) return false;
+  if (!(u->p >= 0.0) || !(u->p < 1.0) || u->first % 8 != 0 || u->first >> 63) return false;
   const double cut = static_cast<double>(static_cast<uint64_t>(u->p * 4294967296.0 + 0.5));
   if (cut > 4294967295.0) return false;
   if (reinterpret_cast<uintptr_t>(u->step) % sizeof(uint64_t) != 0) return false;

@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(1024) weight_sum_kernel(const __grid_constant_
   float g = 0.f;
   if (col < cols)
 #pragma unroll 5
-    for (int r = threadIdx.y; r < p.n; r += 32) g += p.partial[static_cast<int64_t>(r) * 2 * p.D + col];
+    for (int r = threadIdx.y; r < p.n; r += 32) g += __ldcg(p.partial + static_cast<int64_t>(r) * 2 * p.D + col);
   share[threadIdx.y][threadIdx.x] = g;
   __syncthreads();
   g = share[threadIdx.x][threadIdx.y];  // warp y adds column y

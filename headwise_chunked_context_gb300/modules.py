@@ -304,14 +304,15 @@ class _LayerNormFn(torch.autograd.Function):
     def backward(ctx, dy, ds=None):
         s, w, _ = ctx.saved_tensors
         eps, rms, drop = ctx.args
-        if dy is None:  # nothing came through the norm
-            if ds is None:
-                return (None,) * 7
+        if dy is not None:
+            grads = upipe.layer_norm_backward(s, w, _heads(dy), None if ds is None else _heads(ds), eps, rms, ctx.bias,
+                                              drop)
+        elif ds is not None:  # nothing came through the norm
             dx = ds if drop is None else upipe.dropout_backward(drop, _heads(ds))
-            return dx, ds, torch.zeros_like(w), torch.zeros_like(w) if ctx.bias else None, None, None, None
-        dx, dres, dw, db = upipe.layer_norm_backward(s, w, _heads(dy), None if ds is None else _heads(ds), eps, rms,
-                                                     ctx.bias, drop)
-        return dx, dres, dw, db, None, None, None
+            grads = dx, ds, torch.zeros_like(w), torch.zeros_like(w)
+        else:
+            grads = (None,) * 4
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), None, None, None)
 
 
 class LayerNorm(torch.nn.Module):

@@ -1074,7 +1074,7 @@ class Dropout:
     p: chance of an element to be dropped, 0 <= p < 1.
     seed, call: 64-bit numbers; `call` tells the masks of a run apart.
     first: index of the first element of a tensor that is a part of a larger
-    one, a multiple of 8 (a rank's first row times D).
+    one, a multiple of 8 below 2^63 (a rank's first row times D).
     step: int64 CUDA tensor of one element that is added to `call` when the
     kernels run, or None (a captured graph draws a new mask per replay)."""
 
@@ -1087,17 +1087,21 @@ class Dropout:
         for n, v in (("seed", seed), ("call", call), ("first", first)):
             if not 0 <= v < 1 << 64:
                 raise ValueError(f"{n}: expected a number of 64 bits, got {v}")
-        if first % 8:
-            raise ValueError(f"first: expected a multiple of 8, got {first}")
+        if first % 8 or first >> 63:
+            raise ValueError(f"first: expected a multiple of 8 below 2^63, got {first}")
         at = None
         if step is not None:
             if not step.is_cuda or step.dtype != torch.int64 or step.numel() != 1:
                 raise ValueError(f"step: expected one int64 element on a CUDA device, got {tuple(step.shape)} "
                                  f"{step.dtype} on {step.device}")
             at = step.data_ptr()
-        self.p, self.seed, self.call, self.first, self.step = p, int(seed), int(call), int(first), step
-        self._c = DropoutCfg(p, self.seed, self.call, self.first, at)
-        self.ref = ctypes.byref(self._c)
+        c = DropoutCfg(p, int(seed), int(call), int(first), at)
+        for n, v in (("p", p), ("seed", c.seed), ("call", c.call), ("first", c.first), ("step", step), ("_c", c),
+                     ("ref", ctypes.byref(c))):
+            object.__setattr__(self, n, v)
+
+    def __setattr__(self, name, value):  # the kernels read `_c`
+        raise AttributeError(f"{name}: the numbers of a mask do not change; make another")
 
     def __reduce__(self):  # copies and pickles by value: `ref` is an address
         return Dropout, (self.p, self.seed, self.call, self.first, self.step)

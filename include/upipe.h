@@ -558,9 +558,9 @@ int upipe_embed_bwd(const upipe_embed_cfg* cfg, const void* tokens, const upipe_
  * whatever it held.
  *   p      0 <= p < 1 - 2^-33
  *   call   tells the masks of one run apart (layer and step, say)
- *   first  index of the tensor's first element, a multiple of 8: the first
- *          row of a rank's rows times D, so that ranks draw the whole
- *          tensor's mask
+ *   first  index of the tensor's first element, a multiple of 8 below 2^63:
+ *          the first row of a rank's rows times D, so that ranks draw the
+ *          whole tensor's mask
  *   step   device address (8-byte aligned) of a number that is added to
  *          `call` when the kernel runs, or NULL: a captured graph draws a new
  *          mask per replay.  The backward must find the forward's number.   */

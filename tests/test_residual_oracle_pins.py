@@ -137,7 +137,7 @@ def test_embedding_refuses_bad_pointers_and_workspaces(lib):
 
 
 @pytest.mark.parametrize("bad", [dict(p=-0.1), dict(p=1.0), dict(p=1 - 2.0 ** -34), dict(p=float("nan")),
-                                 dict(first=4), dict(step=(1 << 20) + 4)])
+                                 dict(first=4), dict(first=1 << 63), dict(step=(1 << 20) + 4)])
 def test_masks_out_of_range_are_refused(lib, bad):
     d = upipe.DropoutCfg(*({**dict(p=0.1, seed=1, call=2, first=8, step=None), **bad}.values()))
     n = upipe.NormCfg(4, 256, 0, 1e-5)
@@ -221,7 +221,7 @@ def test_binding_refuses_before_any_launch(lib):
 
 def test_dropout_objects_check_and_copy_their_numbers():
     for bad in (dict(p=1.0), dict(p=-0.1), dict(p=float("nan")), dict(p=1 - 2.0 ** -33), dict(p=0.1, seed=-1),
-                dict(p=0.1, seed=1 << 64), dict(p=0.1, call=1 << 64), dict(p=0.1, first=12), dict(p=0.1, first=-8),
+                dict(p=0.1, seed=1 << 64), dict(p=0.1, call=1 << 64), dict(p=0.1, first=12), dict(p=0.1, first=-8), dict(p=0.1, first=1 << 63),
                 dict(p=0.1, step=torch.zeros(1, dtype=torch.int64))):
         with pytest.raises(ValueError):
             upipe.Dropout(**bad)
@@ -229,3 +229,5 @@ def test_dropout_objects_check_and_copy_their_numbers():
     for e in (copy.copy(d), copy.deepcopy(d), pickle.loads(pickle.dumps(d))):
         assert (e.p, e.seed, e.call, e.first, e.step) == (d.p, d.seed, d.call, d.first, None)
         assert e._c is not d._c and (e._c.seed, e._c.call) == (d.seed, d.call)
+    with pytest.raises(AttributeError):
+        d.call = 7
