@@ -593,8 +593,8 @@ GradPlan grad_plan(const upipe_embed_cfg* c) {
 }
 
 cudaError_t launch_small(const SmallParams& p, bool zeros, cudaStream_t st) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(embed_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(embed_small_kernel), kSmallBytes, allowed);
   if (e != cudaSuccess) return e;
   embed_small_kernel<<<zeros ? 152 : 1, kSmallThreads, kSmallBytes, st>>>(p);
   return cudaGetLastError();

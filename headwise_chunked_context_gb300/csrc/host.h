@@ -61,6 +61,18 @@ cudaError_t counted(int kind, cudaStream_t st, F&& launch) {
   return e;
 }
 
+// Allows `kernel` `bytes` of dynamic shared memory on the current device, once
+// per device: `done`, a bit each, belongs to the kernel.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 // Launches a kernel that may be made ready while the one before it on the stream
 // still runs.  Every thread of it begins with after_previous() (sm103_ptx.cuh),
 // so that it touches nothing before that one has ended, and reads what kernels

@@ -623,17 +623,18 @@ Layout layout_of(int64_t L, int D, int most_warps = kMostWarps) {
 static_assert(UPIPE_NORM_MAX_D <= 1024 * warps_of(4), "the longest row fits a CTA");
 
 // blocks: of the ring per warp; weights: whether the weight stands before it.
-template <class K>
-cudaError_t launch_rows(K kernel, const Layout& y, int blocks, bool weights, NormParams& p, cudaStream_t st) {
+template <void (*kKernel)(NormParams)>
+cudaError_t launch_rows(const Layout& y, int blocks, bool weights, NormParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
   const int block = y.nv * 512, warps = y.warps * y.teams;
   const int bytes = warps * blocks * block + (weights ? 2 * y.warps * block : 0);
-  // the same for every call: two threads' calls may set it in any order
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             warps_of(y.nv) * (blocks + (weights ? 2 : 0)) * block);
+  // for the longest rows: the same for every call of the kernel
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kKernel),
+                                   warps_of(y.nv) * (blocks + (weights ? 2 : 0)) * block, allowed);
   if (e != cudaSuccess) return e;
   p.warps = y.warps;
   p.ctas = y.ctas;
-  kernel<<<static_cast<unsigned>(y.ctas), 32 * warps, bytes, st>>>(p);
+  kKernel<<<static_cast<unsigned>(y.ctas), 32 * warps, bytes, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -642,21 +643,21 @@ cudaError_t launch_rows(K kernel, const Layout& y, int blocks, bool weights, Nor
 template <int NV, bool RES, bool DROP>
 cudaError_t launch_fwd_nv(const Layout& y, NormParams& p, cudaStream_t st) {
   constexpr int kBlocks = kFwdRows * (RES ? 2 : 1);
-  if (p.rms && !p.b) return launch_rows(layer_norm_fwd_kernel<NV, RES, DROP, true, false>, y, kBlocks, false, p, st);
+  if (p.rms && !p.b) return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, true, false>>(y, kBlocks, false, p, st);
   if constexpr (NV == 4 && !DROP)
     if (p.D % 1024 == 0)
-      return launch_rows(layer_norm_fwd_kernel<NV, RES, DROP, false, true>, y, kBlocks, false, p, st);
-  return launch_rows(layer_norm_fwd_kernel<NV, RES, DROP, false, false>, y, kBlocks, false, p, st);
+      return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, false, true>>(y, kBlocks, false, p, st);
+  return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, false, false>>(y, kBlocks, false, p, st);
 }
 template <int NV, bool DS, bool DROP, bool FULL, int WARPS>
 cudaError_t launch_heavy(const Layout& y, NormParams& p, cudaStream_t st) {
-  return launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, false, FULL, WARPS>, y, bwd_blocks(DS), true, p, st);
+  return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, FULL, WARPS>>(y, bwd_blocks(DS), true, p, st);
 }
 template <int NV, bool DS, bool DROP>
 cudaError_t launch_bwd_nv(const Layout& y, NormParams& p, bool bias, cudaStream_t st) {
   constexpr int kWarps = warps_of(NV);
   if (p.rms && !bias)
-    return launch_rows(layer_norm_bwd_kernel<NV, DS, DROP, true, false, kWarps>, y, bwd_blocks(DS), true, p, st);
+    return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, true, false, kWarps>>(y, bwd_blocks(DS), true, p, st);
   if constexpr (NV == 4) {
     const bool full = !DROP && p.D % 1024 == 0, few = DS && y.warps * y.teams <= 12;
     if (full && few) return launch_heavy<NV, DS, DROP, !DROP, DS ? 12 : kWarps>(y, p, st);
