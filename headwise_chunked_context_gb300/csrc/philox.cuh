@@ -59,6 +59,15 @@ class Mask {
   // element, and no contraction with a sum that follows: the sum of a mask with
   // p = 0 is the plain sum.
   __device__ __forceinline__ void apply(uint64_t e, float (&v)[8]) {
+    float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    each<false>(e, v, zero);
+  }
+  // r += v behind the mask: a kept element is added, a dropped one leaves r as it is.
+  __device__ __forceinline__ void add(uint64_t e, float (&v)[8], float (&r)[8]) { each<true>(e, v, r); }
+
+ private:
+  template <bool ADD>
+  __device__ __forceinline__ void each(uint64_t e, float (&v)[8], float (&r)[8]) {
     const uint64_t block = first_ + (e >> 2);  // even: the next one has the same upper half
     if (static_cast<uint32_t>(block >> 32) != upper_) enter(static_cast<uint32_t>(block >> 32));
     const uint64_t f = f2_pack(d_.factor, d_.factor);
@@ -69,11 +78,17 @@ class Mask {
       uint32_t w[4];
       draw(static_cast<uint32_t>(block) + h, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i] >= d_.cut ? v[4 * h + i] : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        float& a = v[4 * h + i];
+        if (ADD) {
+          if (w[i] >= d_.cut) r[4 * h + i] = __fadd_rn(r[4 * h + i], a);
+        } else {
+          a = w[i] >= d_.cut ? a : 0.f;
+        }
+      }
     }
   }
 
- private:
   static constexpr uint32_t kA = 0xD2511F53u, kB = 0xCD9E8D57u;
   const Drop& d_;
   uint64_t first_, a_, b_;  // a_: product of the second round, b_: of the first

@@ -100,14 +100,16 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
       if (all || at + j * step < end) {
         float v[8];
         unpack8(u[j], v);
-        mask.apply(static_cast<uint64_t>(row) * p.D + at * 8 + j * step * 8, v);
+        const uint64_t e = static_cast<uint64_t>(row) * p.D + at * 8 + j * step * 8;
         if (RES) {
           float s[8];
           unpack8(r[j], s);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(s[e], v[e]);
+          mask.add(e, v, s);
+          store8(y + at * 8 + j * step * 8, s);
+        } else {
+          mask.apply(e, v);
+          store8(y + at * 8 + j * step * 8, v);
         }
-        store8(y + at * 8 + j * step * 8, v);
       }
     at += kDropVecs * step;
   } while (!FLAT && at < end);
@@ -130,6 +132,7 @@ constexpr int kMostWarps = 32;
 struct NoMask {
   __device__ __forceinline__ NoMask(const Drop&, uint64_t) {}
   __device__ __forceinline__ void apply(uint64_t, float (&)[8]) const {}
+  __device__ __forceinline__ void add(uint64_t, float (&)[8], float (&)[8]) const {}
 };
 
 // FULL: every vector exists.
@@ -305,12 +308,20 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_fwd_kernel(co
       if (RES || DROP) {
         float v[8];
         unpack8(u, v);
-        if (DROP && t.live(j)) mask.apply(static_cast<uint64_t>(row) * static_cast<uint32_t>(p.D) + t.col + j * 256, v);
+        const uint64_t at_e = static_cast<uint64_t>(row) * static_cast<uint32_t>(p.D) + t.col + j * 256;
         if (RES) {
           float r[8];
           unpack8(ld_shared_v4(at + kBlock + j * 512), r);
+          if (!DROP)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(r[e], v[e]);
+            for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(r[e], v[e]);
+          else if (t.live(j))
+            mask.add(at_e, v, r);
+          if (DROP)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = r[e];
+        } else if (t.live(j)) {
+          mask.apply(at_e, v);
         }
         u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                        pack_bf16x2(v[6], v[7]));
@@ -669,7 +680,12 @@ cudaError_t launch_bwd_nv(const Layout& y, NormParams& p, bool bias, cudaStream_
 
 template <bool RES, bool DROP>
 cudaError_t launch_fwd(NormParams& p, cudaStream_t st) {
-  const Layout y = layout_of(p.L, p.D);
+  // With a mask and a residual, rows of one or two warps of four vectors a lane do
+  // better with 12 warps of 16: 131072 x 768 124 us for 144, 65536 x 2048 175 for
+  // 191; longer ones mostly do not (65536 x 2560 221 for 210, 32768 x 3584 169 for
+  // 152, but 32768 x 4096 174 for 187).
+  const bool few = RES && DROP && p.D > 512 && p.D <= 2048 && (p.D <= 1024 || p.D > 1536);
+  const Layout y = layout_of(p.L, p.D, few ? 12 : kMostWarps);
   switch (y.nv) {
     case 1: return launch_fwd_nv<1, RES, DROP>(y, p, st);
     case 2: return launch_fwd_nv<2, RES, DROP>(y, p, st);
