@@ -562,23 +562,39 @@ struct SumParams {
 };
 
 // dw[i] and db[i], the sums over the n rows of partial [n][2][D], in a fixed
-// order: thread row j adds rows j, j + 32, ..., then the 32 shares are added.
-__global__ void __launch_bounds__(1024) weight_sum_kernel(const __grid_constant__ SumParams p) {
+// order: 32 rows of threads take every 32nd row each, four columns a thread; the
+// four rows of a warp are added, then the eight warps' sums.
+constexpr int kSumCols = 32;
+
+__global__ void __launch_bounds__(256) weight_sum_kernel(const __grid_constant__ SumParams p) {
+  __shared__ float4 part[8][kSumCols / 4];
   after_previous();
-  __shared__ float share[32][33];
-  const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D, or D without db
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quad = lane & 7, row = warp * 4 + (lane >> 3);
+  const int col = blockIdx.x * kSumCols + quad * 4;  // of 2 D, or D without db; D is a multiple of 8
   const int cols = p.db ? 2 * p.D : p.D;
-  float g = 0.f;
+  float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
   if (col < cols)
 #pragma unroll 5
-    for (int r = threadIdx.y; r < p.n; r += 32) g += __ldcg(p.partial + static_cast<int64_t>(r) * 2 * p.D + col);
-  share[threadIdx.y][threadIdx.x] = g;
-  __syncthreads();
-  g = share[threadIdx.x][threadIdx.y];  // warp y adds column y
+    for (int r = row; r < p.n; r += 32) {
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(p.partial + static_cast<int64_t>(r) * 2 * p.D + col));
+      g.x += f.x, g.y += f.y, g.z += f.z, g.w += f.w;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) g += __shfl_xor_sync(0xffffffffu, g, o);
-  const int out = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && out < cols) (out < p.D ? p.dw[out] : p.db[out - p.D]) = g;
+  for (int o = 8; o < 32; o <<= 1) {
+    g.x += __shfl_xor_sync(0xffffffffu, g.x, o);
+    g.y += __shfl_xor_sync(0xffffffffu, g.y, o);
+    g.z += __shfl_xor_sync(0xffffffffu, g.z, o);
+    g.w += __shfl_xor_sync(0xffffffffu, g.w, o);
+  }
+  if (lane < 8) part[warp][quad] = g;
+  __syncthreads();
+  const int at = blockIdx.x * kSumCols + threadIdx.x;
+  if (threadIdx.x >= kSumCols || at >= cols) return;
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) s += reinterpret_cast<const float*>(&part[w][0])[threadIdx.x];
+  (at < p.D ? p.dw[at] : p.db[at - p.D]) = s;
 }
 
 // ------------------------------------------------------------------- host
@@ -707,7 +723,7 @@ cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
 cudaError_t launch_weight_sum(const NormParams& p, float* dw, float* db, cudaStream_t st) {
   const SumParams s{p.partial, p.ctas, p.D, dw, db};
   const unsigned cols = static_cast<unsigned>(db ? 2 * p.D : p.D);
-  return launch_next(weight_sum_kernel, (cols + 31) / 32, dim3(32, 32), 0, st, s);
+  return launch_next(weight_sum_kernel, (cols + kSumCols - 1) / kSumCols, 256, 0, st, s);
 }
 
 // The part of a norm's parameters that both directions share.
