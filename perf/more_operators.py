@@ -253,9 +253,9 @@ def _own(s):
             return dict(y=upipe.embed_forward(s["tokens"], s["W"], scale=s["scale"]))
         return dict(dW=upipe.embed_backward(s["tokens"], s["dy"], c["V"], scale=s["scale"]))
     if c["op"] == "drop":
-        if c["back"]:
+        if c["back"] and not c["res"]:
             return dict(y=upipe.dropout_backward(s["drop"], s["x"]))
-        return dict(y=upipe.dropout_forward(s["drop"], s["x"], s["res"]))
+        return dict(y=upipe.dropout_forward(s["drop"], s["x"], s["res"]))  # or onto another gradient
     if not c["back"]:
         y, total = upipe.layer_norm_forward(s["x"], s["w"], s["b"], eps=EPS, rms=c["rms"], residual=s["res"],
                                             dropout=s["drop"])
