@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -276,21 +277,21 @@ def lib() -> ctypes.CDLL:
         L.upipe_window_fwd.argtypes = [win, P, P, P, P, P, P]
         L.upipe_window_bwd.restype = ctypes.c_int
         L.upipe_window_bwd.argtypes = [win, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
-        emb, drop, norm = ctypes.POINTER(EmbedCfg), ctypes.POINTER(DropoutCfg), ctypes.POINTER(NormCfg)
+        # structures by their address (or as bytes in their layout)
         L.upipe_embed_fwd.restype = ctypes.c_int
-        L.upipe_embed_fwd.argtypes = [emb, P, P, rows, P]
+        L.upipe_embed_fwd.argtypes = [P, P, P, P, P]
         L.upipe_embed_workspace_bytes.restype = ctypes.c_size_t
-        L.upipe_embed_workspace_bytes.argtypes = [emb]
+        L.upipe_embed_workspace_bytes.argtypes = [P]
         L.upipe_embed_bwd.restype = ctypes.c_int
-        L.upipe_embed_bwd.argtypes = [emb, P, rows, P, ctypes.c_int, P, ctypes.c_size_t, P]
+        L.upipe_embed_bwd.argtypes = [P, P, P, P, ctypes.c_int, P, ctypes.c_size_t, P]
         L.upipe_dropout_apply.restype = ctypes.c_int
-        L.upipe_dropout_apply.argtypes = [drop, ctypes.c_int64, ctypes.c_int32, rows, rows, rows, P]
+        L.upipe_dropout_apply.argtypes = [P, ctypes.c_int64, ctypes.c_int32, P, P, P, P]
         L.upipe_layer_norm_fwd.restype = ctypes.c_int
-        L.upipe_layer_norm_fwd.argtypes = [norm, drop, rows, rows, P, P, rows, rows, P]
+        L.upipe_layer_norm_fwd.argtypes = [P, P, P, P, P, P, P, P, P]
         L.upipe_layer_norm_workspace_bytes.restype = ctypes.c_size_t
-        L.upipe_layer_norm_workspace_bytes.argtypes = [norm]
+        L.upipe_layer_norm_workspace_bytes.argtypes = [P]
         L.upipe_layer_norm_bwd.restype = ctypes.c_int
-        L.upipe_layer_norm_bwd.argtypes = [norm, drop, rows, P, rows, rows, rows, rows, P, P, P, ctypes.c_size_t, P]
+        L.upipe_layer_norm_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         L.upipe_offload_async.restype = ctypes.c_int
         L.upipe_offload_async.argtypes = [P, P, ctypes.c_size_t, P]
         L.upipe_prefetch_async.restype = ctypes.c_int
@@ -1042,23 +1043,31 @@ def window_backward(cfg: WindowConfig, q, k, v, o, lse, do):
 EMBED_MAX_D, NORM_MAX_D = 65536, 16384
 
 
-def _matrix(t, L, D, name, device):
+# Descriptions as bytes in the structures' layout: half the time of a ctypes
+# structure each, which is what a call of one row consists of.
+_ROWS = struct.Struct("@Pqq").pack       # upipe_rows
+_NORM = struct.Struct("@qiif4x").pack    # upipe_norm_cfg
+_EMBED = struct.Struct("@qiiiif4x").pack  # upipe_embed_cfg
+_BF16 = torch.bfloat16
+
+
+def _matrix(t, shape, name, device):
     """A bf16 [L, D] tensor, its rows at any stride that keeps them 16-byte
     aligned, as the library's description of it; None for none."""
     if t is None:
         return None
-    if t.dtype != torch.bfloat16 or t.shape != (L, D):
-        _expect(t, (L, D), torch.bfloat16, name)
+    if t.dtype is not _BF16 or t.shape != shape:
+        _expect(t, shape, _BF16, name)
     row, one = t.stride()
     p = t.data_ptr()
-    if L == 1:  # the stride of an axis of one says nothing
+    if shape[0] == 1:  # the stride of an axis of one says nothing
         row = 0
-    if one != 1 or row & 7 or p & 15:
+    if one != 1 or (row & 7) or (p & 15):
         raise ValueError(f"{name}: expected rows of contiguous elements on 16-byte boundaries, got strides "
                          f"{(row, one)} at {p:#x}")
     if t.get_device() != device:
         _here(t, name)
-    return ctypes.byref(Rows(p, row, 0))
+    return _ROWS(p, row, 0)
 
 
 def _two(t, name):
@@ -1124,12 +1133,12 @@ def dropout_apply(drop: Dropout, x, res, y, stream=None):
     res, y [L, D] bf16.  y may be x or res."""
     if drop is None:
         raise ValueError("drop: missing")
-    L, D = _two(x, "x")
+    shape = L, D = _two(x, "x")
     if y is None:
         raise ValueError("y: missing")
     dev = _here(x, "x")
-    _check(lib().upipe_dropout_apply(_drop(drop, dev), L, _int32(D, "D"), _matrix(x, L, D, "x", dev),
-                                     _matrix(res, L, D, "res", dev), _matrix(y, L, D, "y", dev),
+    _check(lib().upipe_dropout_apply(_drop(drop, dev), L, _int32(D, "D"), _matrix(x, shape, "x", dev),
+                                     _matrix(res, shape, "res", dev), _matrix(y, shape, "y", dev),
                                      _raw(stream, dev)), "upipe_dropout_apply")
 
 
@@ -1146,17 +1155,16 @@ def _given(t, D, name, device):
 def layer_norm_fwd(x, w, b, y, s=None, eps: float = 1e-5, rms: bool = False, residual=None, dropout=None, stream=None):
     """upipe_layer_norm_fwd: y = norm(s) with weights w and b (or None) [D]
     fp32, s = residual + drop(x) (written; given iff residual or dropout is)."""
-    L, D = _two(x, "x")
+    shape = L, D = _two(x, "x")
     dev = _here(x, "x")
     if (s is None) != (residual is None and dropout is None):
         raise ValueError("s: given iff residual or dropout is")
     if y is None:
         raise ValueError("y: missing")
-    c = NormCfg(L, _int32(D, "D"), int(bool(rms)), eps)
-    _check(lib().upipe_layer_norm_fwd(ctypes.byref(c), _drop(dropout, dev), _matrix(x, L, D, "x", dev),
-                                      _matrix(residual, L, D, "residual", dev), _weight(w, D, "w", dev),
-                                      _given(b, D, "b", dev), _matrix(s, L, D, "s", dev), _matrix(y, L, D, "y", dev),
-                                      _raw(stream, dev)), "upipe_layer_norm_fwd")
+    _check(lib().upipe_layer_norm_fwd(_NORM(L, _int32(D, "D"), bool(rms), eps), _drop(dropout, dev),
+                                      _matrix(x, shape, "x", dev), _matrix(residual, shape, "residual", dev),
+                                      _weight(w, D, "w", dev), _given(b, D, "b", dev), _matrix(s, shape, "s", dev),
+                                      _matrix(y, shape, "y", dev), _raw(stream, dev)), "upipe_layer_norm_fwd")
 
 
 def layer_norm_workspace_bytes(L: int, D: int) -> int:
@@ -1170,17 +1178,17 @@ def layer_norm_bwd(s, w, dy, ds, dres, dx, dw, db, eps: float = 1e-5, rms: bool 
                    stream=None):
     """upipe_layer_norm_bwd: from s, dy and ds (or None) to dres (the gradient
     of s), dx (behind the mask; given iff dropout is), dw and db (or None)."""
-    L, D = _two(s, "s")
+    shape = L, D = _two(s, "s")
     dev = _here(s, "s")
     for t, n in ((dy, "dy"), (dres, "dres")):
         if t is None:
             raise ValueError(f"{n}: missing")
     if (dx is None) != (dropout is None):
         raise ValueError("dx: given iff dropout is")
-    c = ctypes.byref(NormCfg(L, _int32(D, "D"), int(bool(rms)), eps))
-    args = (c, _drop(dropout, dev), _matrix(s, L, D, "s", dev), _weight(w, D, "w", dev), _matrix(dy, L, D, "dy", dev),
-            _matrix(ds, L, D, "ds", dev), _matrix(dres, L, D, "dres", dev), _matrix(dx, L, D, "dx", dev),
-            _weight(dw, D, "dw", dev), _given(db, D, "db", dev))
+    c = _NORM(L, _int32(D, "D"), bool(rms), eps)
+    args = (c, _drop(dropout, dev), _matrix(s, shape, "s", dev), _weight(w, D, "w", dev),
+            _matrix(dy, shape, "dy", dev), _matrix(ds, shape, "ds", dev), _matrix(dres, shape, "dres", dev),
+            _matrix(dx, shape, "dx", dev), _weight(dw, D, "dw", dev), _given(db, D, "db", dev))
     f = lib()
     ws, nbytes = _call_ws(f.upipe_layer_norm_workspace_bytes(c), ws, s.device, stream)
     _check(f.upipe_layer_norm_bwd(*args, ws.data_ptr(), nbytes, _raw(stream, dev)), "upipe_layer_norm_bwd")
@@ -1192,8 +1200,8 @@ def _embed_call(tokens, V, D, master, scale, device):
         raise ValueError("tokens: expected a [L] tensor of int32 or int64")
     if tokens.get_device() != device or not tokens.is_contiguous():
         _on_device(tokens=tokens)
-    c = EmbedCfg(tokens.shape[0], _int32(V, "V"), _int32(D, "D"), int(tokens.dtype == torch.int64), int(master), scale)
-    return ctypes.byref(c), tokens.data_ptr()
+    return _EMBED(tokens.shape[0], _int32(V, "V"), _int32(D, "D"), tokens.dtype == torch.int64, master,
+                  scale), tokens.data_ptr()
 
 
 def embed_fwd(tokens, W, y, scale: float = 1.0, stream=None):
@@ -1207,7 +1215,7 @@ def embed_fwd(tokens, W, y, scale: float = 1.0, stream=None):
     c, at = _embed_call(tokens, V, D, W.dtype == torch.float32, scale, dev)
     if y is None:
         raise ValueError("y: missing")
-    _check(lib().upipe_embed_fwd(c, at, W.data_ptr(), _matrix(y, tokens.shape[0], D, "y", dev), _raw(stream, dev)),
+    _check(lib().upipe_embed_fwd(c, at, W.data_ptr(), _matrix(y, (tokens.shape[0], D), "y", dev), _raw(stream, dev)),
            "upipe_embed_fwd")
 
 
@@ -1228,7 +1236,7 @@ def embed_bwd(tokens, dy, dW, scale: float = 1.0, add: bool = False, ws=None, st
     c, at = _embed_call(tokens, V, D, False, scale, dev)
     if dy is None:
         raise ValueError("dy: missing")
-    m = _matrix(dy, tokens.shape[0], D, "dy", dev)
+    m = _matrix(dy, (tokens.shape[0], D), "dy", dev)
     f = lib()
     ws, nbytes = _call_ws(f.upipe_embed_workspace_bytes(c), ws, dW.device, stream)
     _check(f.upipe_embed_bwd(c, at, m, dW.data_ptr(), int(bool(add)), ws.data_ptr(), nbytes, _raw(stream, dev)),

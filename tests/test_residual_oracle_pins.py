@@ -231,3 +231,11 @@ def test_dropout_objects_check_and_copy_their_numbers():
         assert e._c is not d._c and (e._c.seed, e._c.call) == (d.seed, d.call)
     with pytest.raises(AttributeError):
         d.call = 7
+
+
+def test_descriptions_as_bytes_are_the_structures():
+    """What the binding packs is what the mirrored structures hold, byte for byte
+    (their padding apart from the values is zero in both)."""
+    assert upipe._ROWS(1 << 40, 264, 0) == bytes(upipe.Rows(1 << 40, 264, 0))
+    assert upipe._NORM(77, 1032, True, 1e-5) == bytes(upipe.NormCfg(77, 1032, 1, 1e-5))
+    assert upipe._EMBED(9, 500, 64, True, False, 2.5) == bytes(upipe.EmbedCfg(9, 500, 64, 1, 0, 2.5))
