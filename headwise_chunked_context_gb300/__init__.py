@@ -1,7 +1,8 @@
 """Head-chunked GQA/RoPE causal attention layer for GB300 (sm_103a), with the
-sequence-tiled MLP and loss of the same block, and rotary positions, norms of
+sequence-tiled MLP and loss of the same block, rotary positions, norms of
 queries and keys and windowed attention for layers with projections of their
-own.
+own, and what carries the residual stream between them: token embedding,
+dropout, and layer or RMS norm with the residual sum.
 
 The compute path is the C-ABI library ``libupipe.so`` built from ``csrc/``;
 ``headwise_chunked_context_gb300.upipe`` is its thin ctypes binding,
