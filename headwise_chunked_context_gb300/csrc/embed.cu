@@ -10,8 +10,8 @@
 // order, and cut into chunks of equal length.  A CTA adds up a chunk's runs of
 // equal tokens: runs inside the chunk are a row of dW, the others leave shares,
 // which are added in the chunks' order.  Rows without a token are zeros, written
-// beside the sums by CTAs of their own, which look their rows up in the sorted
-// tokens.
+// by CTAs of their own, beside the sums, looked up in the sorted tokens, or, at
+// small tables and few tokens, beside the sort.
 //
 // What bounds it: HBM.  The gradient reads dy once and writes V rows, most of
 // them zeros at a real vocabulary; the sort, of 4 to 12 bytes a token, is its
@@ -36,7 +36,7 @@ constexpr int kMaxTiles = 304;
 constexpr int kSmall = 8192;         // tokens that one CTA sorts alone
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallWarps = kSmallThreads / 32;
-constexpr int kFwdCols = 512;         // columns that a warp looks up
+constexpr int kFwdCols = 512;        // columns that a warp looks up
 constexpr int kSlice = 2048;         // columns of a CTA of the gradient: a vector of 8 per thread
 constexpr int kMaxChunk = 64;        // positions of a chunk
 constexpr int kZeroRows = 256;       // rows of a CTA that writes zeros, at most
@@ -52,9 +52,8 @@ struct EmbedParams {
   float scale;
   const void* tokens;
   const void* table;
-  const bf16* dy;
-  int64_t row;  // row stride of y or dy
   bf16* y;
+  int64_t row;  // its row stride
 };
 
 __device__ __forceinline__ int64_t token_at(const void* tokens, int wide, int64_t i) {

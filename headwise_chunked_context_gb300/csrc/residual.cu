@@ -35,7 +35,6 @@ struct NormParams {
   int64_t L;
   int D, rms;
   float eps;
-  int dropped;
   Drop drop;
   Mat x, res, s, y;      // forward; backward: s is read
   Mat dy, ds, dres, dx;  // backward
@@ -260,7 +259,7 @@ __device__ __forceinline__ void weight4(const float* w, const Team<NV, FULL>& t,
 
 // Rows of x (and of res) in the ring: the one being worked on and the next.  With
 // two on their way the reads crowd out the writes: RMS norm of 65536 x 5120 takes
-// 227 us for 210, and as many bytes by copies with two rows' writes open 226.
+// 227 us for 210.
 constexpr int kFwdRows = 2;
 
 template <int NV, bool RES, bool DROP, bool LEAN, bool FULL>
@@ -733,9 +732,7 @@ bool norm_params(const upipe_norm_cfg* c, const upipe_dropout* drop, NormParams*
   p->D = c->D;
   p->rms = c->rms;
   p->eps = c->eps;
-  if (!drop) return true;
-  p->dropped = 1;
-  return drop_of(drop, &p->drop);
+  return !drop || drop_of(drop, &p->drop);
 }
 
 }  // namespace
