@@ -181,7 +181,8 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& s, int turn, c
   if (t.lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) slot[i * kMostWarps + t.warp] = v[i];
-  asm volatile("bar.sync %0, %1;" ::"r"(t.id + 1), "r"(t.warps * 32) : "memory");
+  __syncwarp();  // the barrier counts whole warps
+  asm volatile("barrier.sync %0, %1;" ::"r"(t.id + 1), "r"(t.warps * 32) : "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
   for (int k = 0; k < quads; ++k)
@@ -193,24 +194,12 @@ __device__ __forceinline__ void team_sum(float (&v)[N], Slots<N>& s, int turn, c
 }
 
 // This lane's slots in the ring: blocks of a row's part, 512 NV bytes of a warp.
-// ONCE: the row leaves L2 first.  That helps where nothing else is read and the
-// arithmetic is short (RMS norm of 65536 x 5120: forward 210 to 206 us, backward 337
-// to 317) and costs as much with masks (backward 510 to 540).
-template <bool ONCE, int NV, bool FULL>
+template <int NV, bool FULL>
 __device__ __forceinline__ void copy_row(uint32_t block, const bf16* from, const Team<NV, FULL>& t) {
-  uint64_t first = 0;
-  if (ONCE) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (t.live(j)) {
-      if (ONCE)
-        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(block + j * 512),
-                     "l"(from + j * 256), "l"(first)
-                     : "memory");
-      else
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(block + j * 512), "l"(from + j * 256)
-                     : "memory");
-    }
+    if (t.live(j))
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(block + j * 512), "l"(from + j * 256) : "memory");
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -279,8 +268,8 @@ __global__ void __launch_bounds__(warps_of(NV) * 32, 1) layer_norm_fwd_kernel(co
   uint32_t at = base;
   auto start = [&] {
     if (ahead < rows) {
-      copy_row<LEAN && !RES && !DROP>(at, p.x.p + ahead * p.x.row + t.col, t);
-      if (RES) copy_row<false>(at + kBlock, p.res.p + ahead * p.res.row + t.col, t);
+      copy_row(at, p.x.p + ahead * p.x.row + t.col, t);
+      if (RES) copy_row(at + kBlock, p.res.p + ahead * p.res.row + t.col, t);
     }
     commit();
     at = at == base + (S - 1) * T * kBlock ? base : at + T * kBlock;
@@ -374,13 +363,14 @@ __host__ __device__ constexpr int bwd_blocks(bool ds) { return ds ? 5 : 4; }
 //
 // Registers decide: what spills costs more than what is read again.  Held from
 // one pass over the row to the next are s where nothing else needs the room, and
-// g = w dy but where db's sums do; with ds and db there are 12 warps, whose g is
-// held, for 16 that spill (32768 x 4096: 168 us for 215; 65536 x 5120: 433 for
-// 544), without ds 16 that read w twice (146 us for 155).
+// g = w dy but where db's sums do.  With db and rows that leave lanes to spare, 12
+// warps hold g and do not spill where 16 do (65536 x 2560 199 us for 214, with ds
+// 213 for 228; but rows of five and seven warps leave too many of 12 out: 32768 x
+// 5000 242 for 227, 16384 x 7000 202 for 177).
 template <int NV, bool DS, bool DROP, bool LEAN, bool FULL, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int kBlock = NV * 512;
-  constexpr bool kOnce = LEAN && !DS && !DROP, kHoldS = kOnce, kHoldG = LEAN || NV == 1 || WARPS == 12;
+  constexpr bool kHoldS = LEAN && !DS && !DROP, kHoldG = LEAN || NV == 1 || WARPS == 12;
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) Slots<1> means;
   __shared__ __align__(16) Slots<LEAN ? 2 : 3> sums;
@@ -395,15 +385,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) layer_norm_bwd_kernel(const __g
   uint32_t at = 0;  // of the pair of blocks that is filled next: 0 or 2 kBlock
   auto start = [&] {
     if (ahead < rows) {
-      copy_row<kOnce>(base + at, p.s.p + ahead * p.s.row + t.col, t);
-      copy_row<kOnce>(base + at + kBlock, p.dy.p + ahead * p.dy.row + t.col, t);
+      copy_row(base + at, p.s.p + ahead * p.s.row + t.col, t);
+      copy_row(base + at + kBlock, p.dy.p + ahead * p.dy.row + t.col, t);
     }
     commit();
     at ^= 2 * kBlock;
     ahead += step;
   };
   auto start_ds = [&](uint32_t of) {
-    if (of < rows) copy_row<false>(ds_at, p.ds.p + of * p.ds.row + t.col, t);
+    if (of < rows) copy_row(ds_at, p.ds.p + of * p.ds.row + t.col, t);
     commit();
   };
   start();
@@ -675,22 +665,16 @@ cudaError_t launch_fwd_nv(const Layout& y, NormParams& p, cudaStream_t st) {
       return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, false, true>>(y, kBlocks, false, p, st);
   return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, false, false>>(y, kBlocks, false, p, st);
 }
-template <int NV, bool DS, bool DROP, bool FULL, int WARPS>
-cudaError_t launch_heavy(const Layout& y, NormParams& p, cudaStream_t st) {
-  return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, FULL, WARPS>>(y, bwd_blocks(DS), true, p, st);
-}
 template <int NV, bool DS, bool DROP>
-cudaError_t launch_bwd_nv(const Layout& y, NormParams& p, bool bias, cudaStream_t st) {
-  constexpr int kWarps = warps_of(NV);
-  if (p.rms && !bias)
-    return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, true, false, kWarps>>(y, bwd_blocks(DS), true, p, st);
-  if constexpr (NV == 4) {
-    const bool full = !DROP && p.D % 1024 == 0, few = DS && y.warps * y.teams <= 12;
-    if (full && few) return launch_heavy<NV, DS, DROP, !DROP, DS ? 12 : kWarps>(y, p, st);
-    if (few) return launch_heavy<NV, DS, DROP, false, DS ? 12 : kWarps>(y, p, st);
-    if (full) return launch_heavy<NV, DS, DROP, !DROP, kWarps>(y, p, st);
-  }
-  return launch_heavy<NV, DS, DROP, false, kWarps>(y, p, st);
+cudaError_t launch_bwd_nv(const Layout& y, NormParams& p, bool lean, bool few, cudaStream_t st) {
+  constexpr int kWarps = warps_of(NV), kBlocks = bwd_blocks(DS);
+  if (lean) return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, true, false, kWarps>>(y, kBlocks, true, p, st);
+  if constexpr (NV == 4 && (DS || !DROP))
+    if (few) return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, false, 12>>(y, kBlocks, true, p, st);
+  if constexpr (NV == 4 && !DROP)
+    if (p.D % 1024 == 0)
+      return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, true, kWarps>>(y, kBlocks, true, p, st);
+  return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, false, kWarps>>(y, kBlocks, true, p, st);
 }
 
 template <bool RES, bool DROP>
@@ -710,13 +694,16 @@ cudaError_t launch_fwd(NormParams& p, cudaStream_t st) {
 
 template <bool DS, bool DROP>
 cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
-  const bool heavy = DS && (!p.rms || bias) && p.D > 1536;  // see the kernel on registers
-  const Layout y = layout_of(p.L, p.D, heavy ? 12 : kMostWarps);
+  // 12 warps whose registers do not spill for 16 that do: rows of two to four warps
+  // with lanes to spare.
+  const bool lean = p.rms && !bias, full = !DROP && p.D % 1024 == 0;
+  const bool few = !lean && !full && (DS || !DROP) && p.D > 1536 && p.D <= 4096;
+  const Layout y = layout_of(p.L, p.D, few ? 12 : kMostWarps);
   switch (y.nv) {
-    case 1: return launch_bwd_nv<1, DS, DROP>(y, p, bias, st);
-    case 2: return launch_bwd_nv<2, DS, DROP>(y, p, bias, st);
+    case 1: return launch_bwd_nv<1, DS, DROP>(y, p, lean, false, st);
+    case 2: return launch_bwd_nv<2, DS, DROP>(y, p, lean, false, st);
   }
-  return launch_bwd_nv<4, DS, DROP>(y, p, bias, st);
+  return launch_bwd_nv<4, DS, DROP>(y, p, lean, few, st);
 }
 
 cudaError_t launch_weight_sum(const NormParams& p, float* dw, float* db, cudaStream_t st) {
