@@ -363,14 +363,16 @@ __host__ __device__ constexpr int bwd_blocks(bool ds) { return ds ? 5 : 4; }
 //
 // Registers decide: what spills costs more than what is read again.  Held from
 // one pass over the row to the next are s where nothing else needs the room, and
-// g = w dy but where db's sums do.  With db and rows that leave lanes to spare, 12
-// warps hold g and do not spill where 16 do (65536 x 2560 199 us for 214, with ds
-// 213 for 228; but rows of five and seven warps leave too many of 12 out: 32768 x
-// 5000 242 for 227, 16384 x 7000 202 for 177).
+// g = w dy but where db's sums do (whole-warp rows with mask, without ds, hold it
+// all the same: 65536 x 5120 537 us for 598; with ds 622 for 608).  With db and rows
+// that leave lanes to spare, 12 warps hold g and do not spill where 16 do (65536 x
+// 2560 199 us for 208, with ds 215 for 230, with mask too 341 for 372; but rows of
+// five and seven warps leave too many of 12 out: 32768 x 5000 242 for 227, 16384 x
+// 7000 202 for 177).
 template <int NV, bool DS, bool DROP, bool LEAN, bool FULL, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 1) layer_norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int kBlock = NV * 512;
-  constexpr bool kHoldS = LEAN && !DS && !DROP, kHoldG = LEAN || NV == 1 || WARPS == 12;
+  constexpr bool kHoldS = LEAN && !DS && !DROP, kHoldG = LEAN || NV == 1 || WARPS == 12 || (FULL && DROP && !DS);
   extern __shared__ __align__(16) uint8_t shared[];
   __shared__ __align__(16) Slots<1> means;
   __shared__ __align__(16) Slots<LEAN ? 2 : 3> sums;
@@ -619,8 +621,9 @@ cudaError_t launch_dropout(DropParams& p, cudaStream_t st) {
 // one CTA (no more than it takes to give every SM one), and CTAs that walk the
 // rows.  Four vectors a lane make the least of the sums over lanes and warps;
 // fewer, with more warps, where four would stand half empty: forward of 131072
-// rows of 256 24, 27 and 34 us with one, two and four, of 65536 rows of 1536 67,
-// 72 and 73, with the mean and the bias 105, 75 and 75, of 2048 132, 99 and 93.
+// rows of 256 24, 28 and 36 us with one, two and four; with mean and bias, 65536
+// rows of 1536 71 and 72 with two and four, backward 121 and 136, 2048 91 and 93,
+// backward 158 and 133.
 struct Layout {
   int nv, warps, teams, ctas;
 };
@@ -654,13 +657,14 @@ cudaError_t launch_rows(const Layout& y, int blocks, bool weights, NormParams& p
   return cudaGetLastError();
 }
 
-// Rows of whole warps have kernels of their own where that pays, with means and
-// without masks: 32768 x 4096 forward 89 us for 93, backward 132 for 146.
+// Rows of whole warps have kernels of their own where that pays, with means or
+// biases: 65536 x 5120 backward 340 us for 403 (with mask and ds 608 for 726),
+// forward with mask and residual 462 for 503.
 template <int NV, bool RES, bool DROP>
 cudaError_t launch_fwd_nv(const Layout& y, NormParams& p, cudaStream_t st) {
   constexpr int kBlocks = kFwdRows * (RES ? 2 : 1);
   if (p.rms && !p.b) return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, true, false>>(y, kBlocks, false, p, st);
-  if constexpr (NV == 4 && !DROP)
+  if constexpr (NV == 4)
     if (p.D % 1024 == 0)
       return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, false, true>>(y, kBlocks, false, p, st);
   return launch_rows<layer_norm_fwd_kernel<NV, RES, DROP, false, false>>(y, kBlocks, false, p, st);
@@ -671,7 +675,7 @@ cudaError_t launch_bwd_nv(const Layout& y, NormParams& p, bool lean, bool few, c
   if (lean) return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, true, false, kWarps>>(y, kBlocks, true, p, st);
   if constexpr (NV == 4 && (DS || !DROP))
     if (few) return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, false, 12>>(y, kBlocks, true, p, st);
-  if constexpr (NV == 4 && !DROP)
+  if constexpr (NV == 4)
     if (p.D % 1024 == 0)
       return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, true, kWarps>>(y, kBlocks, true, p, st);
   return launch_rows<layer_norm_bwd_kernel<NV, DS, DROP, false, false, kWarps>>(y, kBlocks, true, p, st);
@@ -696,8 +700,8 @@ template <bool DS, bool DROP>
 cudaError_t launch_bwd(NormParams& p, bool bias, cudaStream_t st) {
   // 12 warps whose registers do not spill for 16 that do: rows of two to four warps
   // with lanes to spare.
-  const bool lean = p.rms && !bias, full = !DROP && p.D % 1024 == 0;
-  const bool few = !lean && !full && (DS || !DROP) && p.D > 1536 && p.D <= 4096;
+  const bool lean = p.rms && !bias;
+  const bool few = !lean && p.D % 1024 != 0 && (DS || !DROP) && p.D > 1536 && p.D <= 4096;
   const Layout y = layout_of(p.L, p.D, few ? 12 : kMostWarps);
   switch (y.nv) {
     case 1: return launch_bwd_nv<1, DS, DROP>(y, p, lean, false, st);

@@ -148,7 +148,8 @@ def test_step_on_the_device_is_added_to_the_call():
 # L, D: one vector a row, rows of less than a warp, of one and many vectors per lane, the largest; one row and
 # more rows than are resident
 SHAPES = [(1, 8), (1, 5120), (3, 72), (300, 256), (65, 1000), (33, 1032), (129, 4096), (50, 5120), (1, 16384),
-          (37, 8192), (19, 16384), (21, 12296), (2501, 128), (1300, 520)]
+          (37, 8192), (19, 16384), (21, 12296), (2501, 128), (1300, 520),
+          (1300, 1024), (700, 5120), (701, 2560), (1301, 4096), (399, 7000)]  # several rows a team
 
 
 def _weights(seed, D):
@@ -222,7 +223,7 @@ def _check_norm_bwd(got, s, w, dy, ds, eps, rms, mask):
 @pytest.mark.parametrize("L,D", SHAPES)
 @pytest.mark.parametrize("rms,bias,given,p", [(False, True, False, None), (True, False, True, 0.1),
                                               (False, True, True, None), (True, True, False, 0.5),
-                                              (False, False, True, 0.0)])
+                                              (False, False, True, 0.0), (False, True, True, 0.3)])
 def test_norm_backward_matches_oracle(L, D, rms, bias, given, p):
     s, dy, (w, _) = _randn(3, L, D, std=2.0, mean=-0.5), _randn(4, L, D), _weights(D + 1, D)
     ds = _randn(5, L, D) if given else None
