@@ -10,8 +10,8 @@
 // order, and cut into chunks of equal length.  A CTA adds up a chunk's runs of
 // equal tokens: runs inside the chunk are a row of dW, the others leave shares,
 // which are added in the chunks' order.  Rows without a token are zeros, written
-// by CTAs of their own, beside the sums, looked up in the sorted tokens, or, at
-// small tables and few tokens, beside the sort.
+// by CTAs of their own: beside the sums, looked up in the sorted tokens, those at
+// the table's end beside the sort.
 //
 // What bounds it: HBM.  The gradient reads dy once and writes V rows, most of
 // them zeros at a real vocabulary; the sort, of 4 to 12 bytes a token, is its
@@ -40,7 +40,9 @@ constexpr int kFwdCols = 512;        // columns that a warp looks up
 constexpr int kSlice = 2048;         // columns of a CTA of the gradient: a vector of 8 per thread
 constexpr int kMaxChunk = 64;        // positions of a chunk
 constexpr int kZeroRows = 256;       // rows of a CTA that writes zeros, at most
-constexpr int64_t kSmallTable = int64_t(1) << 29;  // bytes of a table whose zeros are written beside the small sort
+constexpr int kZeroBytes = 1 << 16;  // bytes of them, or those of 32 rows (20000 tokens, 50257 x 768: 71 us, 88 with 768 KB)
+// Of the table's end, set to zero beside a small sort, and beside each launch of a longer one.
+constexpr int64_t kBesideSmall = int64_t(128) << 20, kBesideLaunch = int64_t(16) << 20;
 constexpr int kShort = 16;           // chunks behind its first that a short run reaches at most
 constexpr int kShortCols = 4 * kThreads;       // columns of a CTA that adds a short run's shares
 constexpr int kLongCols = 32, kLongRows = 32;  // of one that adds a long run's: columns, shares at once
@@ -104,6 +106,24 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const __grid_consta
 
 // ------------------------------------------------------------------- sort
 
+// Vectors of dW that CTAs beside the sort, which has no use for most SMs, set to
+// zero: rows with tokens too, which the sums write over.  At the table's end, as
+// frequent tokens mostly have small numbers, where there are more rows than tokens,
+// and no more bytes than the sort takes time for, the rest being written beside the
+// sums (8192 tokens, 128256 x 4096 318 us, 330 with none, 326 with 512 MB; 4099 tokens,
+// 30011 x 1032 37 for 46 with none; 20000 tokens, 50257 x 768 64 for 71; 32768 tokens,
+// 128256 x 4096 365 for 368, with 64 MB a launch 394).
+struct Zeros {
+  float4* dW;
+  int64_t from, end;
+};
+__device__ __forceinline__ void write_zeros(const Zeros& z, int cta, int ctas) {
+  const int64_t stride = static_cast<int64_t>(ctas) * blockDim.x;
+#pragma unroll 8
+  for (int64_t i = z.from + static_cast<int64_t>(cta) * blockDim.x + threadIdx.x; i < z.end; i += stride)
+    z.dW[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 // One pass of the sort: keys by kDigit bits from `shift` on.  The first pass
 // reads the tokens (those without a row get key V, behind all rows), later
 // passes the (key, position) pairs of the pass before.
@@ -115,6 +135,7 @@ struct SortParams {
   int2* out;
   int32_t* counts;  // [tiles][kBins]
   int* joins;       // [2], set to 0 on the way
+  Zeros zeros;      // by the CTAs behind the tiles'
 };
 
 constexpr int kBatch = 4;  // items that a lane has open at once, 32 apart
@@ -171,6 +192,7 @@ __device__ __forceinline__ void count_digits(const SortParams& p, int (*hist)[kB
 __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_constant__ SortParams p) {
   after_previous();
   let_next_start();
+  if (static_cast<int>(blockIdx.x) >= p.tiles) return write_zeros(p.zeros, blockIdx.x - p.tiles, gridDim.x - p.tiles);
   __shared__ int hist[kSortWarps][kBins];
   if (blockIdx.x == 0 && threadIdx.x < 2) p.joins[threadIdx.x] = 0;
   count_digits(p, hist);
@@ -185,6 +207,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_
 __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __grid_constant__ SortParams p) {
   after_previous();
   let_next_start();
+  if (static_cast<int>(blockIdx.x) >= p.tiles) return write_zeros(p.zeros, blockIdx.x - p.tiles, gridDim.x - p.tiles);
   __shared__ int hist[kSortWarps][kBins];
   __shared__ int warp_total[kSortWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -228,48 +251,15 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
 }
 
 // Up to kSmall tokens: one CTA sorts them, pairs in shared memory, a part of them
-// to each warp, per pass as above.  Meanwhile, at tables below kSmallTable, the
-// others write the rows without a token, which they tell by looking through all
-// tokens (4099 tokens, 30011 x 1032: 38 us for 46 with the zeros beside the sums;
-// 1024 tokens, 128256 x 4096: 339 for 297, its few large CTAs write more slowly).
+// to each warp, per pass as above.
 struct SmallParams {
   int L, V, D, wide, passes;
   const void* tokens;
   int2* out;
   int* joins;
-  float* dW;
+  Zeros zeros;
 };
 constexpr int kSmallBytes = 2 * kSmall * sizeof(int2) + kSmallWarps * kBins * sizeof(int);
-constexpr int kGroups = 32;  // groups of 32 rows that a CTA looks for at once
-
-// The CTAs take the groups in turns: together they write from one end of dW to
-// the other.
-__device__ __forceinline__ void zero_rows_without(const SmallParams& p, unsigned* has) {
-  const unsigned ctas = gridDim.x - 1, cta = blockIdx.x - 1;
-  int across = 2;  // threads of a row
-  while (across < 32 && across * 4 < p.D) across *= 2;
-  const int lane = threadIdx.x % across, quads = p.D / 4;
-  const int64_t stretch = static_cast<int64_t>(ctas) * 32 * kGroups;
-  for (int64_t from = 0; from < p.V; from += stretch) {
-    __syncthreads();
-    if (threadIdx.x < kGroups) has[threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.L; i += kSmallThreads) {
-      const int64_t t = token_at(p.tokens, p.wide, i);
-      if (t < from || t >= from + stretch) continue;
-      const unsigned at = static_cast<unsigned>(t - from), group = at / 32;
-      if (group % ctas == cta) atomicOr(&has[group / ctas], 1u << (at % 32));
-    }
-    __syncthreads();
-    for (int k = threadIdx.x / across; k < 32 * kGroups; k += kSmallThreads / across) {
-      const int64_t v = from + static_cast<int64_t>(k / 32 * ctas + cta) * 32 + k % 32;
-      if (v >= p.V || ((has[k / 32] >> (k % 32)) & 1)) continue;
-      float4* to = reinterpret_cast<float4*>(p.dW + v * p.D);
-#pragma unroll 4
-      for (int c = lane; c < quads; c += across) to[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  }
-}
 
 __global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const __grid_constant__ SmallParams p) {
   let_next_start();
@@ -278,7 +268,7 @@ __global__ void __launch_bounds__(kSmallThreads) embed_small_kernel(const __grid
   int2 *from = reinterpret_cast<int2*>(mem), *to = from + kSmall;
   int(*hist)[kBins] = reinterpret_cast<int(*)[kBins]>(mem + 2 * kSmall * sizeof(int2));
   if (blockIdx.x > 0) {
-    zero_rows_without(p, reinterpret_cast<unsigned*>(mem));
+    write_zeros(p.zeros, blockIdx.x - 1, gridDim.x - 1);
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -341,6 +331,7 @@ struct GradParams {
   int chunk, chunks;  // positions of a chunk, chunks
   int add;
   int zero_rows;      // rows of a CTA that writes zeros, at least 32
+  int late;           // rows whose zeros the sort has not written
   float scale;
   const bf16* dy;
   int64_t row;
@@ -404,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 4) embed_bwd_kernel(const __grid_con
         else
           hi = mid;
       }
-      none = v < p.V && (lo == end || __ldcg(&p.items[lo].x) != v);
+      none = v < p.late && (lo == end || __ldcg(&p.items[lo].x) != v);
     }
     const unsigned mask = __ballot_sync(0xffffffffu, none);
     if ((threadIdx.x & 31) == 0) empty[threadIdx.x >> 5] = mask;
@@ -640,13 +631,20 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   std::memset(&g, 0, sizeof(g));
   g.joins = reinterpret_cast<int*>(at + plan.join);
   g.join = reinterpret_cast<int4*>(g.joins) + 1;
-  bool zeros = !add;  // beside the sums
-  const bool beside = zeros && static_cast<int64_t>(c->V) * c->D * 4 < kSmallTable;  // the small sort
+  // Rows from `late` on are set to zero beside the sort, launch by launch.
+  const int launches = c->L <= kSmall ? 1 : 2 * plan.passes;
+  int64_t early = add || c->L >= c->V ? 0 : (c->L <= kSmall ? kBesideSmall : kBesideLaunch * launches) / (4 * c->D);
+  if (early > c->V) early = c->V;
+  g.late = c->V - static_cast<int>(early);
+  const int64_t from = static_cast<int64_t>(g.late) * (c->D / 4), vectors = early * (c->D / 4);
+  auto zeros = [&](int k) {
+    return Zeros{reinterpret_cast<float4*>(dW), from + vectors * k / launches, from + vectors * (k + 1) / launches};
+  };
+  const unsigned fill = early > 0 ? 152 : 0;
   if (c->L <= kSmall) {
     const SmallParams s{static_cast<int>(c->L), c->V, c->D, c->wide, plan.passes, tokens,
-                        reinterpret_cast<int2*>(at + plan.pairs[0]), g.joins, dW};
-    zeros = zeros && !beside;
-    UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT, launch_small(s, beside, st));
+                        reinterpret_cast<int2*>(at + plan.pairs[0]), g.joins, zeros(0)};
+    UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT, launch_small(s, early > 0, st));
     g.items = s.out;
   } else {
     SortParams s;
@@ -664,11 +662,13 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
       s.shift = i * kDigit;
       s.in = reinterpret_cast<const int2*>(at + plan.pairs[(i & 1) ^ 1]);
       s.out = reinterpret_cast<int2*>(at + plan.pairs[i & 1]);
+      s.zeros = zeros(2 * i);
       UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
-                   (i ? launch_next(embed_count_kernel, plan.tiles, kSortThreads, 0, st, s)
-                      : (embed_count_kernel<<<plan.tiles, kSortThreads, 0, st>>>(s), cudaGetLastError())));
+                   (i ? launch_next(embed_count_kernel, plan.tiles + fill, kSortThreads, 0, st, s)
+                      : (embed_count_kernel<<<plan.tiles + fill, kSortThreads, 0, st>>>(s), cudaGetLastError())));
+      s.zeros = zeros(2 * i + 1);
       UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT,
-                   launch_next(embed_scatter_kernel, plan.tiles, kSortThreads, 0, st, s));
+                   launch_next(embed_scatter_kernel, plan.tiles + fill, kSortThreads, 0, st, s));
     }
     g.items = s.out;
   }
@@ -684,8 +684,9 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   g.dW = dW;
   g.share = reinterpret_cast<float*>(at + plan.share);
   const int64_t sums = static_cast<int64_t>(plan.chunks) * ((c->D + kSlice - 1) / kSlice);
-  g.zero_rows = c->D < 1024 ? kZeroRows : 32;
-  const int64_t empty = zeros ? (static_cast<int64_t>(c->V) + g.zero_rows - 1) / g.zero_rows : 0;
+  g.zero_rows = kZeroBytes / (4 * c->D) / 32 * 32;
+  g.zero_rows = g.zero_rows < 32 ? 32 : g.zero_rows < kZeroRows ? g.zero_rows : kZeroRows;
+  const int64_t empty = add ? 0 : (static_cast<int64_t>(g.late) + g.zero_rows - 1) / g.zero_rows;
   UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD,
                launch_next(embed_bwd_kernel, static_cast<unsigned>(sums + empty), kThreads, 0, st, g));
   UPIPE_LAUNCH(UPIPE_KIND_EMBED_BWD, launch_next(embed_join_kernel, 152 * 8, kThreads, 0, st, g));

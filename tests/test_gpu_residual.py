@@ -371,7 +371,11 @@ def test_embedding_matches_oracle(L, V, D, wide, dtype):
 GRADS = [(1, 1, 8, "many"), (1, 5000, 264, "many"), (2, 511, 64, "many"), (300, 512, 256, "many"),
          (77, 1000, 1032, "many"), (2049, 37, 72, "many"), (5000, 300000, 16, "many"), (6000, 262144, 8, "many"),
          (1025, 40, 1000, "one"), (4099, 3001, 128, "few"), (33, 33, 4096, "one"), (4097, 700, 520, "many"),
-         (20000, 9, 24, "many"), (700, 5, 8192, "few"), (40000, 513, 8, "many"), (17000, 20000, 8, "many")]
+         (20000, 9, 24, "many"), (700, 5, 8192, "few"), (40000, 513, 8, "many"), (17000, 20000, 8, "many"),
+         # more rows than tokens: zeros beside the sort at the table's end, of all of it and of a part, beside one
+         # launch, four and six; the longest rows
+         (40, 33000, 1024, "many"), (8192, 8193, 16, "many"), (8200, 17000, 1024, "many"), (8193, 270000, 96, "many"),
+         (9000, 9001, 264, "few"), (20, 40, 65536, "many"), (40, 20, 40000, "many")]
 
 
 @pytest.mark.parametrize("L,V,D,kind", GRADS)
