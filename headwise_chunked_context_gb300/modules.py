@@ -228,12 +228,19 @@ def window_attention(q, k, v, window: int, sinks: int = 0):
 
 # ------------------------------------------------------ the residual stream
 
+def _table(w):
+    """A table in fp32 or bf16, copied where it is not dense from a 16-byte
+    boundary on (a parameter inside a flat buffer)."""
+    w = w if w.dtype in (torch.float32, torch.bfloat16) else w.float()
+    return w if w.is_contiguous() and w.data_ptr() % 16 == 0 else w.clone(memory_format=torch.contiguous_format)
+
+
 class _EmbedFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, w, tokens, scale):
         ctx.save_for_backward(tokens)
         ctx.V, ctx.scale = w.shape[0], scale
-        return upipe.embed_forward(tokens, w, scale)
+        return upipe.embed_forward(tokens, _table(w), scale)
 
     @staticmethod
     @once_differentiable
@@ -245,7 +252,8 @@ class TokenEmbedding(torch.nn.Module):
     """Rows of a table, ``scale * w[tokens]`` rounded to bf16 (upipe_embed_fwd
     / _bwd): tokens [L] int32 or int64 -> [L, D].  A negative token (padding)
     gives zeros and has no gradient, one past the table a row of NaN.  The
-    table is read as the fp32 master parameter that it is."""
+    table is read as the fp32 master parameter that it is (copied, call by
+    call, if it does not start on a 16-byte boundary)."""
 
     def __init__(self, V: int, D: int, scale: float = 1.0, device="cuda", init_std: float = 0.02):
         super().__init__()
@@ -253,8 +261,7 @@ class TokenEmbedding(torch.nn.Module):
         self.w = torch.nn.Parameter(torch.randn(V, D, device=device) * init_std)
 
     def forward(self, tokens):
-        w = self.w if self.w.dtype in (torch.float32, torch.bfloat16) else self.w.float()
-        return _EmbedFn.apply(w.contiguous(), tokens.contiguous(), self.scale)
+        return _EmbedFn.apply(self.w, tokens.contiguous(), self.scale)
 
 
 def _step(drop):

@@ -1,0 +1,38 @@
+"""Embedding, dropout and norms through the autograd front end on tensors that
+stand and change as a training program's do."""
+
+import pytest
+import torch
+
+from headwise_chunked_context_gb300 import upipe
+from headwise_chunked_context_gb300.modules import TokenEmbedding
+from tests.gpu_common import ensure_lib, status_ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_lib()
+
+
+def _randn(seed, *shape):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_a_table_inside_a_flat_buffer_reads_as_one_of_its_own(dtype, at):
+    V, D = 40, 264
+    w, dy = _randn(0, V, D).to(dtype), _randn(1, 50, D)
+    tokens = torch.arange(50, device="cuda") % 37 - 1
+    flat = torch.empty(V * D + 4, dtype=dtype, device="cuda")
+    emb = TokenEmbedding(V, D, scale=3.0)
+    emb.w = torch.nn.Parameter(flat[at:at + V * D].view(V, D).copy_(w))
+    assert emb.w.data_ptr() % 16
+    y = emb(tokens)
+    y.backward(dy)
+    assert torch.equal(y, upipe.embed_forward(tokens, w, 3.0))
+    assert emb.w.grad.dtype == dtype and torch.equal(emb.w.grad, upipe.embed_backward(tokens, dy, V, 3.0).to(dtype))
+    status_ok()
