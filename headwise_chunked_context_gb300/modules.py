@@ -268,17 +268,34 @@ def _step(drop):
     return None if drop is None else drop.step
 
 
+def _writes(drop):
+    """How often drop's step has been written to."""
+    step = _step(drop)
+    return None if step is None or step.is_inference() else step._version
+
+
+def _saved(ctx):
+    """The saved tensors of a call that drew a mask, which its backward draws
+    again.  They raise if the mask's step has changed since; but under activation
+    checkpointing they are the recomputation's, of the step as it is now."""
+    saved = ctx.saved_tensors
+    if _writes(ctx.drop) != ctx.writes:
+        raise RuntimeError("dropout: the step of a mask has changed between the forward and its recomputation, which "
+                           "drew another mask")
+    return saved
+
+
 class _DropoutFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, drop):
         ctx.save_for_backward(drop.step)  # which also sees to it that it is the forward's
-        ctx.drop = drop
+        ctx.drop, ctx.writes = drop, _writes(drop)
         return upipe.dropout_forward(drop, _heads(x), None if residual is None else _heads(residual))
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        ctx.saved_tensors  # raises if the step has changed
+        _saved(ctx)
         dx = upipe.dropout_backward(ctx.drop, _heads(dy)) if ctx.needs_input_grad[0] else None
         return dx, dy if ctx.needs_input_grad[1] else None, None
 
@@ -287,7 +304,10 @@ def dropout(x, drop, residual=None):
     """``residual + drop(x)`` (or ``drop(x)``) for x [L, D] bf16 and the mask
     `drop` (upipe.Dropout; None: nothing is dropped), differentiable.  The
     mask is a function of drop's numbers: give each call of a run numbers of
-    its own, and a recomputation the same."""
+    its own, and a recomputation the same.  A step that changes before the
+    backward raises there; by reentrant checkpointing, or where nothing that
+    the mask is drawn for has a gradient, it cannot be told: change it between
+    training steps only."""
     if drop is None:
         if residual is None:
             return x
@@ -303,14 +323,14 @@ class _LayerNormFn(torch.autograd.Function):
         residual, b = None if residual is None else _heads(residual), None if b is None else b.float()
         y, s = upipe.layer_norm_forward(x, w, b, eps, rms, residual, drop)
         ctx.save_for_backward(s, w, _step(drop))
-        ctx.args, ctx.bias = (eps, rms, drop), b is not None
+        ctx.args, ctx.bias, ctx.drop, ctx.writes = (eps, rms), b is not None, drop, _writes(drop)
         return y if s is x else (y, s)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, ds=None):
-        s, w, _ = ctx.saved_tensors
-        eps, rms, drop = ctx.args
+        s, w, _ = _saved(ctx)
+        (eps, rms), drop = ctx.args, ctx.drop
         if dy is not None:
             grads = upipe.layer_norm_backward(s, w, _heads(dy), None if ds is None else _heads(ds), eps, rms, ctx.bias,
                                               drop)
@@ -327,7 +347,7 @@ class LayerNorm(torch.nn.Module):
     ``y = norm(x)`` for x [L, D] bf16, or with a residual or a mask
     (upipe.Dropout) ``s = residual + drop(x); y = norm(s)`` in one pass, which
     returns (y, s): s is the residual stream behind the sum.  bias None: one
-    for layer norm, none for RMS norm."""
+    for layer norm, none for RMS norm.  Masks and their steps as in `dropout`."""
 
     def __init__(self, D: int, eps: float = 1e-5, rms: bool = False, bias=None, device="cuda"):
         super().__init__()

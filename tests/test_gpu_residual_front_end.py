@@ -3,9 +3,10 @@ stand and change as a training program's do."""
 
 import pytest
 import torch
+from torch.utils.checkpoint import checkpoint
 
 from headwise_chunked_context_gb300 import upipe
-from headwise_chunked_context_gb300.modules import TokenEmbedding
+from headwise_chunked_context_gb300.modules import LayerNorm, TokenEmbedding, dropout
 from tests.gpu_common import ensure_lib, status_ok
 
 pytestmark = pytest.mark.gpu
@@ -35,4 +36,24 @@ def test_a_table_inside_a_flat_buffer_reads_as_one_of_its_own(dtype, at):
     y.backward(dy)
     assert torch.equal(y, upipe.embed_forward(tokens, w, 3.0))
     assert emb.w.grad.dtype == dtype and torch.equal(emb.w.grad, upipe.embed_backward(tokens, dy, V, 3.0).to(dtype))
+    status_ok()
+
+
+@pytest.mark.parametrize("recompute", [False, True])
+def test_a_step_moved_before_the_backward_is_noticed_with_recomputation_too(recompute):
+    L, D = 70, 264
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    d, m, x = upipe.Dropout(0.3, seed=1, call=4, step=step), LayerNorm(D), _randn(2, L, D).requires_grad_()
+    for block in (lambda x: dropout(x, d, x), lambda x: m(x, x, d)[0], lambda x: m(x, None, d)[1]):
+        def run(recompute=recompute):
+            return checkpoint(block, x, use_reentrant=False) if recompute else block(x)
+
+        want = torch.autograd.grad(run(False).float().square().sum(), x)[0]
+        assert torch.equal(torch.autograd.grad(run().float().square().sum(), x)[0], want)
+        step += 1
+        y = run()
+        step += 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation|step .* has changed"):
+            y.float().square().sum().backward()
+        step -= 2
     status_ok()

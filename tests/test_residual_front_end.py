@@ -4,6 +4,7 @@ for where a call would reach it."""
 
 import pytest
 import torch
+from torch.utils.checkpoint import checkpoint
 
 from headwise_chunked_context_gb300 import modules, upipe
 
@@ -42,3 +43,66 @@ def test_tables_reach_the_lookup_dense_on_a_16_byte_boundary(monkeypatch, dtype,
     want = torch.zeros(V, D, dtype=dtype)
     want[3], want[0], want[29] = 2, 1, 1
     assert emb.w.grad.dtype == dtype and torch.equal(emb.w.grad, want)
+
+
+class _Mask:
+    """Stands in for upipe.Dropout: x (1 + step), so that each step is another mask."""
+
+    def __init__(self, step):
+        self.step = step
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    """The calls that dropout and LayerNorm make, of a stand-in's step alone."""
+    def factor(drop):
+        return 1 if drop is None or drop.step is None else 1 + drop.step.to(torch.bfloat16)
+
+    def norm(x, w, b, eps, rms, residual, drop):
+        s = x * factor(drop)
+        return s * w.bfloat16(), s
+
+    def norm_back(s, w, dy, ds, eps, rms, bias, drop):
+        d = dy * w.bfloat16() if ds is None else dy * w.bfloat16() + ds
+        return d * factor(drop), d, (dy * s).float().sum(0), dy.float().sum(0)
+
+    monkeypatch.setattr(upipe, "dropout_forward", lambda drop, x, r=None: x * factor(drop))
+    monkeypatch.setattr(upipe, "dropout_backward", lambda drop, dy: dy * factor(drop))
+    monkeypatch.setattr(upipe, "layer_norm_forward", norm)
+    monkeypatch.setattr(upipe, "layer_norm_backward", norm_back)
+    return modules.LayerNorm(8, device="cpu")
+
+
+@pytest.mark.parametrize("kind", ["dropout", "norm", "sum alone"])
+def test_a_step_moved_before_a_recomputation_is_noticed(plain, kind):
+    """Under activation checkpointing the step that a backward finds saved is the
+    recomputation's: the mask drawn again would be another one, without an error."""
+    step = torch.ones(1, dtype=torch.int64)
+    d, x = _Mask(step), torch.ones(4, 8, dtype=torch.bfloat16, requires_grad=True)
+
+    def block(x):
+        if kind == "dropout":
+            return modules.dropout(x, d)
+        y, s = plain(x, x, d)
+        return s * 2 if kind == "sum alone" else y
+
+    for recompute in (False, True):
+        def run():
+            return checkpoint(block, x, use_reentrant=False) if recompute else block(x)
+
+        run().float().sum().backward()  # as it was
+        step += 1
+        run().float().sum().backward()  # moved between steps
+        y = run()
+        step += 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation|step .* has changed"):
+            y.float().sum().backward()
+
+
+def test_steps_of_inference_mode_run_where_no_backward_follows(plain):
+    with torch.inference_mode():
+        d = _Mask(torch.ones(1, dtype=torch.int64))
+    x = torch.ones(4, 8, dtype=torch.bfloat16)
+    with torch.no_grad():
+        assert torch.equal(modules.dropout(x, d), 2 * x)
+        assert torch.equal(plain(x, None, d)[1], 2 * x)
