@@ -1098,18 +1098,14 @@ class Dropout:
                 raise ValueError(f"{n}: expected a number of 64 bits, got {v}")
         if first % 8 or first >> 63:
             raise ValueError(f"first: expected a multiple of 8 below 2^63, got {first}")
-        at = None
         if step is not None:
-            if not step.is_cuda or step.dtype != torch.int64 or step.numel() != 1:
-                raise ValueError(f"step: expected one int64 element on a CUDA device, got {tuple(step.shape)} "
-                                 f"{step.dtype} on {step.device}")
-            at = step.data_ptr()
-        c = DropoutCfg(p, int(seed), int(call), int(first), at)
+            _counter(step)
+        c = DropoutCfg(p, int(seed), int(call), int(first), None)
         for n, v in (("p", p), ("seed", c.seed), ("call", c.call), ("first", c.first), ("step", step), ("_c", c),
                      ("ref", ctypes.byref(c))):
             object.__setattr__(self, n, v)
 
-    def __setattr__(self, name, value):  # the kernels read `_c`
+    def __setattr__(self, name, value):  # the kernels read `_c`, or a copy of it with the step's address
         raise AttributeError(f"{name}: the numbers of a mask do not change; make another")
 
     def __reduce__(self):  # copies and pickles by value: `ref` is an address
@@ -1119,13 +1115,25 @@ class Dropout:
         return f"Dropout(p={self.p}, seed={self.seed}, call={self.call}, first={self.first}, step={self.step})"
 
 
+def _counter(step):
+    """Address of a mask's step."""
+    if not step.is_cuda or step.dtype != torch.int64 or step.numel() != 1:
+        raise ValueError(f"step: expected one int64 element on a CUDA device, got {tuple(step.shape)} "
+                         f"{step.dtype} on {step.device}")
+    return step.data_ptr()
+
+
 def _drop(drop, device):
-    """The mask's description; its `step` has to be on the call's device."""
+    """The mask's description; its `step`, read where it is now, has to be on
+    the call's device."""
     if drop is None:
         return None
-    if drop.step is not None and drop.step.get_device() != device:
+    if drop.step is None:
+        return drop.ref
+    at = _counter(drop.step)
+    if drop.step.get_device() != device:
         raise ValueError(f"dropout: step is on {drop.step.device}, the call's tensors on cuda:{device}")
-    return drop.ref
+    return ctypes.byref(DropoutCfg(drop.p, drop.seed, drop.call, drop.first, at))
 
 
 def dropout_apply(drop: Dropout, x, res, y, stream=None):

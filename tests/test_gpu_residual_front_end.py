@@ -57,3 +57,13 @@ def test_a_step_moved_before_the_backward_is_noticed_with_recomputation_too(reco
             y.float().square().sum().backward()
         step -= 2
     status_ok()
+
+
+def test_a_step_whose_memory_is_replaced_is_read_where_it_is():
+    x = _randn(3, 40, 520)
+    step = torch.tensor([5], device="cuda")
+    d = upipe.Dropout(0.4, seed=8, call=100, step=step)
+    for n in (5, 9):
+        step.data = torch.tensor([n], device="cuda")  # another tensor's memory; the old one's is free
+        assert torch.equal(upipe.dropout_forward(d, x), upipe.dropout_forward(upipe.Dropout(0.4, seed=8, call=100 + n), x))
+    status_ok()

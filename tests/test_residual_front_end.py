@@ -106,3 +106,37 @@ def test_steps_of_inference_mode_run_where_no_backward_follows(plain):
     with torch.no_grad():
         assert torch.equal(modules.dropout(x, d), 2 * x)
         assert torch.equal(plain(x, None, d)[1], 2 * x)
+
+
+class _Counter:
+    """A CUDA tensor of one int64 element, as far as a mask's description reads it."""
+    is_cuda, dtype, shape, device = True, torch.int64, (1,), "cuda:0"
+
+    def __init__(self):
+        self.at, self.n, self.index = 1 << 20, 1, 0
+
+    def numel(self):
+        return self.n
+
+    def data_ptr(self):
+        return self.at
+
+    def get_device(self):
+        return self.index
+
+
+def test_a_masks_step_is_looked_up_by_each_call():
+    """A counter's memory may be replaced (``step.data = ...``, a module moved): the
+    kernels read where it is, not where it was."""
+    step = _Counter()
+    d = upipe.Dropout(0.25, seed=(1 << 64) - 1, call=3, first=64, step=step)
+    for step.at in (1 << 20, 1 << 24):
+        c = upipe._drop(d, 0)._obj
+        assert (c.p, c.seed, c.call, c.first, c.step) == (0.25, (1 << 64) - 1, 3, 64, step.at)
+    step.n = 0  # its memory is gone
+    with pytest.raises(ValueError, match="step"):
+        upipe._drop(d, 0)
+    step.n, step.index = 1, 1
+    with pytest.raises(ValueError, match="step is on"):
+        upipe._drop(d, 0)
+    assert upipe._drop(upipe.Dropout(0.25, first=8), 0)._obj.step is None
