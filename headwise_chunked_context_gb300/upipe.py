@@ -10,6 +10,7 @@ fallback path, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 from dataclasses import dataclass
@@ -1093,6 +1094,7 @@ class Dropout:
         p = float(p)
         if not 0.0 <= p < 1.0 - 2.0 ** -33:
             raise ValueError(f"p: expected 0 <= p < 1, got {p}")
+        seed, call, first = (operator.index(v) for v in (seed, call, first))  # ctypes would cut a fraction off
         for n, v in (("seed", seed), ("call", call), ("first", first)):
             if not 0 <= v < 1 << 64:
                 raise ValueError(f"{n}: expected a number of 64 bits, got {v}")
@@ -1100,7 +1102,7 @@ class Dropout:
             raise ValueError(f"first: expected a multiple of 8 below 2^63, got {first}")
         if step is not None:
             _counter(step)
-        c = DropoutCfg(p, int(seed), int(call), int(first), None)
+        c = DropoutCfg(p, seed, call, first, None)
         for n, v in (("p", p), ("seed", c.seed), ("call", c.call), ("first", c.first), ("step", step), ("_c", c),
                      ("ref", ctypes.byref(c))):
             object.__setattr__(self, n, v)

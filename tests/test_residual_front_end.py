@@ -140,3 +140,15 @@ def test_a_masks_step_is_looked_up_by_each_call():
     with pytest.raises(ValueError, match="step is on"):
         upipe._drop(d, 0)
     assert upipe._drop(upipe.Dropout(0.25, first=8), 0)._obj.step is None
+
+
+@pytest.mark.parametrize("name", ["seed", "call", "first"])
+def test_a_masks_numbers_are_whole(name):
+    """A part of a number would be cut off: two masks that are told apart by it
+    would be one."""
+    for bad in (1.5, 8.0, "8"):
+        with pytest.raises(TypeError):
+            upipe.Dropout(0.1, **{name: bad})
+    for good in (8, torch.tensor(8), torch.tensor([8]).numpy()[0]):
+        d = upipe.Dropout(0.1, **{name: good})
+        assert getattr(d, name) == 8 and type(getattr(d, name)) is int
