@@ -10,7 +10,6 @@ fallback path, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
 import struct
 from dataclasses import dataclass
@@ -1094,10 +1093,10 @@ class Dropout:
         p = float(p)
         if not 0.0 <= p < 1.0 - 2.0 ** -33:
             raise ValueError(f"p: expected 0 <= p < 1, got {p}")
-        seed, call, first = (operator.index(v) for v in (seed, call, first))  # ctypes would cut a fraction off
         for n, v in (("seed", seed), ("call", call), ("first", first)):
-            if not 0 <= v < 1 << 64:
+            if not 0 <= v < 1 << 64 or int(v) != v:  # a C number's fraction would be cut off
                 raise ValueError(f"{n}: expected a number of 64 bits, got {v}")
+        seed, call, first = int(seed), int(call), int(first)
         if first % 8 or first >> 63:
             raise ValueError(f"first: expected a multiple of 8 below 2^63, got {first}")
         if step is not None:

@@ -146,9 +146,10 @@ def test_a_masks_step_is_looked_up_by_each_call():
 def test_a_masks_numbers_are_whole(name):
     """A part of a number would be cut off: two masks that are told apart by it
     would be one."""
-    for bad in (1.5, 8.0, "8"):
-        with pytest.raises(TypeError):
+    for bad in (0.5, 1.5, 8.25, -0.5, float("nan"), float("inf")):
+        with pytest.raises(ValueError, match=name):
             upipe.Dropout(0.1, **{name: bad})
-    for good in (8, torch.tensor(8), torch.tensor([8]).numpy()[0]):
+    for good in (8, 8.0, torch.tensor(8).numpy()[()]):
         d = upipe.Dropout(0.1, **{name: good})
         assert getattr(d, name) == 8 and type(getattr(d, name)) is int
+    assert getattr(upipe.Dropout(0.1, **{name: 2.0 ** 62}), name) == 1 << 62
