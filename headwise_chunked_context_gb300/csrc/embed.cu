@@ -40,7 +40,7 @@ constexpr int kFwdCols = 512;        // columns that a warp looks up
 constexpr int kSlice = 2048;         // columns of a CTA of the gradient: a vector of 8 per thread
 constexpr int kMaxChunk = 64;        // positions of a chunk
 constexpr int kZeroRows = 256;       // rows of a CTA that writes zeros, at most
-constexpr int kZeroBytes = 1 << 16;  // bytes of them, or those of 32 rows (20000 tokens, 50257 x 768: 71 us, 88 with 768 KB)
+constexpr int kZeroBytes = 1 << 16;  // bytes of them, or those of 32 rows (20000 tokens, 50257 x 768: 63 us, 89 with 768 KB)
 // Of the table's end, set to zero beside a small sort, and beside each launch of a longer one.
 constexpr int64_t kBesideSmall = int64_t(128) << 20, kBesideLaunch = int64_t(16) << 20;
 constexpr int kShort = 16;           // chunks behind its first that a short run reaches at most
@@ -110,9 +110,9 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const __grid_consta
 // zero: rows with tokens too, which the sums write over.  At the table's end, as
 // frequent tokens mostly have small numbers, where there are more rows than tokens,
 // and no more bytes than the sort takes time for, the rest being written beside the
-// sums (8192 tokens, 128256 x 4096 318 us, 330 with none, 326 with 512 MB; 4099 tokens,
-// 30011 x 1032 37 for 46 with none; 20000 tokens, 50257 x 768 64 for 71; 32768 tokens,
-// 128256 x 4096 365 for 368, with 64 MB a launch 394).
+// sums (8192 tokens, 128256 x 4096 316 us, 329 with none, 325 with 512 MB; 4099 tokens,
+// 30011 x 1032 36 for 48 with none; 20000 tokens, 50257 x 768 63 for 70, with 64 MB a
+// launch 68; 32768 tokens, 128256 x 4096 363 for 366, with 64 MB a launch 378).
 struct Zeros {
   float4* dW;
   int64_t from, end;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
 // Up to kSmall tokens: one CTA sorts them, pairs in shared memory, a part of them
 // to each warp, per pass as above.
 struct SmallParams {
-  int L, V, D, wide, passes;
+  int L, V, wide, passes;
   const void* tokens;
   int2* out;
   int* joins;
@@ -342,8 +342,8 @@ struct GradParams {
   int4* join;         // [2][chunks]: first chunk, last chunk, token of each
 };
 
-// The same for a whole warp: the first of the n sorted items whose token is at
-// least v, by 32 probes at once.
+// The first of the n sorted items whose token is at least v, found by a whole warp
+// with 32 probes at once.
 __device__ __forceinline__ int64_t warp_lower_bound(const int2* items, int64_t n, int64_t v) {
   const int lane = threadIdx.x & 31;
   int64_t lo = 0, end = n;  // it is in [lo, end]
@@ -642,7 +642,7 @@ int upipe_embed_bwd(const upipe_embed_cfg* c, const void* tokens, const upipe_ro
   };
   const unsigned fill = early > 0 ? 152 : 0;
   if (c->L <= kSmall) {
-    const SmallParams s{static_cast<int>(c->L), c->V, c->D, c->wide, plan.passes, tokens,
+    const SmallParams s{static_cast<int>(c->L), c->V, c->wide, plan.passes, tokens,
                         reinterpret_cast<int2*>(at + plan.pairs[0]), g.joins, zeros(0)};
     UPIPE_LAUNCH(UPIPE_KIND_EMBED_SORT, launch_small(s, early > 0, st));
     g.items = s.out;
