@@ -304,10 +304,10 @@ def dropout(x, drop, residual=None):
     """``residual + drop(x)`` (or ``drop(x)``) for x [L, D] bf16 and the mask
     `drop` (upipe.Dropout; None: nothing is dropped), differentiable.  The
     mask is a function of drop's numbers: give each call of a run numbers of
-    its own, and a recomputation the same.  A step that changes before the
-    backward raises there; by reentrant checkpointing, or where nothing that
-    the mask is drawn for has a gradient, it cannot be told: change it between
-    training steps only."""
+    its own, and a recomputation the same.  A step that is written to before the
+    backward raises there, whatever it holds then; under reentrant
+    checkpointing, or where nothing that the mask is drawn for has a gradient,
+    it cannot be told: write to it between training steps only."""
     if drop is None:
         if residual is None:
             return x
